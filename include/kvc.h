@@ -279,6 +279,101 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream);
 int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, int32_t n,
                    void* d_out, kvc_stream_t stream);
 
+/* Packed prompts ([PREFIX] model.chunk(tokens[cut:], cache) for a batch whose requests
+ * have cuts and lengths of their own).  Request b brings h_counts[b] >= 0 rows (host, B
+ * entries); the rows lie packed, request after request, T = the sum of the counts in all:
+ *     d_q [T][Hq][d], d_k, d_v [T][Hkv][d]  ->  d_out [T][Hq][d].
+ * q_stride and kv_stride are the elements from one packed row to the next (0 = dense, Hq d
+ * and Hkv d), so that the three may be views of one projection's output; the heads of a
+ * row are dense.  Appends every row as kvc_append_rows does and answers row i of request b
+ * at p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32
+ * and rounded to the cache's type, as the keys are; sums and softmax are fp32.
+ * bf16 caches with head_dim 64 or 128 run on the tensor cores, where the softmax weights
+ * are rounded to bf16 too (relative error at most 2^-8 each, the sum taken over the
+ * rounded weights); other shapes run in fp32 throughout.  What a masked key or value row
+ * holds, infinities and NaN among it, does not reach the result.
+ * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
+ * All tiers but INT8; a ring needs a bf16 cache with W a multiple of 16, and counts of at
+ * most max_chunk (its rows are staged, as kvc_chunk_attn's are).
+ * KVC_ERR_ARG: a negative count, a count above max_chunk on a ring, T > 2^31 - 1, a stride
+ * below the row, or one that is no multiple of 16 bytes where a head's row is one.
+ * KVC_ERR_CAPACITY: as kvc_append_rows; nothing is written.  KVC_ERR_UNSUPPORTED: INT8
+ * caches, other rings. */
+int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k, const void* d_v,
+                    int64_t kv_stride, const int32_t* h_counts, void* d_out, kvc_stream_t stream);
+
+/* ---- whole requests: fork, copy, free; pages: compact --------------------------
+ * [LOOP] §八 Q1, [LEAN] §6.1: requests that branch from one prompt share its pages.  A
+ * physical page of a paged cache may be named by the block tables of several requests.
+ * Any call that is about to write rows into a shared page (append, prompt, chunk) first
+ * maps a page of its own for that request and copies the rows it keeps: forked requests
+ * are independent, and only what they write costs memory.  Such a call needs a free page
+ * for each page it copies (KVC_ERR_CAPACITY otherwise; nothing changes); under stream
+ * capture it returns KVC_ERR_UNSUPPORTED (a replay would copy again, over newer rows):
+ * append once before capturing.  Trim, free and the store give up a request's hold on a
+ * page; the page is free when its last holder gave it up.
+ * These calls keep books on the host (the lengths that kvc_next_positions reports and
+ * the block table): they return KVC_ERR_UNSUPPORTED on a stream under capture, and a
+ * handle whose captured calls were replayed has lengths on the device that the host does
+ * not know. */
+
+/* Requests h_dst[i] become copies of requests h_src[i] (host, n entries each, of [0, B)):
+ * rows, positions, next_position and, in Tier B, the request ID (a branch draws the same
+ * dithers as its source).  What the destinations held is given up.  A source may appear
+ * more than once; a destination may not, nor may it be a source.  A paged cache copies no
+ * rows (see above) and needs no free page; an unpaged one reads the source's rows once and
+ * writes them for every destination.
+ * KVC_ERR_ARG: bad index.  KVC_ERR_UNSUPPORTED: a source with blocks restored by
+ * kvc_int8_restore, or stream capture. */
+int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc_stream_t stream);
+
+/* Requests h_dst[i] of cache `to` become copies of requests h_src[i] of cache `from`, with
+ * rows of their own (on a paged cache, pages of their own).  Both caches on the current
+ * device, with the same dtype, kv_quant, layout, n_kv_heads, head_dim and rope_base (and,
+ * in Tier B, layer and key); paged or not, batch, query heads and, on contiguous caches,
+ * capacity and window may differ; rings are of the same W.  to == from is allowed: a
+ * destination must not be a source then.  The caller orders the streams of the two handles.
+ * KVC_ERR_ARG: other caches or a bad index.  KVC_ERR_CAPACITY: rows beyond the capacity
+ * or RoPE table of `to`, or too few free pages; nothing changes.  KVC_ERR_UNSUPPORTED: as
+ * kvc_fork. */
+int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_t* h_dst,
+             kvc_stream_t stream);
+
+/* Empties the n distinct requests h_b: next_position 0, positions -1, every page given up
+ * (a ring's too).  Other requests are untouched. */
+int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream);
+
+/* Paged caches: moves pages so that every page in use lies below *h_used, their number:
+ * the first *h_used pages of each per-page array (kvc_region) then hold everything.  No
+ * more pages move than have to; requests see no change.  Free pages are taken in ascending
+ * order afterwards.  KVC_ERR_UNSUPPORTED: an unpaged cache, or stream capture. */
+int kvc_compact(kvc_t h, int32_t* h_used, kvc_stream_t stream);
+
+/* Paged caches, host only: free pages, and pages that more than one request holds.
+ * KVC_ERR_UNSUPPORTED: an unpaged cache. */
+int kvc_page_counts(kvc_t h, int32_t* h_free, int32_t* h_shared);
+
+/* ---- rotary positions with several axes -----------------------------------------
+ * Tokens of images and video carry a position on each of several axes (time, height,
+ * width), where a cache's own RoPE knows one.  With rope_base 0 a cache stores keys as
+ * they are given: rotate queries and keys here, then append, decode or prompt.
+ *     y[r][h] = R(angles of row r) x[r][h],    x, y [rows][heads][head_dim] of `dtype`
+ * Row strides x_stride, y_stride in elements (0 = dense); heads of a row are dense.
+ * d_pos: int32 [n_axes][rows], any value; 1 <= n_axes <= 8.  h_sections: host, pairs of each
+ * axis in turn; their sum P <= head_dim/2, the dims from 2P on pass through.  Pair p
+ * belongs to the axis a whose section it lies in, as the section's pair j, and turns by
+ *     d_pos[a][r] * base^(-p/P),  with KVC_ROPE_PER_AXIS  d_pos[a][r] * base^(-j/h_sections[a]).
+ * Its dims are (2p, 2p+1), with KVC_ROPE_HALVES (p, P+p).  Angles are held to 2^-64 of a turn per
+ * position; products and sums in fp32, each rounded once, then rounded to dtype.
+ * d_y may be d_x (same strides); otherwise the two ranges must not overlap.  d_x and d_y
+ * need the alignment of an element; 16-byte aligned rows are faster.
+ * KVC_ERR_ARG: a bad size, section, flag, stride, base (positive and finite) or overlap. */
+enum { KVC_ROPE_HALVES = 1, KVC_ROPE_PER_AXIS = 2 };
+int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride, int32_t dtype,
+                  int64_t rows, int32_t heads, int32_t head_dim, const int32_t* d_pos,
+                  int32_t n_axes, const int32_t* h_sections, double base, int32_t flags,
+                  kvc_stream_t stream);
+
 /* ---- gated fallback of the INT8 tier ----------------------------------
  * [WITCERT] "SGLang 生产级落地与闭环门控修复": once the risk of a head or a block
  * crosses the water line, the lossless block is swapped in from the full-precision
@@ -348,6 +443,12 @@ int kvc_export_bytes(kvc_t h, int32_t which, size_t* bytes);
  * KVC_ERR_ARG), after the work already queued on `stream`; returns when the copy
  * is complete. */
 int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t stream);
+
+/* Host only: where array `which` (KVC_EXPORT_*) lies inside the state buffer, as stored:
+ * byte offset and size.  K and V: [B][Hkv][capacity][d], paged [page_pool][Hkv][16][d] in
+ * physical page order.  For reading on the device, ordered behind the calls that write.
+ * KVC_ERR_ARG: a null pointer or an array the cache does not hold. */
+int kvc_region(kvc_t h, int32_t which, size_t* offset, size_t* bytes);
 
 /* Host mirror of next_position (B entries), kept by the handle.  Enqueued but
  * unexecuted work is already counted. */

@@ -176,7 +176,6 @@ inline cudaStream_t S_(kvc_stream_t s) { return static_cast<cudaStream_t>(s); }
 template <typename T>
 T* at(kvc_handle* h, size_t off) { return reinterpret_cast<T*>(h->state + off); }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // {cos, sin} of angle p * base^(-(2i)/d) (double), each rounded once to fp32.
 void rope_table(double base, int d, int P, float2* out) {
@@ -300,6 +299,7 @@ int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t 
         e = cudaMemsetAsync(h->state + L.table, 0xff, (size_t)s.B * (s.S / kPage) * 4, st);
         h->table_h.assign((size_t)s.B * (s.S / kPage), -1);
         h->page_free.resize(s.pages);
+        h->page_ref.assign(s.pages, 0);
         for (int i = 0; i < s.pages; ++i) h->page_free[i] = i;
         uint64_t x = 0x9E3779B97F4A7C15ull;
         for (int i = s.pages - 1; i > 0; --i) {
@@ -449,8 +449,7 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) {
             for (int lp = (h_cut[b] + kPage - 1) / kPage; lp < npg; ++lp) {
                 int32_t& e = h->table_h[(size_t)b * npg + lp];
                 if (e < 0) continue;
-                h->page_free.push_back(e);
-                e = -1;
+                drop_page(h, e);
                 freed = true;
             }
         if (freed && cudaMemcpyAsync(h->state + h->L.table, h->table_h.data(), h->table_h.size() * 4,
@@ -498,6 +497,42 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
     return KVC_OK;
 }
 
+int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k, const void* d_v, int64_t kv_stride,
+                    const int32_t* h_counts, void* d_out, kvc_stream_t stream) try {
+    if (!h || !on_device(h) || !h_counts) return KVC_ERR_ARG;
+    const Shape& s = h->sh;
+    if (!prompt_supported(s)) return KVC_ERR_UNSUPPORTED;
+    long long total = 0;
+    for (int b = 0; b < s.B; ++b) {
+        if (h_counts[b] < 0 || (s.ring && h_counts[b] > s.max_chunk)) return KVC_ERR_ARG;
+        total += h_counts[b];
+    }
+    if (total > 0x7fffffffLL) return KVC_ERR_ARG;
+    PromptArgs a{d_q, d_k, d_v, d_out, q_stride ? q_stride : (long long)s.Hq * s.d,
+                 kv_stride ? kv_stride : (long long)s.Hkv * s.d};
+    if (a.q_stride < (long long)s.Hq * s.d || a.kv_stride < (long long)s.Hkv * s.d ||
+        (s.d * s.elem % 16 == 0 && (a.q_stride * s.elem % 16 || a.kv_stride * s.elem % 16)))
+        return KVC_ERR_ARG;
+    if (total == 0) return KVC_OK;
+    if (!d_q || !d_k || !d_v || !d_out || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out))
+        return KVC_ERR_ARG;
+    int rc = check_capacity(h, h_counts, 0);
+    if (rc) return rc;
+    cudaStream_t st = S_(stream);
+    if (s.pages) {
+        std::vector<int> from(h->np.begin(), h->np.end()), to(from);
+        for (int b = 0; b < s.B; ++b) to[b] += h_counts[b];
+        if (map_pages(h, from, to, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
+        if (rc) return rc;
+    }
+    if (launch_prompt(h, a, h_counts, st) != cudaSuccess) return KVC_ERR_CUDA;
+    for (int b = 0; b < s.B; ++b) h->np[b] += h_counts[b];
+    h->ring_needs_append = false;
+    return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
+}
+
 int kvc_export_bytes(kvc_t h, int32_t which, size_t* bytes) {
     if (!h || !bytes) return KVC_ERR_ARG;
     const Shape& s = h->sh;
@@ -524,6 +559,33 @@ int kvc_export_bytes(kvc_t h, int32_t which, size_t* bytes) {
         case KVC_EXPORT_XMAP: *bytes = B * Hkv * (S / kQBlock) * 4; return KVC_OK;
         default: return KVC_ERR_ARG;
     }
+}
+
+int kvc_region(kvc_t h, int32_t which, size_t* offset, size_t* bytes) {
+    if (!offset) return KVC_ERR_ARG;
+    int rc = kvc_export_bytes(h, which, bytes);
+    if (rc) return rc;
+    const Shape& s = h->sh;
+    const Layout& L = h->L;
+    // blocks of 16 slots and one KV head, where the per-block arrays are paged
+    const size_t blocks = s.pages ? (size_t)s.pages * s.Hkv : 0;
+    switch (which) {
+        case KVC_EXPORT_K: *offset = L.k; if (blocks) *bytes = blocks * kPage * s.d * s.elem; break;
+        case KVC_EXPORT_V: *offset = L.v; if (blocks) *bytes = blocks * kPage * s.d * s.elem; break;
+        case KVC_EXPORT_POSITIONS: *offset = L.pos; break;
+        case KVC_EXPORT_NEXT_POSITION: *offset = L.next_pos; break;
+        case KVC_EXPORT_KQ: *offset = L.kq; if (blocks) *bytes = blocks * kQBlock * s.d; break;
+        case KVC_EXPORT_VQ: *offset = L.vq; if (blocks) *bytes = blocks * kQBlock * s.d; break;
+        case KVC_EXPORT_SK: *offset = L.sk; if (blocks) *bytes = blocks * 4; break;
+        case KVC_EXPORT_SV: *offset = L.sv; if (blocks) *bytes = blocks * 4; break;
+        case KVC_EXPORT_WITNESS: *offset = L.wit; if (blocks) *bytes = blocks * kQBlock * kBands * 2; break;
+        case KVC_EXPORT_KTAIL: *offset = L.ktail; break;
+        case KVC_EXPORT_VTAIL: *offset = L.vtail; break;
+        case KVC_EXPORT_XMAP: *offset = L.xmap; break;
+        case KVC_EXPORT_PAGE_TABLE: *offset = L.table; break;
+        default: return KVC_ERR_ARG;
+    }
+    return KVC_OK;
 }
 
 int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t stream) {

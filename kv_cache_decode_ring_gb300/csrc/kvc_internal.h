@@ -92,6 +92,8 @@ inline int int8_grid(const Shape& s) {
     return (int)(((int8_qkeys(s) + kQBlock - 1) / kQBlock + bps - 1) / bps) + 1;
 }
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 bool make_shape(const kvc_config& c, Shape* s);
 // Rows per (request, KV head) of a ring's chunk staging: positions from the cut rounded
 // down to 16 up to the last suffix row rounded up to 16.
@@ -161,9 +163,15 @@ bool make_tensor_map_bf16(CUtensorMap* tm, void* base, int rank, const cuuint64_
 cudaError_t launch_append_token(const AppendArgs& a, cudaStream_t st);
 // INT8 gated fallback (int8_gate.cu): drop restored blocks that a trim removed
 cudaError_t int8_drop_restored(kvc_handle* h, const int32_t* h_cut, cudaStream_t st);
-// paged caches (append.cu): map the pages that slots [from, to) of each request need
+// paged caches (pages.cu): give every request b pages of its own for slots [from[b], to[b]),
+// mapping the missing ones and copying those it shares with another request
 cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::vector<int>& to, cudaStream_t st,
                       int* status);
+// one entry of the host block table gives its page up (entry = -1); the page is free once
+// its last holder did
+void drop_page(kvc_handle* h, int32_t& entry);
+// pages that come free when every request with drop[b] != 0 gives up all of its pages
+int pages_released(const kvc_handle* h, const std::vector<char>& drop);
 cudaError_t launch_trim_cuts(int32_t* next_pos, int32_t* pos, const int32_t* cuts, int B, int S, int ring,
                              cudaStream_t st);
 
@@ -184,6 +192,16 @@ cudaError_t launch_decode(const DecodeArgs& d, const CombineArgs& c, bool fast, 
 bool chunk_supported(const Shape& s);
 bool gqa_decode_supported(int d, int g);
 cudaError_t launch_decode_gqa(const DecodeArgs& a, const KvMaps& maps, cudaStream_t st);
+// Packed prompts (prompt.cu): append the rows of every request and attend.
+struct PromptArgs {
+    const void* q;        // row t of the packed rows at t * q_stride elements, [Hq][d] in a row
+    const void* k;        // ... at t * kv_stride, [Hkv][d] in a row, keys not rotated
+    const void* v;
+    void* out;            // [T][Hq][d]
+    long long q_stride, kv_stride;
+};
+bool prompt_supported(const Shape& s);
+cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& a, const int32_t* counts, cudaStream_t st);
 // Chunked suffix attention (chunk.cu).  A contiguous cache has already appended the n
 // suffix rows; a ring first stages them (rotated) next to its resident rows and
 // appends them after the attention (the caller does).
@@ -367,8 +385,9 @@ struct kvc_handle {
     // the free pool entries
     std::vector<int32_t> xmap_h, xn_h, xfree;
     std::vector<int32_t> xlist_h, xent_h;   // mirrors of the per-head lists
-    // paged caches: host mirror of the block table and the free pages
-    std::vector<int32_t> table_h, page_free;
+    // paged caches: host mirror of the block table, the free pages, and how many table
+    // entries name each page (requests forked from one another share pages)
+    std::vector<int32_t> table_h, page_free, page_ref;
     // prefix store: rows saved in each store slot (-1 = empty)
     std::vector<int32_t> store_n;
     // Tier B: host mirror of the request IDs
@@ -380,4 +399,10 @@ struct kvc_handle {
 inline bool on_device(const kvc_handle* h) {
     int dev = -1;
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+// Whether `st` is being captured into a graph (true also where the runtime cannot tell).
+inline bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(st, &c) != cudaSuccess || c != cudaStreamCaptureStatusNone;
 }

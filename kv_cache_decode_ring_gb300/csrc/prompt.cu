@@ -1,0 +1,372 @@
+// prompt.cu -- packed prompts: the rows of every request, each request with a count of its
+// own, appended to the cache and attended causally in one call.
+//
+// [PREFIX] "哪些東西必須一起裁剪" for a batch whose requests have cuts and suffix lengths of
+// their own: request b brings n_b rows (possibly none), packed behind those of request
+// b - 1; its row i sits at position p = c_b + i, c_b its next_position, and attends to
+// positions [max(0, p - W + 1), p] ([LEAN] §2.1), those below c_b from the cache.
+// Keys and queries are rotated in fp32 and rounded to the cache's type, the query as its
+// key is: both products then take the cache's own type.
+//
+// Rows of one (request, KV head) are (token, query head of the group) pairs, token-major:
+// a tile of query rows holds a few tokens' whole groups, so a group's heads share every
+// key and value read, and short prompts still fill a tile.
+//
+// On a ring of W slots, appending first would evict rows that early queries need
+// ([LEAN] §3.4): the rotated rows are staged beside the resident rows from the cut
+// rounded down to 16, attended, and appended afterwards, as the chunk call does.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "async_copy.h"
+#include "kvc_internal.h"
+
+namespace kvc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGroup = 1024;           // requests per launch: their offsets ride in the parameters
+
+// What every kernel of a call knows about its requests [b0, b0 + nb).
+struct Packed {
+    long long row0;                       // packed row of request b0's first row
+    int b0, nb;
+    int off[kMaxGroup + 1];               // request b0 + i brings rows [off[i], off[i + 1]) from row0 on
+};
+
+struct RowArgs {
+    const void* k; const void* v;         // packed rows, stride kv_stride, keys not rotated
+    long long stride;
+    void* kc; void* vc;                   // cache rows
+    __nv_bfloat16* wk; __nv_bfloat16* wv; // ring staging [B][Hkv][ws_rows][d]
+    const int32_t* table;
+    int32_t* pos;
+    const int32_t* next_pos;              // the cut: advanced after every kernel of the call
+    const float2* rope;
+    uint32_t* hdr;
+    int Hkv, d, S, P, ring, bf16, ws_rows;
+    int stage;                            // 1: into the staging rows, with the resident rows they follow
+};
+
+__device__ __forceinline__ bool position_ok(const RowArgs& a, long long p) {
+    return p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P);
+}
+
+// Row of the staging area that holds position p >= cut rounded down to 16.
+__device__ __forceinline__ size_t stage_row(int b, int h, int p, int cut, int Hkv, int ws_rows) {
+    return ((size_t)b * Hkv + h) * ws_rows + (p - (cut & ~15));
+}
+
+constexpr int kRowsPerCta = 8;
+
+// grid (row groups of the longest request, requests).  VEC: bf16 rows in 16-byte units, d a
+// multiple of 8; otherwise a pair per item.  RoPE in fp32, each product and sum rounded
+// once, one rounding to the cache's type: the arithmetic of the other appends.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, const __grid_constant__ Packed g) {
+    const int bi = blockIdx.y, b = g.b0 + bi;
+    const int n = g.off[bi + 1] - g.off[bi];
+    const int cut = a.next_pos[b], d = a.d;
+    const int lead = a.stage ? cut & 15 : 0;                    // resident rows staged before the first new one
+    const int r0 = blockIdx.x * kRowsPerCta - lead;
+    if (n == 0 || r0 >= n) return;
+    const int rows = min(n - r0, kRowsPerCta);
+    const int per = VEC ? d / 8 : d / 2, total = rows * a.Hkv * per;
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+        const int c = i % per, h = (i / per) % a.Hkv, r = r0 + i / (per * a.Hkv);
+        const long long p = (long long)cut + r;
+        if (!a.stage && a.ring && r < n - a.S) continue;        // overwritten later in this call
+        if (!position_ok(a, p)) { atomicOr(a.hdr, kErrPosition); continue; }
+        const int slot = a.ring ? (int)(p % a.S) : (int)p;
+        const size_t crow = kv_row(a.table, b, h, slot, a.Hkv, a.S) * d;
+        const size_t dst = a.stage ? stage_row(b, h, (int)p, cut, a.Hkv, a.ws_rows) * d : crow;
+        void* kd = a.stage ? a.wk : a.kc;
+        void* vd = a.stage ? a.wv : a.vc;
+        const size_t src = (size_t)(g.row0 + g.off[bi] + r) * a.stride + (size_t)h * d;   // (used for r >= 0)
+        if constexpr (VEC) {
+            uint4 ko, vo;
+            if (r < 0) {
+                ko = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kc) + crow + 8 * c);
+                vo = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vc) + crow + 8 * c);
+            } else {
+                ko = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src + 8 * c));
+                vo = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
+                if (a.rope) {
+                    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (d / 2) + 4 * c);
+                    const float4 c0 = __ldg(rp), c1 = __ldg(rp + 1);
+                    uint32_t w[4] = {ko.x, ko.y, ko.z, ko.w};
+                    const float2 cs[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
+                                          make_float2(c1.z, c1.w)};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y0, y1;
+                        rope_pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u), cs[e], y0, y1);
+                        const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
+                        w[e] = *reinterpret_cast<const uint32_t*>(&o2);
+                    }
+                    ko = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(kd) + dst + 8 * c) = ko;
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(vd) + dst + 8 * c) = vo;
+        } else {
+            float k0, k1, v0, v1;
+            if (r < 0) {
+                k0 = ld_elem(a.kc, crow + 2 * c, a.bf16); k1 = ld_elem(a.kc, crow + 2 * c + 1, a.bf16);
+                v0 = ld_elem(a.vc, crow + 2 * c, a.bf16); v1 = ld_elem(a.vc, crow + 2 * c + 1, a.bf16);
+            } else {
+                k0 = ld_elem(a.k, src + 2 * c, a.bf16); k1 = ld_elem(a.k, src + 2 * c + 1, a.bf16);
+                v0 = ld_elem(a.v, src + 2 * c, a.bf16); v1 = ld_elem(a.v, src + 2 * c + 1, a.bf16);
+                if (a.rope) {
+                    const float x0 = k0, x1 = k1;
+                    rope_pair(x0, x1, a.rope[(size_t)p * (d / 2) + c], k0, k1);
+                }
+            }
+            if (a.bf16) {
+                reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(kd) + dst)[c] = __floats2bfloat162_rn(k0, k1);
+                reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(vd) + dst)[c] = __floats2bfloat162_rn(v0, v1);
+            } else {
+                reinterpret_cast<float2*>(static_cast<float*>(kd) + dst)[c] = make_float2(k0, k1);
+                reinterpret_cast<float2*>(static_cast<float*>(vd) + dst)[c] = make_float2(v0, v1);
+            }
+        }
+        if (!a.stage && h == 0 && c == 0) a.pos[(size_t)b * a.S + slot] = (int)p;
+    }
+}
+
+__global__ void prompt_advance_kernel(int32_t* next_pos, const __grid_constant__ Packed g) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < g.nb) next_pos[g.b0 + i] += g.off[i + 1] - g.off[i];
+}
+
+// ---- attention on the CUDA cores: fp32 caches and other head sizes ------------------
+// CTA = 32 query rows (token, head) of one (request, KV head); 8 warps of 4 rows.  Tiles of
+// 64 keys in shared memory as fp32; lane = key for the scores, lane = dim for P.V; the
+// running maximum and sum of a row live in its warp.  Everything in fp32.
+constexpr int kBM = 32, kBN = 64;
+
+struct AttnArgs {
+    const void* q;
+    void* out;
+    long long q_stride;
+    const void* kc; const void* vc;
+    const __nv_bfloat16* wk; const __nv_bfloat16* wv;
+    const int32_t* table;
+    const int32_t* next_pos;              // the cut
+    const float2* rope;
+    uint32_t* hdr;
+    int Hq, Hkv, g, d, S, W, P, ring, bf16, out_bf16, ws_rows;
+    float scale_log2;                     // log2(e) / sqrt(d)
+};
+
+__host__ __device__ constexpr int padded(int d) { return ((d + 3) & ~3) + 4; }
+__host__ __device__ constexpr size_t simt_smem(int d) { return ((size_t)(kBM + 2 * kBN) * padded(d) + kBM * kBN) * 4; }
+
+// ND = ceil(d / 32)
+template <int ND>
+__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a, const __grid_constant__ Packed g) {
+    extern __shared__ float4 smem4[];
+    const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y;
+    const int n = g.off[bi + 1] - g.off[bi];
+    const long long all = (long long)n * a.g, row0 = (long long)blockIdx.x * kBM;
+    if (row0 >= all) return;
+    const int d = a.d, dp = padded(d), d4 = dp - 4;
+    float* sQ = reinterpret_cast<float*>(smem4);
+    float* sK = sQ + kBM * dp;
+    float* sV = sK + kBN * dp;
+    float* sP = sV + kBN * dp;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cut = a.next_pos[b];
+    const int nrow = (int)min((long long)kBM, all - row0);
+    // queries, rotated and rounded to the cache's type
+    for (int i = tid; i < kBM * (d4 / 2); i += kThreads) {
+        const int r = i / (d4 / 2), c = i % (d4 / 2);
+        float y0 = 0.f, y1 = 0.f;
+        if (r < nrow && 2 * c < d) {
+            const int t = (int)((row0 + r) / a.g), hq = h * a.g + (int)((row0 + r) % a.g);
+            const size_t src = (size_t)(g.row0 + g.off[bi] + t) * a.q_stride + (size_t)hq * d + 2 * c;
+            const float x0 = ld_elem(a.q, src, a.bf16), x1 = ld_elem(a.q, src + 1, a.bf16);
+            y0 = x0; y1 = x1;
+            const long long p = (long long)cut + t;
+            if (a.rope && p < a.P) rope_pair(x0, x1, a.rope[(size_t)p * (d / 2) + c], y0, y1);
+            if (a.bf16) { y0 = __bfloat162float(__float2bfloat16_rn(y0)); y1 = __bfloat162float(__float2bfloat16_rn(y1)); }
+        }
+        sQ[r * dp + 2 * c] = y0;
+        sQ[r * dp + 2 * c + 1] = y1;
+    }
+    int p[4], lo[4];                      // the warp's rows: positions and first visible keys (p = -1: no row)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int rr = 4 * warp + r;
+        p[r] = rr < nrow ? cut + (int)((row0 + rr) / a.g) : -1;
+        lo[r] = a.W > 0 ? max(0, p[r] - a.W + 1) : 0;
+    }
+    const int p_first = cut + (int)(row0 / a.g), p_last = cut + (int)((row0 + nrow - 1) / a.g);
+    const int kmin = a.W > 0 ? max(0, p_first - a.W + 1) : 0;
+    const int cal = cut & ~15;
+    float m[4], l[4], acc[4][ND];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        m[r] = -INFINITY; l[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < ND; ++e) acc[r][e] = 0.f;
+    }
+    for (int kb = kmin; kb <= p_last; kb += kBN) {
+        __syncthreads();                  // the previous tile is read
+        for (int i = tid; i < kBN * (d4 / 2); i += kThreads) {
+            const int r = i / (d4 / 2), c = i % (d4 / 2), key = kb + r;
+            float2 k = make_float2(0.f, 0.f), v = k;
+            if (key <= p_last && 2 * c < d) {
+                const bool staged = a.ring && key >= cal;
+                const size_t src = (staged ? stage_row(b, h, key, cut, a.Hkv, a.ws_rows)
+                                           : kv_row(a.table, b, h, a.ring ? key % a.S : key, a.Hkv, a.S)) * d + 2 * c;
+                const void* K = staged ? static_cast<const void*>(a.wk) : a.kc;
+                const void* V = staged ? static_cast<const void*>(a.wv) : a.vc;
+                k = make_float2(ld_elem(K, src, a.bf16), ld_elem(K, src + 1, a.bf16));
+                v = make_float2(ld_elem(V, src, a.bf16), ld_elem(V, src + 1, a.bf16));
+            }
+            *reinterpret_cast<float2*>(sK + r * dp + 2 * c) = k;
+            *reinterpret_cast<float2*>(sV + r * dp + 2 * c) = v;
+        }
+        __syncthreads();
+        float s[4][2] = {};
+        for (int c = 0; c < d4; c += 4) {
+            const float4 k0 = *reinterpret_cast<const float4*>(sK + lane * dp + c);
+            const float4 k1 = *reinterpret_cast<const float4*>(sK + (lane + 32) * dp + c);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(sQ + (4 * warp + r) * dp + c);
+                s[r][0] = fmaf(q.w, k0.w, fmaf(q.z, k0.z, fmaf(q.y, k0.y, fmaf(q.x, k0.x, s[r][0]))));
+                s[r][1] = fmaf(q.w, k1.w, fmaf(q.z, k1.z, fmaf(q.y, k1.y, fmaf(q.x, k1.x, s[r][1]))));
+            }
+        }
+        bool whole = true;                // every key of the tile visible to every row of the warp
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool in0 = kb + lane >= lo[r] && kb + lane <= p[r], in1 = kb + lane + 32 >= lo[r] && kb + lane + 32 <= p[r];
+            whole = whole && __all_sync(0xffffffffu, in0 && in1);
+            const float x0 = in0 ? s[r][0] * a.scale_log2 : -INFINITY, x1 = in1 ? s[r][1] * a.scale_log2 : -INFINITY;
+            float mx = fmaxf(x0, x1);
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(mx, m[r]);
+            const float base = mx == -INFINITY ? 0.f : mx;        // nothing visible so far: every weight 0
+            const float alpha = exp2f(m[r] - base), w0 = exp2f(x0 - base), w1 = exp2f(x1 - base);
+            m[r] = mx;
+            float sum = w0 + w1;
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[r] = l[r] * alpha + sum;
+#pragma unroll
+            for (int e = 0; e < ND; ++e) acc[r][e] *= alpha;
+            sP[(4 * warp + r) * kBN + lane] = w0;
+            sP[(4 * warp + r) * kBN + lane + 32] = w1;
+        }
+        __syncwarp();
+        for (int c = 0; c < kBN; ++c) {
+            float v[ND];
+#pragma unroll
+            for (int e = 0; e < ND; ++e) v[e] = 32 * e + lane < d ? sV[c * dp + 32 * e + lane] : 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                // a masked key adds nothing, whatever its value row holds
+                if (!whole && (kb + c < lo[r] || kb + c > p[r])) continue;
+                const float w = sP[(4 * warp + r) * kBN + c];
+#pragma unroll
+                for (int e = 0; e < ND; ++e) acc[r][e] = fmaf(w, v[e], acc[r][e]);
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (p[r] < 0) continue;
+        const int rr = 4 * warp + r, hq = h * a.g + (int)((row0 + rr) % a.g);
+        const size_t at = ((size_t)(g.row0 + g.off[bi] + (p[r] - cut)) * a.Hq + hq) * d;
+#pragma unroll
+        for (int e = 0; e < ND; ++e) {
+            const int x = 32 * e + lane;
+            if (x >= d) continue;
+            const float o = acc[r][e] / l[r];
+            if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at + x] = __float2bfloat16_rn(o);
+            else static_cast<float*>(a.out)[at + x] = o;
+        }
+    }
+}
+
+template <int ND>
+cudaError_t launch_simt(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
+    auto kernel = prompt_simt_kernel<ND>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), simt_smem(32 * ND))) return e;
+    const dim3 grid((unsigned)(((long long)most * a.g + kBM - 1) / kBM), a.Hkv, g.nb);
+    kernel<<<grid, kThreads, simt_smem(a.d), st>>>(a, g);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attention(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
+    if (a.d <= 64) return launch_simt<2>(a, g, most, st);
+    if (a.d <= 128) return launch_simt<4>(a, g, most, st);
+    return launch_simt<8>(a, g, most, st);
+}
+
+}  // namespace
+
+bool prompt_supported(const Shape& s) { return !s.int8 && (!s.ring || (s.bf16 && s.S % kPage == 0)); }
+
+cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* counts, cudaStream_t st) {
+    const Shape& s = h->sh;
+    auto at = [&](size_t off) { return h->state + off; };
+    RowArgs r{};
+    r.k = p.k; r.v = p.v; r.stride = p.kv_stride;
+    r.kc = at(h->L.k); r.vc = at(h->L.v);
+    if (s.ring) {
+        r.ws_rows = chunk_ws_rows(s);
+        r.wk = reinterpret_cast<__nv_bfloat16*>(at(h->L.cws));
+        r.wv = r.wk + (size_t)s.B * s.Hkv * r.ws_rows * s.d;
+    }
+    r.table = s.pages ? reinterpret_cast<const int32_t*>(at(h->L.table)) : nullptr;
+    r.pos = reinterpret_cast<int32_t*>(at(h->L.pos));
+    int32_t* next_pos = reinterpret_cast<int32_t*>(at(h->L.next_pos));
+    r.next_pos = next_pos;
+    r.rope = s.rope ? reinterpret_cast<const float2*>(at(h->L.rope)) : nullptr;
+    r.hdr = reinterpret_cast<uint32_t*>(at(h->L.hdr));
+    r.Hkv = s.Hkv; r.d = s.d; r.S = s.S; r.P = s.P; r.ring = s.ring; r.bf16 = s.bf16;
+    AttnArgs a{};
+    a.q = p.q; a.out = p.out; a.q_stride = p.q_stride;
+    a.kc = r.kc; a.vc = r.vc; a.wk = r.wk; a.wv = r.wv; a.table = r.table; a.next_pos = next_pos; a.rope = r.rope;
+    a.hdr = r.hdr;
+    a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W; a.P = s.P; a.ring = s.ring; a.bf16 = s.bf16;
+    a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
+    const bool vec = s.bf16 && s.d % 8 == 0;     // the entry point checked alignment and strides
+    long long row0 = 0;
+    for (int b0 = 0; b0 < s.B; b0 += kMaxGroup) {
+        static thread_local Packed g;
+        g.b0 = b0;
+        g.nb = std::min(s.B - b0, kMaxGroup);
+        g.row0 = row0;
+        int most = 0;
+        g.off[0] = 0;
+        for (int i = 0; i < g.nb; ++i) {
+            g.off[i + 1] = g.off[i] + counts[b0 + i];
+            most = std::max(most, counts[b0 + i]);
+        }
+        row0 += g.off[g.nb];
+        if (most == 0) continue;
+        cudaError_t e = cudaSuccess;
+        auto rows = [&](int stage) {
+            r.stage = stage;
+            const dim3 grid((most + (stage ? 15 : 0) + kRowsPerCta - 1) / kRowsPerCta, g.nb);
+            if (vec) prompt_rows_kernel<true><<<grid, kThreads, 0, st>>>(r, g);
+            else prompt_rows_kernel<false><<<grid, kThreads, 0, st>>>(r, g);
+            return cudaGetLastError();
+        };
+        if ((e = rows(s.ring ? 1 : 0)) != cudaSuccess) return e;
+        if ((e = launch_attention(a, g, most, st)) != cudaSuccess) return e;
+        if (s.ring && (e = rows(0)) != cudaSuccess) return e;
+        prompt_advance_kernel<<<(g.nb + 255) / 256, 256, 0, st>>>(next_pos, g);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvc

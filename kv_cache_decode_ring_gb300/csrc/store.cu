@@ -264,22 +264,17 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
         // the requests give back all their pages and map those that the kept rows need
         const int npg = s.S / kPage;
         std::vector<int> from(h->np.begin(), h->np.end()), to(from);
-        long long need = 0, held = 0;
+        long long need = 0;
+        const long long held = pages_released(h, seen);      // pages held by these requests alone
         for (int i = 0; i < n; ++i) {
             const int b = h_b[i], len = h_slots[i] < 0 ? 0 : h->store_n[h_slots[i]];
             const long long lo = s.ring && len > s.S ? len - s.S : 0;
             from[b] = (int)lo; to[b] = h_cuts[i];
-            for (int lp = 0; lp < npg; ++lp) {
-                need += page_touched(s, lp, lo, h_cuts[i]) ? 1 : 0;
-                held += h->table_h[(size_t)b * npg + lp] >= 0 ? 1 : 0;
-            }
+            for (int lp = 0; lp < npg; ++lp) need += page_touched(s, lp, lo, h_cuts[i]) ? 1 : 0;
         }
         if (need > held + (long long)h->page_free.size()) return KVC_ERR_CAPACITY;
         for (int i = 0; i < n; ++i)
-            for (int lp = 0; lp < npg; ++lp) {
-                int32_t& e = h->table_h[(size_t)h_b[i] * npg + lp];
-                if (e >= 0) { h->page_free.push_back(e); e = -1; }
-            }
+            for (int lp = 0; lp < npg; ++lp) drop_page(h, h->table_h[(size_t)h_b[i] * npg + lp]);
         int rc = KVC_OK;
         if (map_pages(h, from, to, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
         if (rc) return rc;               // not reached: the count above guarantees the pages

@@ -26,6 +26,7 @@ KVC_QUANT_NONE, KVC_QUANT_INT8, KVC_QUANT_INT8_DITHER = 0, 1, 2
 (KVC_EXPORT_K, KVC_EXPORT_V, KVC_EXPORT_POSITIONS, KVC_EXPORT_NEXT_POSITION, KVC_EXPORT_KQ, KVC_EXPORT_VQ,
  KVC_EXPORT_SK, KVC_EXPORT_SV, KVC_EXPORT_WITNESS, KVC_EXPORT_KTAIL, KVC_EXPORT_VTAIL, KVC_EXPORT_XMAP,
  KVC_EXPORT_PAGE_TABLE) = range(13)
+KVC_ROPE_HALVES, KVC_ROPE_PER_AXIS = 1, 2
 
 _STATUS_NAMES = {1: "KVC_ERR_ARG", 2: "KVC_ERR_CAPACITY", 3: "KVC_ERR_EVICTED", 4: "KVC_ERR_CUDA",
                  5: "KVC_ERR_UNSUPPORTED", 6: "KVC_ERR_DEVICE"}
@@ -54,7 +55,8 @@ EXPORTED = ["kvc_state_bytes", "kvc_create", "kvc_destroy", "kvc_append", "kvc_a
             "kvc_int8_block_risk", "kvc_int8_gate", "kvc_int8_restore",
             "kvc_pstore_create", "kvc_pstore_destroy", "kvc_pstore_insert", "kvc_pstore_lookup",
             "kvc_store_save", "kvc_store_load", "kvc_store_load_batch", "kvc_set_request_id",
-            "kvc_check_wait_path"]
+            "kvc_check_wait_path", "kvc_prompt_attn", "kvc_fork", "kvc_copy", "kvc_free", "kvc_compact",
+            "kvc_page_counts", "kvc_region", "kvc_rope_axes"]
 
 _lock = threading.Lock()
 _lib = None
@@ -73,7 +75,7 @@ def lib() -> ctypes.CDLL:
             if not os.path.exists(path):
                 raise RuntimeError("libkvc.so is not built (%s); run kv_cache_decode_ring_gb300.build.build()" % path)
             L = ctypes.CDLL(path)
-            P, i32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+            P, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
             cfgp = ctypes.POINTER(kvc_config)
             sig = {
                 "kvc_state_bytes": [cfgp, ctypes.POINTER(u64)],
@@ -102,6 +104,14 @@ def lib() -> ctypes.CDLL:
                 "kvc_store_load_batch": [P, i32, P, P, P, P],
                 "kvc_set_request_id": [P, i32, ctypes.c_uint32, P],
                 "kvc_check_wait_path": [P, P],
+                "kvc_prompt_attn": [P, P, i64, P, P, i64, P, P, P],
+                "kvc_fork": [P, i32, P, P, P],
+                "kvc_copy": [P, P, i32, P, P, P],
+                "kvc_free": [P, i32, P, P],
+                "kvc_compact": [P, ctypes.POINTER(i32), P],
+                "kvc_page_counts": [P, ctypes.POINTER(i32), ctypes.POINTER(i32)],
+                "kvc_region": [P, i32, ctypes.POINTER(u64), ctypes.POINTER(u64)],
+                "kvc_rope_axes": [P, i64, P, i64, i32, i64, i32, i32, P, i32, P, ctypes.c_double, i32, P],
             }
             for name, args in sig.items():
                 fn = getattr(L, name)
@@ -245,6 +255,100 @@ def kvc_trim(h, cuts: Sequence[int], stream=None) -> None:
 def kvc_chunk_attn(h, q, k, v, n: int, out, stream=None) -> None:
     _check(lib().kvc_chunk_attn(h, _dev(q, name="q"), _dev(k, name="k"), _dev(v, name="v"), int(n),
                                 _dev(out, name="out"), _stream(stream)), "kvc_chunk_attn")
+
+
+def _rows(t: torch.Tensor, name="tensor") -> tuple:
+    """(pointer, row stride) of rows [n, heads, d] whose heads are dense; the row stride is free."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 3:
+        raise ValueError("%s must have shape [rows, heads, head_dim], got %s" % (name, tuple(t.shape)))
+    n, heads, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) < heads * d):
+        raise ValueError("%s must have dense heads in each row, got strides %s" % (name, t.stride()))
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else heads * d
+
+
+def _ints(values):
+    """Host int32 array and its length."""
+    v = [int(x) for x in values]
+    return (ctypes.c_int32 * max(len(v), 1))(*v), len(v)
+
+
+def kvc_prompt_attn(h, q, k, v, counts: Sequence[int], out, stream=None) -> None:
+    """Packed prompts: q [T, Hq, d], k and v [T, Hkv, d] (row strides are free, k's equal to v's),
+    ``counts`` rows of each request in turn; out [T, Hq, d] dense.  See include/kvc.h."""
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    if ks != vs:
+        raise ValueError("k and v must have the same row stride")
+    c, _ = _ints(counts)
+    _check(lib().kvc_prompt_attn(h, qp, qs, kp, vp, ks, c, _dev(out, name="out"), _stream(stream)), "kvc_prompt_attn")
+
+
+def kvc_fork(h, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
+    (s, n), (d, m) = _ints(src), _ints(dst)
+    if n != m:
+        raise ValueError("src and dst must have one entry per fork")
+    _check(lib().kvc_fork(h, n, s, d, _stream(stream)), "kvc_fork")
+
+
+def kvc_copy(to, frm, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
+    (s, n), (d, m) = _ints(src), _ints(dst)
+    if n != m:
+        raise ValueError("src and dst must have one entry per copy")
+    _check(lib().kvc_copy(to, frm, n, s, d, _stream(stream)), "kvc_copy")
+
+
+def kvc_free(h, requests: Sequence[int], stream=None) -> None:
+    r, n = _ints(requests)
+    _check(lib().kvc_free(h, n, r, _stream(stream)), "kvc_free")
+
+
+def kvc_compact(h, stream=None) -> int:
+    """Pages in use after the call; they lie at [0, that many) of the pool."""
+    n = ctypes.c_int32(0)
+    _check(lib().kvc_compact(h, ctypes.byref(n), _stream(stream)), "kvc_compact")
+    return n.value
+
+
+def kvc_page_counts(h) -> tuple:
+    """(free pages, pages that more than one request holds)."""
+    free, shared = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(lib().kvc_page_counts(h, ctypes.byref(free), ctypes.byref(shared)), "kvc_page_counts")
+    return free.value, shared.value
+
+
+def kvc_region(h, which: int) -> tuple:
+    """(byte offset, bytes) of a stored array inside the state buffer."""
+    off, n = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(lib().kvc_region(h, int(which), ctypes.byref(off), ctypes.byref(n)), "kvc_region")
+    return off.value, n.value
+
+
+def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=None, halves=False, per_axis=False,
+                  stream=None):
+    """x [rows, heads, d] (bf16 or fp32, heads dense, row stride free) rotated by several axes:
+    ``pos`` int32 [axes, rows], ``sections`` the pairs of each axis.  ``out`` may be x; a new dense
+    tensor if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1); ``per_axis``: a spectrum
+    for each axis.  See include/kvc.h."""
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be bfloat16 or float32, got %s" % x.dtype)
+    xp, xs = _rows(x, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != x.shape:
+        raise ValueError("out must be %s of shape %s" % (x.dtype, tuple(x.shape)))
+    yp, ys = _rows(out, "out")
+    s, n = _ints(sections)
+    _dev(pos, torch.int32, (n, x.shape[0]), "pos")
+    if not x.device == out.device == pos.device:
+        raise ValueError("x, pos and out must be on one device")
+    with torch.cuda.device(x.device):
+        _check(lib().kvc_rope_axes(xp, xs, yp, ys, KVC_BF16 if x.dtype == torch.bfloat16 else KVC_F32, x.shape[0], x.shape[1],
+                                   x.shape[2], ctypes.c_void_p(pos.data_ptr()), n, s, float(base),
+                                   (KVC_ROPE_HALVES if halves else 0) | (KVC_ROPE_PER_AXIS if per_axis else 0),
+                                   _stream(stream)), "kvc_rope_axes")
+    return out
 
 
 def kvc_export_bytes(h, which: int) -> int:
@@ -470,6 +574,56 @@ class Cache:
         _dev(out, self.out_dtype, (self.B, n, self.Hq, self.d), "out")
         kvc_chunk_attn(self.h, q, k, v, n, out, stream)
         return out
+
+    def prompt(self, q, k, v, counts, out=None, stream=None):
+        """Packed prompts: ``counts[b]`` rows of each request in turn, appended and attended.  q [T, Hq, d],
+        k and v [T, Hkv, d] with T >= sum(counts), heads dense, any row stride (views of one projection);
+        rows behind the last request's are neither read nor written."""
+        counts = [int(c) for c in counts]
+        if len(counts) != self.B:
+            raise ValueError("need one count per request")
+        T = q.shape[0]
+        if T < sum(counts):
+            raise ValueError("q has %d rows, the counts sum to %d" % (T, sum(counts)))
+        for t, heads, name in ((q, self.Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")):
+            if t.dtype != self.torch_dtype or tuple(t.shape) != (T, heads, self.d):
+                raise ValueError("%s must be %s of shape %s, got %s %s" % (name, self.torch_dtype, (T, heads, self.d), t.dtype,
+                                                                           tuple(t.shape)))
+        if out is None:
+            out = torch.empty((T, self.Hq, self.d), dtype=self.out_dtype, device=q.device)
+        _dev(out, self.out_dtype, (T, self.Hq, self.d), "out")
+        kvc_prompt_attn(self.h, q, k, v, counts, out, stream)
+        return out
+
+    # whole requests and their pages
+    def fork(self, src, dst, stream=None):
+        """Requests ``dst`` become copies of requests ``src``; a paged cache shares the pages."""
+        kvc_fork(self.h, src, dst, stream)
+
+    def copy_from(self, other: "Cache", src, dst, stream=None):
+        """Requests ``dst`` become copies of ``other``'s requests ``src``, with rows of their own."""
+        kvc_copy(self.h, other.h, src, dst, stream)
+
+    def free(self, requests, stream=None):
+        kvc_free(self.h, requests, stream)
+
+    def compact(self, stream=None) -> int:
+        """Moves the pages in use to the start of the pool; returns their number."""
+        return kvc_compact(self.h, stream)
+
+    def page_counts(self) -> tuple:
+        """(free pages, shared pages)"""
+        return kvc_page_counts(self.h)
+
+    def rows(self) -> tuple:
+        """Views of the stored K and V rows: [B, Hkv, capacity, d], paged [pages, Hkv, 16, d].  For reading,
+        on the stream that the cache's calls run on."""
+        shape = (self.cfg.page_pool, self.Hkv, 16, self.d) if self.cfg.page_pool else (self.B, self.Hkv, self.S, self.d)
+        views = []
+        for which in (KVC_EXPORT_K, KVC_EXPORT_V):
+            off, n = kvc_region(self.h, which)
+            views.append(self.state[off:off + n].view(self.torch_dtype).view(shape))
+        return tuple(views)
 
     def export(self, which, stream=None) -> np.ndarray:
         raw = kvc_export(self.h, which, stream)
