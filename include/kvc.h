@@ -289,8 +289,8 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * at p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32
  * and rounded to the cache's type, as the keys are; sums and softmax are fp32.
  * bf16 caches with head_dim 64 or 128 run on the tensor cores, where the softmax weights
- * are rounded to bf16 too (relative error at most 2^-8 each, the sum taken over the
- * rounded weights); other shapes run in fp32 throughout.  What a masked key or value row
+ * are rounded to bf16 too (relative error at most 2^-8 each; their sum is fp32); other
+ * shapes run in fp32 throughout.  What a masked key or value row
  * holds, infinities and NaN among it, does not reach the result.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
  * All tiers but INT8; a ring needs a bf16 cache with W a multiple of 16, and counts of at

@@ -19,22 +19,12 @@
 #include <cmath>
 #include <vector>
 
-#include "async_copy.h"
-#include "kvc_internal.h"
+#include "prompt.h"
 
 namespace kvc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxGroup = 1024;           // requests per launch: their offsets ride in the parameters
-
-// What every kernel of a call knows about its requests [b0, b0 + nb).
-struct Packed {
-    long long row0;                       // packed row of request b0's first row
-    int b0, nb;
-    int off[kMaxGroup + 1];               // request b0 + i brings rows [off[i], off[i + 1]) from row0 on
-};
-
 struct RowArgs {
     const void* k; const void* v;         // packed rows, stride kv_stride, keys not rotated
     long long stride;
@@ -51,11 +41,6 @@ struct RowArgs {
 
 __device__ __forceinline__ bool position_ok(const RowArgs& a, long long p) {
     return p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P);
-}
-
-// Row of the staging area that holds position p >= cut rounded down to 16.
-__device__ __forceinline__ size_t stage_row(int b, int h, int p, int cut, int Hkv, int ws_rows) {
-    return ((size_t)b * Hkv + h) * ws_rows + (p - (cut & ~15));
 }
 
 constexpr int kRowsPerCta = 8;
@@ -145,20 +130,6 @@ __global__ void prompt_advance_kernel(int32_t* next_pos, const __grid_constant__
 // 64 keys in shared memory as fp32; lane = key for the scores, lane = dim for P.V; the
 // running maximum and sum of a row live in its warp.  Everything in fp32.
 constexpr int kBM = 32, kBN = 64;
-
-struct AttnArgs {
-    const void* q;
-    void* out;
-    long long q_stride;
-    const void* kc; const void* vc;
-    const __nv_bfloat16* wk; const __nv_bfloat16* wv;
-    const int32_t* table;
-    const int32_t* next_pos;              // the cut
-    const float2* rope;
-    uint32_t* hdr;
-    int Hq, Hkv, g, d, S, W, P, ring, bf16, out_bf16, ws_rows;
-    float scale_log2;                     // log2(e) / sqrt(d)
-};
 
 __host__ __device__ constexpr int padded(int d) { return ((d + 3) & ~3) + 4; }
 __host__ __device__ constexpr size_t simt_smem(int d) { return ((size_t)(kBM + 2 * kBN) * padded(d) + kBM * kBN) * 4; }
@@ -338,11 +309,12 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     const bool vec = s.bf16 && s.d % 8 == 0;     // the entry point checked alignment and strides
+    const bool tensor = prompt_tc_supported(s);
     long long row0 = 0;
-    for (int b0 = 0; b0 < s.B; b0 += kMaxGroup) {
+    for (int b0 = 0; b0 < s.B; b0 += kPromptGroup) {
         static thread_local Packed g;
         g.b0 = b0;
-        g.nb = std::min(s.B - b0, kMaxGroup);
+        g.nb = std::min(s.B - b0, kPromptGroup);
         g.row0 = row0;
         int most = 0;
         g.off[0] = 0;
@@ -361,7 +333,8 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
             return cudaGetLastError();
         };
         if ((e = rows(s.ring ? 1 : 0)) != cudaSuccess) return e;
-        if ((e = launch_attention(a, g, most, st)) != cudaSuccess) return e;
+        e = tensor ? launch_prompt_tc(h, a, g, st) : launch_attention(a, g, most, st);
+        if (e != cudaSuccess) return e;
         if (s.ring && (e = rows(0)) != cudaSuccess) return e;
         prompt_advance_kernel<<<(g.nb + 255) / 256, 256, 0, st>>>(next_pos, g);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -1,0 +1,567 @@
+// prompt_tc.cu -- attention of packed prompts on tcgen05 (bf16 caches, head_dim 64 or 128).
+//
+// o = softmax(q K^T / sqrt(d)) V per query row over the keys that it sees, one pass over the
+// keys with a running maximum and sum per row (fp32).  A dense contraction: bound by the
+// tensor cores, whose pace the softmax between the two products has to keep.
+//  * CTA = 256 query rows (token, head of the group) of one (request, KV head), as two
+//    slots of 128 rows; both read the same tiles of 128 keys, walked upwards from the first
+//    key that any of its rows sees.
+//  * Warps 0-3 and 4-7: softmax of slot 0 and 1, thread = row = tensor-memory lane.  Warp 8
+//    issues the tensor copies, one thread of warp 9 every matrix instruction; warps 10 and
+//    11 look over the value rows of boundary tiles.
+//  * Tensor memory: S of the slots in columns [0, 128) and [128, 256), fp32; the weights P
+//    replace the first 64 columns of S as bf16 pairs (the A operand of P.V); O in [256, 384)
+//    and [384, 512).  Q sits in shared memory.
+//  * All operands are bf16: q and the keys as the cache's type holds them, the weights
+//    rounded once (relative error 2^-8, at most 2^8 in size).  fp16 weights (2^-11) would
+//    need the values in fp16 too: a conversion pass over every tile and a narrower range.
+//  * Per slot: S(j) -> softmax(j) -> P.V(j) -> S(j+1), which overwrites the columns that P.V(j)
+//    reads and so waits for it; the slots alternate on the tensor cores.
+//  * A row's reference maximum moves only when a tile exceeds it by more than 2^8 (log2
+//    domain); the softmax thread then rescales its O row itself (no P.V of its slot in flight).
+//  * Masked scores are replaced, not added to, so a masked key may hold anything.  A masked
+//    weight of 0 times a value that is not finite would still spoil a row, so boundary tiles
+//    (where some row sees only some of the keys) have such values replaced by 0 in shared
+//    memory before P.V, and the epilogue adds them back to the rows that see them.
+//  * Key tiles start on multiples of 16.  A contiguous cache is read in 128-row boxes; paged
+//    caches and rings in 16-row boxes, a lane each, from the page, the ring slot or the
+//    staging rows.  Groups past the last key repeat the last one.
+//  * CTAs run longest first (host-sorted items), the KV heads of an item adjacent.
+// Every mbarrier wait is bounded; on expiry the kernel flags the device error word, skips
+// the remaining work, waits (bounded) for its copies and matrix instructions in flight and
+// frees its tensor memory.
+#include <algorithm>
+#include <vector>
+
+#include "prompt.h"
+#include "tcgen05.h"
+
+namespace kvc {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 128;            // rows per slot
+constexpr int kBN = 128;            // keys per tile
+constexpr int kSlots = 2;
+constexpr int kRows = kSlots * kBM;
+constexpr int kThreads = 12 * 32;
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLook = 10;
+constexpr float kLazyMax = 8.f;     // log2-domain headroom of a row's reference maximum
+constexpr int kRegSoftmax = 216, kRegOther = 72, kRegLaunch = 168;
+static_assert(8 * kRegSoftmax + 4 * kRegOther == 12 * kRegLaunch, "register split sums to the launch's registers");
+constexpr int kItems = 512;         // (request, tile) items per launch
+constexpr uint32_t kTmemCols = 512, kColO = 256;
+
+struct Items {
+    int n;
+    int4 e[kItems];                 // (index in the group, tile of 256 rows, packed row of the request, its rows)
+};
+
+template <int D>
+struct Plan {
+    static constexpr int kHalves = D / 64;                 // 64-dim halves: 128-byte rows, 128-byte swizzle
+    static constexpr int kTile = kBN * D * 2;
+    static constexpr int kHalf = kBN * 128;
+    static constexpr int kStages = D == 128 ? 2 : 4;       // of K and of V each
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + kSlots * kTile;
+    static constexpr int kV = kK + kStages * kTile;
+    static constexpr int kBar = kV + kStages * kTile;
+    enum {
+        kKFull = 0,                          // [stage] K copied
+        kKFree = kKFull + kStages,           // [stage] the S products of the tile complete
+        kVFull = kKFree + kStages,
+        kVFree = kVFull + kStages,           // [stage] the P.V products of the tile complete
+        kVClean = kVFree + kStages,          // [stage] V looked over (2 warps)
+        kSFull = kVClean + kStages,          // [slot] S complete
+        kPFull = kSFull + kSlots,            // [slot] P written (4 warps)
+        kODone = kPFull + kSlots,            // [slot] P.V complete
+        kQReady = kODone + kSlots,           // Q of both slots in shared memory (8 warps)
+        kDone = kQReady + 1,                 // every product issued so far complete
+        kBars = kDone + 1
+    };
+    static constexpr int kMisc = kBar + 8 * kBars;         // tensor memory base, abort flag, spoilt flag
+    static constexpr int kBytes = kMisc + 16 + 1024;       // + alignment of the dynamic base
+    static_assert(kBytes <= (int)kMaxSmemPerBlock, "shared memory per block");
+};
+
+__device__ __forceinline__ bool not_finite(uint32_t w) {   // either bf16 of a pair
+    return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmWK, const __grid_constant__ CUtensorMap tmWV,
+                       const __grid_constant__ AttnArgs a, const int b0, const __grid_constant__ Items items) {
+    using L = Plan<D>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* sQ = smem + L::kQ;
+    unsigned char* sK = smem + L::kK;
+    unsigned char* sV = smem + L::kV;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+    volatile int* spoilt = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int kvh = blockIdx.x % a.Hkv;
+    const int4 item = items.e[blockIdx.x / a.Hkv];
+    const int b = b0 + item.x, n = item.w;
+    const int cut = a.next_pos[b];
+    const long long all = (long long)n * a.g, row0 = (long long)item.y * kRows;
+    const int nrow = (int)min((long long)kRows, all - row0);
+    const int t0 = (int)(row0 / a.g);                       // first token of the CTA
+    const int j0 = (int)(row0 - (long long)t0 * a.g);       // ... and its head in the group
+    auto token = [&](int r) { return t0 + (j0 + r) / a.g; };
+    // keys: the CTA's and each slot's first and last, in tiles from k0
+    const int p_first = cut + t0, p_last = cut + token(nrow - 1);
+    auto first_key = [&](int p) { return a.W > 0 ? max(0, p - a.W + 1) : 0; };
+    const int k0 = first_key(p_first) & ~15;
+    const int ntiles = (p_last - k0) / kBN + 1;
+    auto slot_lo = [&](int i) { return kBM * i < nrow ? (first_key(cut + token(kBM * i)) - k0) / kBN : 0; };
+    auto slot_hi = [&](int i) { return kBM * i < nrow ? (cut + token(min(nrow, kBM * (i + 1)) - 1) - k0) / kBN + 1 : 0; };
+    // a tile in which every row of the CTA sees every key
+    auto whole = [&](int kb) { return kb >= first_key(p_last) && kb + kBN - 1 <= p_first; };
+
+    if (tid == 0) {
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(&bar[L::kKFull + s], 1); mbar_init(&bar[L::kKFree + s], 1);
+            mbar_init(&bar[L::kVFull + s], 1); mbar_init(&bar[L::kVFree + s], 1);
+            mbar_init(&bar[L::kVClean + s], 2);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&bar[L::kSFull + s], 1); mbar_init(&bar[L::kPFull + s], 4); mbar_init(&bar[L::kODone + s], 1);
+        }
+        mbar_init(&bar[L::kQReady], 8);
+        mbar_init(&bar[L::kDone], 1);
+        *abort_flag = 0;
+        *spoilt = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // every warpgroup changes its register share together
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+
+    if (warp < 8) {
+        // ================= softmax: warp w serves slot w / 4, rows 32 (w % 4) .. + 31
+        const int slot = warp >> 2, lg = warp & 3;
+        const int row = 32 * lg + lane, r = kBM * slot + row;
+        const uint32_t lane_off = (uint32_t)(32 * lg) << 16;
+        const uint32_t tS = tmem + 128 * slot + lane_off;
+        const uint32_t tO = tmem + kColO + 128 * slot + lane_off;
+        const bool valid = r < nrow;
+        const int t = token(r), hq = kvh * a.g + (j0 + r) % a.g, p = cut + t;
+        const int key_lo = first_key(p);
+        const int lo = slot_lo(slot), hi = slot_hi(slot);
+        // all rows of the slot see all keys of a tile from sl to sh
+        const int sl = first_key(cut + token(min(nrow, kBM * (slot + 1)) - 1)), sh = cut + token(kBM * slot);
+        bool fail = false;
+        {
+            // the row's query, rotated at p in fp32 and rounded to bf16, into the slot's Q tile
+            // (16-byte chunk c of row r at c ^ (r mod 8)), 64 dims at a time
+            unsigned char* qt = sQ + slot * L::kTile;
+#pragma unroll 1
+            for (int hf = 0; hf < L::kHalves; ++hf) {
+                uint4 qv[8];
+                float4 rv[16];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
+                const bool turn = a.rope && valid && p < a.P;
+                if (valid) {
+                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                                      ((size_t)item.z + t) * a.q_stride + (size_t)hq * D + 64 * hf);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + c);
+                }
+                if (turn) {
+                    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (D / 2) + 32 * hf);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) rv[c] = __ldg(rp + c);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 r4 = rv[(4 * c + k) >> 1];
+                            float y0, y1;
+                            rope_pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u),
+                                      (k & 1) ? make_float2(r4.z, r4.w) : make_float2(r4.x, r4.y), y0, y1);
+                            const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&o2);
+                        }
+                        qv[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(qt + hf * L::kHalf + row * 128 + ((c ^ (row & 7)) << 4)) = qv[c];
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::kQReady]);
+        }
+        float m_ref = -INFINITY, l = 0.f;                       // m_ref: of the scores, before scaling
+        const float sc = a.scale_log2, lazy = kLazyMax / sc;
+        for (int j = lo; j < hi; ++j) {
+            const bool w = mbar_wait(&bar[L::kSFull + slot], (uint32_t)((j - lo) & 1)) && !*abort_flag;
+            if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
+            fence_after();
+            float s[kBN];
+            tmem_ld32(tS, s);
+            tmem_ld32(tS + 32, s + 32);
+            tmem_ld32(tS + 64, s + 64);
+            tmem_ld32(tS + 96, s + 96);
+            tmem_wait_ld();
+            const int kb = k0 + kBN * j;
+            if (!(kb >= sl && kb + kBN - 1 <= sh) || nrow < kBM * (slot + 1)) {
+                const int c0 = key_lo - kb, width = valid ? p - key_lo : -1;      // visible: c0 .. c0 + width
+#pragma unroll
+                for (int c = 0; c < kBN; ++c) s[c] = width >= 0 && (uint32_t)(c - c0) <= (uint32_t)width ? s[c] : -INFINITY;
+            }
+            // row maximum: eight independent chains of three-input maxima, then a tree
+            float m8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[8 + e]);
+#pragma unroll
+            for (int c = 16; c < kBN; c += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m8[e] = fmax3(m8[e], s[c + e], s[c + 8 + e]);
+            const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+            bool grow = false;
+            float alpha = 1.f;
+            if (mx > m_ref + lazy) {
+                grow = m_ref != -INFINITY;
+                alpha = grow ? ex2((m_ref - mx) * sc) : 1.f;
+                m_ref = mx;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? alpha : 1.f;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(tO + c, o);
+                    tmem_wait_ld();
+                    uint32_t u[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                    tmem_st32(tO + c, u);
+                }
+                tmem_wait_st();
+            }
+            const float base = m_ref == -INFINITY ? 0.f : m_ref * sc;      // nothing visible so far: weights 0
+            uint32_t pk[kBN / 2];
+            float2 rs[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 nb2 = make_float2(-base, -base), sc2 = make_float2(sc, sc);
+#pragma unroll
+            for (int e = 0; e < kBN / 2; ++e) {
+                const float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), sc2, nb2);
+                const float p0 = ex2(x.x), p1 = ex2(x.y);                   // masked keys: 0
+                rs[e & 3] = __fadd2_rn(rs[e & 3], make_float2(p0, p1));
+                const __nv_bfloat162 t2 = __floats2bfloat162_rn(p0, p1);
+                pk[e] = *reinterpret_cast<const uint32_t*>(&t2);
+            }
+            const float2 r4 = __fadd2_rn(__fadd2_rn(rs[0], rs[1]), __fadd2_rn(rs[2], rs[3]));
+            l = l * alpha + (r4.x + r4.y);
+            tmem_st32(tS, pk);
+            tmem_st32(tS + 32, pk + 32);
+            tmem_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::kPFull + slot]);
+        }
+        if (!fail && hi > lo) {
+            const bool w = mbar_wait(&bar[L::kODone + slot], (uint32_t)((hi - lo - 1) & 1));
+            fail = !__all_sync(0xffffffffu, w);
+        }
+        if (fail) {
+            if (lane == 0) atomicOr(a.hdr, kErrWait);
+            *abort_flag = 1;
+        } else if (hi > lo && !*abort_flag) {
+            fence_after();
+            const float inv = 1.f / l;
+            const size_t orow = (((size_t)item.z + t) * a.Hq + hq) * D;
+            const bool fix = *spoilt != 0;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(tO + c, o);
+                tmem_wait_ld();
+                if (!valid) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= inv;
+                if (fix) {
+                    // values that are not finite, left out of boundary tiles: visible ones count
+                    for (int key = key_lo; key <= p; ++key) {
+                        if (whole(k0 + (key - k0) / kBN * kBN)) { key = k0 + (key - k0) / kBN * kBN + kBN - 1; continue; }
+                        const bool staged = a.ring && key >= (cut & ~15);
+                        const size_t at = staged ? stage_row(b, kvh, key, cut, a.Hkv, a.ws_rows)
+                                                 : kv_row(a.table, b, kvh, a.ring ? key % a.S : key, a.Hkv, a.S);
+                        const uint4* v = reinterpret_cast<const uint4*>(
+                            (staged ? a.wv : static_cast<const __nv_bfloat16*>(a.vc)) + at * D + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 u = v[e];
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float v0 = __uint_as_float(w[k] << 16), v1 = __uint_as_float(w[k] & 0xffff0000u);
+                                if (!isfinite(v0)) o[8 * e + 2 * k] += v0;
+                                if (!isfinite(v1)) o[8 * e + 2 * k + 1] += v1;
+                            }
+                        }
+                    }
+                }
+                if (a.out_bf16) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 t2 = __floats2bfloat162_rn(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
+                            u[k] = *reinterpret_cast<const uint32_t*>(&t2);
+                        }
+                        dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+        }
+    } else if (warp == kWarpCopy) {
+        // ================= tensor copies of K and V tiles
+        const int head_row0 = (b * a.Hkv + kvh) * a.S, cal = cut & ~15;
+        const int ws_row0 = (b * a.Hkv + kvh) * a.ws_rows;
+        auto load_tile = [&](const CUtensorMap* tm, const CUtensorMap* tmw, unsigned char* dst, uint64_t* full, int kb) {
+            if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+            __syncwarp();
+            if (!a.table && !a.ring) {
+                if (lane < L::kHalves) tma_load_2d(dst + lane * L::kHalf, tm, 64 * lane, head_row0 + kb, full);
+            } else if (lane < 8 * L::kHalves) {
+                const int gi = lane & 7, half = lane >> 3;
+                const int pos = min(kb + 16 * gi, p_last & ~15);
+                const CUtensorMap* m = tm;
+                int row;
+                if (a.ring && pos >= cal) {
+                    m = tmw;
+                    row = ws_row0 + (pos - cal);
+                } else {
+                    const int slot = a.ring ? pos % a.S : pos;
+                    row = a.table ? (max(a.table[(size_t)b * (a.S / kPage) + slot / kPage], 0) * a.Hkv + kvh) * kPage
+                                  : head_row0 + slot;
+                }
+                tma_load_2d(dst + half * L::kHalf + gi * 16 * 128, m, 64 * half, row, full);
+            }
+        };
+        bool ok = true;
+        int k_issued = 0, v_issued = 0;
+        for (int j = 0; j < ntiles; ++j) {
+            const int st = j % L::kStages;
+            const uint32_t used = (uint32_t)((j / L::kStages - 1) & 1);
+            if (j >= L::kStages) ok = mbar_wait(&bar[L::kKFree + st], used);
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+            if (!ok) break;
+            load_tile(&tmK, &tmWK, sK + st * L::kTile, &bar[L::kKFull + st], k0 + kBN * j);
+            k_issued = j + 1;
+            if (j >= L::kStages) ok = mbar_wait(&bar[L::kVFree + st], used);
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+            if (!ok) break;
+            load_tile(&tmV, &tmWV, sV + st * L::kTile, &bar[L::kVFull + st], k0 + kBN * j);
+            v_issued = j + 1;
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(a.hdr, kErrWait);
+            // the last copy issued into each stage lands before the CTA can exit
+            for (int j = max(0, k_issued - L::kStages); j < k_issued; ++j)
+                mbar_wait(&bar[L::kKFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
+            for (int j = max(0, v_issued - L::kStages); j < v_issued; ++j)
+                mbar_wait(&bar[L::kVFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
+        }
+        __syncwarp();
+    } else if (warp == kWarpMma) {
+        // ================= one thread issues every matrix instruction
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = instr_desc_bf16(kBM, kBN, false), idesc_pv = instr_desc_bf16(kBM, D, true);
+            const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16), kdesc0 = smem_desc(smem_u32(sK), 16);
+            const uint64_t vdesc0 = smem_desc(smem_u32(sV), L::kHalf);
+            auto koff = [](int s) { return (uint64_t)(((s >> 2) * L::kHalf + (s & 3) * 32) >> 4); };
+            int lo[kSlots], hi[kSlots];
+            for (int i = 0; i < kSlots; ++i) { lo[i] = slot_lo(i); hi[i] = slot_hi(i); }
+            // S_i = Q_i K_j^T, 16 dims per instruction
+            auto issue_s = [&](int i, int j) {
+                const uint64_t qd = qdesc0 + (uint64_t)(i * (L::kTile >> 4));
+                const uint64_t kd = kdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) mma_ss(tmem + 128 * i, qd + koff(s), kd + koff(s), idesc_qk, s > 0);
+                mma_commit(&bar[L::kSFull + i]);
+            };
+            // O_i += P_i V_j: keys 16 s .. + 15 of P sit in columns 8 s .. + 7 of S buffer i
+            auto issue_pv = [&](int i, int j) {
+                const uint64_t vd = vdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+#pragma unroll
+                for (int s = 0; s < kBN / 16; ++s)
+                    mma_ts(tmem + kColO + 128 * i, tmem + 128 * i + 8 * s, vd + (uint64_t)((s * 2048) >> 4), idesc_pv,
+                           (j > lo[i] || s > 0));
+                mma_commit(&bar[L::kODone + i]);
+            };
+            auto wait_ok = [&](int which, uint32_t parity) { return mbar_spin(&bar[which], parity) && !*abort_flag; };
+            auto wait_v = [&](int j) {
+                const uint32_t parity = (uint32_t)((j / L::kStages) & 1);
+                return wait_ok(L::kVFull + j % L::kStages, parity) && wait_ok(L::kVClean + j % L::kStages, parity);
+            };
+            bool ok = wait_ok(L::kQReady, 0);
+            for (int j = -1; j < ntiles && ok; ++j) {
+                const int vs = (j + L::kStages) % L::kStages, jn = j + 1, ks = jn % L::kStages;
+                bool k_seen = false, v_seen = false;
+                for (int i = 0; i < kSlots && ok; ++i) {
+                    if (j >= lo[i] && j < hi[i]) {
+                        if (!v_seen) ok = wait_v(j);
+                        v_seen = true;
+                        ok = ok && wait_ok(L::kPFull + i, (uint32_t)((j - lo[i]) & 1));
+                        if (!ok) break;
+                        fence_after();
+                        issue_pv(i, j);
+                    }
+                    if (jn >= lo[i] && jn < hi[i]) {
+                        if (!k_seen) ok = wait_ok(L::kKFull + ks, (uint32_t)((jn / L::kStages) & 1));
+                        k_seen = true;
+                        // S(j + 1) overwrites the columns that P.V(j) reads
+                        if (ok && jn > lo[i]) ok = wait_ok(L::kODone + i, (uint32_t)((j - lo[i]) & 1));
+                        if (!ok) break;
+                        fence_after();
+                        issue_s(i, jn);
+                    }
+                }
+                if (!ok) break;
+                if (j >= 0) {
+                    // (a tile that no slot multiplied is still waited for: its copy has to land)
+                    if (!v_seen) ok = wait_v(j);
+                    mma_commit(&bar[L::kVFree + vs]);
+                }
+                if (jn < ntiles) {
+                    if (!k_seen) ok = ok && wait_ok(L::kKFull + ks, (uint32_t)((jn / L::kStages) & 1));
+                    mma_commit(&bar[L::kKFree + ks]);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                atomicOr(a.hdr, kErrWait);
+            }
+            // no product may still target the columns when they are freed
+            mma_commit(&bar[L::kDone]);
+            mbar_wait(&bar[L::kDone], 0);
+        }
+        __syncwarp();
+    } else {
+        // ================= value rows of boundary tiles: what is not finite becomes 0
+        const int t = tid - 32 * kWarpLook;
+        bool ok = true;
+        for (int j = 0; j < ntiles; ++j) {
+            const int st = j % L::kStages, kb = k0 + kBN * j;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar[L::kVFull + st], (uint32_t)((j / L::kStages) & 1)) && !*abort_flag);
+            if (!ok) break;
+            if (!whole(kb)) {
+                unsigned char* tile = sV + st * L::kTile;
+                bool any = false;
+#pragma unroll 4
+                for (int q = t; q < L::kTile / 16; q += 64) {
+                    uint4 u = *reinterpret_cast<const uint4*>(tile + 16 * q);
+                    if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
+                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+                            if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
+                        }
+                        *reinterpret_cast<uint4*>(tile + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                        any = true;
+                    }
+                }
+                if (any) *spoilt = 1;
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::kVClean + st]);
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(a.hdr, kErrWait);
+            *abort_flag = 1;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        __syncwarp();
+        fence_after();
+        tmem_free(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items& items, cudaStream_t st) {
+    auto kernel = prompt_attn_kernel<D>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Plan<D>::kBytes)) return e;
+    kernel<<<dim3((unsigned)items.n * a.Hkv), kThreads, Plan<D>::kBytes, st>>>(tm[0], tm[1], tm[2], tm[3], a, b0, items);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prompt_tc_supported(const Shape& s) {
+    const long long rows = s.pages ? (long long)s.pages * s.Hkv * kPage : (long long)s.B * s.Hkv * s.S;
+    const long long staged = s.ring ? (long long)s.B * s.Hkv * chunk_ws_rows(s) : 0;
+    return s.bf16 && !s.int8 && (s.d == 64 || s.d == 128) && rows < (1ll << 31) - kBN && staged < (1ll << 31);
+}
+
+cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packed& g, cudaStream_t st) {
+    const Shape& s = h->sh;
+    CUtensorMap tm[4];
+    const cuuint64_t rows = s.pages ? (cuuint64_t)s.pages * s.Hkv * kPage : (cuuint64_t)s.B * s.Hkv * s.S;
+    const cuuint64_t dims[2] = {(cuuint64_t)s.d, rows}, strides[1] = {(cuuint64_t)s.d * 2};
+    const cuuint32_t box[2] = {64, (s.pages || s.ring) ? (cuuint32_t)kPage : (cuuint32_t)kBN};
+    if (!make_tensor_map_bf16(&tm[0], const_cast<void*>(a.kc), 2, dims, strides, box) ||
+        !make_tensor_map_bf16(&tm[1], const_cast<void*>(a.vc), 2, dims, strides, box))
+        return cudaErrorInvalidValue;
+    tm[2] = tm[0]; tm[3] = tm[1];
+    if (s.ring) {
+        const cuuint64_t wdims[2] = {(cuuint64_t)s.d, (cuuint64_t)s.B * s.Hkv * a.ws_rows};
+        if (!make_tensor_map_bf16(&tm[2], const_cast<__nv_bfloat16*>(a.wk), 2, wdims, strides, box) ||
+            !make_tensor_map_bf16(&tm[3], const_cast<__nv_bfloat16*>(a.wv), 2, wdims, strides, box))
+            return cudaErrorInvalidValue;
+    }
+    // longest first: an item's work is its number of key tiles.  The host's lengths order the
+    // CTAs only; the kernel reads the cut on the device.
+    std::vector<std::pair<int, int4>> work;
+    for (int i = 0; i < g.nb; ++i) {
+        const int n = g.off[i + 1] - g.off[i], cut = h->np[g.b0 + i];
+        const long long all = (long long)n * s.g;
+        for (long long t = 0; t * kRows < all; ++t) {
+            const int first = cut + (int)(t * kRows / s.g), last = cut + (int)((std::min(all, (t + 1) * kRows) - 1) / s.g);
+            const int k0 = (s.W > 0 ? std::max(0, first - s.W + 1) : 0) & ~15;
+            work.push_back({-((last - k0) / kBN + 1), make_int4(i, (int)t, (int)(g.row0 + g.off[i]), n)});
+        }
+    }
+    std::stable_sort(work.begin(), work.end(), [](const auto& x, const auto& y) { return x.first < y.first; });
+    static thread_local Items items;      // 8 KB of kernel parameters: not on the stack
+    for (size_t i0 = 0; i0 < work.size(); i0 += kItems) {
+        items.n = (int)std::min<size_t>(kItems, work.size() - i0);
+        for (int i = 0; i < items.n; ++i) items.e[i] = work[i0 + i].second;
+        const cudaError_t e = s.d == 128 ? launch<128>(tm, a, g.b0, items, st) : launch<64>(tm, a, g.b0, items, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace kvc

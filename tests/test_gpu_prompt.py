@@ -4,9 +4,7 @@ with a cut and a count of its own, against attention in 64 bits over the rows th
 Tolerances.  With weights p_j in fp32 (fp32 caches, head sizes other than 64 and 128) the bound is
 that of the other attention calls (1e-5 or 2e-3, absolute and relative, plus a bf16 output's
 half step).  On the tensor cores each weight is rounded to bf16, p_j (1 + e_j) with |e_j| <= 2^-8,
-and the sum runs over the rounded weights, so the result moves by at most
-    sum p_j |e_j| |v_j - o| / (1 - 2^-8) <= 2^-8 (sum p_j |v_j| + |o|) * 1.004;
-fp32 accumulation of the scores (128 products) and ex2 add relative errors below 2^-13 to a weight.
+so the result moves by at most sum p_j |e_j| |v_j| <= 2^-8 sum p_j |v_j|; fp32 accumulation of the scores (128 products) and ex2 add relative errors below 2^-13 to a weight.
 The bound taken is 1.1 * 2^-8 (sum p_j |v_j| + |o|) plus the output's half step.
 """
 import math
