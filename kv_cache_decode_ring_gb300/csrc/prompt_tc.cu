@@ -7,8 +7,8 @@
 //    slots of 128 rows; both read the same tiles of 128 keys, walked upwards from the first
 //    key that any of its rows sees.
 //  * Warps 0-3 and 4-7: softmax of slot 0 and 1, thread = row = tensor-memory lane.  Warp 8
-//    issues the tensor copies, one thread of warp 9 every matrix instruction; warps 10 and
-//    11 look over the value rows of boundary tiles.
+//    issues the tensor copies, warps 9 and 10 the matrix instructions of a slot each, warp 11
+//    looks over the value rows of boundary tiles.
 //  * Tensor memory: S of the slots in columns [0, 128) and [128, 256), fp32; the weights P
 //    replace the first 64 columns of S as bf16 pairs (the A operand of P.V); O in [256, 384)
 //    and [384, 512).  Q sits in shared memory.
@@ -42,16 +42,15 @@ namespace {
 using namespace tc;
 
 constexpr int kBM = 128;            // rows per slot
-constexpr int kBN = 128;            // keys per tile
 constexpr int kSlots = 2;
 constexpr int kRows = kSlots * kBM;
 constexpr int kThreads = 12 * 32;
-constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLook = 10;
+constexpr int kWarpCopy = 8, kWarpMma = 9, kWarpLook = 11;   // (a matrix warp per slot: 9 and 10)
 constexpr float kLazyMax = 8.f;     // log2-domain headroom of a row's reference maximum
 constexpr int kRegSoftmax = 216, kRegOther = 72, kRegLaunch = 168;
 static_assert(8 * kRegSoftmax + 4 * kRegOther == 12 * kRegLaunch, "register split sums to the launch's registers");
 constexpr int kItems = 512;         // (request, tile) items per launch
-constexpr uint32_t kTmemCols = 512, kColO = 256;
+constexpr uint32_t kTmemCols = 512;
 
 struct Items {
     int n;
@@ -60,26 +59,32 @@ struct Items {
 
 template <int D>
 struct Plan {
+    static constexpr int kBN = D == 128 ? 80 : 128;        // keys per tile: S, P and O of both slots fill tensor memory
+    static constexpr uint32_t kColS = 0, kColP = 2 * kBN;  // S of slot i at kColS + i kBN (fp32) ...
+    static constexpr uint32_t kPStep = D == 128 ? 48 : 64; // ... P at kColP + i kPStep (bf16 pairs)
+    static constexpr uint32_t kColO = kTmemCols - 2 * D;   // ... O at kColO + i D (fp32)
+    static_assert(kColP + kPStep + kBN / 2 <= kColO, "tensor memory columns");
     static constexpr int kHalves = D / 64;                 // 64-dim halves: 128-byte rows, 128-byte swizzle
-    static constexpr int kTile = kBN * D * 2;
-    static constexpr int kHalf = kBN * 128;
-    static constexpr int kStages = D == 128 ? 2 : 4;       // of K and of V each
+    static constexpr int kHalf = kBN * 128;                // of a K or V tile
+    static constexpr int kTile = kHalves * kHalf;
+    static constexpr int kQHalf = kBM * 128;
+    static constexpr int kQTile = kHalves * kQHalf;
+    static constexpr int kStages = 4;                      // of K and of V each
     static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kSlots * kTile;
+    static constexpr int kK = kQ + kSlots * kQTile;
     static constexpr int kV = kK + kStages * kTile;
     static constexpr int kBar = kV + kStages * kTile;
     enum {
         kKFull = 0,                          // [stage] K copied
-        kKFree = kKFull + kStages,           // [stage] the S products of the tile complete
-        kVFull = kKFree + kStages,
-        kVFree = kVFull + kStages,           // [stage] the P.V products of the tile complete
-        kVClean = kVFree + kStages,          // [stage] V looked over (2 warps)
-        kSFull = kVClean + kStages,          // [slot] S complete
-        kPFull = kSFull + kSlots,            // [slot] P written (4 warps)
-        kODone = kPFull + kSlots,            // [slot] P.V complete
-        kQReady = kODone + kSlots,           // Q of both slots in shared memory (8 warps)
-        kDone = kQReady + 1,                 // every product issued so far complete
-        kBars = kDone + 1
+        kVFull = kKFull + kStages,           // [stage] V copied
+        kVClean = kVFull + kStages,          // [stage] V looked over
+        kSFull = kVClean + kStages,          // [slot][stage] S complete
+        kODone = kSFull + kSlots * kStages,  // [slot][stage] P.V complete
+        kSFree = kODone + kSlots * kStages,  // [slot] S read (4 warps)
+        kPFull = kSFree + kSlots,            // [slot] P written (4 warps)
+        kQReady = kPFull + kSlots,           // Q of both slots in shared memory (8 warps)
+        kDone = kQReady + 1,                 // [slot] every product issued so far complete
+        kBars = kDone + kSlots
     };
     static constexpr int kMisc = kBar + 8 * kBars;         // tensor memory base, abort flag, spoilt flag
     static constexpr int kBytes = kMisc + 16 + 1024;       // + alignment of the dynamic base
@@ -96,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmWK, const __grid_constant__ CUtensorMap tmWV,
                        const __grid_constant__ AttnArgs a, const int b0, const __grid_constant__ Items items) {
     using L = Plan<D>;
+    constexpr int kBN = L::kBN;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -122,22 +128,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto first_key = [&](int p) { return a.W > 0 ? max(0, p - a.W + 1) : 0; };
     const int k0 = first_key(p_first) & ~15;
     const int ntiles = (p_last - k0) / kBN + 1;
-    auto slot_lo = [&](int i) { return kBM * i < nrow ? (first_key(cut + token(kBM * i)) - k0) / kBN : 0; };
+    // slot i multiplies tiles [0, slot_hi(i)); the last slot with rows goes through all of them
     auto slot_hi = [&](int i) { return kBM * i < nrow ? (cut + token(min(nrow, kBM * (i + 1)) - 1) - k0) / kBN + 1 : 0; };
-    // a tile in which every row of the CTA sees every key
-    auto whole = [&](int kb) { return kb >= first_key(p_last) && kb + kBN - 1 <= p_first; };
+    // tiles [w0, w1): every row of the CTA sees every key; the others are boundary tiles
+    const int w0 = (first_key(p_last) - k0 + kBN - 1) / kBN, w1 = max(w0, (p_first - k0 + 1) / kBN);
+    // slot i's barrier for tile j (`which`: kSFull or kODone) and its phase: one per stage, so
+    // that the copies, kStages tiles ahead of the products at most, can wait on them too
+    auto stage_bar = [&](int which, int i, int j) { return &bar[which + i * L::kStages + j % L::kStages]; };
+    auto phase = [](int j) { return (uint32_t)((j / L::kStages) & 1); };
 
     if (tid == 0) {
         for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&bar[L::kKFull + s], 1); mbar_init(&bar[L::kKFree + s], 1);
-            mbar_init(&bar[L::kVFull + s], 1); mbar_init(&bar[L::kVFree + s], 1);
-            mbar_init(&bar[L::kVClean + s], 2);
+            mbar_init(&bar[L::kKFull + s], 1);
+            mbar_init(&bar[L::kVFull + s], 1);
+            mbar_init(&bar[L::kVClean + s], 1);
         }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&bar[L::kSFull + s], 1); mbar_init(&bar[L::kPFull + s], 4); mbar_init(&bar[L::kODone + s], 1);
+        for (int i = 0; i < kSlots; ++i) {
+            for (int s = 0; s < L::kStages; ++s) {
+                mbar_init(&bar[L::kSFull + i * L::kStages + s], 1);
+                mbar_init(&bar[L::kODone + i * L::kStages + s], 1);
+            }
+            mbar_init(&bar[L::kSFree + i], 4);
+            mbar_init(&bar[L::kPFull + i], 4);
+            mbar_init(&bar[L::kDone + i], 1);
         }
         mbar_init(&bar[L::kQReady], 8);
-        mbar_init(&bar[L::kDone], 1);
         *abort_flag = 0;
         *spoilt = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -156,19 +171,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = warp >> 2, lg = warp & 3;
         const int row = 32 * lg + lane, r = kBM * slot + row;
         const uint32_t lane_off = (uint32_t)(32 * lg) << 16;
-        const uint32_t tS = tmem + 128 * slot + lane_off;
-        const uint32_t tO = tmem + kColO + 128 * slot + lane_off;
+        const uint32_t tS = tmem + L::kColS + kBN * slot + lane_off;
+        const uint32_t tP = tmem + L::kColP + L::kPStep * slot + lane_off;
+        const uint32_t tO = tmem + L::kColO + D * slot + lane_off;
         const bool valid = r < nrow;
         const int t = token(r), hq = kvh * a.g + (j0 + r) % a.g, p = cut + t;
         const int key_lo = first_key(p);
-        const int lo = slot_lo(slot), hi = slot_hi(slot);
+        const int hi = slot_hi(slot);
         // all rows of the slot see all keys of a tile from sl to sh
         const int sl = first_key(cut + token(min(nrow, kBM * (slot + 1)) - 1)), sh = cut + token(kBM * slot);
         bool fail = false;
         {
             // the row's query, rotated at p in fp32 and rounded to bf16, into the slot's Q tile
             // (16-byte chunk c of row r at c ^ (r mod 8)), 64 dims at a time
-            unsigned char* qt = sQ + slot * L::kTile;
+            unsigned char* qt = sQ + slot * L::kQTile;
 #pragma unroll 1
             for (int hf = 0; hf < L::kHalves; ++hf) {
                 uint4 qv[8];
@@ -203,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(qt + hf * L::kHalf + row * 128 + ((c ^ (row & 7)) << 4)) = qv[c];
+                    *reinterpret_cast<uint4*>(qt + hf * L::kQHalf + row * 128 + ((c ^ (row & 7)) << 4)) = qv[c];
             }
             fence_async_smem();
             __syncwarp();
@@ -211,16 +227,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float m_ref = -INFINITY, l = 0.f;                       // m_ref: of the scores, before scaling
         const float sc = a.scale_log2, lazy = kLazyMax / sc;
-        for (int j = lo; j < hi; ++j) {
-            const bool w = mbar_wait(&bar[L::kSFull + slot], (uint32_t)((j - lo) & 1)) && !*abort_flag;
+        for (int j = 0; j < hi; ++j) {
+            const bool w = wait(stage_bar(L::kSFull, slot, j), phase(j), abort_flag);
             if (!__all_sync(0xffffffffu, w)) { fail = true; break; }
             fence_after();
             float s[kBN];
-            tmem_ld32(tS, s);
-            tmem_ld32(tS + 32, s + 32);
-            tmem_ld32(tS + 64, s + 64);
-            tmem_ld32(tS + 96, s + 96);
+#pragma unroll
+            for (int c = 0; c + 32 <= kBN; c += 32) tmem_ld32(tS + c, s + c);
+            if constexpr (kBN % 32 == 16) tmem_ld16(tS + kBN - 16, s + kBN - 16);
             tmem_wait_ld();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[L::kSFree + slot]);          // S(j + 1) may overwrite it
             const int kb = k0 + kBN * j;
             if (!(kb >= sl && kb + kBN - 1 <= sh) || nrow < kBM * (slot + 1)) {
                 const int c0 = key_lo - kb, width = valid ? p - key_lo : -1;      // visible: c0 .. c0 + width
@@ -243,7 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 alpha = grow ? ex2((m_ref - mx) * sc) : 1.f;
                 m_ref = mx;
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            const bool any = __any_sync(0xffffffffu, grow);
+            // P.V(j - 1) reads P and adds to O: usually done long before the weights are
+            auto done = [&]() -> bool {
+                return j == 0 || __all_sync(0xffffffffu, wait(stage_bar(L::kODone, slot, j - 1), phase(j - 1), abort_flag));
+            };
+            if (any) {
+                if (!done()) { fail = true; break; }
+                fence_after();
                 const float f = grow ? alpha : 1.f;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -271,21 +296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float2 r4 = __fadd2_rn(__fadd2_rn(rs[0], rs[1]), __fadd2_rn(rs[2], rs[3]));
             l = l * alpha + (r4.x + r4.y);
-            tmem_st32(tS, pk);
-            tmem_st32(tS + 32, pk + 32);
+            if (!any && !done()) { fail = true; break; }
+            fence_after();
+#pragma unroll
+            for (int c = 0; c + 32 <= kBN / 2; c += 32) tmem_st32(tP + c, pk + c);
+            if constexpr (kBN / 2 % 32 == 8) tmem_st8(tP + kBN / 2 - 8, pk + kBN / 2 - 8);
             tmem_wait_st();
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[L::kPFull + slot]);
         }
-        if (!fail && hi > lo) {
-            const bool w = mbar_wait(&bar[L::kODone + slot], (uint32_t)((hi - lo - 1) & 1));
+        if (!fail && hi > 0) {
+            const bool w = wait(stage_bar(L::kODone, slot, hi - 1), phase(hi - 1), abort_flag);
             fail = !__all_sync(0xffffffffu, w);
         }
         if (fail) {
             if (lane == 0) atomicOr(a.hdr, kErrWait);
             *abort_flag = 1;
-        } else if (hi > lo && !*abort_flag) {
+        } else if (hi > 0 && !*abort_flag) {
             fence_after();
             const float inv = 1.f / l;
             const size_t orow = (((size_t)item.z + t) * a.Hq + hq) * D;
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fix) {
                     // values that are not finite, left out of boundary tiles: visible ones count
                     for (int key = key_lo; key <= p; ++key) {
-                        if (whole(k0 + (key - k0) / kBN * kBN)) { key = k0 + (key - k0) / kBN * kBN + kBN - 1; continue; }
+                        if ((key - k0) / kBN >= w0 && (key - k0) / kBN < w1) { key = k0 + w1 * kBN - 1; continue; }
                         const bool staged = a.ring && key >= (cut & ~15);
                         const size_t at = staged ? stage_row(b, kvh, key, cut, a.Hkv, a.ws_rows)
                                                  : kv_row(a.table, b, kvh, a.ring ? key % a.S : key, a.Hkv, a.S);
@@ -348,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!a.table && !a.ring) {
                 if (lane < L::kHalves) tma_load_2d(dst + lane * L::kHalf, tm, 64 * lane, head_row0 + kb, full);
-            } else if (lane < 8 * L::kHalves) {
-                const int gi = lane & 7, half = lane >> 3;
+            } else if (lane < kBN / 16 * L::kHalves) {
+                const int gi = lane % (kBN / 16), half = lane / (kBN / 16);
                 const int pos = min(kb + 16 * gi, p_last & ~15);
                 const CUtensorMap* m = tm;
                 int row;
@@ -364,19 +392,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_2d(dst + half * L::kHalf + gi * 16 * 128, m, 64 * half, row, full);
             }
         };
+        // a stage is free when the slots that multiply its tile are done with it
+        const int hi0 = slot_hi(0), hi1 = slot_hi(1);
+        auto free_again = [&](int which, int j) -> bool {
+            return __all_sync(0xffffffffu, (j >= hi0 || wait(stage_bar(which, 0, j), phase(j), abort_flag)) &&
+                                               (j >= hi1 || wait(stage_bar(which, 1, j), phase(j), abort_flag)));
+        };
+        auto looked = [&](int j) -> bool {
+            return __all_sync(0xffffffffu, wait(&bar[L::kVClean + j % L::kStages], phase(j), abort_flag));
+        };
         bool ok = true;
         int k_issued = 0, v_issued = 0;
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % L::kStages;
-            const uint32_t used = (uint32_t)((j / L::kStages - 1) & 1);
-            if (j >= L::kStages) ok = mbar_wait(&bar[L::kKFree + st], used);
-            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-            if (!ok) break;
+            if (j >= L::kStages && !(ok = free_again(L::kSFull, j - L::kStages))) break;
             load_tile(&tmK, &tmWK, sK + st * L::kTile, &bar[L::kKFull + st], k0 + kBN * j);
             k_issued = j + 1;
-            if (j >= L::kStages) ok = mbar_wait(&bar[L::kVFree + st], used);
-            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-            if (!ok) break;
+            if (j >= L::kStages && !(ok = free_again(L::kODone, j - L::kStages) && looked(j - L::kStages))) break;
             load_tile(&tmV, &tmWV, sV + st * L::kTile, &bar[L::kVFull + st], k0 + kBN * j);
             v_issued = j + 1;
         }
@@ -385,113 +417,102 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) atomicOr(a.hdr, kErrWait);
             // the last copy issued into each stage lands before the CTA can exit
             for (int j = max(0, k_issued - L::kStages); j < k_issued; ++j)
-                mbar_wait(&bar[L::kKFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
+                drain(&bar[L::kKFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
             for (int j = max(0, v_issued - L::kStages); j < v_issued; ++j)
-                mbar_wait(&bar[L::kVFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
+                drain(&bar[L::kVFull + j % L::kStages], (uint32_t)((j / L::kStages) & 1));
         }
         __syncwarp();
-    } else if (warp == kWarpMma) {
-        // ================= one thread issues every matrix instruction
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = instr_desc_bf16(kBM, kBN, false), idesc_pv = instr_desc_bf16(kBM, D, true);
-            const uint64_t qdesc0 = smem_desc(smem_u32(sQ), 16), kdesc0 = smem_desc(smem_u32(sK), 16);
-            const uint64_t vdesc0 = smem_desc(smem_u32(sV), L::kHalf);
-            auto koff = [](int s) { return (uint64_t)(((s >> 2) * L::kHalf + (s & 3) * 32) >> 4); };
-            int lo[kSlots], hi[kSlots];
-            for (int i = 0; i < kSlots; ++i) { lo[i] = slot_lo(i); hi[i] = slot_hi(i); }
-            // S_i = Q_i K_j^T, 16 dims per instruction
-            auto issue_s = [&](int i, int j) {
-                const uint64_t qd = qdesc0 + (uint64_t)(i * (L::kTile >> 4));
-                const uint64_t kd = kdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+    } else if (warp < kWarpLook) {
+        // ================= matrix instructions of one slot, one lane issuing.  Per tile: S(j + 1)
+        // as soon as the softmax has read S(j), then P.V(j) when the weights are there
+        constexpr uint32_t idesc_qk = instr_desc_bf16(kBM, kBN, false), idesc_pv = instr_desc_bf16(kBM, D, true);
+        const int slot = warp - kWarpMma, hi = slot_hi(slot);
+        const uint64_t qdesc = smem_desc(smem_u32(sQ) + slot * L::kQTile, 16), kdesc0 = smem_desc(smem_u32(sK), 16);
+        const uint64_t vdesc0 = smem_desc(smem_u32(sV), L::kHalf);
+        const uint32_t tS = tmem + L::kColS + kBN * slot, tP = tmem + L::kColP + L::kPStep * slot, tO = tmem + L::kColO + D * slot;
+        const bool lead = elect_one();
+        auto wait_ok = [&](uint64_t* b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, spin(b, parity, abort_flag)); };
+        // S = Q K_j^T, 16 dims per instruction
+        auto issue_s = [&](int j) {
+            const uint64_t kd = kdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+            if (lead) {
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) mma_ss(tmem + 128 * i, qd + koff(s), kd + koff(s), idesc_qk, s > 0);
-                mma_commit(&bar[L::kSFull + i]);
-            };
-            // O_i += P_i V_j: keys 16 s .. + 15 of P sit in columns 8 s .. + 7 of S buffer i
-            auto issue_pv = [&](int i, int j) {
-                const uint64_t vd = vdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+                for (int s = 0; s < D / 16; ++s)
+                    mma_ss(tS, qdesc + (uint64_t)(((s >> 2) * L::kQHalf + (s & 3) * 32) >> 4),
+                           kd + (uint64_t)(((s >> 2) * L::kHalf + (s & 3) * 32) >> 4), idesc_qk, s > 0);
+                mma_commit(stage_bar(L::kSFull, slot, j));
+            }
+            __syncwarp();
+        };
+        // O += P V_j: keys 16 s .. + 15 of P sit in its columns 8 s .. + 7
+        auto issue_pv = [&](int j) {
+            const uint64_t vd = vdesc0 + (uint64_t)((j % L::kStages) * (L::kTile >> 4));
+            if (lead) {
 #pragma unroll
                 for (int s = 0; s < kBN / 16; ++s)
-                    mma_ts(tmem + kColO + 128 * i, tmem + 128 * i + 8 * s, vd + (uint64_t)((s * 2048) >> 4), idesc_pv,
-                           (j > lo[i] || s > 0));
-                mma_commit(&bar[L::kODone + i]);
-            };
-            auto wait_ok = [&](int which, uint32_t parity) { return mbar_spin(&bar[which], parity) && !*abort_flag; };
-            auto wait_v = [&](int j) {
-                const uint32_t parity = (uint32_t)((j / L::kStages) & 1);
-                return wait_ok(L::kVFull + j % L::kStages, parity) && wait_ok(L::kVClean + j % L::kStages, parity);
-            };
-            bool ok = wait_ok(L::kQReady, 0);
-            for (int j = -1; j < ntiles && ok; ++j) {
-                const int vs = (j + L::kStages) % L::kStages, jn = j + 1, ks = jn % L::kStages;
-                bool k_seen = false, v_seen = false;
-                for (int i = 0; i < kSlots && ok; ++i) {
-                    if (j >= lo[i] && j < hi[i]) {
-                        if (!v_seen) ok = wait_v(j);
-                        v_seen = true;
-                        ok = ok && wait_ok(L::kPFull + i, (uint32_t)((j - lo[i]) & 1));
-                        if (!ok) break;
-                        fence_after();
-                        issue_pv(i, j);
-                    }
-                    if (jn >= lo[i] && jn < hi[i]) {
-                        if (!k_seen) ok = wait_ok(L::kKFull + ks, (uint32_t)((jn / L::kStages) & 1));
-                        k_seen = true;
-                        // S(j + 1) overwrites the columns that P.V(j) reads
-                        if (ok && jn > lo[i]) ok = wait_ok(L::kODone + i, (uint32_t)((j - lo[i]) & 1));
-                        if (!ok) break;
-                        fence_after();
-                        issue_s(i, jn);
-                    }
-                }
-                if (!ok) break;
-                if (j >= 0) {
-                    // (a tile that no slot multiplied is still waited for: its copy has to land)
-                    if (!v_seen) ok = wait_v(j);
-                    mma_commit(&bar[L::kVFree + vs]);
-                }
-                if (jn < ntiles) {
-                    if (!k_seen) ok = ok && wait_ok(L::kKFull + ks, (uint32_t)((jn / L::kStages) & 1));
-                    mma_commit(&bar[L::kKFree + ks]);
-                }
+                    mma_ts(tO, tP + 8 * s, vd + (uint64_t)((s * 2048) >> 4), idesc_pv, (j > 0 || s > 0));
+                mma_commit(stage_bar(L::kODone, slot, j));
             }
-            if (!ok) {
-                *abort_flag = 1;
-                atomicOr(a.hdr, kErrWait);
-            }
-            // no product may still target the columns when they are freed
-            mma_commit(&bar[L::kDone]);
-            mbar_wait(&bar[L::kDone], 0);
+            __syncwarp();
+        };
+        bool ok = hi == 0 || (wait_ok(&bar[L::kQReady], 0) && wait_ok(&bar[L::kKFull], 0));
+        if (ok && hi > 0) {
+            fence_after();
+            issue_s(0);
         }
+        for (int j = 0; j < hi && ok; ++j) {
+            const int st = j % L::kStages, next = (j + 1) % L::kStages;
+            if (j + 1 < hi) {
+                ok = wait_ok(&bar[L::kKFull + next], phase(j + 1)) && wait_ok(&bar[L::kSFree + slot], (uint32_t)(j & 1));
+                if (!ok) break;
+                fence_after();
+                issue_s(j + 1);
+            }
+            ok = wait_ok(&bar[L::kVFull + st], phase(j));
+            if (j < w0 || j >= w1) ok = ok && wait_ok(&bar[L::kVClean + st], phase(j));
+            ok = ok && wait_ok(&bar[L::kPFull + slot], (uint32_t)(j & 1));
+            if (!ok) break;
+            fence_after();
+            issue_pv(j);
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            if (lane == 0) atomicOr(a.hdr, kErrWait);
+        }
+        // no product may still target the columns when they are freed
+        if (lead) mma_commit(&bar[L::kDone + slot]);
+        __syncwarp();
+        drain(&bar[L::kDone + slot], 0);
         __syncwarp();
     } else {
         // ================= value rows of boundary tiles: what is not finite becomes 0
-        const int t = tid - 32 * kWarpLook;
         bool ok = true;
         for (int j = 0; j < ntiles; ++j) {
-            const int st = j % L::kStages, kb = k0 + kBN * j;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar[L::kVFull + st], (uint32_t)((j / L::kStages) & 1)) && !*abort_flag);
+            const int st = j % L::kStages;
+            ok = __all_sync(0xffffffffu, wait(&bar[L::kVFull + st], phase(j), abort_flag));
             if (!ok) break;
-            if (!whole(kb)) {
-                unsigned char* tile = sV + st * L::kTile;
-                bool any = false;
-#pragma unroll 4
-                for (int q = t; q < L::kTile / 16; q += 64) {
-                    uint4 u = *reinterpret_cast<const uint4*>(tile + 16 * q);
-                    if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
-                        uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-                            if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
-                        }
-                        *reinterpret_cast<uint4*>(tile + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-                        any = true;
-                    }
-                }
-                if (any) *spoilt = 1;
-                fence_async_smem();
+            if (j >= w0 && j < w1) {
+                if (lane == 0) mbar_arrive(&bar[L::kVClean + st]);
+                continue;
             }
+            unsigned char* tile = sV + st * L::kTile;
+            bool any = false;
+#pragma unroll 4
+            for (int q = lane; q < L::kTile / 16; q += 32) {
+                const uint4 u = *reinterpret_cast<const uint4*>(tile + 16 * q);
+                if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
+                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+                        if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
+                    }
+                    *reinterpret_cast<uint4*>(tile + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                    any = true;
+                }
+            }
+            if (any) *spoilt = 1;
+            fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[L::kVClean + st]);
         }
@@ -522,15 +543,16 @@ cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items
 bool prompt_tc_supported(const Shape& s) {
     const long long rows = s.pages ? (long long)s.pages * s.Hkv * kPage : (long long)s.B * s.Hkv * s.S;
     const long long staged = s.ring ? (long long)s.B * s.Hkv * chunk_ws_rows(s) : 0;
-    return s.bf16 && !s.int8 && (s.d == 64 || s.d == 128) && rows < (1ll << 31) - kBN && staged < (1ll << 31);
+    return s.bf16 && !s.int8 && (s.d == 64 || s.d == 128) && rows < (1ll << 31) - 128 && staged < (1ll << 31);
 }
 
 cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packed& g, cudaStream_t st) {
     const Shape& s = h->sh;
+    const int bn = s.d == 128 ? Plan<128>::kBN : Plan<64>::kBN;
     CUtensorMap tm[4];
     const cuuint64_t rows = s.pages ? (cuuint64_t)s.pages * s.Hkv * kPage : (cuuint64_t)s.B * s.Hkv * s.S;
     const cuuint64_t dims[2] = {(cuuint64_t)s.d, rows}, strides[1] = {(cuuint64_t)s.d * 2};
-    const cuuint32_t box[2] = {64, (s.pages || s.ring) ? (cuuint32_t)kPage : (cuuint32_t)kBN};
+    const cuuint32_t box[2] = {64, (s.pages || s.ring) ? (cuuint32_t)kPage : (cuuint32_t)bn};
     if (!make_tensor_map_bf16(&tm[0], const_cast<void*>(a.kc), 2, dims, strides, box) ||
         !make_tensor_map_bf16(&tm[1], const_cast<void*>(a.vc), 2, dims, strides, box))
         return cudaErrorInvalidValue;
@@ -550,7 +572,7 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
         for (long long t = 0; t * kRows < all; ++t) {
             const int first = cut + (int)(t * kRows / s.g), last = cut + (int)((std::min(all, (t + 1) * kRows) - 1) / s.g);
             const int k0 = (s.W > 0 ? std::max(0, first - s.W + 1) : 0) & ~15;
-            work.push_back({-((last - k0) / kBN + 1), make_int4(i, (int)t, (int)(g.row0 + g.off[i]), n)});
+            work.push_back({-((last - k0) / bn + 1), make_int4(i, (int)t, (int)(g.row0 + g.off[i]), n)});
         }
     }
     std::stable_sort(work.begin(), work.end(), [](const auto& x, const auto& y) { return x.first < y.first; });
