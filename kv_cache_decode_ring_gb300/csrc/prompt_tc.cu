@@ -89,11 +89,11 @@ struct Plan {
     static constexpr int kMisc = kBar + 8 * kBars;         // tensor memory base, abort flag, spoilt flag
     static constexpr int kBytes = kMisc + 16 + 1024;       // + alignment of the dynamic base
     static_assert(kBytes <= (int)kMaxSmemPerBlock, "shared memory per block");
+    static_assert(kTile % (16 * 8 * 32) == 0, "looked over in rounds of eight chunks a lane");
 };
 
-__device__ __forceinline__ bool not_finite(uint32_t w) {   // either bf16 of a pair
-    return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
-}
+// Bits 15 and 31 tell whether the low and the high bf16 of a pair are not finite.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -175,56 +175,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tP = tmem + L::kColP + L::kPStep * slot + lane_off;
         const uint32_t tO = tmem + L::kColO + D * slot + lane_off;
         const bool valid = r < nrow;
-        const int t = token(r), hq = kvh * a.g + (j0 + r) % a.g, p = cut + t;
+        const int p = cut + token(r);
         const int key_lo = first_key(p);
         const int hi = slot_hi(slot);
         // all rows of the slot see all keys of a tile from sl to sh
         const int sl = first_key(cut + token(min(nrow, kBM * (slot + 1)) - 1)), sh = cut + token(kBM * slot);
         bool fail = false;
+        // the warp's 32 queries, rotated at their positions in fp32 and rounded to bf16, into the
+        // slot's Q tile (16-byte chunk c of row r at c ^ (r mod 8)): D / 8 lanes a row, eight
+        // rounds of loads in flight
         {
-            // the row's query, rotated at p in fp32 and rounded to bf16, into the slot's Q tile
-            // (16-byte chunk c of row r at c ^ (r mod 8)), 64 dims at a time
+            constexpr int kPer = D / 8, kTogether = 32 / kPer, kRounds = 32 / kTogether;
             unsigned char* qt = sQ + slot * L::kQTile;
+            const int c = lane % kPer, r0 = 32 * lg + lane / kPer;             // chunk, first row
+            const int first = j0 + kBM * slot + r0;
+            int tt = t0 + first / a.g, jj = first % a.g;                       // its token and head
 #pragma unroll 1
-            for (int hf = 0; hf < L::kHalves; ++hf) {
+            for (int e0 = 0; e0 < kRounds; e0 += 8) {
                 uint4 qv[8];
-                float4 rv[16];
+                float4 ra[8], rb[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) qv[c] = make_uint4(0u, 0u, 0u, 0u);
-                const bool turn = a.rope && valid && p < a.P;
-                if (valid) {
-                    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                                      ((size_t)item.z + t) * a.q_stride + (size_t)hq * D + 64 * hf);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) qv[c] = __ldg(src + c);
+                for (int e = 0; e < 8; ++e) {
+                    qv[e] = make_uint4(0u, 0u, 0u, 0u);
+                    ra[e] = rb[e] = make_float4(1.f, 0.f, 1.f, 0.f);
+                    if (kBM * slot + r0 + (e0 + e) * kTogether < nrow) {
+                        qv[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)item.z + tt) * a.q_stride +
+                                                                     (size_t)(kvh * a.g + jj) * D) + c);
+                        if (a.rope && cut + tt < a.P) {
+                            const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)(cut + tt) * (D / 2) + 4 * c);
+                            ra[e] = __ldg(rp);
+                            rb[e] = __ldg(rp + 1);
+                        }
+                    }
+                    for (jj += kTogether; jj >= a.g; jj -= a.g) ++tt;
                 }
-                if (turn) {
-                    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (D / 2) + 32 * hf);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) rv[c] = __ldg(rp + c);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+                for (int e = 0; e < 8; ++e) {
+                    const int rr = r0 + (e0 + e) * kTogether;
+                    uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
+                    if (a.rope) {
+                        const float2 cs[4] = {make_float2(ra[e].x, ra[e].y), make_float2(ra[e].z, ra[e].w),
+                                              make_float2(rb[e].x, rb[e].y), make_float2(rb[e].z, rb[e].w)};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float4 r4 = rv[(4 * c + k) >> 1];
                             float y0, y1;
-                            rope_pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u),
-                                      (k & 1) ? make_float2(r4.z, r4.w) : make_float2(r4.x, r4.y), y0, y1);
+                            rope_pair(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u), cs[k], y0, y1);
                             const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
                             w[k] = *reinterpret_cast<const uint32_t*>(&o2);
                         }
-                        qv[c] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    *reinterpret_cast<uint4*>(qt + (c >> 3) * L::kQHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(qt + hf * L::kQHalf + row * 128 + ((c ^ (row & 7)) << 4)) = qv[c];
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[L::kQReady]);
         }
+        // o[0, 32) += the values that are not finite and were left out of boundary tiles, of the
+        // keys that a row sees
+        auto add_spoilt = [&](float* o, int x0, int lo, int hi_key) {
+            for (int key = lo; key <= hi_key; ++key) {
+                if ((key - k0) / kBN >= w0 && (key - k0) / kBN < w1) { key = k0 + w1 * kBN - 1; continue; }
+                const bool staged = a.ring && key >= (cut & ~15);
+                const size_t at = staged ? stage_row(b, kvh, key, cut, a.Hkv, a.ws_rows)
+                                         : kv_row(a.table, b, kvh, a.ring ? key % a.S : key, a.Hkv, a.S);
+                const uint4* v = reinterpret_cast<const uint4*>((staged ? a.wv : static_cast<const __nv_bfloat16*>(a.vc)) + at * D + x0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 u = v[e];
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float v0 = __uint_as_float(w[k] << 16), v1 = __uint_as_float(w[k] & 0xffff0000u);
+                        if (!isfinite(v0)) o[8 * e + 2 * k] += v0;
+                        if (!isfinite(v1)) o[8 * e + 2 * k + 1] += v1;
+                    }
+                }
+            }
+        };
         float m_ref = -INFINITY, l = 0.f;                       // m_ref: of the scores, before scaling
         const float sc = a.scale_log2, lazy = kLazyMax / sc;
         for (int j = 0; j < hi; ++j) {
@@ -316,40 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (hi > 0 && !*abort_flag) {
             fence_after();
             const float inv = 1.f / l;
-            const size_t orow = (((size_t)item.z + t) * a.Hq + hq) * D;
             const bool fix = *spoilt != 0;
+            // through the warp's own rows of the Q tile (its scores are all done), so that a store
+            // covers whole 128-byte lines: 32 dims at a time as fp32, 64 as bf16
+            unsigned char* stage = sQ + slot * L::kQTile + 32 * lg * 128;
+            const int c = lane & 7, first = j0 + kBM * slot + 32 * lg + (lane >> 3);      // store: chunk, first row
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int x0 = 0; x0 < D; x0 += 32) {
                 float o[32];
-                tmem_ld32(tO + c, o);
+                tmem_ld32(tO + x0, o);
                 tmem_wait_ld();
-                if (!valid) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] *= inv;
-                if (fix) {
-                    // values that are not finite, left out of boundary tiles: visible ones count
-                    for (int key = key_lo; key <= p; ++key) {
-                        if ((key - k0) / kBN >= w0 && (key - k0) / kBN < w1) { key = k0 + w1 * kBN - 1; continue; }
-                        const bool staged = a.ring && key >= (cut & ~15);
-                        const size_t at = staged ? stage_row(b, kvh, key, cut, a.Hkv, a.ws_rows)
-                                                 : kv_row(a.table, b, kvh, a.ring ? key % a.S : key, a.Hkv, a.S);
-                        const uint4* v = reinterpret_cast<const uint4*>(
-                            (staged ? a.wv : static_cast<const __nv_bfloat16*>(a.vc)) + at * D + c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 u = v[e];
-                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float v0 = __uint_as_float(w[k] << 16), v1 = __uint_as_float(w[k] & 0xffff0000u);
-                                if (!isfinite(v0)) o[8 * e + 2 * k] += v0;
-                                if (!isfinite(v1)) o[8 * e + 2 * k + 1] += v1;
-                            }
-                        }
-                    }
-                }
+                if (fix && valid) add_spoilt(o, x0, key_lo, p);
                 if (a.out_bf16) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow + c);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t u[4];
@@ -358,39 +367,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const __nv_bfloat162 t2 = __floats2bfloat162_rn(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
                             u[k] = *reinterpret_cast<const uint32_t*>(&t2);
                         }
-                        dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+                        *reinterpret_cast<uint4*>(stage + lane * 128 + (((x0 / 32 % 2 * 4 + e) ^ (lane & 7)) << 4)) =
+                            make_uint4(u[0], u[1], u[2], u[3]);
                     }
+                    if (x0 % 64 == 0) continue;
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                            make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
+                __syncwarp();
+                int tt = t0 + first / a.g, jj = first % a.g;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int rr = (lane >> 3) + 4 * e;
+                    if (kBM * slot + 32 * lg + rr < nrow) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+                        const size_t orow = (((size_t)item.z + tt) * a.Hq + kvh * a.g + jj) * D;
+                        if (a.out_bf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow + x0 / 64 * 64 + 8 * c) = u;
+                        else *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + orow + x0 + 4 * c) = u;
+                    }
+                    for (jj += 4; jj >= a.g; jj -= a.g) ++tt;
+                }
+                __syncwarp();
             }
         }
     } else if (warp == kWarpCopy) {
         // ================= tensor copies of K and V tiles
+        // a lane copies one box: of 128-row boxes a half each, of 16-row boxes a group of a half
+        const bool boxes = a.table || a.ring;
+        const int nbox = boxes ? kBN / 16 * L::kHalves : L::kHalves;
+        const int gi = boxes ? lane % (kBN / 16) : 0, half = boxes ? lane / (kBN / 16) : lane;
         const int head_row0 = (b * a.Hkv + kvh) * a.S, cal = cut & ~15;
         const int ws_row0 = (b * a.Hkv + kvh) * a.ws_rows;
-        auto load_tile = [&](const CUtensorMap* tm, const CUtensorMap* tmw, unsigned char* dst, uint64_t* full, int kb) {
+        // the lane's first row in tile j; a staged row as -1 - row
+        auto row_of = [&](int j) {
+            const int kb = k0 + kBN * j;
+            if (!boxes) return head_row0 + kb;
+            if (lane >= nbox || j >= ntiles) return 0;
+            const int pos = min(kb + 16 * gi, p_last & ~15);
+            if (a.ring && pos >= cal) return -1 - (ws_row0 + (pos - cal));
+            const int slot = a.ring ? pos % a.S : pos;
+            return a.table ? (max(a.table[(size_t)b * (a.S / kPage) + slot / kPage], 0) * a.Hkv + kvh) * kPage : head_row0 + slot;
+        };
+        auto load_tile = [&](const CUtensorMap* tm, const CUtensorMap* tmw, unsigned char* dst, uint64_t* full, int row) {
             if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
             __syncwarp();
-            if (!a.table && !a.ring) {
-                if (lane < L::kHalves) tma_load_2d(dst + lane * L::kHalf, tm, 64 * lane, head_row0 + kb, full);
-            } else if (lane < kBN / 16 * L::kHalves) {
-                const int gi = lane % (kBN / 16), half = lane / (kBN / 16);
-                const int pos = min(kb + 16 * gi, p_last & ~15);
-                const CUtensorMap* m = tm;
-                int row;
-                if (a.ring && pos >= cal) {
-                    m = tmw;
-                    row = ws_row0 + (pos - cal);
-                } else {
-                    const int slot = a.ring ? pos % a.S : pos;
-                    row = a.table ? (max(a.table[(size_t)b * (a.S / kPage) + slot / kPage], 0) * a.Hkv + kvh) * kPage
-                                  : head_row0 + slot;
-                }
-                tma_load_2d(dst + half * L::kHalf + gi * 16 * 128, m, 64 * half, row, full);
-            }
+            if (lane < nbox) tma_load_2d(dst + half * L::kHalf + gi * 16 * 128, row < 0 ? tmw : tm, 64 * half, row < 0 ? -1 - row : row, full);
         };
         // a stage is free when the slots that multiply its tile are done with it
         const int hi0 = slot_hi(0), hi1 = slot_hi(1);
@@ -403,14 +427,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         int k_issued = 0, v_issued = 0;
+        int row = row_of(0);
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % L::kStages;
+            const int ahead = row_of(j + 1);                    // its page number is read while this tile waits
             if (j >= L::kStages && !(ok = free_again(L::kSFull, j - L::kStages))) break;
-            load_tile(&tmK, &tmWK, sK + st * L::kTile, &bar[L::kKFull + st], k0 + kBN * j);
+            load_tile(&tmK, &tmWK, sK + st * L::kTile, &bar[L::kKFull + st], row);
             k_issued = j + 1;
             if (j >= L::kStages && !(ok = free_again(L::kODone, j - L::kStages) && looked(j - L::kStages))) break;
-            load_tile(&tmV, &tmWV, sV + st * L::kTile, &bar[L::kVFull + st], k0 + kBN * j);
+            load_tile(&tmV, &tmWV, sV + st * L::kTile, &bar[L::kVFull + st], row);
             v_issued = j + 1;
+            row = ahead;
         }
         if (!ok) {
             *abort_flag = 1;
@@ -497,18 +524,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             unsigned char* tile = sV + st * L::kTile;
             bool any = false;
-#pragma unroll 4
-            for (int q = lane; q < L::kTile / 16; q += 32) {
-                const uint4 u = *reinterpret_cast<const uint4*>(tile + 16 * q);
-                if (not_finite(u.x) || not_finite(u.y) || not_finite(u.z) || not_finite(u.w)) {
-                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+            for (int q0 = lane; q0 < L::kTile / 16; q0 += 8 * 32) {
+                uint4 u[8];
+                uint32_t bad = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
-                        if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
-                    }
-                    *reinterpret_cast<uint4*>(tile + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 8; ++e) u[e] = *reinterpret_cast<const uint4*>(tile + 16 * (q0 + 32 * e));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) bad |= odd_bits(u[e].x) | odd_bits(u[e].y) | odd_bits(u[e].z) | odd_bits(u[e].w);
+                if (bad & 0x80008000u) {
                     any = true;
+                    for (int q = q0; q < q0 + 8 * 32; q += 32) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(tile + 16 * q);
+                        for (int k = 0; k < 4; ++k) {
+                            if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u;
+                            if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0x0000ffffu;
+                        }
+                    }
                 }
             }
             if (any) *spoilt = 1;
