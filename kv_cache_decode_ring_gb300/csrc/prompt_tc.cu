@@ -182,37 +182,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sl = first_key(cut + token(min(nrow, kBM * (slot + 1)) - 1)), sh = cut + token(kBM * slot);
         bool fail = false;
         // the warp's 32 queries, rotated at their positions in fp32 and rounded to bf16, into the
-        // slot's Q tile (16-byte chunk c of row r at c ^ (r mod 8)): D / 8 lanes a row, eight
+        // slot's Q tile (16-byte chunk c of row r at c ^ (r mod 8)): D / 8 lanes a row, all
         // rounds of loads in flight
+        constexpr int kPer = D / 8, kTogether = 32 / kPer, kRounds = 32 / kTogether;
+        const int dt = kTogether / a.g, dj = kTogether % a.g;
+        auto next_row = [&](int& tt, int& jj) {
+            tt += dt;
+            jj += dj;
+            if (jj >= a.g) { jj -= a.g; ++tt; }
+        };
+        uint4 qv[kRounds];
+        int q_tok[kRounds / 8], q_head[kRounds / 8];                           // token and head of every eighth round's row
         {
-            constexpr int kPer = D / 8, kTogether = 32 / kPer, kRounds = 32 / kTogether;
+            const int r0 = kBM * slot + 32 * lg + lane / kPer;
+            int tt = t0 + (j0 + r0) / a.g, jj = (j0 + r0) % a.g;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (size_t)item.z * a.q_stride +
+                                     (size_t)kvh * a.g * D + 8 * (lane % kPer);
+#pragma unroll
+            for (int e = 0; e < kRounds; ++e) {
+                if (e % 8 == 0) { q_tok[e / 8] = tt; q_head[e / 8] = jj; }
+                qv[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + e * kTogether < nrow) qv[e] = __ldg(reinterpret_cast<const uint4*>(q + tt * a.q_stride + jj * D));
+                next_row(tt, jj);
+            }
+        }
+        {
             unsigned char* qt = sQ + slot * L::kQTile;
             const int c = lane % kPer, r0 = 32 * lg + lane / kPer;             // chunk, first row
-            const int first = j0 + kBM * slot + r0;
-            int tt = t0 + first / a.g, jj = first % a.g;                       // its token and head
-#pragma unroll 1
+#pragma unroll
             for (int e0 = 0; e0 < kRounds; e0 += 8) {
-                uint4 qv[8];
                 float4 ra[8], rb[8];
+                int tt = q_tok[e0 / 8], jj = q_head[e0 / 8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    qv[e] = make_uint4(0u, 0u, 0u, 0u);
                     ra[e] = rb[e] = make_float4(1.f, 0.f, 1.f, 0.f);
-                    if (kBM * slot + r0 + (e0 + e) * kTogether < nrow) {
-                        qv[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)item.z + tt) * a.q_stride +
-                                                                     (size_t)(kvh * a.g + jj) * D) + c);
-                        if (a.rope && cut + tt < a.P) {
-                            const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)(cut + tt) * (D / 2) + 4 * c);
-                            ra[e] = __ldg(rp);
-                            rb[e] = __ldg(rp + 1);
-                        }
+                    if (a.rope && kBM * slot + r0 + (e0 + e) * kTogether < nrow && cut + tt < a.P) {
+                        const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)(cut + tt) * (D / 2) + 4 * c);
+                        ra[e] = __ldg(rp);
+                        rb[e] = __ldg(rp + 1);
                     }
-                    for (jj += kTogether; jj >= a.g; jj -= a.g) ++tt;
+                    next_row(tt, jj);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int rr = r0 + (e0 + e) * kTogether;
-                    uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
+                    uint32_t w[4] = {qv[e0 + e].x, qv[e0 + e].y, qv[e0 + e].z, qv[e0 + e].w};
                     if (a.rope) {
                         const float2 cs[4] = {make_float2(ra[e].x, ra[e].y), make_float2(ra[e].z, ra[e].w),
                                               make_float2(rb[e].x, rb[e].y), make_float2(rb[e].z, rb[e].w)};
@@ -349,7 +363,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // through the warp's own rows of the Q tile (its scores are all done), so that a store
             // covers whole 128-byte lines: 32 dims at a time as fp32, 64 as bf16
             unsigned char* stage = sQ + slot * L::kQTile + 32 * lg * 128;
-            const int c = lane & 7, first = j0 + kBM * slot + 32 * lg + (lane >> 3);      // store: chunk, first row
+            const int c = lane & 7, r1 = kBM * slot + 32 * lg + (lane >> 3);   // store: chunk, first row (then every fourth)
+            const int tok = t0 + (j0 + r1) / a.g, head = (j0 + r1) % a.g, dt4 = 4 / a.g, dj4 = 4 % a.g;
+            const size_t orow = ((size_t)item.z * a.Hq + kvh * a.g) * D;
 #pragma unroll 1
             for (int x0 = 0; x0 < D; x0 += 32) {
                 float o[32];
@@ -378,43 +394,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
                 __syncwarp();
-                int tt = t0 + first / a.g, jj = first % a.g;
+                int tt = tok, jj = head;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int rr = (lane >> 3) + 4 * e;
-                    if (kBM * slot + 32 * lg + rr < nrow) {
+                    if (r1 + 4 * e < nrow) {
                         const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
-                        const size_t orow = (((size_t)item.z + tt) * a.Hq + kvh * a.g + jj) * D;
-                        if (a.out_bf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow + x0 / 64 * 64 + 8 * c) = u;
-                        else *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + orow + x0 + 4 * c) = u;
+                        const size_t at = orow + ((size_t)tt * a.Hq + jj) * D;
+                        if (a.out_bf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + x0 / 64 * 64 + 8 * c) = u;
+                        else *reinterpret_cast<uint4*>(static_cast<float*>(a.out) + at + x0 + 4 * c) = u;
                     }
-                    for (jj += 4; jj >= a.g; jj -= a.g) ++tt;
+                    tt += dt4;
+                    jj += dj4;
+                    if (jj >= a.g) { jj -= a.g; ++tt; }
                 }
                 __syncwarp();
             }
         }
     } else if (warp == kWarpCopy) {
         // ================= tensor copies of K and V tiles
-        // a lane copies one box: of 128-row boxes a half each, of 16-row boxes a group of a half
-        const bool boxes = a.table || a.ring;
-        const int nbox = boxes ? kBN / 16 * L::kHalves : L::kHalves;
-        const int gi = boxes ? lane % (kBN / 16) : 0, half = boxes ? lane / (kBN / 16) : lane;
+        // one box of kBN rows a half on a contiguous cache; else a box per 16 rows, both halves,
+        // whose number a lane looks up and the elected lane issues
+        const bool boxes = a.table || a.ring, lead = elect_one();
         const int head_row0 = (b * a.Hkv + kvh) * a.S, cal = cut & ~15;
         const int ws_row0 = (b * a.Hkv + kvh) * a.ws_rows;
-        // the lane's first row in tile j; a staged row as -1 - row
+        // first row of the lane's group in tile j; a staged row as -1 - row
         auto row_of = [&](int j) {
             const int kb = k0 + kBN * j;
             if (!boxes) return head_row0 + kb;
-            if (lane >= nbox || j >= ntiles) return 0;
-            const int pos = min(kb + 16 * gi, p_last & ~15);
+            if (lane >= kBN / 16 || j >= ntiles) return 0;
+            const int pos = min(kb + 16 * lane, p_last & ~15);
             if (a.ring && pos >= cal) return -1 - (ws_row0 + (pos - cal));
             const int slot = a.ring ? pos % a.S : pos;
             return a.table ? (max(a.table[(size_t)b * (a.S / kPage) + slot / kPage], 0) * a.Hkv + kvh) * kPage : head_row0 + slot;
         };
         auto load_tile = [&](const CUtensorMap* tm, const CUtensorMap* tmw, unsigned char* dst, uint64_t* full, int row) {
-            if (lane == 0) mbar_arrive_expect_tx(full, L::kTile);
+            if (lead) mbar_arrive_expect_tx(full, L::kTile);
+            if (!boxes) {
+                if (lead) {
+#pragma unroll
+                    for (int half = 0; half < L::kHalves; ++half) tma_load_2d(dst + half * L::kHalf, tm, 64 * half, row, full);
+                }
+            } else {
+#pragma unroll
+                for (int gi = 0; gi < kBN / 16; ++gi) {
+                    const int r = __shfl_sync(0xffffffffu, row, gi);
+                    if (lead) tma_load_4d(dst + gi * L::kHalves * 2048, r < 0 ? tmw : tm, 0, 0, 0, (r < 0 ? -1 - r : r) / 8, full);
+                }
+            }
             __syncwarp();
-            if (lane < nbox) tma_load_2d(dst + half * L::kHalf + gi * 16 * 128, row < 0 ? tmw : tm, 64 * half, row < 0 ? -1 - row : row, full);
         };
         // a stage is free when the slots that multiply its tile are done with it
         const int hi0 = slot_hi(0), hi1 = slot_hi(1);
@@ -454,8 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // as soon as the softmax has read S(j), then P.V(j) when the weights are there
         constexpr uint32_t idesc_qk = instr_desc_bf16(kBM, kBN, false), idesc_pv = instr_desc_bf16(kBM, D, true);
         const int slot = warp - kWarpMma, hi = slot_hi(slot);
-        const uint64_t qdesc = smem_desc(smem_u32(sQ) + slot * L::kQTile, 16), kdesc0 = smem_desc(smem_u32(sK), 16);
-        const uint64_t vdesc0 = smem_desc(smem_u32(sV), L::kHalf);
+        // K and V tiles: [half][row] from a contiguous cache, [8 rows][half] from 16-row boxes
+        const bool boxes = a.table || a.ring;
+        const uint32_t half_step = boxes ? 1024 : L::kHalf, group_step = boxes ? L::kHalves * 1024 : 1024;
+        const uint64_t qdesc = smem_desc(smem_u32(sQ) + slot * L::kQTile, 16, 1024), kdesc0 = smem_desc(smem_u32(sK), 16, group_step);
+        const uint64_t vdesc0 = smem_desc(smem_u32(sV), half_step, group_step);
+        const uint64_t khalf = half_step >> 4, vstep = (2 * group_step) >> 4;
         const uint32_t tS = tmem + L::kColS + kBN * slot, tP = tmem + L::kColP + L::kPStep * slot, tO = tmem + L::kColO + D * slot;
         const bool lead = elect_one();
         auto wait_ok = [&](uint64_t* b, uint32_t parity) -> bool { return __all_sync(0xffffffffu, spin(b, parity, abort_flag)); };
@@ -466,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
                     mma_ss(tS, qdesc + (uint64_t)(((s >> 2) * L::kQHalf + (s & 3) * 32) >> 4),
-                           kd + (uint64_t)(((s >> 2) * L::kHalf + (s & 3) * 32) >> 4), idesc_qk, s > 0);
+                           kd + (s >> 2) * khalf + (uint64_t)(((s & 3) * 32) >> 4), idesc_qk, s > 0);
                 mma_commit(stage_bar(L::kSFull, slot, j));
             }
             __syncwarp();
@@ -477,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lead) {
 #pragma unroll
                 for (int s = 0; s < kBN / 16; ++s)
-                    mma_ts(tO, tP + 8 * s, vd + (uint64_t)((s * 2048) >> 4), idesc_pv, (j > 0 || s > 0));
+                    mma_ts(tO, tP + 8 * s, vd + s * vstep, idesc_pv, (j > 0 || s > 0));
                 mma_commit(stage_bar(L::kODone, slot, j));
             }
             __syncwarp();
@@ -562,6 +594,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Tensor map over `rows` rows of d bf16 values, 128-byte swizzle.  Boxes of `bn` rows by 64 dims;
+// or, with `boxes`, of 16 rows and all dims in the order [8 rows][half]: dims (64 of a half, row
+// of 8, half, 8-row group), so that one copy brings a page's rows of a head.
+bool row_map(CUtensorMap* tm, const void* base, long long rows, int d, bool boxes, int bn) {
+    using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                     const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const EncodeTiled enc = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+    }();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)d * 2;
+    const cuuint64_t dims2[2] = {(cuuint64_t)d, (cuuint64_t)rows}, strides2[1] = {row};
+    const cuuint64_t dims4[4] = {64, 8, (cuuint64_t)(d / 64), (cuuint64_t)(rows / 8)}, strides4[3] = {row, 128, 8 * row};
+    const cuuint32_t box2[2] = {64, (cuuint32_t)bn}, box4[4] = {64, 8, (cuuint32_t)(d / 64), 2}, es[4] = {1, 1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, boxes ? 4 : 2, const_cast<void*>(base), boxes ? dims4 : dims2,
+               boxes ? strides4 : strides2, boxes ? box4 : box2, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items& items, cudaStream_t st) {
     auto kernel = prompt_attn_kernel<D>;
@@ -582,17 +637,13 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
     const Shape& s = h->sh;
     const int bn = s.d == 128 ? Plan<128>::kBN : Plan<64>::kBN;
     CUtensorMap tm[4];
-    const cuuint64_t rows = s.pages ? (cuuint64_t)s.pages * s.Hkv * kPage : (cuuint64_t)s.B * s.Hkv * s.S;
-    const cuuint64_t dims[2] = {(cuuint64_t)s.d, rows}, strides[1] = {(cuuint64_t)s.d * 2};
-    const cuuint32_t box[2] = {64, (s.pages || s.ring) ? (cuuint32_t)kPage : (cuuint32_t)bn};
-    if (!make_tensor_map_bf16(&tm[0], const_cast<void*>(a.kc), 2, dims, strides, box) ||
-        !make_tensor_map_bf16(&tm[1], const_cast<void*>(a.vc), 2, dims, strides, box))
-        return cudaErrorInvalidValue;
+    const bool boxes = s.pages || s.ring;
+    const long long rows = s.pages ? (long long)s.pages * s.Hkv * kPage : (long long)s.B * s.Hkv * s.S;
+    if (!row_map(&tm[0], a.kc, rows, s.d, boxes, bn) || !row_map(&tm[1], a.vc, rows, s.d, boxes, bn)) return cudaErrorInvalidValue;
     tm[2] = tm[0]; tm[3] = tm[1];
     if (s.ring) {
-        const cuuint64_t wdims[2] = {(cuuint64_t)s.d, (cuuint64_t)s.B * s.Hkv * a.ws_rows};
-        if (!make_tensor_map_bf16(&tm[2], const_cast<__nv_bfloat16*>(a.wk), 2, wdims, strides, box) ||
-            !make_tensor_map_bf16(&tm[3], const_cast<__nv_bfloat16*>(a.wv), 2, wdims, strides, box))
+        const long long staged = (long long)s.B * s.Hkv * a.ws_rows;
+        if (!row_map(&tm[2], a.wk, staged, s.d, boxes, bn) || !row_map(&tm[3], a.wv, staged, s.d, boxes, bn))
             return cudaErrorInvalidValue;
     }
     // longest first: an item's work is its number of key tiles.  The host's lengths order the

@@ -11,12 +11,11 @@ namespace tc {
 
 // Shared-memory matrix descriptor, 128-byte swizzle, sm_100 format: start address >> 4 (bits
 // 0-13), leading-dimension byte offset >> 4 (16-29), stride-dimension byte offset >> 4
-// (32-45), version 1 (46-47), layout 2 = SWIZZLE_128B (61-63).  K-major operands: 8-row
-// groups 1024 B apart.  MN-major operands additionally step `lbo` bytes to the next 64
-// MN elements.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo) {
+// (32-45), version 1 (46-47), layout 2 = SWIZZLE_128B (61-63).  8-row groups are `sbo` bytes
+// apart; MN-major operands step `lbo` bytes to the next 64 MN elements.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
 // Instruction descriptor, kind::f16 with A and B bf16 (format 1 in bits 7-9 and 10-12) and
@@ -119,6 +118,14 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Tiled tensor copy of rank 4 into shared memory (c0 is the innermost coordinate)
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int c0, int c1, int c2, int c3, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // One lane of the warp (the same every time); the warp is converged.
