@@ -24,6 +24,8 @@ struct AttnArgs {
     const int32_t* next_pos;              // the cut
     const float2* rope;
     uint32_t* hdr;
+    float2* part_ml;                      // split keys: {maximum (log2 domain), sum} and unnormalised sums
+    float* part_acc;                      // of [packed row][Hq][part]
     int Hq, Hkv, g, d, S, W, P, ring, bf16, out_bf16, ws_rows;
     float scale_log2;                     // log2(e) / sqrt(d)
 };

@@ -44,17 +44,21 @@ def rotate(x, pos, base, dtype):
 def attend(q, K, V, cut, window):
     """out and sum p |v| of queries q [n, Hq, d] at cut + i over K, V [L, Hkv, d], all rows, in 64 bits."""
     n, Hq, d = q.shape
-    g = Hq // K.shape[1]
-    qd, Kd, Vd = q.double(), K.double(), V.double()
-    out, mag = torch.empty(n, Hq, d, dtype=torch.float64), torch.empty(n, Hq, d, dtype=torch.float64)
-    for i in range(n):
-        p = cut + i
-        lo = max(0, p - window + 1) if window else 0
-        for h in range(Hq):
-            w = torch.softmax(Kd[lo:p + 1, h // g] @ qd[i, h] / math.sqrt(d), 0)
-            out[i, h] = w @ Vd[lo:p + 1, h // g]
-            mag[i, h] = w @ Vd[lo:p + 1, h // g].abs()
-    return out.numpy(), mag.numpy()
+    L, Hkv = K.shape[:2]
+    qd, Kd, Vd = (x.double().transpose(0, 1) for x in (q, K, V))
+    p = torch.arange(cut, cut + n)[:, None]
+    j = torch.arange(L)
+    seen = (j <= p) & ((j > p - window) if window else (j >= 0))
+    out, mag = torch.empty(Hq, n, d, dtype=torch.float64), torch.empty(Hq, n, d, dtype=torch.float64)
+    for h in range(Hq):
+        k, v = Kd[h * Hkv // Hq], Vd[h * Hkv // Hq]
+        w = torch.softmax((qd[h] @ k.T / math.sqrt(d)).masked_fill(~seen, -math.inf), -1)
+        if torch.isfinite(v).all():
+            out[h], mag[h] = w @ v, w @ v.abs()
+        else:                                               # keys that are not seen add nothing, whatever they hold
+            for i in range(n):
+                out[h, i], mag[h, i] = w[i, seen[i]] @ v[seen[i]], w[i, seen[i]] @ v[seen[i]].abs()
+    return out.transpose(0, 1).numpy(), mag.transpose(0, 1).numpy()
 
 
 class Twin:
@@ -320,6 +324,33 @@ def test_two_handles_on_two_streams():
         t.trim([0, 0])
         again = t.cache.prompt(*x.split([8, 2, 2], 1), [1100, 400])
         assert torch.equal(o, again)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,paged", [(8, 2, 128, 0, True), (2, 2, 128, 0, False), (8, 1, 64, 40, False), (12, 4, 64, 0, True)])
+def test_many_short_units(Hq, Hkv, d, window, paged):
+    # several units of work for every SM, most of one to three tiles, ragged, some requests empty
+    rng = np.random.default_rng(3)
+    B = 150
+    counts = [int(x) for x in rng.choice([0, 1, 5, 40, 64, 65, 130, 260], B)]
+    cuts = [int(x) for x in rng.integers(0, 100, B)]
+    t = Twin("bf16", B, Hq, Hkv, d, 368, window=window, pages=B * 23 if paged else 0, out="f32")
+    t.prefill(cuts)
+    t.prompt(counts)
+    t.prompt([1] * B)
+    t.check_state()
+
+
+@pytest.mark.parametrize("layout,window,paged", [("contiguous", 0, False), ("contiguous", 0, True), ("contiguous", 1500, False), ("ring", 0, True)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 1, 128), (2, 2, 64), (8, 1, 64)])
+def test_few_rows_behind_long_prefixes(Hq, Hkv, d, layout, window, paged):
+    # few rows and many keys: the keys are split over CTAs and joined
+    cap = 2048 if layout == "ring" else 3300
+    cap -= cap % 16 if paged else 0
+    t = Twin("bf16", 2, Hq, Hkv, d, cap, layout, window=window, pages=2 * cap // 16 if paged else 0, max_chunk=64, max_position=4000)
+    t.prefill([3000, 700])
+    for counts in ([1, 1], [0, 1], [3, 0], [20, 9]):
+        t.prompt(counts)
+    t.check_state()
 
 
 def test_more_requests_than_one_launch_holds():
