@@ -292,6 +292,7 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * are rounded to bf16 too (relative error at most 2^-8 each; their sum is fp32); other
  * shapes run in fp32 throughout.  What a masked key or value row
  * holds, infinities and NaN among it, does not reach the result.
+ * d_out must not overlap the inputs; its rows hold intermediate values during the call.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
  * All tiers but INT8; a ring needs a bf16 cache with W a multiple of 16, and counts of at
  * most max_chunk (its rows are staged, as kvc_chunk_attn's are).

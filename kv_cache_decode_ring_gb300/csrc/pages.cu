@@ -20,39 +20,45 @@
 namespace kvc {
 namespace {
 
-constexpr int kTableBatch = 256;
+// Table entries and page pairs ride in kernel parameters, few or many per launch.
+constexpr int kFew = 64, kMany = 1024;
 
+template <int N>
 struct TableUpdates {
     int n;
-    int2 e[kTableBatch];                  // (table index, physical page)
+    int2 e[N];                            // (table index, physical page)
 };
 
-__global__ void table_update_kernel(const TableUpdates u, int32_t* table) {
+template <int N>
+__global__ void table_update_kernel(const __grid_constant__ TableUpdates<N> u, int32_t* table) {
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < u.n) table[u.e[i].x] = u.e[i].y;
 }
 
-cudaError_t upload_table(kvc_handle* h, cudaStream_t st) {
-    return cudaMemcpyAsync(h->state + h->L.table, h->table_h.data(), h->table_h.size() * 4, cudaMemcpyHostToDevice, st);
+template <int N>
+cudaError_t update_some(int32_t* table, const int2* upd, size_t n, cudaStream_t st) {
+    TableUpdates<N> u;
+    u.n = (int)n;
+    std::memcpy(u.e, upd, n * sizeof(int2));
+    table_update_kernel<N><<<((int)n + 255) / 256, 256, 0, st>>>(u, table);
+    return cudaGetLastError();
 }
 
-// The changed entries, as kernel parameters; many at once (a large prefill), the whole table.
+// The changed entries; very many at once (a large prefill), the whole table.
 cudaError_t update_table(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st) {
-    if (upd.size() > 4 * (size_t)kTableBatch) return upload_table(h, st);
     int32_t* table = reinterpret_cast<int32_t*>(h->state + h->L.table);
-    for (size_t i0 = 0; i0 < upd.size(); i0 += kTableBatch) {
-        TableUpdates u;
-        u.n = (int)std::min<size_t>(kTableBatch, upd.size() - i0);
-        std::memcpy(u.e, upd.data() + i0, u.n * sizeof(int2));
-        table_update_kernel<<<1, kTableBatch, 0, st>>>(u, table);
-        cudaError_t e = cudaGetLastError();
+    if (upd.size() > 4 * (size_t)kMany)
+        return cudaMemcpyAsync(table, h->table_h.data(), h->table_h.size() * 4, cudaMemcpyHostToDevice, st);
+    for (size_t i0 = 0; i0 < upd.size(); i0 += kMany) {
+        const size_t n = std::min<size_t>(kMany, upd.size() - i0);
+        const cudaError_t e = n <= kFew ? update_some<kFew>(table, upd.data() + i0, n, st)
+                                        : update_some<kMany>(table, upd.data() + i0, n, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
 // ---- copies of whole pages -------------------------------------------------------
-constexpr int kMoveBatch = 1024;          // page pairs per launch (kernel parameter space)
 constexpr int kMaxParts = 5;              // per-page arrays: K, V or codes, scales, witnesses
 
 // One per-block array: `bytes` per 16 slots of one KV head.
@@ -61,15 +67,17 @@ struct Part {
     long long bytes;
 };
 
+template <int N>
 struct Moves {
     Part part[kMaxParts];
-    int parts, Hkv, n;
-    int2 e[kMoveBatch];                   // (from, to) physical pages
+    int parts, Hkv;
+    int2 e[N];                            // (from, to) physical pages
 };
 
 // grid (page pairs, parts); a page is Hkv * bytes contiguous bytes of each part.  The pages
 // written are disjoint from the pages read.
-__global__ void __launch_bounds__(256) move_pages_kernel(const __grid_constant__ Moves m) {
+template <int N>
+__global__ void __launch_bounds__(256) move_pages_kernel(const __grid_constant__ Moves<N> m) {
     const int2 e = m.e[blockIdx.x];
     const Part p = m.part[blockIdx.y];
     const size_t page = (size_t)m.Hkv * p.bytes;
@@ -113,16 +121,20 @@ int parts_of(const kvc_handle* h, Part* p) {
     return n;
 }
 
-cudaError_t move_pages(kvc_handle* h, const std::vector<int2>& pairs, cudaStream_t st) {
-    if (pairs.empty()) return cudaSuccess;
-    Moves m;
+template <int N>
+cudaError_t move_some(const kvc_handle* h, const int2* pairs, size_t n, cudaStream_t st) {
+    static thread_local Moves<N> m;
     m.parts = parts_of(h, m.part);
     m.Hkv = h->sh.Hkv;
-    for (size_t i0 = 0; i0 < pairs.size(); i0 += kMoveBatch) {
-        m.n = (int)std::min<size_t>(kMoveBatch, pairs.size() - i0);
-        std::memcpy(m.e, pairs.data() + i0, m.n * sizeof(int2));
-        move_pages_kernel<<<dim3(m.n, m.parts), 256, 0, st>>>(m);
-        cudaError_t e = cudaGetLastError();
+    std::memcpy(m.e, pairs, n * sizeof(int2));
+    move_pages_kernel<N><<<dim3((unsigned)n, m.parts), 256, 0, st>>>(m);
+    return cudaGetLastError();
+}
+
+cudaError_t move_pages(const kvc_handle* h, const std::vector<int2>& pairs, cudaStream_t st) {
+    for (size_t i0 = 0; i0 < pairs.size(); i0 += kMany) {
+        const size_t n = std::min<size_t>(kMany, pairs.size() - i0);
+        const cudaError_t e = n <= kFew ? move_some<kFew>(h, pairs.data() + i0, n, st) : move_some<kMany>(h, pairs.data() + i0, n, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -146,7 +158,7 @@ struct CopyGroup {
 
 struct CopySide {
     Part part[kMaxParts];
-    const int32_t* table;                 // paged: block table, else nullptr
+    int32_t* table;                       // paged: block table, else nullptr
     int32_t* pos;
     int32_t* next_pos;
     __nv_bfloat16* ktail; __nv_bfloat16* vtail;
@@ -157,6 +169,7 @@ struct CopySide {
 struct CopyArgs {
     CopySide from, to;
     int parts, Hkv, d, ring, int8;
+    int share;                            // destinations take the source's pages (none: give theirs up)
     CopyGroup group[kCopyGroups];
     int target[kCopyTargets];
 };
@@ -164,7 +177,7 @@ struct CopyArgs {
 // grid (max of ceil(rows / 128) and destinations, Hkv + 1, groups).  Plane y < Hkv: KV head
 // y's rows of the group's source, read once and written to each of its destinations; its
 // scales, witnesses and exact tail for the INT8 tiers.  Plane Hkv, a CTA per destination:
-// positions, next_position and request ID.
+// positions, next_position, request ID and (share) block-table entries.
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __grid_constant__ CopyArgs a) {
     const CopyGroup g = a.group[blockIdx.z];
@@ -180,6 +193,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __gri
             const int hi = a.ring ? a.to.S : min(a.to.S, max(g.len, old));
             for (int s = threadIdx.x; s < hi; s += kCopyThreads)
                 pb[s] = g.src < 0 ? -1 : a.ring ? a.from.pos[(size_t)g.src * a.from.S + s] : s < g.len ? s : -1;
+            if (a.share) {
+                const int npg = a.to.S / kPage;
+                for (int lp = threadIdx.x; lp < npg; lp += kCopyThreads)
+                    a.to.table[(size_t)b * npg + lp] = g.src < 0 ? -1 : a.from.table[(size_t)g.src * npg + lp];
+            }
             __syncthreads();              // every thread has read the old next_position
             if (threadIdx.x == 0) {
                 a.to.next_pos[b] = g.len;
@@ -250,7 +268,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __gri
 void side_of(kvc_handle* h, CopySide* c) {
     const Shape& s = h->sh;
     parts_of(h, c->part);
-    c->table = s.pages ? reinterpret_cast<const int32_t*>(h->state + h->L.table) : nullptr;
+    c->table = s.pages ? reinterpret_cast<int32_t*>(h->state + h->L.table) : nullptr;
     c->pos = reinterpret_cast<int32_t*>(h->state + h->L.pos);
     c->next_pos = reinterpret_cast<int32_t*>(h->state + h->L.next_pos);
     if (s.int8) {
@@ -263,9 +281,10 @@ void side_of(kvc_handle* h, CopySide* c) {
 
 // Destinations dst[i] of `to` take the rows of requests src[i] of `from` (src[i] < 0:
 // nothing).  rows_of(b): slots whose rows move.  Destinations of one source share its reads.
+// share: a paged cache's destinations name the source's pages (the host table already does).
 template <typename Rows>
 cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<int>& src, const std::vector<int>& dst,
-                          Rows rows_of, cudaStream_t st) {
+                          Rows rows_of, bool share, cudaStream_t st) {
     const Shape& s = to->sh;
     static thread_local CopyArgs a;       // 5 KB of kernel parameters: not on the stack
     a = CopyArgs{};
@@ -273,7 +292,7 @@ cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<in
     side_of(to, &a.to);
     Part parts[kMaxParts];
     a.parts = parts_of(to, parts);
-    a.Hkv = s.Hkv; a.d = s.d; a.ring = s.ring; a.int8 = s.int8;
+    a.Hkv = s.Hkv; a.d = s.d; a.ring = s.ring; a.int8 = s.int8; a.share = share;
     std::vector<int> order(src.size());
     for (size_t i = 0; i < order.size(); ++i) order[i] = (int)i;
     std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return src[x] < src[y]; });
@@ -437,7 +456,6 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {
         const int npg = s.S / kPage;
-        std::vector<int2> upd;
         for (int i = 0; i < n; ++i)
             for (int lp = 0; lp < npg; ++lp) {
                 const int32_t page = h->table_h[(size_t)src[i] * npg + lp];
@@ -446,12 +464,10 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
                 if (page >= 0) ++h->page_ref[page];
                 drop_page(h, e);
                 e = page;
-                upd.push_back(make_int2(dst[i] * npg + lp, page));
             }
-        if (update_table(h, upd, st) != cudaSuccess) return KVC_ERR_CUDA;
     }
     const bool shared = s.pages > 0;       // rows stay where they are
-    if (copy_requests(h, h, src, dst, [&](int b) { return shared ? 0 : held_rows(h, b); }, st) != cudaSuccess)
+    if (copy_requests(h, h, src, dst, [&](int b) { return shared ? 0 : held_rows(h, b); }, shared, st) != cudaSuccess)
         return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         h->np[dst[i]] = h->np[src[i]];
@@ -511,7 +527,7 @@ int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_
         if (update_table(to, gone, st) != cudaSuccess) return KVC_ERR_CUDA;
     }
     if (drop_restored(to, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
-    if (copy_requests(to, from, src, dst, [&](int b) { return held_rows(from, b); }, st) != cudaSuccess) return KVC_ERR_CUDA;
+    if (copy_requests(to, from, src, dst, [&](int b) { return held_rows(from, b); }, false, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         to->np[dst[i]] = from->np[src[i]];
         if (s.dither) to->req_id_h[dst[i]] = from->req_id_h[src[i]];
@@ -534,17 +550,10 @@ int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream) try {
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {
         const int npg = s.S / kPage;
-        std::vector<int2> upd;
         for (int b : dst)
-            for (int lp = 0; lp < npg; ++lp) {
-                int32_t& e = h->table_h[(size_t)b * npg + lp];
-                if (e < 0) continue;
-                drop_page(h, e);
-                upd.push_back(make_int2(b * npg + lp, -1));
-            }
-        if (update_table(h, upd, st) != cudaSuccess) return KVC_ERR_CUDA;
+            for (int lp = 0; lp < npg; ++lp) drop_page(h, h->table_h[(size_t)b * npg + lp]);
     }
-    if (copy_requests(h, h, none, dst, [](int) { return 0; }, st) != cudaSuccess) return KVC_ERR_CUDA;
+    if (copy_requests(h, h, none, dst, [](int) { return 0; }, s.pages > 0, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int b : dst) h->np[b] = 0;
     return KVC_OK;
 } catch (...) {

@@ -37,10 +37,29 @@ struct RowArgs {
     uint32_t* hdr;
     int Hkv, d, S, P, ring, bf16, ws_rows;
     int stage;                            // 1: into the staging rows, with the resident rows they follow
+    const void* q;                        // packed queries to rotate into `out` for the tensor-core kernel (else nullptr):
+    __nv_bfloat16* out;                   // head h of packed row t at (t Hq + h) out_head elements
+    long long q_stride;
+    int Hq, out_head;
 };
 
 __device__ __forceinline__ bool position_ok(const RowArgs& a, long long p) {
     return p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P);
+}
+
+// Four pairs of a bf16 row, rotated by the {cos, sin} at rp.
+__device__ __forceinline__ uint4 turned(uint4 u, const float2* rp) {
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(rp)), c1 = __ldg(reinterpret_cast<const float4*>(rp) + 1);
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const float2 cs[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y), make_float2(c1.z, c1.w)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float y0, y1;
+        rope_pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u), cs[e], y0, y1);
+        const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
+        w[e] = *reinterpret_cast<const uint32_t*>(&o2);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 constexpr int kRowsPerCta = 8;
@@ -50,6 +69,8 @@ constexpr int kRowsPerCta = 8;
 // once, one rounding to the cache's type: the arithmetic of the other appends.
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, const __grid_constant__ Packed g) {
+    dep_wait();                                        // launched dependent: see launch_dep
+    dep_release();
     const int bi = blockIdx.y, b = g.b0 + bi;
     const int n = g.off[bi + 1] - g.off[bi];
     const int cut = a.next_pos[b], d = a.d;
@@ -58,6 +79,18 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
     if (n == 0 || r0 >= n) return;
     const int rows = min(n - r0, kRowsPerCta);
     const int per = VEC ? d / 8 : d / 2, total = rows * a.Hkv * per;
+    if constexpr (VEC) {
+        // queries, as the tensor-core attention takes them
+        const int queries = a.q ? rows * a.Hq * per : 0;
+        for (int i = threadIdx.x; i < queries; i += kThreads) {
+            const int c = i % per, h = (i / per) % a.Hq, r = r0 + i / (per * a.Hq);
+            const long long p = (long long)cut + r;
+            if (r < 0 || !position_ok(a, p)) continue;
+            const size_t t = (size_t)(g.row0 + g.off[bi] + r);
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + (size_t)h * d + 8 * c));
+            *reinterpret_cast<uint4*>(a.out + (t * a.Hq + h) * a.out_head + 8 * c) = turned(u, a.rope + (size_t)p * (d / 2) + 4 * c);
+        }
+    }
     for (int i = threadIdx.x; i < total; i += kThreads) {
         const int c = i % per, h = (i / per) % a.Hkv, r = r0 + i / (per * a.Hkv);
         const long long p = (long long)cut + r;
@@ -77,21 +110,7 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
             } else {
                 ko = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src + 8 * c));
                 vo = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
-                if (a.rope) {
-                    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (d / 2) + 4 * c);
-                    const float4 c0 = __ldg(rp), c1 = __ldg(rp + 1);
-                    uint32_t w[4] = {ko.x, ko.y, ko.z, ko.w};
-                    const float2 cs[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
-                                          make_float2(c1.z, c1.w)};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y0, y1;
-                        rope_pair(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u), cs[e], y0, y1);
-                        const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
-                        w[e] = *reinterpret_cast<const uint32_t*>(&o2);
-                    }
-                    ko = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                if (a.rope) ko = turned(ko, a.rope + (size_t)p * (d / 2) + 4 * c);
             }
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(kd) + dst + 8 * c) = ko;
             *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(vd) + dst + 8 * c) = vo;
@@ -121,6 +140,8 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
 }
 
 __global__ void prompt_advance_kernel(int32_t* next_pos, const __grid_constant__ Packed g) {
+    dep_wait();
+    dep_release();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < g.nb) next_pos[g.b0 + i] += g.off[i + 1] - g.off[i];
 }
@@ -138,6 +159,8 @@ __host__ __device__ constexpr size_t simt_smem(int d) { return ((size_t)(kBM + 2
 template <int ND>
 __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a, const __grid_constant__ Packed g) {
     extern __shared__ float4 smem4[];
+    dep_wait();
+    dep_release();
     const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y;
     const int n = g.off[bi + 1] - g.off[bi];
     const long long all = (long long)n * a.g, row0 = (long long)blockIdx.x * kBM;
@@ -269,8 +292,7 @@ cudaError_t launch_simt(const AttnArgs& a, const Packed& g, int most, cudaStream
     auto kernel = prompt_simt_kernel<ND>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), simt_smem(32 * ND))) return e;
     const dim3 grid((unsigned)(((long long)most * a.g + kBM - 1) / kBM), a.Hkv, g.nb);
-    kernel<<<grid, kThreads, simt_smem(a.d), st>>>(a, g);
-    return cudaGetLastError();
+    return launch_dep(kernel, grid, dim3(kThreads), simt_smem(a.d), st, a, g);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
@@ -310,6 +332,11 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     const bool vec = s.bf16 && s.d % 8 == 0;     // the entry point checked alignment and strides
     const bool tensor = prompt_tc_supported(s);
+    if (tensor && s.rope) {
+        r.q = p.q; r.q_stride = p.q_stride; r.Hq = s.Hq;
+        r.out = static_cast<__nv_bfloat16*>(p.out);
+        r.out_head = s.out_bf16 ? s.d : 2 * s.d;
+    }
     long long row0 = 0;
     for (int b0 = 0; b0 < s.B; b0 += kPromptGroup) {
         static thread_local Packed g;
@@ -328,16 +355,17 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
         auto rows = [&](int stage) {
             r.stage = stage;
             const dim3 grid((most + (stage ? 15 : 0) + kRowsPerCta - 1) / kRowsPerCta, g.nb);
-            if (vec) prompt_rows_kernel<true><<<grid, kThreads, 0, st>>>(r, g);
-            else prompt_rows_kernel<false><<<grid, kThreads, 0, st>>>(r, g);
-            return cudaGetLastError();
+            return launch_dep(vec ? prompt_rows_kernel<true> : prompt_rows_kernel<false>, grid, dim3(kThreads), 0, st, r, g);
         };
         if ((e = rows(s.ring ? 1 : 0)) != cudaSuccess) return e;
         e = tensor ? launch_prompt_tc(h, a, g, st) : launch_attention(a, g, most, st);
         if (e != cudaSuccess) return e;
-        if (s.ring && (e = rows(0)) != cudaSuccess) return e;
-        prompt_advance_kernel<<<(g.nb + 255) / 256, 256, 0, st>>>(next_pos, g);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (s.ring) {
+            r.q = nullptr;                                // d_out holds the output by now
+            if ((e = rows(0)) != cudaSuccess) return e;
+            r.q = tensor && s.rope ? p.q : nullptr;
+        }
+        if ((e = launch_dep(prompt_advance_kernel, dim3((g.nb + 255) / 256), dim3(256), 0, st, next_pos, g)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -10,9 +10,9 @@
 //    adjacent.  Where units are few and long, their keys are split over several CTAs
 //    and a second kernel joins the parts.
 //  * Warps 0-3 and 4-7: softmax of slot 0 and 1, thread = row = tensor-memory lane.  Warp 8
-//    issues the tensor copies, warp 9 looks over the value rows of boundary tiles, warps 10 and
-//    11 load and rotate the queries of the next unit while this one runs, warps 12-15 issue
-//    the matrix instructions: each slot's two products from a warp of their own (with one warp
+//    issues the tensor copies, warp 9 looks over the value rows of boundary tiles, warp 10
+//    copies the queries of the next unit while this one runs, warps 12-15 issue the matrix
+//    instructions: each slot's two products from a warp of their own (with one warp
 //    for both, its waits and issues, one after the other, took longer than the products).
 //  * Tensor memory: S of both slots (fp32), their weights P (bf16 pairs, the A operand of P.V) and
 //    O (fp32) in columns of their own: with d = 128 that leaves tiles of 80 keys, with d = 64
@@ -21,6 +21,10 @@
 //  * All operands are bf16: q and the keys as the cache's type holds them, the weights
 //    rounded once (relative error 2^-8, at most 2^8 in size).  fp16 weights (2^-11) would
 //    need the values in fp16 too: a conversion pass over every tile and a narrower range.
+//  * With RoPE the queries come rotated, in d_out's rows (prompt_rows_kernel): a unit copies its
+//    queries from the rows that it writes at its end.  Rotating them here, by two warps beside
+//    the softmax, took longer than a short unit's products (ragged prompts 0.30 against
+//    0.20 ms).
 //  * A row's reference maximum moves only when a tile exceeds it by more than 2^8 (log2
 //    domain); the softmax thread then rescales its O row itself (no P.V of its slot in flight).
 //  * Masked scores are replaced, not added to, so a masked key may hold anything.  A masked
@@ -48,7 +52,7 @@ constexpr int kBM = 128;            // rows per slot
 constexpr int kSlots = 2;
 constexpr int kThreads = 16 * 32;
 constexpr int kWarpCopy = 8, kWarpLook = 9, kWarpLoad = 10, kWarpMma = 12;
-constexpr int kLoadWarps = 2, kMmaWarps = 4;     // matrix warps: S and P.V of slot 0, then of slot 1
+constexpr int kMmaWarps = 4;       // matrix warps: S and P.V of slot 0, then of slot 1
 constexpr float kLazyMax = 8.f;     // log2-domain headroom of a row's reference maximum
 constexpr int kRegLaunch = 128;
 constexpr int kItems = 512;         // items (a tile of rows of a request, a part of its keys) per launch
@@ -76,7 +80,7 @@ struct Plan {
     static constexpr int kQTile = kHalves * kQHalf;
     static constexpr int kStages = D == 128 ? 3 : 4;       // of K and of V each
     static constexpr int kQBufs = D == 128 ? 3 : 4;        // Q tiles: slot s of unit i is tile q = 2 i + s, in buffer q mod kQBufs
-    static constexpr int kRegSoftmax = D == 128 ? 176 : 184, kRegIssue = D == 128 ? 80 : 72, kRegMma = D == 128 ? 80 : 72;
+    static constexpr int kRegSoftmax = 192, kRegIssue = 64, kRegMma = 64;
     static_assert(8 * kRegSoftmax + 4 * kRegIssue + 4 * kRegMma == 16 * kRegLaunch, "register split sums to the launch's registers");
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + kQBufs * kQTile;
@@ -90,9 +94,8 @@ struct Plan {
         kODone = kSFull + kSlots * kStages,  // [slot][stage] P.V complete
         kSFree = kODone + kSlots * kStages,  // [slot] S read (4 warps)
         kPFull = kSFree + kSlots,            // [slot] P written (4 warps)
-        kQRaw = kPFull + kSlots,             // [Q buffer] copied
-        kQFree = kQRaw + kQBufs,             // [Q buffer] the slot's rows of the unit are written (4 warps)
-        kQFull = kQFree + kQBufs,            // [slot][unit mod 2] Q rotated and the unit's description written (2 warps)
+        kQFree = kPFull + kSlots,            // [Q buffer] the slot's rows of the unit are written (4 warps)
+        kQFull = kQFree + kQBufs,            // [slot][unit mod 2] Q copied and the unit's description written
         kDone = kQFull + 2 * kSlots,         // [matrix warp] every product issued so far complete
         kBars = kDone + kMmaWarps
     };
@@ -197,10 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar[L::kPFull + i], 4);
         }
         for (int i = 0; i < L::kQBufs; ++i) {
-            mbar_init(&bar[L::kQRaw + i], 1);
             mbar_init(&bar[L::kQFree + i], 4);
         }
-        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&bar[L::kQFull + i], kLoadWarps);
+        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&bar[L::kQFull + i], 1);
         for (int i = 0; i < kMmaWarps; ++i) mbar_init(&bar[L::kDone + i], 1);
         *abort_flag = 0;
         for (int i = 0; i < kAhead; ++i) spoilt[i] = 0;
@@ -211,6 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const uint32_t tmem = *tmem_slot;
+    dep_wait();                                        // launched dependent (see launch_dep): global memory from here on
+    dep_release();
     // every warpgroup changes its register share together
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
     else if (warp < kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegIssue));
@@ -595,76 +599,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++i;
         }
-    } else {
-        // ================= queries of the next unit: copied (rows of 128 bytes a half, token-
-        // major), then rotated in place at their positions in fp32 and rounded to bf16, every
-        // other token by either warp.  A lane holds one 16-byte chunk of a token's {cos, sin} row
-        // and turns it in every head.
-        constexpr int kPer = D / 8, kTogether = 32 / kPer, kTokens = 4;        // tokens a round; rounds in flight
-        const int lw = warp - kWarpLoad, c = lane % kPer;
+    } else if (warp == kWarpLoad) {
+        // ================= queries of the next unit (rows of 128 bytes a half, token-major)
         const bool lead = elect_one();
-        Unit w{};
-        for (int rd = 0, q = 0; rd * G < nunits && ok; q & 1 ? ++rd, ++q : ++q) {
-            const int slot = q & 1, i = q >> 1, buf = q % L::kQBufs;
-            const uint32_t uses = (uint32_t)(q / L::kQBufs);
-            if (slot == 0) {
-                while (rd * G < nunits && mine(rd) >= nunits) ++rd;
-                if (rd * G >= nunits) break;
-                w = unit_of<D>(a, items, b0, mine(rd));
-            }
-            if (uses > 0 && !(ok = all_ok(wait(&bar[L::kQFree + buf], (uses - 1) & 1, abort_flag)))) break;
-            unsigned char* qt = sQ + buf * L::kQTile;
-            if (lw == 0 && lead) {
-                if (slot == 0) unit_in(i) = w;
-                mbar_arrive_expect_tx(&bar[L::kQRaw + buf], L::kHalves * T * a.g * 128);
+        int q = 0;
+        for (int rd = 0; rd * G < nunits && ok; ++rd) {
+            if (mine(rd) >= nunits) continue;
+            const Unit w = unit_of<D>(a, items, b0, mine(rd));
+            for (int slot = 0; slot < kSlots; ++slot, ++q) {
+                const int i = q >> 1, buf = q % L::kQBufs, uses = q / L::kQBufs;
+                if (uses > 0 && !(ok = all_ok(wait(&bar[L::kQFree + buf], (uint32_t)((uses - 1) & 1), abort_flag)))) break;
+                if (lead) {
+                    if (slot == 0) unit_in(i) = w;
+                    mbar_arrive_expect_tx(q_full(slot, i), L::kHalves * T * a.g * 128);
 #pragma unroll
-                for (int half = 0; half < L::kHalves; ++half)
-                    tma_load_3d(qt + half * L::kQHalf, &tmQ, 64 * half, w.kvh * a.g, w.row + w.t0 + slot * T, &bar[L::kQRaw + buf]);
-            }
-            __syncwarp();
-            if (!(ok = all_ok(drain(&bar[L::kQRaw + buf], uses & 1)))) break;
-            if (a.rope) {
-                const int n = min(T, w.ntok - slot * T);        // the slot's tokens (none: below 0)
-                const float4* rope = reinterpret_cast<const float4*>(a.rope + (size_t)(w.cut + w.t0 + slot * T) * (D / 2) + 4 * c);
-#pragma unroll 1
-                for (int tok0 = lw * kTogether + lane / kPer; tok0 < n; tok0 += kTokens * kLoadWarps * kTogether) {
-                    float4 ra[kTokens], rb[kTokens];
-#pragma unroll
-                    for (int e = 0; e < kTokens; ++e) {
-                        const int tok = tok0 + e * kLoadWarps * kTogether;
-                        if (tok < n && w.cut + w.t0 + slot * T + tok < a.P) {
-                            ra[e] = __ldg(rope + (size_t)tok * (D / 4));
-                            rb[e] = __ldg(rope + (size_t)tok * (D / 4) + 1);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < kTokens; ++e) {
-                        const int tok = tok0 + e * kLoadWarps * kTogether;
-                        if (tok >= n || w.cut + w.t0 + slot * T + tok >= a.P) continue;
-                        const float2 cs[4] = {make_float2(ra[e].x, ra[e].y), make_float2(ra[e].z, ra[e].w),
-                                              make_float2(rb[e].x, rb[e].y), make_float2(rb[e].z, rb[e].w)};
-#pragma unroll 4
-                        for (int h = 0; h < a.g; ++h) {
-                            const int rr = tok * a.g + h;
-                            uint4* at = reinterpret_cast<uint4*>(qt + (c >> 3) * L::kQHalf + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
-                            const uint4 u = *at;
-                            uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                float y0, y1;
-                                rope_pair(__uint_as_float(x[y] << 16), __uint_as_float(x[y] & 0xffff0000u), cs[y], y0, y1);
-                                const __nv_bfloat162 o2 = __floats2bfloat162_rn(y0, y1);
-                                x[y] = *reinterpret_cast<const uint32_t*>(&o2);
-                            }
-                            *at = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
-                    }
+                    for (int half = 0; half < L::kHalves; ++half)
+                        tma_load_3d(sQ + buf * L::kQTile + half * L::kQHalf, &tmQ, 64 * half, w.kvh * a.g, w.row + w.t0 + slot * T,
+                                    q_full(slot, i));
                 }
+                __syncwarp();
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full(slot, i));
         }
+        // the last copies land before the CTA can exit
+        for (int p = max(0, q - L::kQBufs); p < q; ++p) drain(q_full(p & 1, p >> 1), (uint32_t)((p >> 2) & 1));
+        __syncwarp();
     }
     if (!ok) {
         if (lane == 0) atomicOr(a.hdr, kErrWait);
@@ -681,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of split keys: a warp per (row, head); lanes over the dims.
 __global__ void __launch_bounds__(256) prompt_join_kernel(const AttnArgs a, long long rows, int parts) {
+    dep_wait();
+    dep_release();
     const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (at >= rows) return;
@@ -732,9 +692,8 @@ cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items
     auto kernel = prompt_attn_kernel<D>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Plan<D>::kBytes)) return e;
     const long long units = (long long)items.n * a.Hkv;
-    kernel<<<dim3((unsigned)std::min<long long>(units, sms)), kThreads, Plan<D>::kBytes, st>>>(tm[0], tm[1], tm[2], tm[3], tm[4], a, b0,
-                                                                                             items);
-    return cudaGetLastError();
+    return launch_dep(kernel, dim3((unsigned)std::min<long long>(units, sms)), dim3(kThreads), Plan<D>::kBytes, st, tm[0], tm[1], tm[2],
+                      tm[3], tm[4], a, b0, items);
 }
 
 }  // namespace
@@ -763,9 +722,11 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
     const int T = kBM / s.g;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)s.d, (cuuint64_t)s.Hq, (cuuint64_t)(g.row0 + g.off[g.nb])};
-        const cuuint64_t strides[2] = {(cuuint64_t)s.d * 2, (cuuint64_t)a.q_stride * 2};
+        // (rotated ones lie in d_out, at the start of each head's output)
+        const cuuint64_t head = (cuuint64_t)s.d * (s.rope && !s.out_bf16 ? 4 : 2);
+        const cuuint64_t strides[2] = {head, s.rope ? head * s.Hq : (cuuint64_t)a.q_stride * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)s.g, (cuuint32_t)T};
-        if (!make_tensor_map_bf16(&tm[4], const_cast<void*>(a.q), 3, dims, strides, box)) return cudaErrorInvalidValue;
+        if (!make_tensor_map_bf16(&tm[4], s.rope ? a.out : const_cast<void*>(a.q), 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     // longest first: an item's work is its number of key tiles.  The host's lengths order the
     // units and choose the split only; the kernel reads the cut on the device.
@@ -812,8 +773,7 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
         part.part_ml += g.row0 * s.Hq * items.parts;
         part.part_acc += g.row0 * s.Hq * items.parts * s.d;
         part.out = static_cast<char*>(a.out) + (size_t)g.row0 * s.Hq * s.d * (s.out_bf16 ? 2 : 4);
-        prompt_join_kernel<<<(unsigned)((rows_out + 7) / 8), 256, 0, st>>>(part, rows_out, items.parts);
-        return cudaGetLastError();
+        return launch_dep(prompt_join_kernel, dim3((unsigned)((rows_out + 7) / 8)), dim3(256), 0, st, part, rows_out, items.parts);
     }
     return cudaSuccess;
 }

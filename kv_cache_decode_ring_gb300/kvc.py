@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 from typing import Optional, Sequence
 
 import numpy as np
@@ -69,6 +70,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """The loaded library.  Raises if it has not been built (no fallback path exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -128,12 +131,12 @@ def _check(rc: int, where: str):
         raise KvcError(rc, where)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dev(t: Optional[torch.Tensor], dtype=None, shape=None, name="tensor") -> ctypes.c_void_p:
@@ -263,16 +266,19 @@ def _rows(t: torch.Tensor, name="tensor") -> tuple:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dim() != 3:
         raise ValueError("%s must have shape [rows, heads, head_dim], got %s" % (name, tuple(t.shape)))
-    n, heads, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d) or (n > 1 and t.stride(0) < heads * d):
+    (n, heads, d), (row, head, dim) = t.shape, t.stride()
+    if (d > 1 and dim != 1) or (heads > 1 and head != d) or (n > 1 and row < heads * d):
         raise ValueError("%s must have dense heads in each row, got strides %s" % (name, t.stride()))
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if n > 1 else heads * d
+    return t.data_ptr(), row if n > 1 else heads * d
 
 
 def _ints(values):
-    """Host int32 array and its length."""
-    v = [int(x) for x in values]
-    return (ctypes.c_int32 * max(len(v), 1))(*v), len(v)
+    """Host int32 array (keep it alive during the call; its address is ``buffer_info()[0]``)."""
+    return values if isinstance(values, array) and values.typecode == "i" else array("i", values)
+
+
+def _at(a: array) -> int:
+    return a.buffer_info()[0]
 
 
 def kvc_prompt_attn(h, q, k, v, counts: Sequence[int], out, stream=None) -> None:
@@ -281,27 +287,30 @@ def kvc_prompt_attn(h, q, k, v, counts: Sequence[int], out, stream=None) -> None
     (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
     if ks != vs:
         raise ValueError("k and v must have the same row stride")
-    c, _ = _ints(counts)
-    _check(lib().kvc_prompt_attn(h, qp, qs, kp, vp, ks, c, _dev(out, name="out"), _stream(stream)), "kvc_prompt_attn")
+    c = _ints(counts)
+    _check(lib().kvc_prompt_attn(h, qp, qs, kp, vp, ks, _at(c), _dev(out, name="out"), _stream(stream)), "kvc_prompt_attn")
+
+
+def _pairs(src, dst) -> tuple:
+    s, d = _ints(src), _ints(dst)
+    if len(s) != len(d):
+        raise ValueError("src and dst must have one entry per request")
+    return s, d
 
 
 def kvc_fork(h, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
-    (s, n), (d, m) = _ints(src), _ints(dst)
-    if n != m:
-        raise ValueError("src and dst must have one entry per fork")
-    _check(lib().kvc_fork(h, n, s, d, _stream(stream)), "kvc_fork")
+    s, d = _pairs(src, dst)
+    _check(lib().kvc_fork(h, len(s), _at(s), _at(d), _stream(stream)), "kvc_fork")
 
 
 def kvc_copy(to, frm, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
-    (s, n), (d, m) = _ints(src), _ints(dst)
-    if n != m:
-        raise ValueError("src and dst must have one entry per copy")
-    _check(lib().kvc_copy(to, frm, n, s, d, _stream(stream)), "kvc_copy")
+    s, d = _pairs(src, dst)
+    _check(lib().kvc_copy(to, frm, len(s), _at(s), _at(d), _stream(stream)), "kvc_copy")
 
 
 def kvc_free(h, requests: Sequence[int], stream=None) -> None:
-    r, n = _ints(requests)
-    _check(lib().kvc_free(h, n, r, _stream(stream)), "kvc_free")
+    r = _ints(requests)
+    _check(lib().kvc_free(h, len(r), _at(r), _stream(stream)), "kvc_free")
 
 
 def kvc_compact(h, stream=None) -> int:
@@ -339,15 +348,22 @@ def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=No
     elif out.dtype != x.dtype or out.shape != x.shape:
         raise ValueError("out must be %s of shape %s" % (x.dtype, tuple(x.shape)))
     yp, ys = _rows(out, "out")
-    s, n = _ints(sections)
-    _dev(pos, torch.int32, (n, x.shape[0]), "pos")
+    s = _ints(sections)
+    rows, heads, d = x.shape
+    pp = _dev(pos, torch.int32, (len(s), rows), "pos")
     if not x.device == out.device == pos.device:
         raise ValueError("x, pos and out must be on one device")
-    with torch.cuda.device(x.device):
-        _check(lib().kvc_rope_axes(xp, xs, yp, ys, KVC_BF16 if x.dtype == torch.bfloat16 else KVC_F32, x.shape[0], x.shape[1],
-                                   x.shape[2], ctypes.c_void_p(pos.data_ptr()), n, s, float(base),
-                                   (KVC_ROPE_HALVES if halves else 0) | (KVC_ROPE_PER_AXIS if per_axis else 0),
-                                   _stream(stream)), "kvc_rope_axes")
+    flags = (KVC_ROPE_HALVES if halves else 0) | (KVC_ROPE_PER_AXIS if per_axis else 0)
+
+    def call():
+        _check(lib().kvc_rope_axes(xp, xs, yp, ys, KVC_BF16 if x.dtype == torch.bfloat16 else KVC_F32, rows, heads, d, pp, len(s),
+                                   _at(s), float(base), flags, _stream(stream)), "kvc_rope_axes")
+
+    if x.device.index == torch.cuda.current_device():
+        call()
+    else:
+        with torch.cuda.device(x.device):
+            call()
     return out
 
 
@@ -579,14 +595,14 @@ class Cache:
         """Packed prompts: ``counts[b]`` rows of each request in turn, appended and attended.  q [T, Hq, d],
         k and v [T, Hkv, d] with T >= sum(counts), heads dense, any row stride (views of one projection);
         rows behind the last request's are neither read nor written."""
-        counts = [int(c) for c in counts]
+        counts = _ints(counts)
         if len(counts) != self.B:
             raise ValueError("need one count per request")
-        T = q.shape[0]
-        if T < sum(counts):
-            raise ValueError("q has %d rows, the counts sum to %d" % (T, sum(counts)))
+        T, total = q.shape[0], sum(counts)
+        if T < total:
+            raise ValueError("q has %d rows, the counts sum to %d" % (T, total))
         for t, heads, name in ((q, self.Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")):
-            if t.dtype != self.torch_dtype or tuple(t.shape) != (T, heads, self.d):
+            if t.dtype != self.torch_dtype or t.shape != (T, heads, self.d):
                 raise ValueError("%s must be %s of shape %s, got %s %s" % (name, self.torch_dtype, (T, heads, self.d), t.dtype,
                                                                            tuple(t.shape)))
         if out is None:
