@@ -47,11 +47,9 @@ __device__ __forceinline__ bool position_ok(const RowArgs& a, long long p) {
     return p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P);
 }
 
-// Four pairs of a bf16 row, rotated by the {cos, sin} at rp.
-__device__ __forceinline__ uint4 turned(uint4 u, const float2* rp) {
-    const float4 c0 = __ldg(reinterpret_cast<const float4*>(rp)), c1 = __ldg(reinterpret_cast<const float4*>(rp) + 1);
+// Four pairs of a bf16 row, rotated in fp32, each product and sum rounded once.
+__device__ __forceinline__ uint4 turned(const uint4 u, const float2* cs) {
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    const float2 cs[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y), make_float2(c1.z, c1.w)};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float y0, y1;
@@ -64,11 +62,10 @@ __device__ __forceinline__ uint4 turned(uint4 u, const float2* rp) {
 
 constexpr int kRowsPerCta = 8;
 
-// grid (row groups of the longest request, requests).  VEC: bf16 rows in 16-byte units, d a
-// multiple of 8; otherwise a pair per item.  RoPE in fp32, each product and sum rounded
-// once, one rounding to the cache's type: the arithmetic of the other appends.
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, const __grid_constant__ Packed g) {
+// Rows of any head size and type, a pair per item.  grid (row groups of the longest request,
+// requests).  RoPE in fp32, each product and sum rounded once, one rounding to the cache's
+// type: the arithmetic of the other appends.
+__global__ void __launch_bounds__(kThreads) prompt_pairs_kernel(const RowArgs a, const __grid_constant__ Packed g) {
     dep_wait();                                        // launched dependent: see launch_dep
     dep_release();
     const int bi = blockIdx.y, b = g.b0 + bi;
@@ -78,19 +75,7 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
     const int r0 = blockIdx.x * kRowsPerCta - lead;
     if (n == 0 || r0 >= n) return;
     const int rows = min(n - r0, kRowsPerCta);
-    const int per = VEC ? d / 8 : d / 2, total = rows * a.Hkv * per;
-    if constexpr (VEC) {
-        // queries, as the tensor-core attention takes them
-        const int queries = a.q ? rows * a.Hq * per : 0;
-        for (int i = threadIdx.x; i < queries; i += kThreads) {
-            const int c = i % per, h = (i / per) % a.Hq, r = r0 + i / (per * a.Hq);
-            const long long p = (long long)cut + r;
-            if (r < 0 || !position_ok(a, p)) continue;
-            const size_t t = (size_t)(g.row0 + g.off[bi] + r);
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + (size_t)h * d + 8 * c));
-            *reinterpret_cast<uint4*>(a.out + (t * a.Hq + h) * a.out_head + 8 * c) = turned(u, a.rope + (size_t)p * (d / 2) + 4 * c);
-        }
-    }
+    const int per = d / 2, total = rows * a.Hkv * per;
     for (int i = threadIdx.x; i < total; i += kThreads) {
         const int c = i % per, h = (i / per) % a.Hkv, r = r0 + i / (per * a.Hkv);
         const long long p = (long long)cut + r;
@@ -102,41 +87,94 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
         void* kd = a.stage ? a.wk : a.kc;
         void* vd = a.stage ? a.wv : a.vc;
         const size_t src = (size_t)(g.row0 + g.off[bi] + r) * a.stride + (size_t)h * d;   // (used for r >= 0)
-        if constexpr (VEC) {
-            uint4 ko, vo;
-            if (r < 0) {
-                ko = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kc) + crow + 8 * c);
-                vo = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vc) + crow + 8 * c);
-            } else {
-                ko = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src + 8 * c));
-                vo = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src + 8 * c));
-                if (a.rope) ko = turned(ko, a.rope + (size_t)p * (d / 2) + 4 * c);
-            }
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(kd) + dst + 8 * c) = ko;
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(vd) + dst + 8 * c) = vo;
+        float k0, k1, v0, v1;
+        if (r < 0) {
+            k0 = ld_elem(a.kc, crow + 2 * c, a.bf16); k1 = ld_elem(a.kc, crow + 2 * c + 1, a.bf16);
+            v0 = ld_elem(a.vc, crow + 2 * c, a.bf16); v1 = ld_elem(a.vc, crow + 2 * c + 1, a.bf16);
         } else {
-            float k0, k1, v0, v1;
-            if (r < 0) {
-                k0 = ld_elem(a.kc, crow + 2 * c, a.bf16); k1 = ld_elem(a.kc, crow + 2 * c + 1, a.bf16);
-                v0 = ld_elem(a.vc, crow + 2 * c, a.bf16); v1 = ld_elem(a.vc, crow + 2 * c + 1, a.bf16);
-            } else {
-                k0 = ld_elem(a.k, src + 2 * c, a.bf16); k1 = ld_elem(a.k, src + 2 * c + 1, a.bf16);
-                v0 = ld_elem(a.v, src + 2 * c, a.bf16); v1 = ld_elem(a.v, src + 2 * c + 1, a.bf16);
-                if (a.rope) {
-                    const float x0 = k0, x1 = k1;
-                    rope_pair(x0, x1, a.rope[(size_t)p * (d / 2) + c], k0, k1);
-                }
+            k0 = ld_elem(a.k, src + 2 * c, a.bf16); k1 = ld_elem(a.k, src + 2 * c + 1, a.bf16);
+            v0 = ld_elem(a.v, src + 2 * c, a.bf16); v1 = ld_elem(a.v, src + 2 * c + 1, a.bf16);
+            if (a.rope) {
+                const float x0 = k0, x1 = k1;
+                rope_pair(x0, x1, a.rope[(size_t)p * (d / 2) + c], k0, k1);
             }
-            if (a.bf16) {
-                reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(kd) + dst)[c] = __floats2bfloat162_rn(k0, k1);
-                reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(vd) + dst)[c] = __floats2bfloat162_rn(v0, v1);
-            } else {
-                reinterpret_cast<float2*>(static_cast<float*>(kd) + dst)[c] = make_float2(k0, k1);
-                reinterpret_cast<float2*>(static_cast<float*>(vd) + dst)[c] = make_float2(v0, v1);
-            }
+        }
+        if (a.bf16) {
+            reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(kd) + dst)[c] = __floats2bfloat162_rn(k0, k1);
+            reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(vd) + dst)[c] = __floats2bfloat162_rn(v0, v1);
+        } else {
+            reinterpret_cast<float2*>(static_cast<float*>(kd) + dst)[c] = make_float2(k0, k1);
+            reinterpret_cast<float2*>(static_cast<float*>(vd) + dst)[c] = make_float2(v0, v1);
         }
         if (!a.stage && h == 0 && c == 0) a.pos[(size_t)b * a.S + slot] = (int)p;
     }
+}
+
+// bf16 rows with d a multiple of 8, in 16-byte units: the same arithmetic.  Bound by HBM.  A
+// thread holds one unit of a row's {cos, sin} and takes kHeads heads of that row, every load
+// issued first.  grid (row groups of the longest request, requests, head groups: those of the
+// rotated queries (where the tensor-core attention takes them), then those of keys and
+// values); a CTA covers 256 / (d / 8) rows.
+constexpr int kHeads = 8;
+
+__global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, const __grid_constant__ Packed g) {
+    dep_wait();
+    dep_release();
+    const int bi = blockIdx.y, b = g.b0 + bi;
+    const int n = g.off[bi + 1] - g.off[bi];
+    const int cut = a.next_pos[b], d = a.d, per = d / 8;
+    const int lead = a.stage ? cut & 15 : 0;                    // resident rows staged before the first new one
+    const int c = threadIdx.x % per, r = blockIdx.x * (kThreads / per) + threadIdx.x / per - lead;
+    if (threadIdx.x / per >= kThreads / per || r >= n) return;
+    const long long p = (long long)cut + r;
+    if (!position_ok(a, p)) { atomicOr(a.hdr, kErrPosition); return; }
+    float2 cs[4] = {};
+    if (a.rope && r >= 0) {
+        const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (d / 2) + 4 * c);
+        const float4 c0 = __ldg(rp), c1 = __ldg(rp + 1);
+        cs[0] = make_float2(c0.x, c0.y); cs[1] = make_float2(c0.z, c0.w);
+        cs[2] = make_float2(c1.x, c1.y); cs[3] = make_float2(c1.z, c1.w);
+    }
+    const long long t = g.row0 + g.off[bi] + r;                 // (packed row, for r >= 0)
+    const int qgroups = a.q ? (a.Hq + kHeads - 1) / kHeads : 0;
+    uint4 u[kHeads];
+    if ((int)blockIdx.z < qgroups) {
+        if (r < 0) return;
+        const int h0 = blockIdx.z * kHeads, nh = min(kHeads, a.Hq - h0);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + t * a.q_stride + (size_t)h0 * d + 8 * c);
+        __nv_bfloat16* dst = a.out + (t * a.Hq + h0) * a.out_head + 8 * c;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < nh) u[h] = __ldg(src + h * per);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < nh) *reinterpret_cast<uint4*>(dst + (size_t)h * a.out_head) = turned(u[h], cs);
+        return;
+    }
+    if (!a.stage && a.ring && r < n - a.S) return;              // overwritten later in this call
+    const int h0 = ((int)blockIdx.z - qgroups) * (kHeads / 2), nh = min(kHeads / 2, a.Hkv - h0);
+    const int slot = a.ring ? (int)(p % a.S) : (int)p;
+    // heads of a row lie S rows apart (16 in a page), of the staging area ws_rows
+    const size_t crow = kv_row(a.table, b, h0, slot, a.Hkv, a.S), cstep = a.table ? kPage : a.S;
+    const size_t drow = a.stage ? stage_row(b, h0, (int)p, cut, a.Hkv, a.ws_rows) : crow, dstep = a.stage ? (size_t)a.ws_rows : cstep;
+    const __nv_bfloat16* ks = r < 0 ? static_cast<const __nv_bfloat16*>(a.kc) + crow * d : static_cast<const __nv_bfloat16*>(a.k) + t * a.stride + (size_t)h0 * d;
+    const __nv_bfloat16* vs = r < 0 ? static_cast<const __nv_bfloat16*>(a.vc) + crow * d : static_cast<const __nv_bfloat16*>(a.v) + t * a.stride + (size_t)h0 * d;
+    const size_t sstep = r < 0 ? cstep * d : d;
+#pragma unroll
+    for (int h = 0; h < kHeads / 2; ++h)
+        if (h < nh) {
+            u[2 * h] = *reinterpret_cast<const uint4*>(ks + h * sstep + 8 * c);
+            u[2 * h + 1] = *reinterpret_cast<const uint4*>(vs + h * sstep + 8 * c);
+        }
+    __nv_bfloat16* kd = (a.stage ? a.wk : static_cast<__nv_bfloat16*>(a.kc)) + drow * d + 8 * c;
+    __nv_bfloat16* vd = (a.stage ? a.wv : static_cast<__nv_bfloat16*>(a.vc)) + drow * d + 8 * c;
+#pragma unroll
+    for (int h = 0; h < kHeads / 2; ++h)
+        if (h < nh) {
+            *reinterpret_cast<uint4*>(kd + h * dstep * d) = a.rope && r >= 0 ? turned(u[2 * h], cs) : u[2 * h];
+            *reinterpret_cast<uint4*>(vd + h * dstep * d) = u[2 * h + 1];
+        }
+    if (!a.stage && h0 == 0 && c == 0) a.pos[(size_t)b * a.S + slot] = (int)p;
 }
 
 __global__ void prompt_advance_kernel(int32_t* next_pos, const __grid_constant__ Packed g) {
@@ -330,7 +368,8 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W; a.P = s.P; a.ring = s.ring; a.bf16 = s.bf16;
     a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
-    const bool vec = s.bf16 && s.d % 8 == 0;     // the entry point checked alignment and strides
+    // the entry point checked alignment and strides (grid z: head groups)
+    const bool vec = s.bf16 && s.d % 8 == 0 && s.Hq <= 4 * 65535;
     const bool tensor = prompt_tc_supported(s);
     if (tensor && s.rope) {
         r.q = p.q; r.q_stride = p.q_stride; r.Hq = s.Hq;
@@ -354,8 +393,10 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
         cudaError_t e = cudaSuccess;
         auto rows = [&](int stage) {
             r.stage = stage;
-            const dim3 grid((most + (stage ? 15 : 0) + kRowsPerCta - 1) / kRowsPerCta, g.nb);
-            return launch_dep(vec ? prompt_rows_kernel<true> : prompt_rows_kernel<false>, grid, dim3(kThreads), 0, st, r, g);
+            const int longest = most + (stage ? 15 : 0), per_cta = vec ? kThreads / (s.d / 8) : kRowsPerCta;
+            const int groups = (r.q ? (s.Hq + kHeads - 1) / kHeads : 0) + (s.Hkv + kHeads / 2 - 1) / (kHeads / 2);
+            const dim3 grid((longest + per_cta - 1) / per_cta, g.nb, vec ? groups : 1);
+            return launch_dep(vec ? prompt_rows_kernel : prompt_pairs_kernel, grid, dim3(kThreads), 0, st, r, g);
         };
         if ((e = rows(s.ring ? 1 : 0)) != cudaSuccess) return e;
         e = tensor ? launch_prompt_tc(h, a, g, st) : launch_attention(a, g, most, st);

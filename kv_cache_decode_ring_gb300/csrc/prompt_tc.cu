@@ -10,8 +10,8 @@
 //    adjacent.  Where units are few and long, their keys are split over several CTAs
 //    and a second kernel joins the parts.
 //  * Warps 0-3 and 4-7: softmax of slot 0 and 1, thread = row = tensor-memory lane.  Warp 8
-//    issues the tensor copies, warp 9 looks over the value rows of boundary tiles, warp 10
-//    copies the queries of the next unit while this one runs, warps 12-15 issue the matrix
+//    issues the tensor copies of keys and values, warp 9 those of the next unit's queries, warps
+//    10 and 11 look over the value rows of boundary tiles, warps 12-15 issue the matrix
 //    instructions: each slot's two products from a warp of their own (with one warp
 //    for both, its waits and issues, one after the other, took longer than the products).
 //  * Tensor memory: S of both slots (fp32), their weights P (bf16 pairs, the A operand of P.V) and
@@ -51,7 +51,8 @@ using namespace tc;
 constexpr int kBM = 128;            // rows per slot
 constexpr int kSlots = 2;
 constexpr int kThreads = 16 * 32;
-constexpr int kWarpCopy = 8, kWarpLook = 9, kWarpLoad = 10, kWarpMma = 12;
+constexpr int kWarpCopy = 8, kWarpLoad = 9, kWarpLook = 10, kWarpMma = 12;
+constexpr int kLookWarps = 2;
 constexpr int kMmaWarps = 4;       // matrix warps: S and P.V of slot 0, then of slot 1
 constexpr float kLazyMax = 8.f;     // log2-domain headroom of a row's reference maximum
 constexpr int kRegLaunch = 128;
@@ -89,7 +90,7 @@ struct Plan {
     enum {
         kKFull = 0,                          // [stage] K copied
         kVFull = kKFull + kStages,           // [stage] V copied
-        kVClean = kVFull + kStages,          // [stage] V looked over
+        kVClean = kVFull + kStages,          // [stage] V looked over (2 warps)
         kSFull = kVClean + kStages,          // [slot][stage] S complete
         kODone = kSFull + kSlots * kStages,  // [slot][stage] P.V complete
         kSFree = kODone + kSlots * kStages,  // [slot] S read (4 warps)
@@ -100,8 +101,9 @@ struct Plan {
         kBars = kDone + kMmaWarps
     };
     static constexpr int kUnits = kBar + 8 * kBars;        // descriptions: kAhead of 16 words
-    static constexpr int kMisc = kUnits + kAhead * 64;     // tensor memory base, abort flag, units with spoilt values
-    static constexpr int kBytes = kMisc + 8 + 4 * kAhead + 1024;   // + alignment of the dynamic base
+    static constexpr int kMisc = kUnits + kAhead * 64;     // tensor memory base, units with spoilt values
+    static constexpr int kPlace = kMisc + 8 + 4 * kAhead;  // place of a slot's row in the output, in rows of heads
+    static constexpr int kBytes = kPlace + 4 * kBM + 1024; // + alignment of the dynamic base
     static_assert(kBytes <= (int)kMaxSmemPerBlock, "shared memory per block");
     static_assert(kTile % (16 * 8 * 32) == 0, "looked over in rounds of eight chunks a lane");
 };
@@ -122,7 +124,7 @@ struct Unit {
 __device__ __forceinline__ int first_key(const AttnArgs& a, int p) { return a.W > 0 ? max(0, p - a.W + 1) : 0; }
 
 template <int D>
-__device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Items& items, int b0, int u) {
+__device__ __noinline__ Unit unit_of(const AttnArgs& a, const Items& items, int b0, int u) {
     constexpr int kBN = Plan<D>::kBN;
     Unit w;
     const int4 e = items.e[u / a.Hkv];
@@ -164,8 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + L::kBar);
     static_assert(sizeof(Unit) <= 64, "a unit's description");
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
     volatile int* spoilt = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);   // [unit mod kAhead]: 1 + the unit
+
+    int* place = reinterpret_cast<int*>(smem + L::kPlace);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nunits = items.n * a.Hkv, G = gridDim.x, T = kBM / a.g;      // T: tokens a slot
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&bar[L::kKFull + s], 1);
             mbar_init(&bar[L::kVFull + s], 1);
-            mbar_init(&bar[L::kVClean + s], 1);
+            mbar_init(&bar[L::kVClean + s], kLookWarps);
         }
         for (int i = 0; i < kSlots; ++i) {
             for (int s = 0; s < L::kStages; ++s) {
@@ -204,10 +207,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&bar[L::kQFull + i], 1);
         for (int i = 0; i < kMmaWarps; ++i) mbar_init(&bar[L::kDone + i], 1);
-        *abort_flag = 0;
         for (int i = 0; i < kAhead; ++i) spoilt[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (tid < kBM) place[tid] = tid / a.g * a.Hq + tid % a.g;
     if (warp == kWarpMma) tmem_alloc(tmem_slot, kTmemCols);
     fence_before();
     __syncthreads();
@@ -228,12 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + L::kColS + kBN * slot + lane_off;
         const uint32_t tP = tmem + L::kColP + L::kPStep * slot + lane_off;
         const uint32_t tO = tmem + L::kColO + D * slot + lane_off;
-        const int r = 32 * lg + lane, mine_tok = slot * T + r / a.g, mine_head = r % a.g;   // the row's token in the unit
+        const int r = 32 * lg + lane, mine_tok = slot * T + r / a.g;               // the row's token in the unit
         const float sc = a.scale_log2, lazy = kLazyMax / sc;
         int k = 0;                                              // tiles so far
         for (int rd = 0, i = 0; rd * G < nunits && ok; ++rd) {
             if (mine(rd) >= nunits) continue;
-            if (!(ok = all_ok(wait(q_full(slot, i), (uint32_t)((i >> 1) & 1), abort_flag)))) break;
+            if (!(ok = all_ok(wait(q_full(slot, i), (uint32_t)((i >> 1) & 1))))) break;
             const Unit& w = unit_in(i);
             const int nt = w.nt, ntok = w.ntok, k0 = w.k0, w0 = w.w0, w1 = w.w1;
             const bool valid = r < T * a.g && mine_tok < ntok, some = slot * T < ntok;     // this row's, the slot's
@@ -243,11 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool full = T * a.g == kBM && ntok >= (slot + 1) * T;
             float m_ref = -INFINITY, l = 0.f;                   // m_ref: of the scores, before scaling
             for (int j = 0; j < nt; ++j, ++k) {
-                if (!(ok = all_ok(wait(stage_bar(L::kSFull, slot, k), phase(k), abort_flag)))) break;
+                if (!(ok = all_ok(wait(stage_bar(L::kSFull, slot, k), phase(k))))) break;
                 fence_after();
                 // P.V of the tile before reads P and adds to O: usually done long before the weights are
                 auto done = [&]() -> bool {
-                    return j == 0 || all_ok(wait(stage_bar(L::kODone, slot, k - 1), phase(k - 1), abort_flag));
+                    return j == 0 || all_ok(wait(stage_bar(L::kODone, slot, k - 1), phase(k - 1)));
                 };
                 if (!some) {                                    // no rows: the products run on, nothing is read
                     __syncwarp();
@@ -266,9 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&bar[L::kSFree + slot]);          // the next S may overwrite it
                 const int kb = k0 + kBN * j;
                 if (!(kb >= sl && kb + kBN - 1 <= sh) || !full) {
-                    const int c0 = key_lo - kb, width = valid ? p - key_lo : -1;      // visible: c0 .. c0 + width
+                    // (key by key: skipping groups of keys that all or none of the warp's rows see took
+                    // registers that the other tiles need: 1.71 against 1.52 ms for 16384 tokens)
+                    const int c0 = valid ? key_lo - kb : kBN, c1 = valid ? p - kb : -1;       // visible: c0 .. c1
 #pragma unroll
-                    for (int c = 0; c < kBN; ++c) s[c] = width >= 0 && (uint32_t)(c - c0) <= (uint32_t)width ? s[c] : -INFINITY;
+                    for (int c = 0; c < kBN; ++c) s[c] = c >= c0 && c <= c1 ? s[c] : -INFINITY;
                 }
                 // row maximum: eight independent chains of three-input maxima, then a tree
                 float m8[8];
@@ -328,21 +333,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::kPFull + slot]);
             }
-            if (ok && nt > 0) ok = all_ok(wait(stage_bar(L::kODone, slot, k - 1), phase(k - 1), abort_flag));
+            if (ok && nt > 0) ok = all_ok(wait(stage_bar(L::kODone, slot, k - 1), phase(k - 1)));
             if (!ok) break;
             if (some) {
                 fence_after();
                 const bool parts = items.parts > 1;             // unnormalised sums with their maximum, to be joined
                 const float inv = parts ? 1.f : 1.f / l;
-                const bool fix = nt > 0 && spoilt[i % kAhead] == i + 1, bf16 = a.out_bf16 && !parts;
+                const bool bf16 = a.out_bf16 && !parts;
                 // through the warp's own rows of the unit's Q tile (its scores are all done), so that a
                 // store covers whole 128-byte lines: 32 dims at a time as fp32, 64 as bf16
                 unsigned char* stage = sQ + q_buf(slot, i) * L::kQTile + 32 * lg * 128;
-                const int c = lane & 7, r1 = 32 * lg + (lane >> 3);                // store: chunk, first row (then every fourth)
-                const int tok = slot * T + r1 / a.g, head = r1 % a.g, dt4 = 4 / a.g, dj4 = 4 % a.g;
-                const size_t orow = (size_t)(w.row + w.t0) * a.Hq + w.kvh * a.g;   // (rows of heads)
+                const int c = lane & 7, nv = min(T, ntok - slot * T) * a.g;        // the slot's rows
+                const size_t orow = (size_t)(w.row + w.t0 + slot * T) * a.Hq + w.kvh * a.g;
+                // (32 dims as fp32 or 64 as bf16: 128 bytes a round)
+                const long long row_bytes = parts ? (long long)items.parts * D * 4 : D * (bf16 ? 2 : 4);
+                char* dst = (parts ? reinterpret_cast<char*>(a.part_acc + (size_t)w.part * D) : static_cast<char*>(a.out)) +
+                            orow * row_bytes + 16 * c;
                 if (parts && valid)
-                    a.part_ml[(orow + (size_t)mine_tok * a.Hq + mine_head) * items.parts + w.part] =
+                    a.part_ml[(orow + place[r]) * items.parts + w.part] =
                         make_float2(m_ref == -INFINITY ? -INFINITY : m_ref * sc, l);
 #pragma unroll 1
                 for (int x0 = 0; x0 < D; x0 += 32) {
@@ -356,29 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] *= inv;
-                    if (fix && valid) {
-                        // values that are not finite, left out of boundary tiles: those that the row sees
-                        for (int key = max(key_lo, k0); key <= min(p, k0 + nt * kBN - 1); ++key) {
-                            const int j = (key - k0) / kBN;
-                            if (j >= w0 && j < w1) { key = k0 + w1 * kBN - 1; continue; }
-                            const bool staged = a.ring && key >= (w.cut & ~15);
-                            const size_t at = staged ? stage_row(w.b, w.kvh, key, w.cut, a.Hkv, a.ws_rows)
-                                                     : kv_row(a.table, w.b, w.kvh, a.ring ? key % a.S : key, a.Hkv, a.S);
-                            const uint4* v = reinterpret_cast<const uint4*>(
-                                (staged ? a.wv : static_cast<const __nv_bfloat16*>(a.vc)) + at * D + x0);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint4 u = v[e];
-                                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const float v0 = __uint_as_float(x[q] << 16), v1 = __uint_as_float(x[q] & 0xffff0000u);
-                                    if (!isfinite(v0)) o[8 * e + 2 * q] += v0;
-                                    if (!isfinite(v1)) o[8 * e + 2 * q + 1] += v1;
-                                }
-                            }
-                        }
-                    }
                     if (bf16) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -399,24 +384,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                     __syncwarp();
-                    int tt = tok, jj = head;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int rr = (lane >> 3) + 4 * e;
-                        if (r1 + 4 * e < T * a.g && tt < ntok) {
-                            const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
-                            const size_t at = orow + (size_t)tt * a.Hq + jj;
-                            if (bf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at * D + x0 / 64 * 64 + 8 * c) = u;
-                            else *reinterpret_cast<uint4*>((parts ? a.part_acc + (at * items.parts + w.part) * D
-                                                                  : static_cast<float*>(a.out) + at * D) + x0 + 4 * c) = u;
-                        }
-                        tt += dt4;
-                        jj += dj4;
-                        if (jj >= a.g) { jj -= a.g; ++tt; }
+                        const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
+                        if (32 * lg + rr < nv) *reinterpret_cast<uint4*>(dst + (long long)place[32 * lg + rr] * row_bytes) = u;
                     }
+                    dst += 128;
                     __syncwarp();
                 }
                 fence_before();                                 // O is read before the next unit's products write it
+                if (nt > 0 && spoilt[i % kAhead] == i + 1 && valid) {
+                    // values that are not finite, left out of boundary tiles: those that the row sees are
+                    // added to what it wrote
+                    char* at = static_cast<char*>(parts ? static_cast<void*>(a.part_acc + (size_t)w.part * D) : a.out) + (orow + place[r]) * row_bytes;
+#pragma unroll 1
+                    for (int key = max(key_lo, k0); key <= min(p, k0 + nt * kBN - 1); ++key) {
+                        const int j = (key - k0) / kBN;
+                        if (j >= w0 && j < w1) { key = k0 + w1 * kBN - 1; continue; }
+                        const bool staged = a.ring && key >= (w.cut & ~15);
+                        const __nv_bfloat16* v = staged ? a.wv + stage_row(w.b, w.kvh, key, w.cut, a.Hkv, a.ws_rows) * D
+                                                        : static_cast<const __nv_bfloat16*>(a.vc) +
+                                                              kv_row(a.table, w.b, w.kvh, a.ring ? key % a.S : key, a.Hkv, a.S) * D;
+#pragma unroll 1
+                        for (int x = 0; x < D; ++x) {
+                            const float add = __bfloat162float(v[x]);
+                            if (isfinite(add)) continue;
+                            if (bf16) {
+                                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(at) + x;
+                                *o = __float2bfloat16_rn(__bfloat162float(*o) + add);
+                            } else {
+                                reinterpret_cast<float*>(at)[x] += add;
+                            }
+                        }
+                    }
+                }
             }
             fence_async_smem();                                 // the tile's rows held output: the next copy comes after
             __syncwarp();
@@ -446,9 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // a stage is free when both slots are done with its tile
         auto free_again = [&](int which, int k) -> bool {
-            return all_ok(wait(stage_bar(which, 0, k), phase(k), abort_flag) && wait(stage_bar(which, 1, k), phase(k), abort_flag));
+            return all_ok(wait(stage_bar(which, 0, k), phase(k)) && wait(stage_bar(which, 1, k), phase(k)));
         };
-        auto looked = [&](int k) -> bool { return all_ok(wait(&bar[L::kVClean + k % L::kStages], phase(k), abort_flag)); };
+        auto looked = [&](int k) -> bool { return all_ok(wait(&bar[L::kVClean + k % L::kStages], phase(k))); };
         int k = 0, k_issued = 0, v_issued = 0;
         for (int rd = 0; rd * G < nunits && ok; ++rd) {
             if (mine(rd) >= nunits) continue;
@@ -481,10 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (!ok) {
-            *abort_flag = 1;
             // the last copy issued into each stage lands before the CTA can exit
-            for (int q = max(0, k_issued - L::kStages); q < k_issued; ++q) drain(&bar[L::kKFull + q % L::kStages], phase(q));
-            for (int q = max(0, v_issued - L::kStages); q < v_issued; ++q) drain(&bar[L::kVFull + q % L::kStages], phase(q));
+            for (int q = max(0, k_issued - L::kStages); q < k_issued; ++q) wait(&bar[L::kKFull + q % L::kStages], phase(q));
+            for (int q = max(0, v_issued - L::kStages); q < v_issued; ++q) wait(&bar[L::kVFull + q % L::kStages], phase(q));
         }
         __syncwarp();
     } else if (warp >= kWarpMma) {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // K and V tiles: [half][row] from a contiguous cache, [8 rows][half] from 16-row boxes
         const bool boxes = a.table || a.ring;
         const uint32_t half_step = boxes ? 1024 : L::kHalf, group_step = boxes ? L::kHalves * 1024 : 1024;
-        auto wait_ok = [&](uint64_t* b, uint32_t parity) -> bool { return all_ok(wait(b, parity, abort_flag)); };
+        auto wait_ok = [&](uint64_t* b, uint32_t parity) -> bool { return all_ok(wait(b, parity)); };
         int k = 0;
         if (scores) {
             const uint32_t q0 = desc_lo(smem_u32(sQ), 16), qhi = desc_hi(1024);
@@ -551,13 +552,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++i;
             }
         }
-        if (!ok) *abort_flag = 1;
         // no product may still target the columns when they are freed
         if (lead) mma_commit(&bar[L::kDone + warp - kWarpMma]);
         __syncwarp();
-        drain(&bar[L::kDone + warp - kWarpMma], 0);
+        wait(&bar[L::kDone + warp - kWarpMma], 0);
         __syncwarp();
-    } else if (warp == kWarpLook) {
+    } else if (warp >= kWarpLook) {
         // ================= value rows of boundary tiles: what is not finite becomes 0
         int k = 0;
         for (int rd = 0, i = 0; rd * G < nunits && ok; ++rd) {
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < w.nt; ++j, ++k) {
                 const int st = k % L::kStages;
                 // (every tile in turn: a barrier's parity tells neighbouring phases apart only)
-                if (!(ok = all_ok(wait(&bar[L::kVFull + st], phase(k), abort_flag)))) break;
+                if (!(ok = all_ok(wait(&bar[L::kVFull + st], phase(k))))) break;
                 if (j >= w.w0 && j < w.w1) {
                     if (lane == 0) mbar_arrive(&bar[L::kVClean + st]);
                     continue;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unsigned char* tile = sV + st * L::kTile;
                 bool any = false;
 #pragma unroll 1
-                for (int q0 = lane; q0 < L::kTile / 16; q0 += 8 * 32) {
+                for (int q0 = 8 * 32 * (warp - kWarpLook) + lane; q0 < L::kTile / 16; q0 += 8 * 32 * kLookWarps) {
                     uint4 u[8];
                     uint32_t bad = 0;
 #pragma unroll
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit w = unit_of<D>(a, items, b0, mine(rd));
             for (int slot = 0; slot < kSlots; ++slot, ++q) {
                 const int i = q >> 1, buf = q % L::kQBufs, uses = q / L::kQBufs;
-                if (uses > 0 && !(ok = all_ok(wait(&bar[L::kQFree + buf], (uint32_t)((uses - 1) & 1), abort_flag)))) break;
+                if (uses > 0 && !(ok = all_ok(wait(&bar[L::kQFree + buf], (uint32_t)((uses - 1) & 1))))) break;
                 if (lead) {
                     if (slot == 0) unit_in(i) = w;
                     mbar_arrive_expect_tx(q_full(slot, i), L::kHalves * T * a.g * 128);
@@ -621,13 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // the last copies land before the CTA can exit
-        for (int p = max(0, q - L::kQBufs); p < q; ++p) drain(q_full(p & 1, p >> 1), (uint32_t)((p >> 2) & 1));
+        for (int p = max(0, q - L::kQBufs); p < q; ++p) wait(q_full(p & 1, p >> 1), (uint32_t)((p >> 2) & 1));
         __syncwarp();
     }
-    if (!ok) {
-        if (lane == 0) atomicOr(a.hdr, kErrWait);
-        *abort_flag = 1;
-    }
+    if (!ok && lane == 0) atomicOr(a.hdr, kErrWait);
     fence_before();
     __syncthreads();
     if (warp == kWarpMma) {

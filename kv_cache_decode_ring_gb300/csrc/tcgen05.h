@@ -137,46 +137,20 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Non-blocking check that phase `parity` of an mbarrier has completed.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+// Bounded wait for phase `parity` of an mbarrier: 2^24 tries, of which each suspends for a while
+// (about a second in all); false when it gave up.  One short loop: it stands at many places
+// of kernels whose instructions have to stay cached.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        "{\n .reg .pred p, q;\n .reg .b32 n;\n mov.b32 n, 0;\n"
+        "LOOP:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n add.u32 n, n, 1;\n"
+        " setp.lt.u32 q, n, 0x1000000;\n @q bra LOOP;\n"
+        "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
-}
-
-// Bounded waits (about a second, counted in SM clocks); false when they give up or when
-// another role of the CTA has (`*abort`, looked at only while waiting).  spin() polls
-// without suspending: for the warps that issue the matrix instructions.
-constexpr long long kWaitClocks = 2000000000ll;
-
-__device__ __forceinline__ bool spin(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_test(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (int it = 0;; ++it) {
-        if (mbar_test(bar, parity)) return true;
-        if ((it & 63) == 63 && (*abort || clock64() - t0 > kWaitClocks)) return false;
-    }
-}
-
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort || clock64() - t0 > kWaitClocks) return false;
-    }
-}
-
-// the same for copies and products already issued, which land whatever else happened
-__device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity))
-        if (clock64() - t0 > kWaitClocks) return false;
-    return true;
 }
 
 }  // namespace tc
