@@ -11,9 +11,9 @@
 // sincospif of that is off by less than 2^-24 pi from the rounding to fp32, plus its own
 // error.  F is the double-precision frequency, so a position p adds p theta 2^-53.
 //
-// Bound by HBM: x read once, y written once.  The sines of a row are shared by all heads,
-// so a CTA computes them once for a few rows into shared memory, and its threads then
-// stream the rows in 16-byte units.
+// Bound by HBM: x read once, y written once.  A thread keeps one 16-byte unit's place in a
+// row (with halves, the unit and its partner), works out that unit's sines once and takes
+// the row's heads eight at a time, every load issued before the first product.
 #include <cmath>
 #include <cstring>
 
@@ -32,6 +32,7 @@ struct RopeArgs {
     const int32_t* pos;                   // [axes][rows]
     long long rows, xs, ys;               // row strides in elements
     int heads, d, pairs, rows_per_cta, halves, in_place;
+    int units, heads_per_cta;             // units of a row that a CTA's threads take (rotated first); heads per grid y
     uint64_t turn[kMaxPairs];             // frequency, turns per position * 2^64
     uint8_t axis[kMaxPairs];
 };
@@ -50,64 +51,61 @@ template <typename T> __device__ __forceinline__ T from_f(float x);
 template <> __device__ __forceinline__ float from_f(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
 
-// VEC elements are 16 bytes.  grid (row groups, head groups): a CTA's sines serve its
-// rows' heads [h0, h1).  Work item: one head's unit of a row; with halves, a unit of the
-// first half and its partner in the second.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-    extern __shared__ float2 cs[];                        // [rows_per_cta][pairs]
-    const long long r0 = (long long)blockIdx.x * a.rows_per_cta;
-    const int nr = (int)min((long long)a.rows_per_cta, a.rows - r0);
-    for (int i = threadIdx.x; i < nr * a.pairs; i += kThreads) {
-        const int r = i / a.pairs, p = i % a.pairs;
-        cs[i] = cos_sin(a.turn[p], a.pos[a.axis[p] * a.rows + r0 + r]);
-    }
-    __syncthreads();
-    const int hper = (a.heads + gridDim.y - 1) / gridDim.y, h0 = blockIdx.y * hper;
-    const int nh = min(a.heads - h0, hper);
-    if (nh <= 0) return;
-    const T* X = static_cast<const T*>(a.x);
-    T* Y = static_cast<T*>(a.y);
+constexpr int kHeads = 8;                 // heads that a CTA takes where rows are few
+
+// VEC elements are 16 bytes.  grid (row groups, head groups); thread = (row, unit).
+// kFlight heads in flight: eight units a thread either way.
+template <typename T, int VEC, bool HALVES>
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+    const int u = threadIdx.x % a.units;
+    const long long r = (long long)blockIdx.x * a.rows_per_cta + threadIdx.x / a.units;
+    if (threadIdx.x / a.units >= a.rows_per_cta || r >= a.rows) return;
+    const int h1 = min(a.heads, ((int)blockIdx.y + 1) * a.heads_per_cta);
     union Pack { uint4 u; T e[VEC]; };
-    const int rot = 2 * a.pairs;
-    // units of a head: rotated ones (pairs of units with halves), then those that pass through
-    const int nrot = a.halves ? a.pairs / VEC : rot / VEC, units = nrot + (a.in_place ? 0 : (a.d - rot) / VEC);
-    const int total = nr * nh * units;
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-        const int u = i % units, rh = i / units, r = rh / nh, h = h0 + rh % nh;
-        const T* x = X + (r0 + r) * a.xs + (long long)h * a.d;
-        T* y = Y + (r0 + r) * a.ys + (long long)h * a.d;
-        const float2* c = cs + r * a.pairs;
-        if (u >= nrot) {
-            const int o = rot + (u - nrot) * VEC;
-            *reinterpret_cast<uint4*>(y + o) = *reinterpret_cast<const uint4*>(x + o);
-        } else if (a.halves) {
-            const int o = u * VEC;
-            Pack p, q;
-            p.u = *reinterpret_cast<const uint4*>(x + o);
-            q.u = *reinterpret_cast<const uint4*>(x + a.pairs + o);
+    const int nrot = HALVES ? a.pairs / VEC : 2 * a.pairs / VEC;
+    const bool pass = u >= nrot;                         // a unit behind the rotated dims
+    const int o = pass ? 2 * a.pairs + (u - nrot) * VEC : u * VEC, partner = a.pairs;
+    const T* x = static_cast<const T*>(a.x) + r * a.xs + o;
+    T* y = static_cast<T*>(a.y) + r * a.ys + o;
+    constexpr int kPairs = HALVES ? VEC : VEC / 2, kFlight = HALVES ? 4 : 8;
+    Pack p[kFlight], q[HALVES ? kFlight : 1];
+    auto load = [&](int h0) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float y0, y1;
-                rope_pair(to_f(p.e[e]), to_f(q.e[e]), c[o + e], y0, y1);
-                p.e[e] = from_f<T>(y0);
-                q.e[e] = from_f<T>(y1);
+        for (int e = 0; e < kFlight; ++e)
+            if (h0 + e < h1) {
+                p[e].u = *reinterpret_cast<const uint4*>(x + (h0 + e) * a.d);
+                if (HALVES && !pass) q[HALVES ? e : 0].u = *reinterpret_cast<const uint4*>(x + (h0 + e) * a.d + partner);
             }
-            *reinterpret_cast<uint4*>(y + o) = p.u;
-            *reinterpret_cast<uint4*>(y + a.pairs + o) = q.u;
-        } else {
-            const int o = u * VEC;
-            Pack p;
-            p.u = *reinterpret_cast<const uint4*>(x + o);
+    };
+    int h0 = blockIdx.y * a.heads_per_cta;
+    load(h0);
+    float2 cs[kPairs];
+    if (!pass) {
+        const int p0 = HALVES ? o : o / 2;
 #pragma unroll
-            for (int e = 0; e < VEC; e += 2) {
-                float y0, y1;
-                rope_pair(to_f(p.e[e]), to_f(p.e[e + 1]), c[(o + e) / 2], y0, y1);
-                p.e[e] = from_f<T>(y0);
-                p.e[e + 1] = from_f<T>(y1);
+        for (int e = 0; e < kPairs; ++e) cs[e] = cos_sin(a.turn[p0 + e], a.pos[a.axis[p0 + e] * a.rows + r]);
+    }
+    for (;;) {
+#pragma unroll
+        for (int e = 0; e < kFlight; ++e)
+            if (h0 + e < h1) {
+                if (!pass) {
+#pragma unroll
+                    for (int k = 0; k < kPairs; ++k) {
+                        T& e0 = p[e].e[HALVES ? k : 2 * k];
+                        T& e1 = HALVES ? q[HALVES ? e : 0].e[k] : p[e].e[HALVES ? k : 2 * k + 1];
+                        float y0, y1;
+                        rope_pair(to_f(e0), to_f(e1), cs[k], y0, y1);
+                        e0 = from_f<T>(y0);
+                        e1 = from_f<T>(y1);
+                    }
+                    if (HALVES) *reinterpret_cast<uint4*>(y + (h0 + e) * a.d + partner) = q[HALVES ? e : 0].u;
+                }
+                *reinterpret_cast<uint4*>(y + (h0 + e) * a.d) = p[e].u;
             }
-            *reinterpret_cast<uint4*>(y + o) = p.u;
-        }
+        h0 += kFlight;
+        if (h0 >= h1) break;
+        load(h0);
     }
 }
 
@@ -188,22 +186,30 @@ extern "C" int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64
     a.heads = heads; a.d = head_dim; a.pairs = pairs;
     a.halves = flags & KVC_ROPE_HALVES ? 1 : 0;
     a.in_place = d_x == d_y;
-    a.rows_per_cta = 4;
-    const long long groups = (rows + a.rows_per_cta - 1) / a.rows_per_cta;
-    if (groups > 0x7fffffffLL) return KVC_ERR_ARG;
-    const size_t smem = (size_t)a.rows_per_cta * pairs * sizeof(float2);
     const int vec = 16 / elem;
     // 16-byte units: every unit aligned and whole within the rotated dims (a half of them)
     const bool wide = aligned16(d_x) && aligned16(d_y) && head_dim % vec == 0 && a.xs % vec == 0 && a.ys % vec == 0 &&
                       (a.halves ? pairs % vec == 0 : 2 * pairs % vec == 0);
-    const dim3 grid((unsigned)groups, 1);
+    a.units = (a.halves ? pairs : 2 * pairs) / vec + (a.in_place ? 0 : (head_dim - 2 * pairs) / vec);
+    a.rows_per_cta = wide ? kThreads / a.units : 4;
+    const long long groups = (rows + a.rows_per_cta - 1) / a.rows_per_cta;
+    if (groups > 0x7fffffffLL) return KVC_ERR_ARG;
+    // many rows: a CTA takes every head of its rows; few (a decode step): eight each, to fill the GPU
+    a.heads_per_cta = wide && groups < 608 ? kHeads : heads;
+    const unsigned hgroups = (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta);
+    if (hgroups > 65535) return KVC_ERR_ARG;
+    const dim3 grid((unsigned)groups, hgroups);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t smem = (size_t)a.rows_per_cta * pairs * sizeof(float2);
+    auto launch = [&](auto kernel, size_t bytes) { kernel<<<grid, kThreads, bytes, st>>>(a); };
     if (dtype == KVC_BF16) {
-        if (wide) rope_kernel<__nv_bfloat16, 8><<<grid, kThreads, smem, st>>>(a);
-        else rope_pairs_kernel<__nv_bfloat16><<<grid, kThreads, smem, st>>>(a);
+        if (!wide) launch(rope_pairs_kernel<__nv_bfloat16>, smem);
+        else if (a.halves) launch(rope_kernel<__nv_bfloat16, 8, true>, 0);
+        else launch(rope_kernel<__nv_bfloat16, 8, false>, 0);
     } else {
-        if (wide) rope_kernel<float, 4><<<grid, kThreads, smem, st>>>(a);
-        else rope_pairs_kernel<float><<<grid, kThreads, smem, st>>>(a);
+        if (!wide) launch(rope_pairs_kernel<float>, smem);
+        else if (a.halves) launch(rope_kernel<float, 4, true>, 0);
+        else launch(rope_kernel<float, 4, false>, 0);
     }
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
