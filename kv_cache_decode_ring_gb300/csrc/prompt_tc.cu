@@ -64,6 +64,7 @@ constexpr int kSplitTiles = 4;      // ... of no fewer tiles than this
 
 struct Items {
     int n, parts;
+    int boxed;                      // 32 rows of a slot are whole tokens: tmO has boxes for them
     int4 e[kItems];                 // (index in the group | part << 16, first token, packed row of the request, its tokens)
 };
 
@@ -154,7 +155,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CUtensorMap tmWK, const __grid_constant__ CUtensorMap tmWV,
-                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ AttnArgs a, const int b0, const __grid_constant__ Items items) {
+                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmO,
+                       const __grid_constant__ AttnArgs a, const int b0, const __grid_constant__ Items items) {
     using L = Plan<D>;
     constexpr int kBN = L::kBN;
     extern __shared__ unsigned char smem_raw[];
@@ -269,11 +271,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&bar[L::kSFree + slot]);          // the next S may overwrite it
                 const int kb = k0 + kBN * j;
                 if (!(kb >= sl && kb + kBN - 1 <= sh) || !full) {
-                    // (key by key: skipping groups of keys that all or none of the warp's rows see took
-                    // registers that the other tiles need: 1.71 against 1.52 ms for 16384 tokens)
+                    // (a word of visible keys per 16, which the compiler spreads over predicates: two
+                    // comparisons a key took 3 to 6 % longer on short prompts; skipping groups that
+                    // all or none of the warp's rows see costs the other tiles registers)
                     const int c0 = valid ? key_lo - kb : kBN, c1 = valid ? p - kb : -1;       // visible: c0 .. c1
 #pragma unroll
-                    for (int c = 0; c < kBN; ++c) s[c] = c >= c0 && c <= c1 ? s[c] : -INFINITY;
+                    for (int q = 0; q < kBN; q += 16) {
+                        const int x0 = min(max(c0 - q, 0), 16), x1 = min(max(c1 - q + 1, 0), 16);
+                        const uint32_t seen = (0xffffffffu << x0) & ~(0xffffffffu << x1);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) s[q + c] = seen >> c & 1 ? s[q + c] : -INFINITY;
+                    }
                 }
                 // row maximum: eight independent chains of three-input maxima, then a tree
                 float m8[8];
@@ -340,15 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool parts = items.parts > 1;             // unnormalised sums with their maximum, to be joined
                 const float inv = parts ? 1.f : 1.f / l;
                 const bool bf16 = a.out_bf16 && !parts;
-                // through the warp's own rows of the unit's Q tile (its scores are all done), so that a
-                // store covers whole 128-byte lines: 32 dims at a time as fp32, 64 as bf16
-                unsigned char* stage = sQ + q_buf(slot, i) * L::kQTile + 32 * lg * 128;
+                // through the warp's own rows of the unit's Q tile (its scores are all done): where the
+                // warp's rows are whole tokens, all there and bf16, a tensor copy takes them out; else
+                // 128 bytes of each row at a time (32 dims as fp32, 64 as bf16), lines stored whole
+                unsigned char* tile = sQ + q_buf(slot, i) * L::kQTile + 32 * lg * 128;
+                unsigned char* stage = tile;
                 const int c = lane & 7, nv = min(T, ntok - slot * T) * a.g;        // the slot's rows
                 const size_t orow = (size_t)(w.row + w.t0 + slot * T) * a.Hq + w.kvh * a.g;
                 // (32 dims as fp32 or 64 as bf16: 128 bytes a round)
                 const long long row_bytes = parts ? (long long)items.parts * D * 4 : D * (bf16 ? 2 : 4);
                 char* dst = (parts ? reinterpret_cast<char*>(a.part_acc + (size_t)w.part * D) : static_cast<char*>(a.out)) +
                             orow * row_bytes + 16 * c;
+                const bool spoilt_unit = nt > 0 && spoilt[i % kAhead] == i + 1;
+                const bool boxed = items.boxed && !spoilt_unit && bf16 && 32 * lg + 32 <= nv;
                 if (parts && valid)
                     a.part_ml[(orow + place[r]) * items.parts + w.part] =
                         make_float2(m_ref == -INFINITY ? -INFINITY : m_ref * sc, l);
@@ -365,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] *= inv;
                     if (bf16) {
+                        if (boxed) stage = tile + x0 / 64 * L::kQHalf;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             uint32_t u[4];
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(stage + lane * 128 + (((x0 / 32 % 2 * 4 + e) ^ (lane & 7)) << 4)) =
                                 make_uint4(u[0], u[1], u[2], u[3]);
                         }
-                        if (x0 % 64 == 0) continue;
+                        if (boxed || x0 % 64 == 0) continue;
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -394,7 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 fence_before();                                 // O is read before the next unit's products write it
-                if (nt > 0 && spoilt[i % kAhead] == i + 1 && valid) {
+                if (boxed) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int half = 0; half < L::kHalves; ++half)
+                            tma_store_3d(&tmO, tile + half * L::kQHalf, 64 * half, w.kvh * a.g,
+                                         w.row + w.t0 + slot * T + 32 * lg / a.g);
+                        tma_store_read();
+                    }
+                    __syncwarp();
+                }
+                if (spoilt_unit && valid) {
                     // values that are not finite, left out of boundary tiles: those that the row sees are
                     // added to what it wrote
                     char* at = static_cast<char*>(parts ? static_cast<void*>(a.part_acc + (size_t)w.part * D) : a.out) + (orow + place[r]) * row_bytes;
@@ -690,7 +715,7 @@ cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Plan<D>::kBytes)) return e;
     const long long units = (long long)items.n * a.Hkv;
     return launch_dep(kernel, dim3((unsigned)std::min<long long>(units, sms)), dim3(kThreads), Plan<D>::kBytes, st, tm[0], tm[1], tm[2],
-                      tm[3], tm[4], a, b0, items);
+                      tm[3], tm[4], tm[5], a, b0, items);
 }
 
 }  // namespace
@@ -705,7 +730,7 @@ bool prompt_tc_supported(const Shape& s) {
 cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packed& g, cudaStream_t st) {
     const Shape& s = h->sh;
     const int bn = s.d == 128 ? Plan<128>::kBN : Plan<64>::kBN;
-    CUtensorMap tm[5];
+    CUtensorMap tm[6];
     const bool boxes = s.pages || s.ring;
     const long long rows = s.pages ? (long long)s.pages * s.Hkv * kPage : (long long)s.B * s.Hkv * s.S;
     if (!row_map(&tm[0], a.kc, rows, s.d, boxes, bn) || !row_map(&tm[1], a.vc, rows, s.d, boxes, bn)) return cudaErrorInvalidValue;
@@ -724,6 +749,16 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
         const cuuint64_t strides[2] = {head, s.rope ? head * s.Hq : (cuuint64_t)a.q_stride * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)s.g, (cuuint32_t)T};
         if (!make_tensor_map_bf16(&tm[4], s.rope ? a.out : const_cast<void*>(a.q), 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    // outputs, for units whose rows are bf16 and there in full: boxes of a warp's 32 rows
+    static thread_local Items items;      // 8 KB of kernel parameters: not on the stack
+    items.boxed = s.out_bf16 && 32 % s.g == 0;
+    tm[5] = tm[4];
+    if (items.boxed) {
+        const cuuint64_t dims[3] = {(cuuint64_t)s.d, (cuuint64_t)s.Hq, (cuuint64_t)(g.row0 + g.off[g.nb])};
+        const cuuint64_t strides[2] = {(cuuint64_t)s.d * 2, (cuuint64_t)s.d * 2 * s.Hq};
+        const cuuint32_t box[3] = {64, (cuuint32_t)s.g, (cuuint32_t)(32 / s.g)};
+        if (!make_tensor_map_bf16(&tm[5], a.out, 3, dims, strides, box)) return cudaErrorInvalidValue;
     }
     // longest first: an item's work is its number of key tiles.  The host's lengths order the
     // units and choose the split only; the kernel reads the cut on the device.
@@ -745,7 +780,6 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
     if (units * 2 <= h->num_sms && longest >= 2 * kSplitTiles)
         parts = std::min<long long>({h->num_sms / units, (long long)longest / kSplitTiles, (long long)s.B * s.max_splits / packed, kMaxParts,
                                      kItems / (long long)work.size()});
-    static thread_local Items items;      // 8 KB of kernel parameters: not on the stack
     items.parts = (int)std::max(1ll, parts);
     AttnArgs part = a;
     if (items.parts > 1) {
