@@ -292,14 +292,19 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * are rounded to bf16 too (relative error at most 2^-8 each; their sum is fp32); other
  * shapes run in fp32 throughout.  What a masked key or value row
  * holds, infinities and NaN among it, does not reach the result.
- * d_out must not overlap the inputs; its rows hold intermediate values during the call.
+ * d_out must not overlap the ranges that the inputs span (from their first row to their last);
+ * its rows hold intermediate values during the call.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
  * All tiers but INT8; a ring needs a bf16 cache with W a multiple of 16, and counts of at
  * most max_chunk (its rows are staged, as kvc_chunk_attn's are).
+ * A captured call appends at the device's next_position.  A replay that passes the capacity, or
+ * on a paged cache the pages mapped at capture (those of that one call), writes no row there
+ * and sets the error word that kvc_device_status reads.
  * KVC_ERR_ARG: a negative count, a count above max_chunk on a ring, T > 2^31 - 1, a stride
- * below the row, or one that is no multiple of 16 bytes where a head's row is one.
+ * below the row or of 2^38 elements, or one that is no multiple of 16 bytes where a head's
+ * row is one, or an overlap.
  * KVC_ERR_CAPACITY: as kvc_append_rows; nothing is written.  KVC_ERR_UNSUPPORTED: INT8
- * caches, other rings. */
+ * caches, other rings, more than 65534 query heads. */
 int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k, const void* d_v,
                     int64_t kv_stride, const int32_t* h_counts, void* d_out, kvc_stream_t stream);
 
@@ -316,7 +321,9 @@ int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k,
  * These calls keep books on the host (the lengths that kvc_next_positions reports and
  * the block table): they return KVC_ERR_UNSUPPORTED on a stream under capture, and a
  * handle whose captured calls were replayed has lengths on the device that the host does
- * not know. */
+ * not know.  On a paged cache a graph holds the page numbers of its capture: after any of
+ * them (but kvc_page_counts) capture anew.  All but kvc_compact and kvc_page_counts return
+ * KVC_ERR_UNSUPPORTED with more than 65534 KV heads. */
 
 /* Requests h_dst[i] become copies of requests h_src[i] (host, n entries each, of [0, B)):
  * rows, positions, next_position and, in Tier B, the request ID (a branch draws the same

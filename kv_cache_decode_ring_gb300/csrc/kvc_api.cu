@@ -511,10 +511,19 @@ int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k,
     PromptArgs a{d_q, d_k, d_v, d_out, q_stride ? q_stride : (long long)s.Hq * s.d,
                  kv_stride ? kv_stride : (long long)s.Hkv * s.d};
     if (a.q_stride < (long long)s.Hq * s.d || a.kv_stride < (long long)s.Hkv * s.d ||
+        a.q_stride >= (1LL << 38) || a.kv_stride >= (1LL << 38) ||
         (s.d * s.elem % 16 == 0 && (a.q_stride * s.elem % 16 || a.kv_stride * s.elem % 16)))
         return KVC_ERR_ARG;
     if (total == 0) return KVC_OK;
     if (!d_q || !d_k || !d_v || !d_out || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out))
+        return KVC_ERR_ARG;
+    auto overlaps_out = [&](const void* x, long long stride, long long row) {
+        const uintptr_t o = reinterpret_cast<uintptr_t>(d_out), i = reinterpret_cast<uintptr_t>(x);
+        const uintptr_t on = (uintptr_t)total * s.Hq * s.d * (s.out_bf16 ? 2 : 4), in = ((uintptr_t)(total - 1) * stride + row) * s.elem;
+        return i < o + on && o < i + in;
+    };
+    if (overlaps_out(d_q, a.q_stride, (long long)s.Hq * s.d) || overlaps_out(d_k, a.kv_stride, (long long)s.Hkv * s.d) ||
+        overlaps_out(d_v, a.kv_stride, (long long)s.Hkv * s.d))
         return KVC_ERR_ARG;
     int rc = check_capacity(h, h_counts, 0);
     if (rc) return rc;

@@ -92,6 +92,8 @@ inline int int8_grid(const Shape& s) {
     return (int)(((int8_qkeys(s) + kQBlock - 1) / kQBlock + bps - 1) / bps) + 1;
 }
 
+constexpr int kMaxGridHeads = 65534;      // heads (and one more plane) along a grid's y or z axis
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool make_shape(const kvc_config& c, Shape* s);

@@ -451,7 +451,7 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
     for (int i = 0; i < n; ++i)
         if (has_restored(h, h_src[i])) return KVC_ERR_UNSUPPORTED;
     if (n == 0) return KVC_OK;
-    if (capturing(st)) return KVC_ERR_UNSUPPORTED;
+    if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
     std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n);
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {
@@ -499,7 +499,7 @@ int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_
         if ((!s.ring && len > s.S) || (s.rope && len > s.P)) return KVC_ERR_CAPACITY;
     }
     if (n == 0) return KVC_OK;
-    if (capturing(st)) return KVC_ERR_UNSUPPORTED;
+    if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
     std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n);
     if (s.pages) {
         // the destinations give back their pages and map those that the rows need
@@ -545,7 +545,7 @@ int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream) try {
     std::vector<char> seen;
     if (!distinct(h_b, n, s.B, &seen)) return KVC_ERR_ARG;
     if (n == 0) return KVC_OK;
-    if (capturing(st)) return KVC_ERR_UNSUPPORTED;
+    if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
     std::vector<int> dst(h_b, h_b + n), none(n, -1);
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {

@@ -43,8 +43,11 @@ struct RowArgs {
     int Hq, out_head;
 };
 
-__device__ __forceinline__ bool position_ok(const RowArgs& a, long long p) {
-    return p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P);
+// Whether request b's row at p may be written: the host checked what it knows, but a captured
+// call replayed too often passes the capacity, or the pages mapped when it was captured.
+__device__ __forceinline__ bool position_ok(const RowArgs& a, int b, long long p) {
+    if (!(p >= 0 && p <= 0x7ffffffeLL && (a.ring || p < a.S) && (!a.rope || p < a.P))) return false;
+    return !a.table || __ldg(a.table + (size_t)b * (a.S / kPage) + (int)(p % a.S) / kPage) >= 0;
 }
 
 // Four pairs of a bf16 row, rotated in fp32, each product and sum rounded once.
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) prompt_pairs_kernel(const RowArgs a,
         const int c = i % per, h = (i / per) % a.Hkv, r = r0 + i / (per * a.Hkv);
         const long long p = (long long)cut + r;
         if (!a.stage && a.ring && r < n - a.S) continue;        // overwritten later in this call
-        if (!position_ok(a, p)) { atomicOr(a.hdr, kErrPosition); continue; }
+        if (!position_ok(a, b, p)) { atomicOr(a.hdr, kErrPosition); continue; }
         const int slot = a.ring ? (int)(p % a.S) : (int)p;
         const size_t crow = kv_row(a.table, b, h, slot, a.Hkv, a.S) * d;
         const size_t dst = a.stage ? stage_row(b, h, (int)p, cut, a.Hkv, a.ws_rows) * d : crow;
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) prompt_rows_kernel(const RowArgs a, 
     const int c = threadIdx.x % per, r = blockIdx.x * (kThreads / per) + threadIdx.x / per - lead;
     if (threadIdx.x / per >= kThreads / per || r >= n) return;
     const long long p = (long long)cut + r;
-    if (!position_ok(a, p)) { atomicOr(a.hdr, kErrPosition); return; }
+    if (!position_ok(a, b, p)) { atomicOr(a.hdr, kErrPosition); return; }
     float2 cs[4] = {};
     if (a.rope && r >= 0) {
         const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (d / 2) + 4 * c);
@@ -244,12 +247,16 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a,
 #pragma unroll
         for (int e = 0; e < ND; ++e) acc[r][e] = 0.f;
     }
-    for (int kb = kmin; kb <= p_last; kb += kBN) {
+    const int ntiles = p_last >= kmin ? (p_last - kmin) / kBN + 1 : 0;
+    for (int j = 0; j < ntiles; ++j) {
+        // (positions past the capacity, flagged above, have no rows to read)
+        const int kb = kmin + kBN * j, left = (a.ring ? p_last : min(p_last, a.S - 1)) - kb;
         __syncthreads();                  // the previous tile is read
         for (int i = tid; i < kBN * (d4 / 2); i += kThreads) {
-            const int r = i / (d4 / 2), c = i % (d4 / 2), key = kb + r;
+            const int r = i / (d4 / 2), c = i % (d4 / 2);
             float2 k = make_float2(0.f, 0.f), v = k;
-            if (key <= p_last && 2 * c < d) {
+            if (r <= left && 2 * c < d) {
+                const int key = kb + r;
                 const bool staged = a.ring && key >= cal;
                 const size_t src = (staged ? stage_row(b, h, key, cut, a.Hkv, a.ws_rows)
                                            : kv_row(a.table, b, h, a.ring ? key % a.S : key, a.Hkv, a.S)) * d + 2 * c;
@@ -276,7 +283,8 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a,
         bool whole = true;                // every key of the tile visible to every row of the warp
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const bool in0 = kb + lane >= lo[r] && kb + lane <= p[r], in1 = kb + lane + 32 >= lo[r] && kb + lane + 32 <= p[r];
+            const int c0 = lo[r] - kb, c1 = p[r] - kb;             // visible: keys c0 .. c1 of the tile
+            const bool in0 = lane >= c0 && lane <= c1, in1 = lane + 32 >= c0 && lane + 32 <= c1;
             whole = whole && __all_sync(0xffffffffu, in0 && in1);
             const float x0 = in0 ? s[r][0] * a.scale_log2 : -INFINITY, x1 = in1 ? s[r][1] * a.scale_log2 : -INFINITY;
             float mx = fmaxf(x0, x1);
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a,
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 // a masked key adds nothing, whatever its value row holds
-                if (!whole && (kb + c < lo[r] || kb + c > p[r])) continue;
+                if (!whole && (c < lo[r] - kb || c > p[r] - kb)) continue;
                 const float w = sP[(4 * warp + r) * kBN + c];
 #pragma unroll
                 for (int e = 0; e < ND; ++e) acc[r][e] = fmaf(w, v[e], acc[r][e]);
@@ -341,7 +349,9 @@ cudaError_t launch_attention(const AttnArgs& a, const Packed& g, int most, cudaS
 
 }  // namespace
 
-bool prompt_supported(const Shape& s) { return !s.int8 && (!s.ring || (s.bf16 && s.S % kPage == 0)); }
+bool prompt_supported(const Shape& s) {
+    return !s.int8 && s.Hq <= kMaxGridHeads && (!s.ring || (s.bf16 && s.S % kPage == 0));
+}
 
 cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* counts, cudaStream_t st) {
     const Shape& s = h->sh;
@@ -368,8 +378,8 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W; a.P = s.P; a.ring = s.ring; a.bf16 = s.bf16;
     a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
-    // the entry point checked alignment and strides (grid z: head groups)
-    const bool vec = s.bf16 && s.d % 8 == 0 && s.Hq <= 4 * 65535;
+    // the entry point checked alignment and strides
+    const bool vec = s.bf16 && s.d % 8 == 0;
     const bool tensor = prompt_tc_supported(s);
     if (tensor && s.rope) {
         r.q = p.q; r.q_stride = p.q_stride; r.Hq = s.Hq;

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::kSFree + slot]);          // the next S may overwrite it
                 const int kb = k0 + kBN * j;
-                if (!(kb >= sl && kb + kBN - 1 <= sh) || !full) {
+                if (!(kb >= sl && sh - kb >= kBN - 1) || !full) {
                     // (a word of visible keys per 16, which the compiler spreads over predicates: two
                     // comparisons a key took 3 to 6 % longer on short prompts; skipping groups that
                     // all or none of the warp's rows see costs the other tiles registers)
@@ -421,12 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (spoilt_unit && valid) {
                     // values that are not finite, left out of boundary tiles: those that the row sees are
-                    // added to what it wrote
+                    // added to what it wrote (positions past the capacity have no rows to read)
+                    const int c_last = min((a.ring ? p : min(p, a.S - 1)) - k0, nt * kBN - 1);
                     char* at = static_cast<char*>(parts ? static_cast<void*>(a.part_acc + (size_t)w.part * D) : a.out) + (orow + place[r]) * row_bytes;
 #pragma unroll 1
-                    for (int key = max(key_lo, k0); key <= min(p, k0 + nt * kBN - 1); ++key) {
-                        const int j = (key - k0) / kBN;
-                        if (j >= w0 && j < w1) { key = k0 + w1 * kBN - 1; continue; }
+                    for (int c = max(key_lo - k0, 0); c <= c_last; ++c) {
+                        const int j = c / kBN, key = k0 + c;
+                        if (j >= w0 && j < w1) { c = w1 * kBN - 1; continue; }
                         const bool staged = a.ring && key >= (w.cut & ~15);
                         const __nv_bfloat16* v = staged ? a.wv + stage_row(w.b, w.kvh, key, w.cut, a.Hkv, a.ws_rows) * D
                                                         : static_cast<const __nv_bfloat16*>(a.vc) +
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // where the lane's group of tile j lies: its page (read a tile ahead), or its first row
             auto page_of = [&](int j) {
                 return a.table && lane < kBN / 16 && j < w.nt
-                           ? __ldg(a.table + (size_t)w.b * (a.S / kPage) + (min(w.k0 + kBN * j + 16 * lane, w.p_last & ~15) / kPage) % (a.S / kPage))
+                           ? __ldg(a.table + (size_t)w.b * (a.S / kPage) + ((w.k0 + min(kBN * j + 16 * lane, (w.p_last & ~15) - w.k0)) / kPage) % (a.S / kPage))
                            : 0;
             };
             int page = page_of(0);
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int ahead = page_of(j + 1);
                 int row = head_row0 + w.k0 + kBN * j;
                 if (boxes) {
-                    const int pos = min(w.k0 + kBN * j + 16 * lane, w.p_last & ~15);
+                    const int pos = w.k0 + min(kBN * j + 16 * lane, (w.p_last & ~15) - w.k0);
                     if (a.ring && pos >= cal) row = -1 - (ws_row0 + (pos - cal));      // a staged row
                     else row = a.table ? (max(page, 0) * a.Hkv + w.kvh) * kPage : head_row0 + pos % a.S;
                 }

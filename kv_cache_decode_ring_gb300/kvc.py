@@ -605,6 +605,8 @@ class Cache:
             if t.dtype != self.torch_dtype or t.shape != (T, heads, self.d):
                 raise ValueError("%s must be %s of shape %s, got %s %s" % (name, self.torch_dtype, (T, heads, self.d), t.dtype,
                                                                            tuple(t.shape)))
+            if t.device != self.state.device:
+                raise ValueError("%s must be on %s, got %s" % (name, self.state.device, t.device))
         if out is None:
             out = torch.empty((T, self.Hq, self.d), dtype=self.out_dtype, device=q.device)
         _dev(out, self.out_dtype, (T, self.Hq, self.d), "out")

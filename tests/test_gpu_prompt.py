@@ -310,6 +310,37 @@ def test_captured_call_replays_from_the_device_positions():
         assert np.array_equal(a.cache.export(which), b.cache.export(which))
 
 
+@pytest.mark.parametrize("dtype,d,paged", [("bf16", 128, False), ("bf16", 64, True), ("bf16", 96, True), ("f32", 64, False), ("f32", 64, True)])
+def test_replays_past_the_capacity_are_reported(dtype, d, paged):
+    # the host counts a captured call once; replays that run out of rows or of mapped pages
+    # write nothing there, leave the other requests' rows alone and set the device error
+    t = Twin(dtype, 2, 4, 2, d, 64, pages=8 if paged else 0)
+    t.prefill([40, 20])
+    qkv = t.draw(12, 8).cuda()
+    q, k, v = qkv.split([4, 2, 2], 1)
+    out = torch.empty(12, 4, d, dtype=t.cache.out_dtype, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        t.cache.prompt(q, k, v, [0, 12], out)          # request 1: rows 20 .. 31, pages up to slot 31 mapped
+    g.replay()
+    assert t.cache.device_status() == 0
+    before = [x.clone() for x in t.cache.rows()]
+    replays = 4                                        # 32 .. 79: past the mapped pages, past the capacity
+    for _ in range(replays):
+        g.replay()
+    assert t.cache.device_status() == 1
+    assert t.cache.device_status() == 0            # read and cleared
+    if paged:
+        for x, y in zip(t.cache.rows(), before):
+            assert torch.equal(x, y)
+    else:
+        for x, y in zip(t.cache.rows(), before):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1, :, :32], y[1, :, :32])
+    assert list(t.cache.export(kvc.KVC_EXPORT_NEXT_POSITION)) == [40, 32 + 12 * replays]
+
+
 def test_two_handles_on_two_streams():
     ts = [Twin("bf16", 2, 8, 2, 128, 1200, out="f32") for _ in range(2)]
     qkvs = [t.draw(1500, 12).cuda() for t in ts]
@@ -368,7 +399,7 @@ def test_refusals():
     for counts in ([1], [20, 21], [1, 2, 3]):
         with pytest.raises(ValueError):
             c.prompt(q, k, v, counts)
-    for x in ((q.float(), k, v), (q[:, :3], k, v), (q.transpose(0, 1).contiguous().transpose(0, 1), k, v), (q, k[:30], v)):
+    for x in ((q.float(), k, v), (q[:, :3], k, v), (q, k.cpu(), v), (q.transpose(0, 1).contiguous().transpose(0, 1), k, v), (q, k[:30], v)):
         with pytest.raises(ValueError):
             c.prompt(*x, [1, 2])
     with pytest.raises(ValueError):
@@ -385,6 +416,18 @@ def test_refusals():
     assert list(c.next_positions()) == [0, 0] and (c.export(kvc.KVC_EXPORT_POSITIONS) == -1).all()
     odd = torch.zeros(40 * 8 * 128 + 8, dtype=torch.bfloat16, device="cuda")[1:1 + 40 * 8 * 128].view(40, 8, 128)
     refused(kvc.KVC_ERR_ARG, lambda: c.prompt(*odd.split([4, 2, 2], 1), [1, 1]))                        # 2-byte aligned
+    same = Twin("bf16", 2, 4, 2, 128, 64, out="bf16").cache
+    buf = torch.zeros(40, 12, 128, dtype=torch.bfloat16, device="cuda")
+    spare = torch.zeros(80, 4, 128, dtype=torch.bfloat16, device="cuda")
+    for x, out in ((buf[:, :8].split([4, 2, 2], 1), buf.view(-1)[8 * 128:][:40 * 4 * 128].view(40, 4, 128)),   # between its rows
+                   ((q, k, v), q), ((q, spare.view(160, 2, 128)[2:42], v), spare[:40])):
+        refused(kvc.KVC_ERR_ARG, lambda: same.prompt(*x, [2, 3], out))
+    one = kvc._ints([1, 0])
+    refused(kvc.KVC_ERR_ARG, lambda: kvc._check(kvc.lib().kvc_prompt_attn(
+        c.h, q.data_ptr(), 1 << 38, k.data_ptr(), v.data_ptr(), 0, kvc._at(one), buf.data_ptr(), 0), "stride"))
+    wide = kvc.Cache(kvc.make_config("f32", "contiguous", None, 1, 70000, 70000, 2, 16))
+    refused(kvc.KVC_ERR_UNSUPPORTED, lambda: wide.prompt(*(torch.zeros(1, 70000, 2, device="cuda") for _ in range(3)), [1]))
+    refused(kvc.KVC_ERR_UNSUPPORTED, lambda: wide.free([0]))
     c.prompt(q, k, v, [0, 0])                                                                            # nothing to do
     int8 = kvc.Cache(kvc.make_config("bf16", "contiguous", "int8", 2, 4, 2, 128, 64))
     refused(kvc.KVC_ERR_UNSUPPORTED, lambda: int8.prompt(q, k, v, [1, 1]))
