@@ -284,14 +284,15 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * entries); the rows lie packed, request after request, T = the sum of the counts in all:
  *     d_q [T][Hq][d], d_k, d_v [T][Hkv][d]  ->  d_out [T][Hq][d].
  * q_stride and kv_stride are the elements from one packed row to the next (0 = dense, Hq d
- * and Hkv d), so that the three may be views of one projection's output; the heads of a
- * row are dense.  Appends every row as kvc_append_rows does and answers row i of request b
- * at p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32
- * and rounded to the cache's type, as the keys are; sums and softmax are fp32.
- * bf16 caches with head_dim 64 or 128 run on the tensor cores, where the softmax weights
- * are rounded to bf16 too (relative error at most 2^-8 each; their sum is fp32); other
- * shapes run in fp32 throughout.  What a masked key or value row
- * holds, infinities and NaN among it, does not reach the result.
+ * and Hkv d), so that the three may be views of one projection's output (aligned to an
+ * element where a head's row is no multiple of 16 bytes); the heads of a row are dense.
+ * Appends every row as kvc_append_rows does and answers row i of request b at
+ * p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32 and
+ * rounded to the cache's type, as the keys are; sums and softmax are fp32.  bf16 caches with
+ * head_dim 64 or 128 run on the tensor cores, where the softmax weights are rounded to bf16
+ * too (relative error at most 2^-8 each; their sum is fp32); other shapes run in fp32
+ * throughout.  What a masked key or value row holds, infinities and NaN among it, does not
+ * reach the result.
  * d_out must not overlap the ranges that the inputs span (from their first row to their last);
  * its rows hold intermediate values during the call.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.

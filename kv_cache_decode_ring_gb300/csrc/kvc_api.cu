@@ -515,8 +515,9 @@ int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k,
         (s.d * s.elem % 16 == 0 && (a.q_stride * s.elem % 16 || a.kv_stride * s.elem % 16)))
         return KVC_ERR_ARG;
     if (total == 0) return KVC_OK;
-    if (!d_q || !d_k || !d_v || !d_out || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out))
-        return KVC_ERR_ARG;
+    // (rows that are no multiple of 16 bytes are read by elements)
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(d_q) | reinterpret_cast<uintptr_t>(d_k) | reinterpret_cast<uintptr_t>(d_v);
+    if (!d_q || !d_k || !d_v || !d_out || !aligned16(d_out) || bits % (s.d * s.elem % 16 ? s.elem : 16)) return KVC_ERR_ARG;
     auto overlaps_out = [&](const void* x, long long stride, long long row) {
         const uintptr_t o = reinterpret_cast<uintptr_t>(d_out), i = reinterpret_cast<uintptr_t>(x);
         const uintptr_t on = (uintptr_t)total * s.Hq * s.d * (s.out_bf16 ? 2 : 4), in = ((uintptr_t)(total - 1) * stride + row) * s.elem;

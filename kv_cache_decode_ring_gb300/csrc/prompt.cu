@@ -187,34 +187,139 @@ __global__ void prompt_advance_kernel(int32_t* next_pos, const __grid_constant__
     if (i < g.nb) next_pos[g.b0 + i] += g.off[i + 1] - g.off[i];
 }
 
+// Joins the parts of split keys: a warp per (row, head); lanes over the dims.
+__global__ void __launch_bounds__(256) prompt_join_kernel(const AttnArgs a, long long row0, long long rows) {
+    dep_wait();
+    dep_release();
+    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5), at = row0 + i;
+    const int lane = threadIdx.x & 31;
+    if (i >= rows) return;
+    const float2* ml = a.part_ml + at * a.parts;
+    float m = -INFINITY;
+    for (int q = 0; q < a.parts; ++q) m = fmaxf(m, ml[q].x);
+    float l = 0.f, o[8] = {};
+    for (int q = 0; q < a.parts; ++q) {
+        const float2 x = ml[q];
+        if (x.y == 0.f) continue;                     // the part holds no key that the row sees
+        const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - m);    // (no finite score: its sum is not a number)
+        l += f * x.y;
+        const float* acc = a.part_acc + (at * a.parts + q) * a.d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (32 * e + lane < a.d) o[e] += f * acc[32 * e + lane];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int x = 32 * e + lane;
+        if (x >= a.d) continue;
+        const float v = o[e] / l;
+        if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at * a.d + x] = __float2bfloat16_rn(v);
+        else static_cast<float*>(a.out)[at * a.d + x] = v;
+    }
+}
+
 // ---- attention on the CUDA cores: fp32 caches and other head sizes ------------------
-// CTA = 32 query rows (token, head) of one (request, KV head); 8 warps of 4 rows.  Tiles of
-// 64 keys in shared memory as fp32; lane = key for the scores, lane = dim for P.V; the
-// running maximum and sum of a row live in its warp.  Everything in fp32.
-constexpr int kBM = 32, kBN = 64;
+// CTA = 8 R query rows (token, head) of one (request, KV head); 8 warps of R rows.  Tiles of 64
+// keys in shared memory as fp32; a lane scores two keys, then holds a run of the output's
+// dims; the running maximum and sum of a row live in its warp.  Everything in fp32.
+// Bound by what shared memory returns to registers, 4 cycles a 16-byte load of a warp: with
+// R = 8, 10 loads feed 64 products of each lane in the scores and 12 feed 128 in P.V (products:
+// 16 and 32 cycles); with R = 4 6 feed 32 and 8 feed 64.  So R = 8 wherever CTAs of
+// 64 rows fill the SMs.  Half warps of 8 x 4 and 8 x 8 products a lane load less, but with half
+// the warps they took longer: 1090 against 950 us (4 requests of 2000 rows, 8 fp32 heads of
+// 128: 35 TFLOP/s), where one CTA after the other and no loads ahead took 2050.
+// The next tile's keys are copied while the values of this one are used, its values while the
+// next scores are.  CTAs start in the order of the keys that they see, most first (1130 -> 950).
+constexpr int kBN = 64;
 
-__host__ __device__ constexpr int padded(int d) { return ((d + 3) & ~3) + 4; }
-__host__ __device__ constexpr size_t simt_smem(int d) { return ((size_t)(kBM + 2 * kBN) * padded(d) + kBM * kBN) * 4; }
+__host__ __device__ constexpr int round4(int d) { return (d + 3) & ~3; }
+// keys: rows of an odd number of 16-byte units, so that 8 lanes read 8 rows without conflicts
+__host__ __device__ constexpr int key_step(int d) { return round4(d) / 4 % 2 ? round4(d) : round4(d) + 4; }
+__host__ __device__ constexpr size_t simt_smem(int d, int R) {
+    return ((size_t)(8 * R + kBN) * round4(d) + (size_t)kBN * key_step(d) + 8 * R * kBN) * 4;
+}
 
-// ND = ceil(d / 32)
-template <int ND>
-__global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a, const __grid_constant__ Packed g) {
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+    const int n = there ? 16 : 0;                     // 0: zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(n) : "memory");
+}
+
+enum { kLoadPairs, kLoadAsync, kLoadWide };           // rows of pairs; fp32 rows of 16-byte units; bf16 ones
+
+// DIMS: 64 (head_dim up to it), 128 or 256.
+template <int DIMS, int R, int LOAD>
+__global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_kernel(const AttnArgs a, const __grid_constant__ Packed g) {
+    constexpr int kBM = 8 * R, VW = DIMS == 64 ? 2 : 4, NV = DIMS == 256 ? 2 : 1;      // a lane's dims: NV runs of VW
     extern __shared__ float4 smem4[];
     dep_wait();
     dep_release();
-    const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y;
+    const int bi = blockIdx.x / a.Hkv, b = g.b0 + bi, h = blockIdx.x % a.Hkv;
     const int n = g.off[bi + 1] - g.off[bi];
-    const long long all = (long long)n * a.g, row0 = (long long)blockIdx.x * kBM;
-    if (row0 >= all) return;
-    const int d = a.d, dp = padded(d), d4 = dp - 4;
+    // the rows that see most keys first (of all requests); their keys in parts
+    const int part = (int)blockIdx.y % a.parts;
+    const long long at_tile = (long long)blockIdx.z * (gridDim.y / a.parts) + blockIdx.y / a.parts;
+    const long long all = (long long)n * a.g, row0 = ((all + kBM - 1) / kBM - 1 - at_tile) * kBM;
+    if (row0 < 0) return;
+    const int d = a.d, d4 = round4(d), kp = key_step(d);
     float* sQ = reinterpret_cast<float*>(smem4);
-    float* sK = sQ + kBM * dp;
-    float* sV = sK + kBN * dp;
-    float* sP = sV + kBN * dp;
+    float* sK = sQ + kBM * d4;
+    float* sV = sK + kBN * kp;
+    float* sP = sV + kBN * d4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cut = a.next_pos[b];
     const int nrow = (int)min((long long)kBM, all - row0);
+    const int p_first = cut + (int)(row0 / a.g), p_last = cut + (int)((row0 + nrow - 1) / a.g);
+    const int kmin = a.W > 0 ? max(0, p_first - a.W + 1) : 0;
+    const int cal = cut & ~15;
+    const int tiles = p_last >= kmin ? (p_last - kmin) / kBN + 1 : 0;
+    const int j0 = (int)((long long)tiles * part / a.parts), ntiles = (int)((long long)tiles * (part + 1) / a.parts);
+
+    // rows of tile j into shared memory (what: 0 keys, 1 values), eight lanes a row
+    auto fill = [&](int j, int what) {
+        // (positions past the capacity, flagged before, have no rows to read)
+        const int kb = kmin + kBN * j, left = (a.ring ? p_last : min(p_last, a.S - 1)) - kb;
+        float* dst = what ? sV : sK;
+        const int step = what ? d4 : kp;
+#pragma unroll
+        for (int half = 0; half < kBN / 32; ++half) {
+            const int r = 32 * half + tid / 8, c0 = tid % 8, key = kb + r;
+            const bool there = r <= left, staged = there && a.ring && key >= cal;
+            const size_t row = !there ? 0 : (staged ? stage_row(b, h, key, cut, a.Hkv, a.ws_rows)
+                                                    : kv_row(a.table, b, h, a.ring ? key % a.S : key, a.Hkv, a.S)) * d;
+            const void* src = staged ? (what ? static_cast<const void*>(a.wv) : a.wk) : (what ? a.vc : a.kc);
+            if constexpr (LOAD == kLoadAsync) {
+                const float* x = static_cast<const float*>(src) + row;
+#pragma unroll 8
+                for (int c = c0; c < d / 4; c += 8) copy16(dst + r * step + 4 * c, x + 4 * c, there);
+            } else if constexpr (LOAD == kLoadWide) {
+                const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(src) + row);
+#pragma unroll 4
+                for (int c = c0; c < d / 8; c += 8) {
+                    const uint4 u = there ? x[c] : make_uint4(0, 0, 0, 0);
+                    float4* y = reinterpret_cast<float4*>(dst + r * step + 8 * c);
+                    y[0] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                    y[1] = make_float4(__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u),
+                                       __uint_as_float(u.w << 16), __uint_as_float(u.w & 0xffff0000u));
+                }
+            } else {
+#pragma unroll 4
+                for (int c = c0; c < d4 / 2; c += 8) {
+                    const bool in = there && 2 * c < d;
+                    *reinterpret_cast<float2*>(dst + r * step + 2 * c) =
+                        in ? make_float2(ld_elem(src, row + 2 * c, a.bf16), ld_elem(src, row + 2 * c + 1, a.bf16)) : make_float2(0.f, 0.f);
+                }
+            }
+        }
+    };
+    auto landed = [&]() {
+        if constexpr (LOAD == kLoadAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    };
+
+    if (j0 < ntiles) fill(j0, 0);
     // queries, rotated and rounded to the cache's type
+#pragma unroll 4
     for (int i = tid; i < kBM * (d4 / 2); i += kThreads) {
         const int r = i / (d4 / 2), c = i % (d4 / 2);
         float y0 = 0.f, y1 = 0.f;
@@ -227,127 +332,176 @@ __global__ void __launch_bounds__(kThreads) prompt_simt_kernel(const AttnArgs a,
             if (a.rope && p < a.P) rope_pair(x0, x1, a.rope[(size_t)p * (d / 2) + c], y0, y1);
             if (a.bf16) { y0 = __bfloat162float(__float2bfloat16_rn(y0)); y1 = __bfloat162float(__float2bfloat16_rn(y1)); }
         }
-        sQ[r * dp + 2 * c] = y0;
-        sQ[r * dp + 2 * c + 1] = y1;
+        *reinterpret_cast<float2*>(sQ + r * d4 + 2 * c) = make_float2(y0, y1);
     }
-    int p[4], lo[4];                      // the warp's rows: positions and first visible keys (p = -1: no row)
+    // the warp's rows: positions relative to kmin (-1: no row) and first visible keys
+    int p[R], lo[R];
+    float m[R], l[R];
+    float2 acc[R][NV * VW / 2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int rr = 4 * warp + r;
-        p[r] = rr < nrow ? cut + (int)((row0 + rr) / a.g) : -1;
-        lo[r] = a.W > 0 ? max(0, p[r] - a.W + 1) : 0;
-    }
-    const int p_first = cut + (int)(row0 / a.g), p_last = cut + (int)((row0 + nrow - 1) / a.g);
-    const int kmin = a.W > 0 ? max(0, p_first - a.W + 1) : 0;
-    const int cal = cut & ~15;
-    float m[4], l[4], acc[4][ND];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
+        const int rr = R * warp + r, at = cut + (int)((row0 + rr) / a.g);
+        p[r] = rr < nrow ? at - kmin : -1;
+        lo[r] = a.W > 0 ? max(0, at - a.W + 1) - kmin : 0;
         m[r] = -INFINITY; l[r] = 0.f;
 #pragma unroll
-        for (int e = 0; e < ND; ++e) acc[r][e] = 0.f;
+        for (int e = 0; e < NV * VW / 2; ++e) acc[r][e] = make_float2(0.f, 0.f);
     }
-    const int ntiles = p_last >= kmin ? (p_last - kmin) / kBN + 1 : 0;
-    for (int j = 0; j < ntiles; ++j) {
-        // (positions past the capacity, flagged above, have no rows to read)
-        const int kb = kmin + kBN * j, left = (a.ring ? p_last : min(p_last, a.S - 1)) - kb;
-        __syncthreads();                  // the previous tile is read
-        for (int i = tid; i < kBN * (d4 / 2); i += kThreads) {
-            const int r = i / (d4 / 2), c = i % (d4 / 2);
-            float2 k = make_float2(0.f, 0.f), v = k;
-            if (r <= left && 2 * c < d) {
-                const int key = kb + r;
-                const bool staged = a.ring && key >= cal;
-                const size_t src = (staged ? stage_row(b, h, key, cut, a.Hkv, a.ws_rows)
-                                           : kv_row(a.table, b, h, a.ring ? key % a.S : key, a.Hkv, a.S)) * d + 2 * c;
-                const void* K = staged ? static_cast<const void*>(a.wk) : a.kc;
-                const void* V = staged ? static_cast<const void*>(a.wv) : a.vc;
-                k = make_float2(ld_elem(K, src, a.bf16), ld_elem(K, src + 1, a.bf16));
-                v = make_float2(ld_elem(V, src, a.bf16), ld_elem(V, src + 1, a.bf16));
-            }
-            *reinterpret_cast<float2*>(sK + r * dp + 2 * c) = k;
-            *reinterpret_cast<float2*>(sV + r * dp + 2 * c) = v;
-        }
-        __syncthreads();
-        float s[4][2] = {};
-        for (int c = 0; c < d4; c += 4) {
-            const float4 k0 = *reinterpret_cast<const float4*>(sK + lane * dp + c);
-            const float4 k1 = *reinterpret_cast<const float4*>(sK + (lane + 32) * dp + c);
+    float* myP = sP + R * warp * kBN;
+    for (int j = j0; j < ntiles; ++j) {
+        landed();                         // keys of this tile; the values before are used
+        fill(j, 1);
+        float2 s2[R][2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 q = *reinterpret_cast<const float4*>(sQ + (4 * warp + r) * dp + c);
-                s[r][0] = fmaf(q.w, k0.w, fmaf(q.z, k0.z, fmaf(q.y, k0.y, fmaf(q.x, k0.x, s[r][0]))));
-                s[r][1] = fmaf(q.w, k1.w, fmaf(q.z, k1.z, fmaf(q.y, k1.y, fmaf(q.x, k1.x, s[r][1]))));
+        for (int r = 0; r < R; ++r) s2[r][0] = s2[r][1] = make_float2(0.f, 0.f);
+#pragma unroll 2
+        for (int c = 0; c < d4; c += 4) {
+            const float4 k0 = *reinterpret_cast<const float4*>(sK + lane * kp + c);
+            const float4 k1 = *reinterpret_cast<const float4*>(sK + (lane + 32) * kp + c);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(sQ + (R * warp + r) * d4 + c);
+                s2[r][0] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k0.x, k0.y), s2[r][0]);
+                s2[r][1] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k1.x, k1.y), s2[r][1]);
+                s2[r][0] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k0.z, k0.w), s2[r][0]);
+                s2[r][1] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k1.z, k1.w), s2[r][1]);
             }
         }
+        const int kb = kBN * j;           // (relative to kmin)
         bool whole = true;                // every key of the tile visible to every row of the warp
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < R; ++r) {
             const int c0 = lo[r] - kb, c1 = p[r] - kb;             // visible: keys c0 .. c1 of the tile
             const bool in0 = lane >= c0 && lane <= c1, in1 = lane + 32 >= c0 && lane + 32 <= c1;
-            whole = whole && __all_sync(0xffffffffu, in0 && in1);
-            const float x0 = in0 ? s[r][0] * a.scale_log2 : -INFINITY, x1 = in1 ? s[r][1] * a.scale_log2 : -INFINITY;
+            whole = whole && c0 <= 0 && c1 >= kBN - 1;
+            const float x0 = in0 ? (s2[r][0].x + s2[r][0].y) * a.scale_log2 : -INFINITY;
+            const float x1 = in1 ? (s2[r][1].x + s2[r][1].y) * a.scale_log2 : -INFINITY;
             float mx = fmaxf(x0, x1);
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             mx = fmaxf(mx, m[r]);
             const float base = mx == -INFINITY ? 0.f : mx;        // nothing visible so far: every weight 0
             const float alpha = exp2f(m[r] - base), w0 = exp2f(x0 - base), w1 = exp2f(x1 - base);
             m[r] = mx;
-            float sum = w0 + w1;
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l[r] = l[r] * alpha + sum;
+            l[r] = l[r] * alpha + (w0 + w1);                      // the lane's keys; joined at the end
 #pragma unroll
-            for (int e = 0; e < ND; ++e) acc[r][e] *= alpha;
-            sP[(4 * warp + r) * kBN + lane] = w0;
-            sP[(4 * warp + r) * kBN + lane + 32] = w1;
+            for (int e = 0; e < NV * VW / 2; ++e) acc[r][e] = make_float2(acc[r][e].x * alpha, acc[r][e].y * alpha);
+            myP[r * kBN + lane] = w0;
+            myP[r * kBN + lane + 32] = w1;
         }
-        __syncwarp();
-        for (int c = 0; c < kBN; ++c) {
-            float v[ND];
+        landed();                         // values of this tile; its keys are used
+        if (j + 1 < ntiles) fill(j + 1, 0);
+        auto weigh = [&](int c, bool all_seen) {
 #pragma unroll
-            for (int e = 0; e < ND; ++e) v[e] = 32 * e + lane < d ? sV[c * dp + 32 * e + lane] : 0.f;
+            for (int v = 0; v < NV; ++v) {
+                const int x = VW * (32 * v + lane);
+                if (x >= d4) continue;
+                float2 w4[4][VW / 2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                // a masked key adds nothing, whatever its value row holds
-                if (!whole && (c < lo[r] - kb || c > p[r] - kb)) continue;
-                const float w = sP[(4 * warp + r) * kBN + c];
+                for (int e = 0; e < 4; ++e)
+                    if constexpr (VW == 2) {
+                        w4[e][0] = *reinterpret_cast<const float2*>(sV + (c + e) * d4 + x);
+                    } else {
+                        const float4 y = *reinterpret_cast<const float4*>(sV + (c + e) * d4 + x);
+                        w4[e][0] = make_float2(y.x, y.y); w4[e][VW / 2 - 1] = make_float2(y.z, y.w);
+                    }
 #pragma unroll
-                for (int e = 0; e < ND; ++e) acc[r][e] = fmaf(w, v[e], acc[r][e]);
+                for (int r = 0; r < R; ++r) {
+                    const float4 w = *reinterpret_cast<const float4*>(myP + r * kBN + c);
+                    const float we[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // a masked key adds nothing, whatever its value row holds
+                        if (!all_seen && (kb + c + e < lo[r] || kb + c + e > p[r])) continue;
+#pragma unroll
+                        for (int q = 0; q < VW / 2; ++q)
+                            acc[r][v * VW / 2 + q] = __ffma2_rn(make_float2(we[e], we[e]), w4[e][q], acc[r][v * VW / 2 + q]);
+                    }
+                }
             }
+        };
+        if (whole) {
+#pragma unroll 2
+            for (int c = 0; c < kBN; c += 4) weigh(c, true);
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < kBN; c += 4) weigh(c, false);
         }
-        __syncwarp();
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
+        float sum = l[r];
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (p[r] < 0) continue;
-        const int rr = 4 * warp + r, hq = h * a.g + (int)((row0 + rr) % a.g);
-        const size_t at = ((size_t)(g.row0 + g.off[bi] + (p[r] - cut)) * a.Hq + hq) * d;
+        const int rr = R * warp + r, t = (int)((row0 + rr) / a.g), hq = h * a.g + (int)((row0 + rr) % a.g);
+        const size_t row = (size_t)(g.row0 + g.off[bi] + t) * a.Hq + hq, at = row * d;
+        if (a.parts > 1 && lane == 0) a.part_ml[row * a.parts + part] = make_float2(m[r], sum);
 #pragma unroll
-        for (int e = 0; e < ND; ++e) {
-            const int x = 32 * e + lane;
+        for (int e = 0; e < NV * VW; ++e) {
+            const int x = VW * (32 * (e / VW) + lane) + e % VW;
             if (x >= d) continue;
-            const float o = acc[r][e] / l[r];
-            if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at + x] = __float2bfloat16_rn(o);
+            const float y = e % 2 ? acc[r][e / 2].y : acc[r][e / 2].x, o = y / sum;
+            if (a.parts > 1) a.part_acc[(row * a.parts + part) * d + x] = y;        // unnormalised, to be joined
+            else if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at + x] = __float2bfloat16_rn(o);
             else static_cast<float*>(a.out)[at + x] = o;
         }
     }
 }
 
-template <int ND>
-cudaError_t launch_simt(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
-    auto kernel = prompt_simt_kernel<ND>;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), simt_smem(32 * ND))) return e;
-    const dim3 grid((unsigned)(((long long)most * a.g + kBM - 1) / kBM), a.Hkv, g.nb);
-    return launch_dep(kernel, grid, dim3(kThreads), simt_smem(a.d), st, a, g);
+template <int DIMS, int R, int LOAD>
+cudaError_t launch_rows(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
+    auto kernel = prompt_simt_kernel<DIMS, R, LOAD>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), simt_smem(DIMS, R))) return e;
+    const long long tiles = ((long long)most * a.g + 8 * R - 1) / (8 * R), per = std::min<long long>(tiles, 65535 / a.parts);
+    const dim3 grid((unsigned)(a.Hkv * g.nb), (unsigned)(per * a.parts), (unsigned)((tiles + per - 1) / per));
+    return launch_dep(kernel, grid, dim3(kThreads), simt_smem(a.d, R), st, a, g);
 }
 
-cudaError_t launch_attention(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
-    if (a.d <= 64) return launch_simt<2>(a, g, most, st);
-    if (a.d <= 128) return launch_simt<4>(a, g, most, st);
-    return launch_simt<8>(a, g, most, st);
+template <int DIMS>
+cudaError_t launch_simt(const AttnArgs& a, const Packed& g, int most, bool tall, cudaStream_t st) {
+    const int load = a.bf16 ? (a.d % 8 == 0 ? kLoadWide : kLoadPairs) : (a.d % 4 == 0 ? kLoadAsync : kLoadPairs);
+    switch (load) {
+        case kLoadAsync: return tall ? launch_rows<DIMS, 8, kLoadAsync>(a, g, most, st) : launch_rows<DIMS, 4, kLoadAsync>(a, g, most, st);
+        case kLoadWide: return tall ? launch_rows<DIMS, 8, kLoadWide>(a, g, most, st) : launch_rows<DIMS, 4, kLoadWide>(a, g, most, st);
+        default: return launch_rows<DIMS, 4, kLoadPairs>(a, g, most, st);
+    }
+}
+
+cudaError_t launch_attention(const kvc_handle* h, const AttnArgs& args, const Packed& g, int most, cudaStream_t st) {
+    AttnArgs a = args;
+    // CTAs of 64 rows where they fill the SMs, else of 32 (two requests of 1000 rows, 8 heads of
+    // 256: 347 against 410 us).  Few CTAs split their keys, two tiles each at least (a row behind
+    // 2000 keys: 161 -> 31 us), as far as the workspace of the decode's split reaches.  The
+    // host's lengths choose the shape and the split only.
+    long long ctas[2] = {0, 0}, seen = 0;
+    for (int i = 0; i < g.nb; ++i) {
+        const long long n = g.off[i + 1] - g.off[i];
+        for (int t = 0; t < 2; ++t) ctas[t] += (n * a.g + 32 * t + 31) / (32 * t + 32) * a.Hkv;
+        if (n > 0) seen = std::max(seen, h->np[g.b0 + i] + n);
+    }
+    const bool tall = ctas[1] >= h->num_sms;
+    const long long longest = (a.W > 0 ? std::min(seen, (long long)a.W + 64) : seen) / kBN + 1;
+    const long long room = (long long)h->sh.B * h->sh.max_splits / g.off[g.nb];
+    a.parts = (int)std::max(1ll, std::min({2 * h->num_sms / ctas[tall], longest / 2, room, (long long)kMaxKeyParts}));
+    if (a.parts > 1) split_workspace(h, g, a.parts, &a);
+    const cudaError_t e = a.d <= 64    ? launch_simt<64>(a, g, most, tall, st)
+                          : a.d <= 128 ? launch_simt<128>(a, g, most, tall, st)
+                                       : launch_simt<256>(a, g, most, tall, st);
+    return e == cudaSuccess && a.parts > 1 ? launch_join(a, g, st) : e;
 }
 
 }  // namespace
+
+void split_workspace(const kvc_handle* h, const Packed& g, int parts, AttnArgs* a) {
+    a->parts = parts;
+    const long long first = g.row0 * a->Hq * parts;
+    a->part_ml = reinterpret_cast<float2*>(h->state + h->L.part_ml) - first;
+    a->part_acc = reinterpret_cast<float*>(h->state + h->L.part_acc) - first * a->d;
+}
+
+cudaError_t launch_join(const AttnArgs& a, const Packed& g, cudaStream_t st) {
+    const long long rows = (long long)g.off[g.nb] * a.Hq;
+    return launch_dep(prompt_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, a, g.row0 * a.Hq, rows);
+}
 
 bool prompt_supported(const Shape& s) {
     return !s.int8 && s.Hq <= kMaxGridHeads && (!s.ring || (s.bf16 && s.S % kPage == 0));
@@ -377,6 +531,7 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.hdr = r.hdr;
     a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W; a.P = s.P; a.ring = s.ring; a.bf16 = s.bf16;
     a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
+    a.parts = 1;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     // the entry point checked alignment and strides
     const bool vec = s.bf16 && s.d % 8 == 0;
@@ -409,7 +564,7 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
             return launch_dep(vec ? prompt_rows_kernel : prompt_pairs_kernel, grid, dim3(kThreads), 0, st, r, g);
         };
         if ((e = rows(s.ring ? 1 : 0)) != cudaSuccess) return e;
-        e = tensor ? launch_prompt_tc(h, a, g, st) : launch_attention(a, g, most, st);
+        e = tensor ? launch_prompt_tc(h, a, g, st) : launch_attention(h, a, g, most, st);
         if (e != cudaSuccess) return e;
         if (s.ring) {
             r.q = nullptr;                                // d_out holds the output by now

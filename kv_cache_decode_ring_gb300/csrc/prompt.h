@@ -27,6 +27,7 @@ struct AttnArgs {
     float2* part_ml;                      // split keys: {maximum (log2 domain), sum} and unnormalised sums
     float* part_acc;                      // of [packed row][Hq][part]
     int Hq, Hkv, g, d, S, W, P, ring, bf16, out_bf16, ws_rows;
+    int parts;                            // 1: no split
     float scale_log2;                     // log2(e) / sqrt(d)
 };
 
@@ -34,6 +35,13 @@ struct AttnArgs {
 __device__ __forceinline__ size_t stage_row(int b, int h, int p, int cut, int Hkv, int ws_rows) {
     return ((size_t)b * Hkv + h) * ws_rows + (p - (cut & ~15));
 }
+
+constexpr int kMaxKeyParts = 32;             // parts that a request's keys are split into
+
+// The split's workspace in the state (rows of this group only: they are packed from 0 in it) as
+// the attention kernels address it, by packed row, and the kernel that joins the parts.
+void split_workspace(const kvc_handle* h, const Packed& g, int parts, AttnArgs* a);
+cudaError_t launch_join(const AttnArgs& a, const Packed& g, cudaStream_t st);
 
 // Tensor-core attention (prompt_tc.cu): bf16, d = 64 or 128.  `rows` of the cache (of the
 // staging area) are addressed with 32-bit coordinates.

@@ -59,7 +59,6 @@ constexpr int kRegLaunch = 128;
 constexpr int kItems = 512;         // items (a tile of rows of a request, a part of its keys) per launch
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAhead = 8;           // units whose descriptions are kept in shared memory
-constexpr int kMaxParts = 32;       // parts that a unit's keys are split into
 constexpr int kSplitTiles = 4;      // ... of no fewer tiles than this
 
 struct Items {
@@ -660,33 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of split keys: a warp per (row, head); lanes over the dims.
-__global__ void __launch_bounds__(256) prompt_join_kernel(const AttnArgs a, long long rows, int parts) {
-    dep_wait();
-    dep_release();
-    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (at >= rows) return;
-    const float2* ml = a.part_ml + at * parts;
-    float m = -INFINITY;
-    for (int q = 0; q < parts; ++q) m = fmaxf(m, ml[q].x);
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const int per = a.d / 32;
-    for (int q = 0; q < parts; ++q) {
-        const float2 x = ml[q];
-        if (x.y == 0.f) continue;                     // the part holds no key that the row sees
-        const float f = x.x == -INFINITY ? 1.f : ex2(x.x - m);      // (no finite score: its sum is not a number)
-        l += f * x.y;
-        const float* acc = a.part_acc + (at * parts + q) * a.d + lane * per;
-        for (int e = 0; e < per; ++e) o[e] += f * acc[e];
-    }
-    for (int e = 0; e < per; ++e) {
-        const float v = o[e] / l;
-        if (a.out_bf16) static_cast<__nv_bfloat16*>(a.out)[at * a.d + lane * per + e] = __float2bfloat16_rn(v);
-        else static_cast<float*>(a.out)[at * a.d + lane * per + e] = v;
-    }
-}
-
 // Tensor map over `rows` rows of d bf16 values, 128-byte swizzle.  Boxes of `bn` rows by 64 dims;
 // or, with `boxes`, of 16 rows and all dims in the order [8 rows][half]: dims (64 of a half, row
 // of 8, half, 8-row group), so that one copy brings a page's rows of a head.
@@ -779,15 +751,11 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
     const int longest = work.empty() ? 0 : -work[0].first;
     long long parts = 1;
     if (units * 2 <= h->num_sms && longest >= 2 * kSplitTiles)
-        parts = std::min<long long>({h->num_sms / units, (long long)longest / kSplitTiles, (long long)s.B * s.max_splits / packed, kMaxParts,
+        parts = std::min<long long>({h->num_sms / units, (long long)longest / kSplitTiles, (long long)s.B * s.max_splits / packed, kMaxKeyParts,
                                      kItems / (long long)work.size()});
     items.parts = (int)std::max(1ll, parts);
     AttnArgs part = a;
-    if (items.parts > 1) {
-        // (the split workspace is addressed by packed row within the group)
-        part.part_ml = reinterpret_cast<float2*>(h->state + h->L.part_ml) - g.row0 * s.Hq * items.parts;
-        part.part_acc = reinterpret_cast<float*>(h->state + h->L.part_acc) - g.row0 * s.Hq * items.parts * s.d;
-    }
+    if (items.parts > 1) split_workspace(h, g, items.parts, &part);
     const size_t per = kItems / items.parts;
     for (size_t i0 = 0; i0 < work.size(); i0 += per) {
         const int m = (int)std::min<size_t>(per, work.size() - i0);
@@ -800,13 +768,7 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
         const cudaError_t e = s.d == 128 ? launch<128>(tm, part, g.b0, items, h->num_sms, st) : launch<64>(tm, part, g.b0, items, h->num_sms, st);
         if (e != cudaSuccess) return e;
     }
-    if (items.parts > 1) {
-        const long long rows_out = packed * s.Hq;
-        part.part_ml += g.row0 * s.Hq * items.parts;
-        part.part_acc += g.row0 * s.Hq * items.parts * s.d;
-        part.out = static_cast<char*>(a.out) + (size_t)g.row0 * s.Hq * s.d * (s.out_bf16 ? 2 : 4);
-        return launch_dep(prompt_join_kernel, dim3((unsigned)((rows_out + 7) / 8)), dim3(256), 0, st, part, rows_out, items.parts);
-    }
+    if (items.parts > 1) return launch_join(part, g, st);
     return cudaSuccess;
 }
 

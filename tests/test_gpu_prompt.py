@@ -384,6 +384,18 @@ def test_few_rows_behind_long_prefixes(Hq, Hkv, d, layout, window, paged):
     t.check_state()
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 128), ("f32", 6), ("f32", 80), ("f32", 256), ("bf16", 96), ("bf16", 250)])
+@pytest.mark.parametrize("window,paged", [(0, False), (0, True), (900, False)])
+def test_few_rows_behind_long_prefixes_on_the_cuda_cores(dtype, d, window, paged):
+    # as above, and calls of many rows, whose keys are not split
+    cap = 1504
+    t = Twin(dtype, 3, 4, 1, d, cap, window=window, pages=3 * cap // 16 if paged else 0, max_position=4000)
+    t.prefill([1300, 0, 257])
+    for counts in ([1, 1, 1], [0, 1, 0], [9, 0, 3], [90, 64, 1], [1, 0, 40]):
+        t.prompt(counts)
+    t.check_state()
+
+
 def test_more_requests_than_one_launch_holds():
     B = 1100
     t = Twin("bf16", B, 2, 1, 64, 16, base=0.0, out="f32")
