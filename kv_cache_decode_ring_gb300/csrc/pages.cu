@@ -67,22 +67,30 @@ struct Part {
     long long bytes;
 };
 
+// Page `to` takes the bytes of page `from` (< 0: none); table entry `entry` (< 0: none) names it.
+struct Move {
+    int entry, from, to;
+};
+
 template <int N>
 struct Moves {
     Part part[kMaxParts];
+    int32_t* table;
     int parts, Hkv;
-    int2 e[N];                            // (from, to) physical pages
+    Move e[N];
 };
 
-// grid (page pairs, parts); a page is Hkv * bytes contiguous bytes of each part.  The pages
-// written are disjoint from the pages read.
+// grid (moves, parts); a page is Hkv * bytes contiguous bytes of each part.  The pages written
+// are disjoint from the pages read.
 template <int N>
 __global__ void __launch_bounds__(256) move_pages_kernel(const __grid_constant__ Moves<N> m) {
-    const int2 e = m.e[blockIdx.x];
+    const Move e = m.e[blockIdx.x];
+    if (e.entry >= 0 && blockIdx.y == 0 && threadIdx.x == 0) m.table[e.entry] = e.to;
+    if (e.from < 0) return;
     const Part p = m.part[blockIdx.y];
     const size_t page = (size_t)m.Hkv * p.bytes;
-    const char* from = p.base + (size_t)e.x * page;
-    char* to = p.base + (size_t)e.y * page;
+    const char* from = p.base + (size_t)e.from * page;
+    char* to = p.base + (size_t)e.to * page;
     if (page % 16 == 0) {
         const uint4* f = reinterpret_cast<const uint4*>(from);
         uint4* t = reinterpret_cast<uint4*>(to);
@@ -122,19 +130,20 @@ int parts_of(const kvc_handle* h, Part* p) {
 }
 
 template <int N>
-cudaError_t move_some(const kvc_handle* h, const int2* pairs, size_t n, cudaStream_t st) {
+cudaError_t move_some(const kvc_handle* h, const Move* moves, size_t n, cudaStream_t st) {
     static thread_local Moves<N> m;
     m.parts = parts_of(h, m.part);
     m.Hkv = h->sh.Hkv;
-    std::memcpy(m.e, pairs, n * sizeof(int2));
+    m.table = reinterpret_cast<int32_t*>(h->state + h->L.table);
+    std::memcpy(m.e, moves, n * sizeof(Move));
     move_pages_kernel<N><<<dim3((unsigned)n, m.parts), 256, 0, st>>>(m);
     return cudaGetLastError();
 }
 
-cudaError_t move_pages(const kvc_handle* h, const std::vector<int2>& pairs, cudaStream_t st) {
-    for (size_t i0 = 0; i0 < pairs.size(); i0 += kMany) {
-        const size_t n = std::min<size_t>(kMany, pairs.size() - i0);
-        const cudaError_t e = n <= kFew ? move_some<kFew>(h, pairs.data() + i0, n, st) : move_some<kMany>(h, pairs.data() + i0, n, st);
+cudaError_t move_pages(const kvc_handle* h, const std::vector<Move>& moves, cudaStream_t st) {
+    for (size_t i0 = 0; i0 < moves.size(); i0 += kMany) {
+        const size_t n = std::min<size_t>(kMany, moves.size() - i0);
+        const cudaError_t e = n <= kFew ? move_some<kFew>(h, moves.data() + i0, n, st) : move_some<kMany>(h, moves.data() + i0, n, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -335,6 +344,13 @@ int held_rows(const kvc_handle* h, int b) {
     return std::min(n, s.S);
 }
 
+// No block-table entry of request b from this one on names a page: a contiguous cache maps no
+// page behind its rows.
+int held_pages(const kvc_handle* h, int b) {
+    const Shape& s = h->sh;
+    return s.ring ? s.S / kPage : (h->np[b] + kPage - 1) / kPage;
+}
+
 // Restored INT8 blocks live in a pool of their own, which copies do not follow.
 bool has_restored(const kvc_handle* h, int b) {
     if (h->xn_h.empty()) return false;
@@ -421,17 +437,23 @@ cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::ve
             if (x.old >= 0) ++h->page_ref[x.old];
         return cudaSuccess;
     }
-    std::vector<int2> upd, moves;
+    // one launch for copies and their table entries
+    std::vector<int2> upd;
+    std::vector<Move> moves;
     for (const Need& x : need) {
         const int page = h->page_free.back();
         h->page_free.pop_back();
         h->page_ref[page] = 1;
         h->table_h[x.idx] = page;
-        upd.push_back(make_int2(x.idx, page));
-        if (x.keep) moves.push_back(make_int2(x.old, page));
+        if (x.keep) moves.push_back(Move{x.idx, x.old, page});
+        else upd.push_back(make_int2(x.idx, page));
     }
-    cudaError_t e = move_pages(h, moves, st);
-    return e != cudaSuccess ? e : update_table(h, upd, st);
+    if (!moves.empty() && upd.size() <= kFew) {
+        for (const int2& u : upd) moves.push_back(Move{u.x, -1, u.y});
+        upd.clear();
+    }
+    const cudaError_t e = move_pages(h, moves, st);
+    return e != cudaSuccess || upd.empty() ? e : update_table(h, upd, st);
 }
 
 }  // namespace kvc
@@ -457,7 +479,7 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
     if (s.pages) {
         const int npg = s.S / kPage;
         for (int i = 0; i < n; ++i)
-            for (int lp = 0; lp < npg; ++lp) {
+            for (int lp = 0, held = std::max(held_pages(h, src[i]), held_pages(h, dst[i])); lp < held; ++lp) {
                 const int32_t page = h->table_h[(size_t)src[i] * npg + lp];
                 int32_t& e = h->table_h[(size_t)dst[i] * npg + lp];
                 if (e == page) continue;
@@ -551,7 +573,7 @@ int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream) try {
     if (s.pages) {
         const int npg = s.S / kPage;
         for (int b : dst)
-            for (int lp = 0; lp < npg; ++lp) drop_page(h, h->table_h[(size_t)b * npg + lp]);
+            for (int lp = 0, held = held_pages(h, b); lp < held; ++lp) drop_page(h, h->table_h[(size_t)b * npg + lp]);
     }
     if (copy_requests(h, h, none, dst, [](int) { return 0; }, s.pages > 0, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int b : dst) h->np[b] = 0;
@@ -570,13 +592,13 @@ int kvc_compact(kvc_t h, int32_t* h_used, kvc_stream_t stream) try {
     // pages at and past `used` move into the free ones below it: sources and destinations
     // are disjoint, and no page moves that need not
     std::vector<int32_t> to(s.pages, -1);
-    std::vector<int2> moves;
+    std::vector<Move> moves;
     int hole = 0;
     for (int p = used; p < s.pages; ++p) {
         if (h->page_ref[p] == 0) continue;
         while (h->page_ref[hole] != 0) ++hole;
         to[p] = hole;
-        moves.push_back(make_int2(p, hole));
+        moves.push_back(Move{-1, p, hole});
         ++hole;
     }
     if (!moves.empty()) {
@@ -588,9 +610,9 @@ int kvc_compact(kvc_t h, int32_t* h_used, kvc_stream_t stream) try {
             e = to[e];
             upd.push_back(make_int2((int)i, e));
         }
-        for (const int2& m : moves) {
-            h->page_ref[m.y] = h->page_ref[m.x];
-            h->page_ref[m.x] = 0;
+        for (const Move& m : moves) {
+            h->page_ref[m.to] = h->page_ref[m.from];
+            h->page_ref[m.from] = 0;
         }
         if (update_table(h, upd, st) != cudaSuccess) return KVC_ERR_CUDA;
     }

@@ -201,9 +201,8 @@ def kvc_append(h, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
 
 def kvc_append_rows(h, k: torch.Tensor, v: torch.Tensor, n: int, counts: Optional[Sequence[int]] = None,
                     stream=None) -> None:
-    c = None if counts is None else (ctypes.c_int32 * len(counts))(*[int(x) for x in counts])
-    _check(lib().kvc_append_rows(h, _dev(k, name="k"), _dev(v, name="v"), int(n),
-                                 ctypes.cast(c, ctypes.c_void_p) if c is not None else None, _stream(stream)),
+    c = None if counts is None else _whole(counts)
+    _check(lib().kvc_append_rows(h, _dev(k, name="k"), _dev(v, name="v"), int(n), None if c is None else _at(c), _stream(stream)),
            "kvc_append_rows")
 
 
@@ -251,8 +250,8 @@ def kvc_decode_attn_noalloc(h, q, out, stream=None) -> None:
 
 
 def kvc_trim(h, cuts: Sequence[int], stream=None) -> None:
-    c = (ctypes.c_int32 * len(cuts))(*[int(x) for x in cuts])
-    _check(lib().kvc_trim(h, ctypes.cast(c, ctypes.c_void_p), _stream(stream)), "kvc_trim")
+    c = _whole(cuts)
+    _check(lib().kvc_trim(h, _at(c), _stream(stream)), "kvc_trim")
 
 
 def kvc_chunk_attn(h, q, k, v, n: int, out, stream=None) -> None:
@@ -275,6 +274,14 @@ def _rows(t: torch.Tensor, name="tensor") -> tuple:
 def _ints(values):
     """Host int32 array (keep it alive during the call; its address is ``buffer_info()[0]``)."""
     return values if isinstance(values, array) and values.typecode == "i" else array("i", values)
+
+
+def _whole(values):
+    """_ints of any numbers, fractions cut off."""
+    try:
+        return _ints(values)
+    except TypeError:
+        return array("i", [int(x) for x in values])
 
 
 def _at(a: array) -> int:
@@ -334,36 +341,38 @@ def kvc_region(h, which: int) -> tuple:
     return off.value, n.value
 
 
+_ROPE_DTYPES = {torch.bfloat16: KVC_BF16, torch.float32: KVC_F32}
+
+
 def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=None, halves=False, per_axis=False,
                   stream=None):
     """x [rows, heads, d] (bf16 or fp32, heads dense, row stride free) rotated by several axes:
     ``pos`` int32 [axes, rows], ``sections`` the pairs of each axis.  ``out`` may be x; a new dense
     tensor if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1); ``per_axis``: a spectrum
     for each axis.  See include/kvc.h."""
-    if x.dtype not in (torch.bfloat16, torch.float32):
+    dtype = _ROPE_DTYPES.get(x.dtype)
+    if dtype is None:
         raise ValueError("x must be bfloat16 or float32, got %s" % x.dtype)
     xp, xs = _rows(x, "x")
+    rows, heads, d = shape = x.shape
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype or out.shape != x.shape:
-        raise ValueError("out must be %s of shape %s" % (x.dtype, tuple(x.shape)))
-    yp, ys = _rows(out, "out")
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.shape != shape:
+        raise ValueError("out must be %s of shape %s" % (x.dtype, tuple(shape)))
+    yp, ys = (xp, xs) if out is x else _rows(out, "out")
     s = _ints(sections)
-    rows, heads, d = x.shape
     pp = _dev(pos, torch.int32, (len(s), rows), "pos")
-    if not x.device == out.device == pos.device:
+    device = x.get_device()
+    if not device == out.get_device() == pos.get_device():
         raise ValueError("x, pos and out must be on one device")
     flags = (KVC_ROPE_HALVES if halves else 0) | (KVC_ROPE_PER_AXIS if per_axis else 0)
-
-    def call():
-        _check(lib().kvc_rope_axes(xp, xs, yp, ys, KVC_BF16 if x.dtype == torch.bfloat16 else KVC_F32, rows, heads, d, pp, len(s),
-                                   _at(s), float(base), flags, _stream(stream)), "kvc_rope_axes")
-
-    if x.device.index == torch.cuda.current_device():
-        call()
-    else:
-        with torch.cuda.device(x.device):
-            call()
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return kvc_rope_axes(x, pos, s, base, out, halves, per_axis, stream)
+    st = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    rc = lib().kvc_rope_axes(xp, xs, yp, ys, dtype, rows, heads, d, pp, len(s), s.buffer_info()[0], base, flags, st)
+    if rc:
+        _check(rc, "kvc_rope_axes")
     return out
 
 
@@ -598,17 +607,19 @@ class Cache:
         counts = _ints(counts)
         if len(counts) != self.B:
             raise ValueError("need one count per request")
-        T, total = q.shape[0], sum(counts)
+        T, total, device = q.shape[0], sum(counts), self.state.get_device()
         if T < total:
             raise ValueError("q has %d rows, the counts sum to %d" % (T, total))
         for t, heads, name in ((q, self.Hq, "q"), (k, self.Hkv, "k"), (v, self.Hkv, "v")):
             if t.dtype != self.torch_dtype or t.shape != (T, heads, self.d):
                 raise ValueError("%s must be %s of shape %s, got %s %s" % (name, self.torch_dtype, (T, heads, self.d), t.dtype,
                                                                            tuple(t.shape)))
-            if t.device != self.state.device:
+            if t.get_device() != device:
                 raise ValueError("%s must be on %s, got %s" % (name, self.state.device, t.device))
         if out is None:
             out = torch.empty((T, self.Hq, self.d), dtype=self.out_dtype, device=q.device)
+        if out.get_device() != device:
+            raise ValueError("out must be on %s, got %s" % (self.state.device, out.device))
         _dev(out, self.out_dtype, (T, self.Hq, self.d), "out")
         kvc_prompt_attn(self.h, q, k, v, counts, out, stream)
         return out
