@@ -263,6 +263,8 @@ __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs
 // Many rows per request (non-INT8).  CTA (row tile, KV head, request) writes
 // rows; next_position is only read here and advanced by advance_kernel.
 __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs a, const Group g) {
+    dep_wait();                           // launched dependent (see launch_dep); no early release:
+                                          // 36,000 CTAs of one call took 8 us longer with it
     const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y;
     const int cnt = g.val[bi];
     const int np = a.next_pos[b];
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs 
 // Same per-pair arithmetic and rounding as append_rows_kernel (RoPE in fp32, one bf16
 // rounding per element; values copied bit for bit); the inputs are 16-byte aligned.
 __global__ void __launch_bounds__(kThreads) append_rows_vec_kernel(const AppendArgs a, const Group g) {
+    dep_wait();                           // (as above)
     const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y;
     const int cnt = g.val[bi];
     const int np = a.next_pos[b];
@@ -411,6 +414,8 @@ __global__ void __launch_bounds__(kThreads) tail_kernel(const AppendArgs a, cons
 }
 
 __global__ void advance_kernel(int32_t* next_pos, const Group g) {
+    dep_wait();
+    dep_release();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < g.nb) next_pos[g.b0 + i] += g.val[i];
 }
@@ -418,6 +423,8 @@ __global__ void advance_kernel(int32_t* next_pos, const Group g) {
 // Trim: CTA per request.  Contiguous: slots [cut, old next_position) become
 // empty.  Ring: every slot holding a position >= cut becomes empty.
 __global__ void trim_kernel(int32_t* next_pos, int32_t* pos, const Group g, int S, int ring) {
+    dep_wait();
+    dep_release();
     const int bi = blockIdx.x, b = g.b0 + bi;
     const int cut = g.val[bi];
     const int np = next_pos[b];
@@ -444,20 +451,22 @@ cudaError_t launch_append_token(const AppendArgs& a, cudaStream_t st) {
 
 cudaError_t launch_append_rows_group(const AppendArgs& a, const Group& g, cudaStream_t st) {
     if (!a.int8) {
+        cudaError_t e;
         const bool vec = a.bf16 && a.d % 8 == 0 && a.d / 8 <= kThreads &&
                          reinterpret_cast<uintptr_t>(a.k) % 16 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 &&
                          a.sb % 8 == 0 && a.sh % 8 == 0 && a.sr % 8 == 0;
         if (vec) {
             const int rows_per_cta = kThreads / (a.d / 8);
             dim3 grid((a.n + rows_per_cta - 1) / rows_per_cta, a.Hkv, g.nb);
-            append_rows_vec_kernel<<<grid, kThreads, 0, st>>>(a, g);
+            e = launch_dep(append_rows_vec_kernel, grid, dim3(kThreads), 0, st, a, g);
         } else {
             const int half = a.d / 2;
             const int rows_per_cta = kThreads / half > 0 ? kThreads / half : 1;
             dim3 grid((a.n + rows_per_cta - 1) / rows_per_cta, a.Hkv, g.nb);
-            append_rows_kernel<<<grid, kThreads, 0, st>>>(a, g);
+            e = launch_dep(append_rows_kernel, grid, dim3(kThreads), 0, st, a, g);
         }
-        advance_kernel<<<(g.nb + 255) / 256, 256, 0, st>>>(a.next_pos, g);
+        if (e != cudaSuccess) return e;
+        return launch_dep(advance_kernel, dim3((g.nb + 255) / 256), dim3(256), 0, st, a.next_pos, g);
     } else {
         dim3 grid((a.n + kQBlock - 1) / kQBlock + 1, a.Hkv, g.nb);
         quantize_rows_kernel<<<grid, kThreads, quant_smem(a.d), st>>>(a, g);
@@ -491,8 +500,7 @@ cudaError_t launch_trim_cuts(int32_t* next_pos, int32_t* pos, const int32_t* cut
         g.b0 = b0;
         g.nb = B - b0 < kMaxGroup ? B - b0 : kMaxGroup;
         for (int i = 0; i < g.nb; ++i) g.val[i] = cuts[b0 + i];
-        trim_kernel<<<g.nb, 256, 0, st>>>(next_pos, pos, g, S, ring);
-        cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dep(trim_kernel, dim3(g.nb), dim3(256), 0, st, next_pos, pos, g, S, ring);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

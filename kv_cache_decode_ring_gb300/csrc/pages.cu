@@ -31,17 +31,18 @@ struct TableUpdates {
 
 template <int N>
 __global__ void table_update_kernel(const __grid_constant__ TableUpdates<N> u, int32_t* table) {
+    dep_wait();                           // launched dependent, as every kernel here: see launch_dep
+    dep_release();
     const int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i < u.n) table[u.e[i].x] = u.e[i].y;
 }
 
 template <int N>
 cudaError_t update_some(int32_t* table, const int2* upd, size_t n, cudaStream_t st) {
-    TableUpdates<N> u;
+    static thread_local TableUpdates<N> u;
     u.n = (int)n;
     std::memcpy(u.e, upd, n * sizeof(int2));
-    table_update_kernel<N><<<((int)n + 255) / 256, 256, 0, st>>>(u, table);
-    return cudaGetLastError();
+    return launch_dep(table_update_kernel<N>, dim3(((int)n + 255) / 256), dim3(256), 0, st, u, table);
 }
 
 // The changed entries; very many at once (a large prefill), the whole table.
@@ -85,6 +86,7 @@ struct Moves {
 template <int N>
 __global__ void __launch_bounds__(256) move_pages_kernel(const __grid_constant__ Moves<N> m) {
     const Move e = m.e[blockIdx.x];
+    dep_wait();
     if (e.entry >= 0 && blockIdx.y == 0 && threadIdx.x == 0) m.table[e.entry] = e.to;
     if (e.from < 0) return;
     const Part p = m.part[blockIdx.y];
@@ -136,8 +138,7 @@ cudaError_t move_some(const kvc_handle* h, const Move* moves, size_t n, cudaStre
     m.Hkv = h->sh.Hkv;
     m.table = reinterpret_cast<int32_t*>(h->state + h->L.table);
     std::memcpy(m.e, moves, n * sizeof(Move));
-    move_pages_kernel<N><<<dim3((unsigned)n, m.parts), 256, 0, st>>>(m);
-    return cudaGetLastError();
+    return launch_dep(move_pages_kernel<N>, dim3((unsigned)n, m.parts), dim3(256), 0, st, m);
 }
 
 cudaError_t move_pages(const kvc_handle* h, const std::vector<Move>& moves, cudaStream_t st) {
@@ -189,6 +190,8 @@ struct CopyArgs {
 // positions, next_position, request ID and (share) block-table entries.
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __grid_constant__ CopyArgs a) {
+    dep_wait();
+    dep_release();
     const CopyGroup g = a.group[blockIdx.z];
     const int h = blockIdx.y;
     const int* target = a.target + g.first;
@@ -328,9 +331,7 @@ cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<in
         }
         const int per = kCopyBlocks * kPage;
         dim3 grid(std::max((most + per - 1) / per, widest), s.Hkv + 1, ng);
-        if (wide) copy_requests_kernel<uint4><<<grid, kCopyThreads, 0, st>>>(a);
-        else copy_requests_kernel<uint32_t><<<grid, kCopyThreads, 0, st>>>(a);
-        cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dep(wide ? copy_requests_kernel<uint4> : copy_requests_kernel<uint32_t>, grid, dim3(kCopyThreads), 0, st, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

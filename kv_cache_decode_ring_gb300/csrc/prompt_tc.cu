@@ -218,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = *tmem_slot;
     dep_wait();                                        // launched dependent (see launch_dep): global memory from here on
-    dep_release();
     // every warpgroup changes its register share together
     if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
     else if (warp < kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegIssue));

@@ -57,6 +57,8 @@ constexpr int kHeads = 8;                 // heads that a CTA takes where rows a
 // kFlight heads in flight: eight units a thread either way.
 template <typename T, int VEC, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+    dep_wait();                                          // launched dependent: see launch_dep
+    dep_release();
     const int u = threadIdx.x % a.units;
     const long long r = (long long)blockIdx.x * a.rows_per_cta + threadIdx.x / a.units;
     if (threadIdx.x / a.units >= a.rows_per_cta || r >= a.rows) return;
@@ -113,6 +115,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const __grid_constant
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs a) {
     extern __shared__ float2 cs[];
+    dep_wait();
+    dep_release();
     const long long r0 = (long long)blockIdx.x * a.rows_per_cta;
     const int nr = (int)min((long long)a.rows_per_cta, a.rows - r0);
     for (int i = threadIdx.x; i < nr * a.pairs; i += kThreads) {
@@ -201,7 +205,8 @@ extern "C" int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64
     const dim3 grid((unsigned)groups, hgroups);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const size_t smem = (size_t)a.rows_per_cta * pairs * sizeof(float2);
-    auto launch = [&](auto kernel, size_t bytes) { kernel<<<grid, kThreads, bytes, st>>>(a); };
+    cudaError_t e = cudaSuccess;
+    auto launch = [&](void (*kernel)(RopeArgs), size_t bytes) { e = launch_dep(kernel, grid, dim3(kThreads), bytes, st, a); };
     if (dtype == KVC_BF16) {
         if (!wide) launch(rope_pairs_kernel<__nv_bfloat16>, smem);
         else if (a.halves) launch(rope_kernel<__nv_bfloat16, 8, true>, 0);
@@ -211,5 +216,5 @@ extern "C" int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64
         else if (a.halves) launch(rope_kernel<float, 4, true>, 0);
         else launch(rope_kernel<float, 4, false>, 0);
     }
-    return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
+    return e == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
