@@ -65,7 +65,7 @@ TRAFFIC_PER_BYTE = {
     "prefix-reuse-store": ("chunk.cu", "de37e058599ee090", (83959552 + 3649792) / 60850176),   # the same chunk launch
     # the store's batched row copy (8 requests' cuts, 297.9 MB read + written): writes still in L2
     # at the end of the launch are not counted, so the ratio is below 1
-    "store-load": ("store.cu", "817adec9d1411abf", (149277440 + 95578624) / 297918464),
+    "store-load": ("store.cu", "b2f0ffa7416b534c", (149272576 + 95569152) / 297918464),
 }
 
 
