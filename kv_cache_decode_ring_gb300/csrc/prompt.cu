@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads) prompt_pairs_kernel(const RowArgs a,
     }
 }
 
-// bf16 rows with d a multiple of 8, in 16-byte units: the same arithmetic.  Bound by HBM.  A
+// bf16 rows with d a multiple of 8, in 16-byte units: the same arithmetic.  Bound by HBM: 11,000
+// rows of 32 + 2 x 8 heads of 128 in 40 us, 6.5 TB/s.  A
 // thread holds one unit of a row's {cos, sin} and takes kHeads heads of that row, every load
 // issued first.  grid (row groups of the longest request, requests, head groups: those of the
 // rotated queries (where the tensor-core attention takes them), then those of keys and
