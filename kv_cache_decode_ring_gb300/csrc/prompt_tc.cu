@@ -339,61 +339,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::kPFull + slot]);
             }
+            const bool parts = items.parts > 1;                 // unnormalised sums with their maximum, to be joined
+            const float inv = parts ? 1.f : 1.f / l;
+            const bool bf16 = a.out_bf16 && !parts;
+            // through the warp's own rows of the unit's Q tile (its scores are all done): where the
+            // warp's rows are whole tokens, all there and bf16, a tensor copy takes them out; else
+            // 128 bytes of each row at a time (32 dims as fp32, 64 as bf16), lines stored whole
+            unsigned char* tile = sQ + q_buf(slot, i) * L::kQTile + 32 * lg * 128;
+            const int c = lane & 7, nv = min(T, ntok - slot * T) * a.g;        // the slot's rows
+            const size_t orow = (size_t)(w.row + w.t0 + slot * T) * a.Hq + w.kvh * a.g;
+            const long long row_bytes = parts ? (long long)items.parts * D * 4 : D * (bf16 ? 2 : 4);
+            char* dst = (parts ? reinterpret_cast<char*>(a.part_acc + (size_t)w.part * D) : static_cast<char*>(a.out)) +
+                        orow * row_bytes + 16 * c;
             if (ok && nt > 0) ok = all_ok(wait(stage_bar(L::kODone, slot, k - 1), phase(k - 1)));
             if (!ok) break;
             if (some) {
                 fence_after();
-                const bool parts = items.parts > 1;             // unnormalised sums with their maximum, to be joined
-                const float inv = parts ? 1.f : 1.f / l;
-                const bool bf16 = a.out_bf16 && !parts;
-                // through the warp's own rows of the unit's Q tile (its scores are all done): where the
-                // warp's rows are whole tokens, all there and bf16, a tensor copy takes them out; else
-                // 128 bytes of each row at a time (32 dims as fp32, 64 as bf16), lines stored whole
-                unsigned char* tile = sQ + q_buf(slot, i) * L::kQTile + 32 * lg * 128;
-                unsigned char* stage = tile;
-                const int c = lane & 7, nv = min(T, ntok - slot * T) * a.g;        // the slot's rows
-                const size_t orow = (size_t)(w.row + w.t0 + slot * T) * a.Hq + w.kvh * a.g;
-                // (32 dims as fp32 or 64 as bf16: 128 bytes a round)
-                const long long row_bytes = parts ? (long long)items.parts * D * 4 : D * (bf16 ? 2 : 4);
-                char* dst = (parts ? reinterpret_cast<char*>(a.part_acc + (size_t)w.part * D) : static_cast<char*>(a.out)) +
-                            orow * row_bytes + 16 * c;
                 const bool spoilt_unit = nt > 0 && spoilt[i % kAhead] == i + 1;
                 const bool boxed = items.boxed && !spoilt_unit && bf16 && 32 * lg + 32 <= nv;
                 if (parts && valid)
                     a.part_ml[(orow + place[r]) * items.parts + w.part] =
                         make_float2(m_ref == -INFINITY ? -INFINITY : m_ref * sc, l);
-#pragma unroll 1
-                for (int x0 = 0; x0 < D; x0 += 32) {
-                    float o[32];
-                    if (nt > 0) {
-                        tmem_ld32(tO + x0, o);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
-                    if (bf16) {
-                        if (boxed) stage = tile + x0 / 64 * L::kQHalf;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t u[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const __nv_bfloat162 t2 = __floats2bfloat162_rn(o[8 * e + 2 * q], o[8 * e + 2 * q + 1]);
-                                u[q] = *reinterpret_cast<const uint32_t*>(&t2);
-                            }
-                            *reinterpret_cast<uint4*>(stage + lane * 128 + (((x0 / 32 % 2 * 4 + e) ^ (lane & 7)) << 4)) =
-                                make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                        if (boxed || x0 % 64 == 0) continue;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    }
+                auto lines_out = [&](const unsigned char* stage) {       // 128 bytes of each of the warp's rows
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -403,6 +370,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     dst += 128;
                     __syncwarp();
+                };
+#pragma unroll 1
+                for (int x0 = 0; x0 < D; x0 += 64) {
+                    float o[64];
+                    if (nt > 0) {
+                        tmem_ld32(tO + x0, o);
+                        tmem_ld32(tO + x0 + 32, o + 32);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) o[e] = 0.f;
+                    }
+                    if (bf16) {
+                        unsigned char* stage = boxed ? tile + x0 / 64 * L::kQHalf : tile;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const __nv_bfloat162 t2 = __floats2bfloat162_rn(o[8 * e + 2 * q] * inv, o[8 * e + 2 * q + 1] * inv);
+                                u[q] = *reinterpret_cast<const uint32_t*>(&t2);
+                            }
+                            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                        if (!boxed) lines_out(stage);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<float4*>(tile + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                    make_float4(o[32 * h + 4 * e] * inv, o[32 * h + 4 * e + 1] * inv, o[32 * h + 4 * e + 2] * inv,
+                                                o[32 * h + 4 * e + 3] * inv);
+                            lines_out(tile);
+                        }
+                    }
                 }
                 fence_before();                                 // O is read before the next unit's products write it
                 if (boxed) {
