@@ -317,8 +317,10 @@ int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k,
  * are independent, and only what they write costs memory.  Such a call needs a free page
  * for each page it copies (KVC_ERR_CAPACITY otherwise; nothing changes); under stream
  * capture it returns KVC_ERR_UNSUPPORTED (a replay would copy again, over newer rows):
- * append once before capturing.  Trim, free and the store give up a request's hold on a
- * page; the page is free when its last holder gave it up.
+ * append once before capturing.  Replays on a ring go round to each of its pages, so there a
+ * captured call is refused while a request that it brings rows for shares any page: append W
+ * rows first, or branch with kvc_copy, whose pages are the branch's own.  Trim, free and the
+ * store give up a request's hold on a page; the page is free when its last holder gave it up.
  * These calls keep books on the host (the lengths that kvc_next_positions reports and
  * the block table): they return KVC_ERR_UNSUPPORTED on a stream under capture, and a
  * handle whose captured calls were replayed has lengths on the device that the host does

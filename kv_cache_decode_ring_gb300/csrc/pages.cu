@@ -410,11 +410,20 @@ int pages_released(const kvc_handle* h, const std::vector<char>& drop) {
 // contiguous bf16/fp32 cache, and never on a contiguous INT8 cache (the rows of an
 // incomplete block sit in the exact tail, its page is written when the block completes).
 // A copy is refused under stream capture (KVC_ERR_UNSUPPORTED): a replay would bring the
-// old page's bytes back over rows that earlier replays wrote.
+// old page's bytes back over rows that earlier replays wrote.  On a ring so is a write by a
+// request that shares any page: replays advance on the device and come round to it, where no
+// host looks who else holds it.  (A contiguous cache's later pages are unmapped: the kernels
+// flag rows there.)
 cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::vector<int>& to, cudaStream_t st,
                       int* status) {
     const Shape& s = h->sh;
     const int np = s.S / kPage;
+    if (s.ring && capturing(st))
+        for (int b = 0; b < s.B; ++b)
+            for (int lp = 0; to[b] > from[b] && lp < np; ++lp) {
+                const int32_t e = h->table_h[(size_t)b * np + lp];
+                if (e >= 0 && h->page_ref[e] > 1) { *status = KVC_ERR_UNSUPPORTED; return cudaSuccess; }
+            }
     struct Need { int idx, old; bool keep; };
     std::vector<Need> need;                // table indices to map, in request and page order
     for (int b = 0; b < s.B; ++b) {

@@ -404,3 +404,64 @@ def test_prompt_fork_decode_free_together():
             paged.fork([5, 2], [1, 4])
             plain.fork([5, 2], [1, 4])
     assert paged.device_status() == 0 and plain.device_status() == 0
+
+
+def ring_after_a_fork():
+    """A wrapped paged ring forked, one row appended to every request: one page of four is each branch's own."""
+    m = Model(B=3, d=128, cap=64, layout="ring", pages=16)
+    m.append_rows([70, 0, 5])
+    m.fork([0], [1])
+    m.append()
+    assert m.cache.page_counts()[1] == 3
+    return m
+
+
+def test_captured_writes_into_a_ring_need_every_page_to_be_private():
+    # replays go round the ring: a page that is shared would be written by them sooner or later, although
+    # the captured call itself stays in a page of its own
+    m = ring_after_a_fork()
+    c = m.cache
+    x = [torch.zeros(*s, 128, dtype=torch.bfloat16, device="cuda") for s in ((3, 2), (3, 2, 1), (2, 4), (2, 2), (3, 1, 4), (3, 1, 2))]
+    step, rows, q, kv, cq, ckv = x
+    free = c.page_counts()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for f, a in ((c.append, (step, step)), (c.append_rows, (rows, rows)), (c.append_rows, (rows, rows, [0, 1, 0])),
+                     (c.prompt, (q, kv, kv, [1, 0, 1])), (c.chunk, (cq, ckv, ckv))):
+            with pytest.raises(kvc.KvcError) as e:
+                f(*a)
+            assert e.value.code == kvc.KVC_ERR_UNSUPPORTED
+        torch.zeros(1, device="cuda")
+    assert c.page_counts() == free
+    m.check()
+    # a request whose pages are its own may be captured beside them
+    g = torch.cuda.CUDAGraph()
+    tok = m.rows([7])
+    with torch.cuda.graph(g):
+        c.append_rows(*(t[:, :, None].expand(3, -1, 1, -1).contiguous() for t in tok), counts=[0, 0, 1])
+    g.replay()
+    m.ids[2].append(7)
+    m.check()
+
+
+@pytest.mark.parametrize("call", ["append_rows", "prompt"])
+def test_replays_round_a_private_ring_leave_its_branches_alone(call):
+    m = ring_after_a_fork()
+    c = m.cache
+    m.append_rows([64, 0, 0])                                   # request 0 has written all of its pages
+    assert c.page_counts()[1] == 0
+    m.check()
+    others = {w: c.export(w)[1:] for w in (kvc.KVC_EXPORT_K, kvc.KVC_EXPORT_V, kvc.KVC_EXPORT_POSITIONS)}
+    tok = m.rows([9])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        if call == "prompt":
+            c.prompt(torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda"), *tok, [1, 0, 0])
+        else:
+            c.append_rows(*(t[:, :, None].expand(3, -1, 1, -1).contiguous() for t in tok), counts=[1, 0, 0])
+    for _ in range(80):
+        g.replay()
+    assert c.device_status() == 0
+    for w, want in others.items():
+        assert np.array_equal(c.export(w)[1:], want)
+    assert list(c.export(kvc.KVC_EXPORT_NEXT_POSITION)) == [70 + 1 + 64 + 80, 71, 6]
