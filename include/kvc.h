@@ -160,13 +160,17 @@ int kvc_destroy(kvc_t h);
  * (ring); positions[slot] = pos; next_position = pos + 1.  INT8: the row goes
  * to the request's exact tail block; the 16th row of a block quantizes the
  * block and writes its witnesses.  KVC_ERR_CAPACITY if a contiguous cache is
- * full (nothing is written). */
+ * full (nothing is written).  A captured call appends at the device's next_position; a
+ * replay past the capacity or the RoPE table, or on a paged cache past the pages mapped at
+ * capture, writes nothing for that request and sets the error word that
+ * kvc_device_status reads. */
 int kvc_append(kvc_t h, const void* d_k, const void* d_v, kvc_stream_t stream);
 
 /* Append up to n tokens per request, in order, from d_k, d_v [B][Hkv][n][d]
  * (prefill).  h_counts (host, B entries, NULL = n for all) limits request b to
  * its first h_counts[b] rows.  Same per-row semantics as kvc_append; on a ring
- * only the rows that stay resident are written. */
+ * only the rows that stay resident are written.  Replays write no row past the capacity
+ * or the mapped pages either, but next_position counts every row. */
 int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n,
                     const int32_t* h_counts, kvc_stream_t stream);
 

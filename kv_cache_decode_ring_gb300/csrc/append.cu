@@ -34,6 +34,13 @@ __device__ __forceinline__ bool position_ok(const AppendArgs& a, long long p) {
     return true;
 }
 
+// Whether a page is mapped for `slot` of request b.  The host maps the pages of every call, but a
+// captured call replays on from there: rows behind its pages are not written (kv_row and int8_block
+// would put them into page 0, which is some request's) and flagged.
+__device__ __forceinline__ bool page_mapped(const AppendArgs& a, int b, int slot) {
+    return !a.table || a.table[(size_t)b * (a.S / kPage) + slot / kPage] >= 0;
+}
+
 // Stored value of element pair (2i, 2i+1) of a key row at position p.
 __device__ __forceinline__ void key_pair(const AppendArgs& a, const void* src, size_t off, int i,
                                          int p, float& y0, float& y1) {
@@ -145,6 +152,10 @@ __device__ void quantize_block(const AppendArgs& a, const float* sK, const float
 // CTA of the request reads next_position[b] first; the last of them to finish (an
 // arrival counter, reset by that CTA) writes positions[slot] and advances
 // next_position[b], so no CTA can read the advanced value.
+// PAGED: rows go to the slot's page, read once beside the rows' loads; a row without one is flagged
+// (page_mapped).  One kernel for both took 2.25 us an append where these take 2.15, and 2.31 paged
+// (16 requests of 8 KV heads of 128).
+template <bool PAGED>
 __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs a) {
     extern __shared__ float smem[];
     dep_wait();                                        // launched dependent: see launch_dep
@@ -160,6 +171,10 @@ __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs
     const int d = a.d, half = d / 2;
     const int slot = a.ring ? p % a.S : p;
     const int tslot = p % kQBlock;                     // INT8: the row's place in the exact tail
+    const int page = PAGED ? a.table[(size_t)b * (a.S / kPage) + slot / kPage] : 0;
+    auto cache_row = [&](int h) {                      // (as kv_row)
+        return PAGED ? ((size_t)page * a.Hkv + h) * kPage + slot % kPage : ((size_t)b * a.Hkv + h) * a.S + slot;
+    };
     if (a.bf16 && d % 8 == 0) {
         // 8 elements (16 bytes) per item, kU items per thread with every load issued
         // before any arithmetic: one round trip for the whole row set.  The rows go to
@@ -186,13 +201,14 @@ __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs
                     cs[u][1] = __ldg(r + 1);
                 }
             }
+            if (PAGED && page < 0) break;
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 const int idx = base + u * blockDim.x;
                 if (idx >= n) continue;
                 const int h = h0 + idx / vec, c = idx % vec;
                 const size_t dst = (a.int8 ? (((size_t)b * a.Hkv + h) * kQBlock + tslot)
-                                           : kv_row(a.table, b, h, slot, a.Hkv, a.S)) * d + 8 * c;
+                                           : cache_row(h)) * d + 8 * c;
                 uint4 ko = kx[u];
                 if (a.rope) {
                     uint32_t w[4] = {kx[u].x, kx[u].y, kx[u].z, kx[u].w};
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs
                 *reinterpret_cast<uint4*>(vdst + dst) = vx[u];
             }
         }
-        if (a.int8 && tslot == kQBlock - 1) {
+        if (a.int8 && page >= 0 && tslot == kQBlock - 1) {
             // the 16th row completes the block: every KV head quantizes its 16 tail rows
             float* sK = smem;
             float* sV = smem + kQBlock * d;
@@ -231,16 +247,20 @@ __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs
         }
     } else {
         // fp32 caches and other head sizes (never INT8: that tier is bf16 with d % 16 == 0)
-        for (int idx = threadIdx.x; idx < nh * half; idx += blockDim.x) {
+        for (int idx = threadIdx.x; page >= 0 && idx < nh * half; idx += blockDim.x) {
             const int h = h0 + idx / half, i = idx % half;
             const size_t src = ((size_t)b * a.Hkv + h) * d;
-            const size_t dst = kv_row(a.table, b, h, slot, a.Hkv, a.S) * d;
+            const size_t dst = cache_row(h) * d;
             float y0, y1;
             key_pair(a, a.k, src, i, p, y0, y1);
             store_pair(a.kc, dst + 2 * i, y0, y1, a.bf16);
             store_pair(a.vc, dst + 2 * i, ld_elem(a.v, src + 2 * i, a.bf16),
                        ld_elem(a.v, src + 2 * i + 1, a.bf16), a.bf16);
         }
+    }
+    if (PAGED && page < 0) {                           // (every CTA of the request returns here)
+        if (threadIdx.x == 0 && blockIdx.y == 0) flag(a.hdr, kErrPosition);
+        return;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -281,6 +301,10 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs 
     }
     const int slot = a.ring ? (int)(p % a.S) : (int)p;
     const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr;
+    if (!page_mapped(a, b, slot)) {
+        flag(a.hdr, kErrPosition);
+        return;
+    }
     const size_t dst = kv_row(a.table, b, h, slot, a.Hkv, a.S) * d;
     float y0, y1;
     key_pair(a, a.k, src, i, (int)p, y0, y1);
@@ -330,6 +354,10 @@ __global__ void __launch_bounds__(kThreads) append_rows_vec_kernel(const AppendA
         }
         ko = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (!page_mapped(a, b, slot)) {
+        flag(a.hdr, kErrPosition);
+        return;
+    }
     const size_t dst = kv_row(a.table, b, h, slot, a.Hkv, a.S) * a.d + 8 * (size_t)c;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.kc) + dst) = ko;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.vc) + dst) = vx;
@@ -350,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const AppendArg
     if (p0 + kQBlock > np + cnt) return;             // block not completed by this call
     // a ring keeps the newest S/16 complete blocks: one overwritten later in this call is skipped
     if (a.ring && p0 < ((np + cnt) / kQBlock) * kQBlock - a.S) return;
-    if (!position_ok(a, (long long)p0 + kQBlock - 1)) {
+    if (!position_ok(a, (long long)p0 + kQBlock - 1) || !page_mapped(a, b, a.ring ? p0 % a.S : p0)) {
         if (threadIdx.x == 0) flag(a.hdr, kErrPosition);
         return;
     }
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) tail_kernel(const AppendArgs a, cons
         const int h = idx / ((end - first) * half);
         const int rem = idx % ((end - first) * half);
         const int p = first + rem / half, i = rem % half;
-        if (!position_ok(a, p)) { flag(a.hdr, kErrPosition); continue; }
+        if (!position_ok(a, p) || !page_mapped(a, b, a.ring ? p % a.S : p)) { flag(a.hdr, kErrPosition); continue; }
         const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)(p - np) * a.sr;
         const size_t tail = (((size_t)b * a.Hkv + h) * kQBlock + p % kQBlock) * d;
         float k0, k1;
@@ -446,7 +474,8 @@ size_t quant_smem(int d) { return (size_t)(2 * kQBlock * d + 64) * sizeof(float)
 
 cudaError_t launch_append_token(const AppendArgs& a, cudaStream_t st) {
     const size_t smem = a.int8 ? quant_smem(a.d) : 0;
-    return launch_dep(append_token_kernel, dim3(a.B, (a.Hkv + a.hpc - 1) / a.hpc), dim3(kThreads), smem, st, a);
+    return launch_dep(a.table ? append_token_kernel<true> : append_token_kernel<false>,
+                      dim3(a.B, (a.Hkv + a.hpc - 1) / a.hpc), dim3(kThreads), smem, st, a);
 }
 
 cudaError_t launch_append_rows_group(const AppendArgs& a, const Group& g, cudaStream_t st) {

@@ -315,7 +315,7 @@ __device__ __forceinline__ void rope_pair(float x0, float x1, float2 cs, float& 
 __device__ __forceinline__ size_t kv_row(const int32_t* table, int b, int h, int slot, int Hkv, int S) {
     if (!table) return ((size_t)b * Hkv + h) * S + slot;
     int page = table[(size_t)b * (S / kPage) + slot / kPage];
-    page = page < 0 ? 0 : page;       // never taken: every slot read or written is mapped first
+    page = page < 0 ? 0 : page;       // reads of a replay past its mapped pages (flagged); no write gets here
     return ((size_t)page * Hkv + h) * kPage + (slot % kPage);
 }
 
@@ -349,7 +349,7 @@ __host__ __device__ __forceinline__ Int8Window int8_window(int len, int S, int W
 __host__ __device__ __forceinline__ size_t int8_block(const int32_t* table, int b, int h, int k, int Hkv, int S) {
     if (!table) return ((size_t)b * Hkv + h) * (S / kQBlock) + k;
     int page = table[(size_t)b * (S / kQBlock) + k];
-    page = page < 0 ? 0 : page;       // never taken: every block read or written is mapped first
+    page = page < 0 ? 0 : page;       // (as kv_row)
     return (size_t)page * Hkv + h;
 }
 

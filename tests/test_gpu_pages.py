@@ -465,3 +465,49 @@ def test_replays_round_a_private_ring_leave_its_branches_alone(call):
     for w, want in others.items():
         assert np.array_equal(c.export(w)[1:], want)
     assert list(c.export(kvc.KVC_EXPORT_NEXT_POSITION)) == [70 + 1 + 64 + 80, 71, 6]
+
+
+@pytest.mark.parametrize("call", ["append", "append_rows"])
+@pytest.mark.parametrize("kind", [dict(d=128), dict(d=6), dict(dtype="f32"), dict(quant="int8"), dict(quant="int8-dither", d=128)],
+                         ids=lambda k: "-".join("%s=%s" % kv for kv in k.items()))
+def test_replayed_appends_past_the_mapped_pages_are_reported(kind, call):
+    # a captured call maps the pages of its own rows; replays that leave them write nothing, wherever the
+    # pool's pages lie (page 0 holds live rows here), and set the device error
+    m = Model(B=2, cap=64, pages=8, **kind)
+    m.append_rows([40, 24])
+    assert m.cache.compact() == 5
+    tok = [t.expand(2, -1, -1).contiguous() for t in m.rows([5])]
+    rows = [t[:, :, None].contiguous() for t in tok]
+    m.cache.append(*tok)                                            # (loads the kernels before the capture)
+    m.ids = [x + [5] for x in m.ids]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.cache.append(*tok) if call == "append" else m.cache.append_rows(*rows)
+    for _ in range(7):                                              # up to slots 47 and 31, the last of their pages
+        g.replay()
+    m.ids = [x + [5] * 7 for x in m.ids]
+    c = m.cache
+    assert c.device_status() == 0 and list(c.export(kvc.KVC_EXPORT_NEXT_POSITION)) == [48, 32]
+    fresh = Model(B=2, cap=64, pages=0, **kind)
+    names = [kvc.KVC_EXPORT_K, kvc.KVC_EXPORT_V] if not m.quant else [kvc.KVC_EXPORT_KQ, kvc.KVC_EXPORT_VQ, kvc.KVC_EXPORT_SK, kvc.KVC_EXPORT_SV,
+                                                                    kvc.KVC_EXPORT_KTAIL, kvc.KVC_EXPORT_VTAIL]
+    names += [kvc.KVC_EXPORT_WITNESS] if m.quant == "int8" else []
+    stored = [c.state[off:off + n] for off, n in (kvc.kvc_region(c.h, w) for w in names)]
+    before, positions = [x.clone() for x in stored], c.export(kvc.KVC_EXPORT_POSITIONS)
+    for _ in range(20):
+        g.replay()
+    assert c.device_status() == 1 and c.device_status() == 0        # read and cleared
+    for w, x, y in zip(names, stored, before):
+        assert torch.equal(x, y), w
+    assert np.array_equal(c.export(kvc.KVC_EXPORT_POSITIONS), positions)
+    assert list(c.export(kvc.KVC_EXPORT_NEXT_POSITION)) == ([48, 32] if call == "append" else [68, 52])
+    # what the valid rows hold is what one call after another would have written
+    k, v = (torch.stack(x).transpose(1, 2).contiguous()
+            for x in zip(*(fresh.rows((ids + [0] * 48)[:48]) for ids in m.ids)))
+    fresh.cache.append_rows(k, v, counts=[48, 32])
+    for b, n in enumerate((48, 32)):
+        for w in names:
+            if w in (kvc.KVC_EXPORT_KTAIL, kvc.KVC_EXPORT_VTAIL):
+                continue
+            per = n if w in (kvc.KVC_EXPORT_K, kvc.KVC_EXPORT_V, kvc.KVC_EXPORT_KQ, kvc.KVC_EXPORT_VQ, kvc.KVC_EXPORT_WITNESS) else n // 16
+            assert np.array_equal(c.export(w)[b][:, :per], fresh.cache.export(w)[b][:, :per]), (w, b)
