@@ -181,7 +181,9 @@ int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n,
  *     out = softmax(q . K^T / sqrt(d)) . V            d_out: [B][Hq][d]
  * evaluated as split-K flash decoding with an online softmax and a cross-split
  * combine, fp32 accumulation, rounded once to the output dtype.  Needs at least
- * one cached token per request, and on a ring an append after any trim.
+ * one cached token per request; KVC_ERR_ARG too while a request of a ring lacks a key of
+ * that window: a ring that wrapped and was then trimmed (or loaded short of a slot's end)
+ * has overwritten it, until the request itself appends.
  * INT8 caches also return, per (request, query head), the witness bound
  * ([WITCERT] "频带酉性与双层证书"):
  *     c_t = (1/sqrt d) sum_b ||q_b|| w_{t,b}   for every cached token in the window,
@@ -256,7 +258,8 @@ int kvc_decode_attn_noalloc(kvc_t h, const void* d_q, void* d_out, kvc_stream_t 
  * = cut).  h_cut: host, B entries, 0 <= cut <= next_position.  Rows at
  * positions >= cut are dropped (positions set to -1).  A ring accepts the cut
  * only if every position the next query needs is still resident, i.e. with
- * lo = max(0, cut-W+1): lo == cut or lo >= max(0, next_position-W); an INT8
+ * lo = max(0, cut-W+1): lo == cut or lo >= max(0, top-W), top the largest next_position
+ * since the ring last held lo (what earlier trims dropped had overwritten rows); an INT8
  * cache only if no quantized block is split (cut % 16 == 0 or cut within the
  * exact tail).  Otherwise KVC_ERR_EVICTED and nothing changes. */
 int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream);
@@ -541,7 +544,7 @@ int kvc_store_save(kvc_t h, int32_t slot, int32_t b, int32_t n, kvc_stream_t str
  * slot holds nothing or cut exceeds its length; KVC_ERR_EVICTED if a ring slot no
  * longer holds rows that the token at `cut` would attend to (the kvc_trim rule);
  * KVC_ERR_CAPACITY if a paged cache lacks pages (nothing changes).  On a ring, as
- * after kvc_trim, the next call on the handle must append. */
+ * after kvc_trim, the request may have to append before the next decode. */
 int kvc_store_load(kvc_t h, int32_t slot, int32_t b, int32_t cut, kvc_stream_t stream);
 
 /* kvc_store_load for n requests at once (h_slots, h_b, h_cuts: host arrays of n

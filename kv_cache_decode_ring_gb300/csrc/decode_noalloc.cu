@@ -57,7 +57,7 @@ extern "C" int kvc_decode_attn_noalloc(kvc_t h, const void* d_q, void* d_out, kv
     if (s.int8) return KVC_ERR_UNSUPPORTED;
     for (int b = 0; b < s.B; ++b)
         if (h->np[b] < 1) return KVC_ERR_ARG;
-    if (s.ring && h->ring_needs_append) return KVC_ERR_ARG;
+    if (!windows_held(h)) return KVC_ERR_ARG;
 
     // scratch this call needs; refuse anything beyond the fixed array
     const size_t rows = (size_t)s.B * s.Hq * s.max_splits;

@@ -270,7 +270,8 @@ int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t 
     h->cfg = *cfg; h->sh = s; h->L = L; h->state = static_cast<char*>(d_state); h->bytes = bytes;
     h->np.assign(s.B, 0);
     h->store_n.assign(s.store_slots, -1);
-    h->ring_needs_append = false;
+    h->held_lo.assign(s.B, 0);
+    h->store_lo.assign(s.store_slots, 0);
     h->has_kv_maps = false;
     if (s.gqa) {
         // the GQA decode reads 16-row tiles of the K and V caches by tensor copy
@@ -354,8 +355,7 @@ int kvc_append(kvc_t h, const void* d_k, const void* d_v, kvc_stream_t stream) {
     }
     AppendArgs a = append_args(h, d_k, d_v, 1);
     if (launch_append_token(a, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
-    for (auto& p : h->np) ++p;
-    h->ring_needs_append = false;
+    for (int b = 0; b < h->sh.B; ++b) add_rows(h, b, 1);
     return KVC_OK;
 }
 
@@ -381,9 +381,7 @@ int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n, const 
     }
     AppendArgs a = append_args(h, d_k, d_v, n);
     if (launch_append_rows_counts(a, h->counts.data(), S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
-    bool any = false;
-    for (int b = 0; b < s.B; ++b) { h->np[b] += h->counts[b]; any |= h->counts[b] > 0; }
-    if (any) h->ring_needs_append = false;
+    for (int b = 0; b < s.B; ++b) add_rows(h, b, h->counts[b]);
     return KVC_OK;
 }
 
@@ -393,7 +391,7 @@ int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float*
     const Shape& s = h->sh;
     for (int b = 0; b < s.B; ++b)
         if (h->np[b] < 1) return KVC_ERR_ARG;                 // nothing cached to attend to
-    if (s.ring && h->ring_needs_append) return KVC_ERR_ARG;
+    if (!windows_held(h)) return KVC_ERR_ARG;
     cudaStream_t st = S_(stream);
     if (s.dither && (d_cmax || d_tanh || d_ct)) return KVC_ERR_ARG;      // Tier B returns no bound
     if (s.int8) {
@@ -430,11 +428,7 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) {
     for (int b = 0; b < s.B; ++b) {
         const int cut = h_cut[b], np = h->np[b];
         if (cut < 0 || cut > np) return KVC_ERR_ARG;
-        if (s.ring) {
-            const int lo = cut - s.S + 1 > 0 ? cut - s.S + 1 : 0;
-            const int resident = np - s.S > 0 ? np - s.S : 0;
-            if (!(lo == cut || lo >= resident)) return KVC_ERR_EVICTED;
-        }
+        if (s.ring && !ring_cut_ok(h, h->held_lo[b], cut)) return KVC_ERR_EVICTED;
         if (s.int8 && (cut % kQBlock) && cut < (np / kQBlock) * kQBlock) return KVC_ERR_EVICTED;
     }
     if (launch_trim_cuts(at<int32_t>(h, h->L.next_pos), at<int32_t>(h, h->L.pos), h_cut, s.B, s.S, s.ring,
@@ -456,8 +450,10 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) {
                                      cudaMemcpyHostToDevice, S_(stream)) != cudaSuccess)
             return KVC_ERR_CUDA;
     }
-    for (int b = 0; b < s.B; ++b) h->np[b] = h_cut[b];
-    if (s.ring) h->ring_needs_append = true;
+    for (int b = 0; b < s.B; ++b) {
+        h->np[b] = h_cut[b];
+        if (s.ring && h->held_lo[b] > h_cut[b]) h->held_lo[b] = h_cut[b];
+    }
     return KVC_OK;
 }
 
@@ -485,8 +481,7 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
         // staged beside the resident rows, attended, and only then appended
         if (launch_chunk(h, d_q, d_k, d_v, d_out, n, st) != cudaSuccess) return KVC_ERR_CUDA;
         if (launch_append_rows_counts(a, h->counts.data(), st) != cudaSuccess) return KVC_ERR_CUDA;
-        for (auto& p : h->np) p += n;
-        h->ring_needs_append = false;
+        for (int b = 0; b < s.B; ++b) add_rows(h, b, n);
         return KVC_OK;
     }
     // the suffix rows join the cache first (rotated keys, positions cut .. cut+n-1) ...
@@ -536,8 +531,7 @@ int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k,
         if (rc) return rc;
     }
     if (launch_prompt(h, a, h_counts, st) != cudaSuccess) return KVC_ERR_CUDA;
-    for (int b = 0; b < s.B; ++b) h->np[b] += h_counts[b];
-    h->ring_needs_append = false;
+    for (int b = 0; b < s.B; ++b) add_rows(h, b, h_counts[b]);
     return KVC_OK;
 } catch (...) {
     return KVC_ERR_ARG;      // out of host memory

@@ -379,7 +379,9 @@ struct kvc_handle {
     int device;
     int num_sms;
     std::vector<int32_t> np;      // host mirror of next_position
-    bool ring_needs_append;        // a ring was trimmed and has not appended since
+    // rings: positions [held_lo[b], np[b]) are all in their slots.  Appends move it up to np - W; a
+    // trim does not bring back what the dropped rows overwrote, so it stays
+    std::vector<int32_t> held_lo;
     std::vector<int32_t> counts;   // host staging for append_rows counts
     kvc::KvMaps kv_maps;           // built at create when the GQA decode serves the shape
     bool has_kv_maps;
@@ -391,7 +393,7 @@ struct kvc_handle {
     // entries name each page (requests forked from one another share pages)
     std::vector<int32_t> table_h, page_free, page_ref;
     // prefix store: rows saved in each store slot (-1 = empty)
-    std::vector<int32_t> store_n;
+    std::vector<int32_t> store_n, store_lo;   // (and their held_lo)
     // Tier B: host mirror of the request IDs
     std::vector<uint32_t> req_id_h;
 };
@@ -401,6 +403,26 @@ struct kvc_handle {
 inline bool on_device(const kvc_handle* h) {
     int dev = -1;
     return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+// Request b has n rows more.
+inline void add_rows(kvc_handle* h, int b, int n) {
+    h->np[b] += n;
+    if (h->sh.ring && n > 0 && h->np[b] - h->sh.S > h->held_lo[b]) h->held_lo[b] = h->np[b] - h->sh.S;
+}
+
+// Whether the window of every request's newest row is there: not on a ring that was trimmed (or
+// loaded short of its end) after it wrapped, until the request appends.
+inline bool windows_held(const kvc_handle* h) {
+    for (int b = 0; h->sh.ring && b < h->sh.B; ++b)
+        if (h->held_lo[b] > 0 && h->held_lo[b] > h->np[b] - h->sh.S) return false;
+    return true;
+}
+
+// Whether a ring's request that holds [held, ...) can go on at `cut`: the row there sees [cut - W + 1, cut].
+inline bool ring_cut_ok(const kvc_handle* h, int held, int cut) {
+    const int lo = cut - h->sh.S + 1 > 0 ? cut - h->sh.S + 1 : 0;
+    return lo == cut || lo >= held;
 }
 
 // Whether `st` is being captured into a graph (true also where the runtime cannot tell).

@@ -506,6 +506,7 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
         return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         h->np[dst[i]] = h->np[src[i]];
+        h->held_lo[dst[i]] = h->held_lo[src[i]];
         if (s.dither) h->req_id_h[dst[i]] = h->req_id_h[src[i]];
     }
     return KVC_OK;
@@ -565,9 +566,9 @@ int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_
     if (copy_requests(to, from, src, dst, [&](int b) { return held_rows(from, b); }, false, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         to->np[dst[i]] = from->np[src[i]];
+        to->held_lo[dst[i]] = from->held_lo[src[i]];
         if (s.dither) to->req_id_h[dst[i]] = from->req_id_h[src[i]];
     }
-    if (s.ring && from->ring_needs_append) to->ring_needs_append = true;
     return KVC_OK;
 } catch (...) {
     return KVC_ERR_ARG;      // out of host memory
@@ -589,7 +590,7 @@ int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream) try {
             for (int lp = 0, held = held_pages(h, b); lp < held; ++lp) drop_page(h, h->table_h[(size_t)b * npg + lp]);
     }
     if (copy_requests(h, h, none, dst, [](int) { return 0; }, s.pages > 0, st) != cudaSuccess) return KVC_ERR_CUDA;
-    for (int b : dst) h->np[b] = 0;
+    for (int b : dst) h->np[b] = h->held_lo[b] = 0;
     return KVC_OK;
 } catch (...) {
     return KVC_ERR_ARG;      // out of host memory

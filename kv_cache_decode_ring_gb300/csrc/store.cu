@@ -2,6 +2,7 @@
 // "查詢流程與快取所有權"): the host policy object that picks the stored prefill a
 // query reuses and how many of its rows, and the device copies of one request's
 // rows between the cache and a store slot of the state buffer.
+#include <algorithm>
 #include <cstring>
 #include <new>
 #include <string>
@@ -234,6 +235,7 @@ int kvc_store_save(kvc_t h, int32_t slot, int32_t b, int32_t n, kvc_stream_t str
     a.item[0] = StoreItem{slot, b, 0, s.ring ? s.S : n};
     if (launch_store_copy(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVC_ERR_CUDA;
     h->store_n[slot] = n;
+    h->store_lo[slot] = h->held_lo[b];
     return KVC_OK;
 }
 
@@ -252,12 +254,7 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
         seen[b] = 1;
         const int len = slot < 0 ? 0 : h->store_n[slot];
         if (len < 0 || cut < 0 || cut > len) return KVC_ERR_ARG;
-        if (s.ring && cut > 0) {
-            // the token at `cut` attends to [cut - S + 1, cut); the slot holds [len - S, len)
-            const int lo = cut - s.S + 1 > 0 ? cut - s.S + 1 : 0;
-            const int resident = len - s.S > 0 ? len - s.S : 0;
-            if (lo < resident) return KVC_ERR_EVICTED;
-        }
+        if (s.ring && cut > 0 && !ring_cut_ok(h, h->store_lo[slot], cut)) return KVC_ERR_EVICTED;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.pages) {
@@ -291,8 +288,10 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
         }
         if (launch_store_copy(a, st) != cudaSuccess) return KVC_ERR_CUDA;
     }
-    for (int i = 0; i < n; ++i) h->np[h_b[i]] = h_cuts[i];
-    if (s.ring) h->ring_needs_append = true;
+    for (int i = 0; i < n; ++i) {
+        h->np[h_b[i]] = h_cuts[i];
+        h->held_lo[h_b[i]] = s.ring && h_cuts[i] > 0 ? std::min(h->store_lo[h_slots[i]], h_cuts[i]) : 0;
+    }
     return KVC_OK;
 }
 

@@ -511,3 +511,112 @@ def test_replayed_appends_past_the_mapped_pages_are_reported(kind, call):
                 continue
             per = n if w in (kvc.KVC_EXPORT_K, kvc.KVC_EXPORT_V, kvc.KVC_EXPORT_KQ, kvc.KVC_EXPORT_VQ, kvc.KVC_EXPORT_WITNESS) else n // 16
             assert np.array_equal(c.export(w)[b][:, :per], fresh.cache.export(w)[b][:, :per]), (w, b)
+
+
+def test_a_trimmed_ring_waits_for_a_row_of_every_request_that_lost_one():
+    # a wrapped ring has overwritten the first key of the window of the row at cut - 1: until the request
+    # appends, its decode would lack that key.  Rows of other requests do not lift the guard
+    for quant, rows in ((None, "append_rows"), (None, "prompt"), ("int8", "append_rows")):
+        m = Model(B=3, d=64, cap=48, layout="ring", quant=quant)
+        m.append_rows([100, 20, 130])
+        m.trim([99, 20, 130])
+        q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+
+        def decodes():
+            calls = [m.cache.decode] + ([] if quant else [lambda q: kvc.kvc_decode_attn_noalloc(m.cache.h, q, torch.empty_like(q))])
+            answers = set()
+            for f in calls:
+                try:
+                    f(q)
+                    answers.add(True)
+                except kvc.KvcError as e:
+                    assert e.code == kvc.KVC_ERR_ARG
+                    answers.add(False)
+            assert len(answers) == 1
+            return answers.pop()
+
+        assert not decodes()
+        m.append_rows([0, 3, 1], rows == "prompt")
+        assert not decodes(), (quant, rows)
+        m.fork([0], [1])                                          # the branch lacks the same key
+        m.append_rows([1, 0, 0], rows == "prompt")
+        assert not decodes()
+        m.append_rows([0, 1, 0], rows == "prompt")
+        assert decodes()
+        m.check()
+        m.trim([len(x) - (b == 2) for b, x in enumerate(m.ids)])
+        m.free([2])
+        m.append_rows([0, 0, 1], rows == "prompt")               # an empty request lacks nothing
+        m.check()
+
+
+def test_a_ring_trimmed_before_it_wrapped_decodes():
+    # every key of the window is still there, as it is where the trim dropped nothing
+    m = Model(B=2, d=64, cap=48, layout="ring")
+    m.append_rows([40, 100])
+    m.trim([31, 100])
+    m.check()
+
+
+def test_copies_carry_the_ring_guard_of_the_request():
+    a, b = (Model(B=2, d=64, cap=48, layout="ring") for _ in range(2))
+    a.append_rows([100, 60])
+    b.append_rows([7, 60])
+    a.trim([99, 60])
+    b.copy_from(a, [1], [0])                                      # a request that lacks nothing
+    b.check()
+    b.copy_from(a, [0], [1])
+    with pytest.raises(kvc.KvcError) as e:
+        b.cache.decode(torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"))
+    assert e.value.code == kvc.KVC_ERR_ARG
+    b.append_rows([0, 1])
+    b.check()
+
+
+def test_a_loaded_ring_waits_for_a_row_too():
+    cfg = kvc.make_config("f32", "ring", None, 2, 2, 2, 16, 16, max_position=200, store_slots=1)
+    c = kvc.Cache(cfg)
+    k = torch.randn(2, 2, 40, 16, device="cuda")
+    q = torch.randn(2, 2, 16, device="cuda")
+    c.append_rows(k, k)
+    want = c.decode(q)
+    c.store_save(0, 0, 40)
+    c.store_load(0, 1, 39)
+    row = k[:, :, 39:].contiguous()
+    c.append_rows(row, row, counts=[1, 0])
+    with pytest.raises(kvc.KvcError) as e:
+        c.decode(q)
+    assert e.value.code == kvc.KVC_ERR_ARG
+    c.append_rows(k[:1, :, 39:].expand(2, -1, -1, -1).contiguous(), k[:1, :, 39:].expand(2, -1, -1, -1).contiguous(), counts=[0, 1])
+    assert torch.equal(c.decode(q[:1].expand(2, -1, -1).contiguous())[1], want[0])
+    c.store_load(0, 1, 40)                                        # whole: nothing is missing
+    assert torch.equal(c.decode(q[:1].expand(2, -1, -1).contiguous())[1], want[0])
+
+
+def test_what_trimmed_rows_overwrote_stays_lost():
+    # one step back at a time goes no further than one step: position 39 overwrote 23, which 38 attends to
+    cfg = kvc.make_config("f32", "ring", None, 1, 2, 2, 16, 16, max_position=200, store_slots=1)
+    c = kvc.Cache(cfg)
+    k = torch.randn(1, 2, 40, 16, device="cuda")
+    c.append_rows(k, k)
+    c.trim([39])
+    c.trim([39])
+    c.store_save(0, 0, 39)
+    for f in (lambda: c.trim([38]), lambda: c.store_load(0, 0, 38)):
+        with pytest.raises(kvc.KvcError) as e:
+            f()
+        assert e.value.code == kvc.KVC_ERR_EVICTED
+    c.store_load(0, 0, 39)
+    with pytest.raises(kvc.KvcError):
+        c.decode(k[:, :, 0].contiguous())
+    row = k[:, :, 39:].contiguous()
+    c.append_rows(row, row)
+    fresh = kvc.Cache(cfg)
+    fresh.append_rows(k, k)
+    q = torch.randn(1, 2, 16, device="cuda")
+    assert torch.equal(c.decode(q), fresh.decode(q))
+    c.trim([0])                                                   # from nothing, everything is possible again
+    c.append_rows(k[:, :, :3].contiguous(), k[:, :, :3].contiguous())
+    c.decode(q)
+    c.trim([1])
+    c.decode(q)
