@@ -478,11 +478,11 @@ int kvc_next_positions(kvc_t h, int32_t* h_out);
  * clears it. */
 int kvc_device_status(kvc_t h, kvc_stream_t stream, int32_t* h_status);
 
-/* Health check of the failure path: enqueues one CTA that waits, with the same
- * bounded wait the kernels use for their copies, on a barrier that nothing
- * signals.  The wait gives up after its bound (about one second), sets bit 1 of
- * the device error word and returns; nothing faults and the context stays
- * usable.  A following kvc_device_status reports the bit (and clears it). */
+/* Health check of the failure path: enqueues one CTA that waits, with the bounded
+ * waits the kernels use for their copies (by time, and by tries in kvc_prompt_attn),
+ * on a barrier that nothing signals.  Both give up after their bound (about one
+ * second), bit 1 of the device error word is set and the kernel returns; nothing
+ * faults and the context stays usable.  A following kvc_device_status reports the bit (and clears it). */
 int kvc_check_wait_path(kvc_t h, kvc_stream_t stream);
 
 /* Host only.  Rows of a stored prefill that a new query can reuse ([PREFIX]

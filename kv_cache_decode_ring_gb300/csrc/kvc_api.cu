@@ -7,6 +7,7 @@
 
 #include "async_copy.h"
 #include "kvc_internal.h"
+#include "tcgen05.h"
 
 namespace kvc {
 
@@ -34,8 +35,9 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// One CTA waits on an mbarrier that nothing arrives at: the bounded wait gives up and
-// flags the error word, as a kernel whose copy never lands would.
+// One CTA waits on an mbarrier that nothing arrives at, one warp with each of the bounded waits
+// (by time; by tries, as the prompt kernel does): both give up and the error word is flagged, as
+// by a kernel whose copy never lands.
 __global__ void wait_path_kernel(uint32_t* hdr) {
     __shared__ __align__(8) uint64_t bar;
     if (threadIdx.x == 0) {
@@ -43,7 +45,10 @@ __global__ void wait_path_kernel(uint32_t* hdr) {
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    if (threadIdx.x == 0 && !mbar_wait(&bar, 0)) atomicOr(hdr, kErrWait);
+    bool ended = false;
+    if (threadIdx.x == 0) ended = mbar_wait(&bar, 0);
+    if (threadIdx.x == 32) ended = tc::wait(&bar, 0);
+    if (!__syncthreads_or(ended) && threadIdx.x == 0) atomicOr(hdr, kErrWait);
 }
 
 }  // namespace
@@ -710,7 +715,7 @@ int kvc_device_status(kvc_t h, kvc_stream_t stream, int32_t* h_status) {
 
 int kvc_check_wait_path(kvc_t h, kvc_stream_t stream) {
     if (!h || !on_device(h)) return KVC_ERR_ARG;
-    wait_path_kernel<<<1, 32, 0, S_(stream)>>>(at<uint32_t>(h, h->L.hdr));
+    wait_path_kernel<<<1, 64, 0, S_(stream)>>>(at<uint32_t>(h, h->L.hdr));
     return cudaGetLastError() == cudaSuccess ? KVC_OK : KVC_ERR_CUDA;
 }
 

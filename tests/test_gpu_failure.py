@@ -36,3 +36,15 @@ def test_bounded_wait_is_reported_and_the_context_survives():
         model.append(host(k1), host(v1))
         assert_close(cache.decode(q.cuda()), model.decode(host(q)), w.dtype, "decode after the failed wait")
     assert cache.device_status() == 0
+
+
+def test_every_bounded_wait_ends_within_seconds():
+    # by time and by tries: both bounds are about a second, and the two run out side by side
+    cache = kvc.Cache.from_workload(wl.small("failure", B=1, Hq=2, Hkv=2, d=64, capacity=16, rope_base=0.0, seed=1))
+    torch.cuda.synchronize()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    kvc.kvc_check_wait_path(cache.h)
+    end.record()
+    assert cache.device_status() == 2
+    assert 100 < begin.elapsed_time(end) < 5000
