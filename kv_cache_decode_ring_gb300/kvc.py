@@ -139,6 +139,23 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor in memory of ``stream``, which will write it: memory of the current stream may still
+    be in use there by work enqueued before its last owner let go of it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    device = torch.device(device)
+    raw = _stream(stream)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if raw == torch._C._cuda_getCurrentRawStream(index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (1 is the legacy default stream by its special handle)
+        stream = torch.cuda.default_stream(index) if raw in (0, 1) else torch.cuda.ExternalStream(raw, index)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dev(t: Optional[torch.Tensor], dtype=None, shape=None, name="tensor") -> ctypes.c_void_p:
     if t is None:
         return ctypes.c_void_p(0)
@@ -348,7 +365,7 @@ def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=No
                   stream=None):
     """x [rows, heads, d] (bf16 or fp32, heads dense, row stride free) rotated by several axes:
     ``pos`` int32 [axes, rows], ``sections`` the pairs of each axis.  ``out`` may be x; a new dense
-    tensor if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1); ``per_axis``: a spectrum
+    tensor (memory of ``stream``) if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1); ``per_axis``: a spectrum
     for each axis.  See include/kvc.h."""
     dtype = _ROPE_DTYPES.get(x.dtype)
     if dtype is None:
@@ -356,7 +373,7 @@ def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=No
     xp, xs = _rows(x, "x")
     rows, heads, d = shape = x.shape
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(shape, x.dtype, x.device, stream)
     elif out.dtype != x.dtype or out.shape != shape:
         raise ValueError("out must be %s of shape %s" % (x.dtype, tuple(shape)))
     yp, ys = (xp, xs) if out is x else _rows(out, "out")
@@ -515,7 +532,8 @@ class PrefixStore:
 
 class Cache:
     """A KV cache of one layer on the current CUDA device: the state buffer (a torch
-    uint8 tensor) plus its library handle.  Thin wrapper over the functions above."""
+    uint8 tensor) plus its library handle.  Thin wrapper over the functions above.
+    Outputs that a call makes for itself are memory of the stream it runs on."""
 
     _EXPORT_DTYPES = {KVC_EXPORT_POSITIONS: np.int32, KVC_EXPORT_NEXT_POSITION: np.int32, KVC_EXPORT_KQ: np.int8,
                       KVC_EXPORT_VQ: np.int8, KVC_EXPORT_SK: np.float32, KVC_EXPORT_SV: np.float32,
@@ -530,7 +548,7 @@ class Cache:
         else:
             self.out_dtype = torch.float32 if cfg.out_dtype == KVC_F32 + 1 else torch.bfloat16
         nbytes = kvc_state_bytes(cfg)
-        self.state = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.state = _empty(nbytes, torch.uint8, device, stream)
         self.h = kvc_create(cfg, self.state, stream)
 
     @classmethod
@@ -579,7 +597,7 @@ class Cache:
     def decode(self, q, out=None, cmax=None, tanh=None, ct=None, stream=None):
         _dev(q, self.torch_dtype, (self.B, self.Hq, self.d), "q")
         if out is None:
-            out = torch.empty(q.shape, dtype=self.out_dtype, device=q.device)
+            out = _empty(q.shape, self.out_dtype, q.device, stream)
         _dev(out, self.out_dtype, (self.B, self.Hq, self.d), "out")
         kvc_decode_attn(self.h, q, out, cmax, tanh, ct, stream)
         return out
@@ -595,7 +613,7 @@ class Cache:
         _dev(k, self.torch_dtype, (self.B, n, self.Hkv, self.d), "k")
         _dev(v, self.torch_dtype, (self.B, n, self.Hkv, self.d), "v")
         if out is None:
-            out = torch.empty(q.shape, dtype=self.out_dtype, device=q.device)
+            out = _empty(q.shape, self.out_dtype, q.device, stream)
         _dev(out, self.out_dtype, (self.B, n, self.Hq, self.d), "out")
         kvc_chunk_attn(self.h, q, k, v, n, out, stream)
         return out
@@ -617,7 +635,7 @@ class Cache:
             if t.get_device() != device:
                 raise ValueError("%s must be on %s, got %s" % (name, self.state.device, t.device))
         if out is None:
-            out = torch.empty((T, self.Hq, self.d), dtype=self.out_dtype, device=q.device)
+            out = _empty((T, self.Hq, self.d), self.out_dtype, q.device, stream)
         if out.get_device() != device:
             raise ValueError("out must be on %s, got %s" % (self.state.device, out.device))
         _dev(out, self.out_dtype, (T, self.Hq, self.d), "out")
@@ -678,7 +696,7 @@ class Cache:
         """Per complete block, the largest c_t over its tokens and the KV head's query heads."""
         _dev(ct, torch.float32, (self.B, self.Hq, self.S), "ct")
         if risk is None:
-            risk = torch.empty((self.B, self.Hkv, self.S // 16), dtype=torch.float32, device=ct.device)
+            risk = _empty((self.B, self.Hkv, self.S // 16), torch.float32, ct.device, stream)
         _dev(risk, torch.float32, (self.B, self.Hkv, self.S // 16), "risk")
         kvc_int8_block_risk(self.h, ct, risk, stream)
         return risk
