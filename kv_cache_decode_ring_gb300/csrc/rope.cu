@@ -16,6 +16,7 @@
 // the row's heads eight at a time, every load issued before the first product: 64 us for 32760
 // tokens of 24 bf16 heads of 128 (6.3 TB/s; a thread per unit, its sines worked out again for
 // every head, took 74).
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -200,10 +201,10 @@ extern "C" int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64
     a.rows_per_cta = wide ? kThreads / a.units : 4;
     const long long groups = (rows + a.rows_per_cta - 1) / a.rows_per_cta;
     if (groups > 0x7fffffffLL) return KVC_ERR_ARG;
-    // many rows: a CTA takes every head of its rows; few (a decode step): eight each, to fill the GPU
-    a.heads_per_cta = wide && groups < 608 ? kHeads : heads;
+    // many rows: a CTA takes every head of its rows; few (a decode step): eight each, to fill the GPU,
+    // or more where a grid would not hold the groups
+    a.heads_per_cta = wide && groups < 608 ? std::max(kHeads, (heads + 65534) / 65535) : heads;
     const unsigned hgroups = (unsigned)((heads + a.heads_per_cta - 1) / a.heads_per_cta);
-    if (hgroups > 65535) return KVC_ERR_ARG;
     const dim3 grid((unsigned)groups, hgroups);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const size_t smem = (size_t)a.rows_per_cta * pairs * sizeof(float2);

@@ -144,3 +144,12 @@ def test_refusals(bad):
 
 def test_no_rows_is_no_work():
     assert _raw(rows=0) == kvc.KVC_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,d,rows", [(600000, 8, 2), (65536 * 8 + 1, 16, 1)])
+def test_few_rows_of_very_many_heads(heads, d, rows):
+    x = torch.randn(rows, heads, d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    pos = torch.tensor([[5, 1000][:rows]], dtype=torch.int32, device="cuda")
+    out = kvc.kvc_rope_axes(x, pos, [d // 2], 10000.0)
+    check(x, pos, [d // 2], 10000.0, out, False, False)
