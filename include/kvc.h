@@ -385,7 +385,9 @@ int kvc_page_counts(kvc_t h, int32_t* h_free, int32_t* h_shared);
  * position; products and sums in fp32, each rounded once, then rounded to dtype.
  * d_y may be d_x (same strides); otherwise the two ranges must not overlap.  d_x and d_y
  * need the alignment of an element; 16-byte aligned rows are faster.
- * KVC_ERR_ARG: a bad size, section, flag, stride, base (positive and finite) or overlap. */
+ * KVC_ERR_ARG: a bad size (heads * head_dim up to 2^24, rows and strides up to 2^31, head_dim
+ * even and up to 256), section, flag, stride, base (positive and finite, as every frequency has
+ * to be) or overlap. */
 enum { KVC_ROPE_HALVES = 1, KVC_ROPE_PER_AXIS = 2 };
 int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride, int32_t dtype,
                   int64_t rows, int32_t heads, int32_t head_dim, const int32_t* d_pos,

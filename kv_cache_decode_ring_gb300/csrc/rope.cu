@@ -184,9 +184,8 @@ extern "C" int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64
         for (int j = 0; j < h_sections[i]; ++j, ++p) {
             const double e = (flags & KVC_ROPE_PER_AXIS) ? (double)j / h_sections[i] : (double)p / pairs;
             const double t = std::pow(base, -e) * 0.15915494309189533577;   // turns per position: theta / 2 pi
-            const double f = t - std::floor(t);
-            const double scaled = std::ldexp(f, 64);
-            a.turn[p] = scaled >= 18446744073709551615.0 ? 0 : (uint64_t)scaled;
+            if (!std::isfinite(t)) return KVC_ERR_ARG;       // a base near 0
+            a.turn[p] = (uint64_t)std::ldexp(t - std::floor(t), 64);   // (below 2^64: a double below 1 times 2^64)
             a.axis[p] = (uint8_t)i;
         }
     a.x = d_x; a.y = d_y; a.pos = d_pos; a.rows = rows;

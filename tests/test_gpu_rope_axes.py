@@ -153,3 +153,8 @@ def test_few_rows_of_very_many_heads(heads, d, rows):
     pos = torch.tensor([[5, 1000][:rows]], dtype=torch.int32, device="cuda")
     out = kvc.kvc_rope_axes(x, pos, [d // 2], 10000.0)
     check(x, pos, [d // 2], 10000.0, out, False, False)
+
+
+@pytest.mark.parametrize("bad", [dict(base=5e-324, sections=(16, 16)), dict(base=5e-324, sections=(31, 1), flags=2)], ids=["all", "axis"])
+def test_refuses_frequencies_beyond_a_doubles_range(bad):
+    assert _raw(**bad) == kvc.KVC_ERR_ARG
