@@ -381,8 +381,10 @@ int kvc_page_counts(kvc_t h, int32_t* h_free, int32_t* h_shared);
  * axis in turn; their sum P <= head_dim/2, the dims from 2P on pass through.  Pair p
  * belongs to the axis a whose section it lies in, as the section's pair j, and turns by
  *     d_pos[a][r] * base^(-p/P),  with KVC_ROPE_PER_AXIS  d_pos[a][r] * base^(-j/h_sections[a]).
- * Its dims are (2p, 2p+1), with KVC_ROPE_HALVES (p, P+p).  Angles are held to 2^-64 of a turn per
- * position; products and sums in fp32, each rounded once, then rounded to dtype.
+ * Its dims are (2p, 2p+1), with KVC_ROPE_HALVES (p, P+p).  The frequency is a double and the
+ * position times it is reduced to a turn exactly, then rounded to fp32: an angle of x radians is
+ * off by x 2^-51 + 1e-7 at most.  Products and sums in fp32, each rounded once, then rounded to
+ * dtype.
  * d_y may be d_x (same strides); otherwise the two ranges must not overlap.  d_x and d_y
  * need the alignment of an element; 16-byte aligned rows are faster.
  * KVC_ERR_ARG: a bad size (heads * head_dim up to 2^24, rows and strides up to 2^31, head_dim

@@ -9,7 +9,8 @@
 // mod 2^64 is the angle in turns with wrap-around for free (one 64-bit multiply).  Its top
 // 32 bits, read as a signed number, are the angle in half turns on [-1, 1) times 2^31:
 // sincospif of that is off by less than 2^-24 pi from the rounding to fp32, plus its own
-// error.  F is the double-precision frequency, so a position p adds p theta 2^-53.
+// error.  F is the double-precision frequency (pow and a product: relative error below 2^-51), so
+// a position p adds p theta 2^-51 at most.
 //
 // Bound by HBM: x read once, y written once.  A thread keeps one 16-byte unit's place in a
 // row (with halves, the unit and its partner), works out that unit's sines once and takes
