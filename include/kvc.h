@@ -53,7 +53,8 @@ typedef void* kvc_stream_t; /* a cudaStream_t */
 
 /* ---- status codes ---------------------------------------------------- */
 #define KVC_OK 0
-#define KVC_ERR_ARG 1          /* null pointer, bad shape/dtype/size, call out of order */
+#define KVC_ERR_ARG 1          /* null pointer, bad shape/dtype/size, call out of order,
+                                  or out of host memory */
 #define KVC_ERR_CAPACITY 2     /* contiguous cache full: position >= max_seq_len
                                   ([LOOP] §三 "assert pos < max_seq_len"), or a
                                   position beyond the RoPE table */

@@ -136,7 +136,7 @@ extern "C" int kvc_int8_block_risk(kvc_t h, const float* d_ct, float* d_risk, kv
 }
 
 extern "C" int kvc_int8_gate(const float* h_risk, int32_t B, int32_t Hkv, int32_t nblk, double tau,
-                             int32_t max_blocks, int32_t* h_sel, int32_t* h_n_sel) {
+                             int32_t max_blocks, int32_t* h_sel, int32_t* h_n_sel) try {
     if (!h_risk || !h_n_sel || B < 1 || Hkv < 1 || nblk < 0 || max_blocks < 0 || (max_blocks > 0 && !h_sel))
         return KVC_ERR_ARG;
     struct Cand { float r; int32_t b, h, k; size_t idx; };
@@ -159,10 +159,12 @@ extern "C" int kvc_int8_gate(const float* h_risk, int32_t B, int32_t Hkv, int32_
     }
     *h_n_sel = n;
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 extern "C" int kvc_int8_restore(kvc_t h, const int32_t* h_blocks, int32_t n, const void* d_k_full,
-                                const void* d_v_full, kvc_stream_t stream) {
+                                const void* d_v_full, kvc_stream_t stream) try {
     if (!h || !on_device(h) || n < 0 || (n > 0 && (!h_blocks || !d_k_full || !d_v_full)) || !h->sh.int8)
         return KVC_ERR_ARG;
     if (h->sh.dither) return KVC_ERR_UNSUPPORTED;
@@ -214,4 +216,6 @@ extern "C" int kvc_int8_restore(kvc_t h, const int32_t* h_blocks, int32_t n, con
         if (cudaGetLastError() != cudaSuccess) return KVC_ERR_CUDA;
     }
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }

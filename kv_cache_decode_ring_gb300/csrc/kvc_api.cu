@@ -2,7 +2,7 @@
 // mirror of next_position, RoPE table, and kernel launches.
 #include <cmath>
 #include <cstring>
-#include <new>
+#include <memory>
 #include <vector>
 
 #include "async_copy.h"
@@ -22,7 +22,9 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
     for (const Grant& g : granted)
         if (g.kernel == kernel && g.device == dev && g.bytes >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) granted.push_back(Grant{kernel, dev, bytes});
+    if (e == cudaSuccess) {
+        try { granted.push_back(Grant{kernel, dev, bytes}); } catch (...) {}   // not remembered: granted again
+    }
     return e;
 }
 
@@ -263,15 +265,15 @@ int kvc_state_bytes(const kvc_config* cfg, size_t* bytes) {
     return KVC_OK;
 }
 
-int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t stream, kvc_t* out) {
+int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t stream, kvc_t* out) try {
     if (!cfg || !d_state || !out) return KVC_ERR_ARG;
     if (reinterpret_cast<uintptr_t>(d_state) & 255u) return KVC_ERR_ARG;
     Shape s;
     if (!make_shape(*cfg, &s)) return KVC_ERR_ARG;
     Layout L = make_layout(s);
     if (bytes < L.total) return KVC_ERR_ARG;
-    kvc_handle* h = new (std::nothrow) kvc_handle();
-    if (!h) return KVC_ERR_ARG;
+    std::unique_ptr<kvc_handle> own(new kvc_handle());
+    kvc_handle* h = own.get();
     h->cfg = *cfg; h->sh = s; h->L = L; h->state = static_cast<char*>(d_state); h->bytes = bytes;
     h->np.assign(s.B, 0);
     h->store_n.assign(s.store_slots, -1);
@@ -286,14 +288,12 @@ int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t 
         const cuuint32_t box[2] = {64, 16};
         if (!make_tensor_map_bf16(&h->kv_maps.k, h->state + L.k, 2, dims, strides, box) ||
             !make_tensor_map_bf16(&h->kv_maps.v, h->state + L.v, 2, dims, strides, box)) {
-            delete h;
             return KVC_ERR_CUDA;
         }
         h->has_kv_maps = true;
     }
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
-        delete h;
         return KVC_ERR_CUDA;
     }
     cudaStream_t st = S_(stream);
@@ -336,9 +336,11 @@ int kvc_create(const kvc_config* cfg, void* d_state, size_t bytes, kvc_stream_t 
         if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     }
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e != cudaSuccess) { delete h; return KVC_ERR_CUDA; }
-    *out = h;
+    if (e != cudaSuccess) return KVC_ERR_CUDA;
+    *out = own.release();
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_destroy(kvc_t h) {
@@ -347,7 +349,7 @@ int kvc_destroy(kvc_t h) {
     return KVC_OK;
 }
 
-int kvc_append(kvc_t h, const void* d_k, const void* d_v, kvc_stream_t stream) {
+int kvc_append(kvc_t h, const void* d_k, const void* d_v, kvc_stream_t stream) try {
     if (!h || !on_device(h) || !d_k || !d_v || !aligned16(d_k) || !aligned16(d_v)) return KVC_ERR_ARG;
     int rc = check_capacity(h, nullptr, 1);
     if (rc) return rc;
@@ -362,10 +364,12 @@ int kvc_append(kvc_t h, const void* d_k, const void* d_v, kvc_stream_t stream) {
     if (launch_append_token(a, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
     for (int b = 0; b < h->sh.B; ++b) add_rows(h, b, 1);
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n, const int32_t* h_counts,
-                    kvc_stream_t stream) {
+                    kvc_stream_t stream) try {
     if (!h || !on_device(h) || n < 0 || !aligned16(d_k) || !aligned16(d_v)) return KVC_ERR_ARG;
     if (n == 0) return KVC_OK;
     if (!d_k || !d_v) return KVC_ERR_ARG;
@@ -388,6 +392,8 @@ int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n, const 
     if (launch_append_rows_counts(a, h->counts.data(), S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
     for (int b = 0; b < s.B; ++b) add_rows(h, b, h->counts[b]);
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float* d_tanh, float* d_ct,
@@ -427,7 +433,7 @@ int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float*
     return KVC_OK;
 }
 
-int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) {
+int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) try {
     if (!h || !on_device(h) || !h_cut) return KVC_ERR_ARG;
     const Shape& s = h->sh;
     for (int b = 0; b < s.B; ++b) {
@@ -460,10 +466,12 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) {
         if (s.ring && h->held_lo[b] > h_cut[b]) h->held_lo[b] = h_cut[b];
     }
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, int32_t n, void* d_out,
-                   kvc_stream_t stream) {
+                   kvc_stream_t stream) try {
     if (!h || !on_device(h) || !d_q || !d_k || !d_v || !d_out || n < 1) return KVC_ERR_ARG;
     if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out)) return KVC_ERR_ARG;
     const Shape& s = h->sh;
@@ -495,6 +503,8 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
     // ... then every suffix query attends over its window
     if (launch_chunk(h, d_q, d_k, d_v, d_out, n, st) != cudaSuccess) return KVC_ERR_CUDA;
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k, const void* d_v, int64_t kv_stride,
@@ -597,7 +607,7 @@ int kvc_region(kvc_t h, int32_t which, size_t* offset, size_t* bytes) {
     return KVC_OK;
 }
 
-int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t stream) {
+int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t stream) try {
     size_t need = 0;
     int rc = kvc_export_bytes(h, which, &need);
     if (rc) return rc;
@@ -684,6 +694,8 @@ int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t s
         }
     }
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_set_request_id(kvc_t h, int32_t b, uint32_t request_id, kvc_stream_t stream) {

@@ -172,8 +172,9 @@ cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::ve
 // one entry of the host block table gives its page up (entry = -1); the page is free once
 // its last holder did
 void drop_page(kvc_handle* h, int32_t& entry);
-// pages that come free when every request with drop[b] != 0 gives up all of its pages
-int pages_released(const kvc_handle* h, const std::vector<char>& drop);
+// ... the distinct requests reqs[i] give all their pages up and map those of slots [lo[i], hi[i])
+cudaError_t remap_pages(kvc_handle* h, const std::vector<int>& reqs, const std::vector<int>& lo,
+                        const std::vector<int>& hi, cudaStream_t st, int* status);
 cudaError_t launch_trim_cuts(int32_t* next_pos, int32_t* pos, const int32_t* cuts, int B, int S, int ring,
                              cudaStream_t st);
 

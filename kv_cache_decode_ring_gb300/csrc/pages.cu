@@ -294,12 +294,20 @@ void side_of(kvc_handle* h, CopySide* c) {
     c->S = s.S;
 }
 
+// Copies in the order of their sources (worked out before anything changes).
+std::vector<int> by_source(const std::vector<int>& src) {
+    std::vector<int> order(src.size());
+    for (size_t i = 0; i < order.size(); ++i) order[i] = (int)i;
+    std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return src[x] < src[y]; });
+    return order;
+}
+
 // Destinations dst[i] of `to` take the rows of requests src[i] of `from` (src[i] < 0:
 // nothing).  rows_of(b): slots whose rows move.  Destinations of one source share its reads.
 // share: a paged cache's destinations name the source's pages (the host table already does).
 template <typename Rows>
 cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<int>& src, const std::vector<int>& dst,
-                          Rows rows_of, bool share, cudaStream_t st) {
+                          const std::vector<int>& order, Rows rows_of, bool share, cudaStream_t st) {
     const Shape& s = to->sh;
     static thread_local CopyArgs a;       // 5 KB of kernel parameters: not on the stack
     a = CopyArgs{};
@@ -308,9 +316,6 @@ cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<in
     Part parts[kMaxParts];
     a.parts = parts_of(to, parts);
     a.Hkv = s.Hkv; a.d = s.d; a.ring = s.ring; a.int8 = s.int8; a.share = share;
-    std::vector<int> order(src.size());
-    for (size_t i = 0; i < order.size(); ++i) order[i] = (int)i;
-    std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return src[x] < src[y]; });
     const bool wide = (s.int8 ? s.d : s.d * s.elem) % 16 == 0;
     size_t i = 0;
     while (i < order.size()) {
@@ -391,17 +396,35 @@ void drop_page(kvc_handle* h, int32_t& entry) {
     entry = -1;
 }
 
-int pages_released(const kvc_handle* h, const std::vector<char>& drop) {
-    const int npg = h->sh.S / kPage;
+// Too few pages: nothing changes and *status = KVC_ERR_CAPACITY.  Everything is allocated before
+// the books change, here and below: a call that runs out of host memory leaves them as they were.
+cudaError_t remap_pages(kvc_handle* h, const std::vector<int>& reqs, const std::vector<int>& lo,
+                        const std::vector<int>& hi, cudaStream_t st, int* status) {
+    const Shape& s = h->sh;
+    const size_t npg = s.S / kPage, n = reqs.size();
     std::vector<int32_t> left(h->page_ref);
-    int n = 0;
-    for (int b = 0; b < h->sh.B; ++b)
-        if (drop[b])
-            for (int lp = 0; lp < npg; ++lp) {
-                const int32_t e = h->table_h[(size_t)b * npg + lp];
-                if (e >= 0 && --left[e] == 0) ++n;
-            }
-    return n;
+    std::vector<int2> upd;                 // entries that were mapped or will be: the new page
+    upd.reserve(n * npg);
+    long long need = 0, released = 0;
+    for (size_t i = 0; i < n; ++i)
+        for (size_t lp = 0; lp < npg; ++lp) {
+            const size_t idx = reqs[i] * npg + lp;
+            const int32_t e = h->table_h[idx];
+            const bool touched = page_touched(s, (int)lp, lo[i], hi[i]);
+            need += touched;
+            if (e >= 0 && --left[e] == 0) ++released;
+            if (e >= 0 || touched) upd.push_back(make_int2((int)idx, touched ? 1 : -1));
+        }
+    *status = need > released + (long long)h->page_free.size() ? KVC_ERR_CAPACITY : KVC_OK;
+    if (*status != KVC_OK) return cudaSuccess;
+    for (const int2& u : upd) drop_page(h, h->table_h[u.x]);
+    for (int2& u : upd) {
+        if (u.y < 0) continue;
+        u.y = h->table_h[u.x] = h->page_free.back();
+        h->page_free.pop_back();
+        h->page_ref[u.y] = 1;
+    }
+    return update_table(h, upd, st);
 }
 
 // From the host free list; the device table follows on `st`.  On exhaustion nothing
@@ -426,33 +449,43 @@ cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::ve
             }
     struct Need { int idx, old; bool keep; };
     std::vector<Need> need;                // table indices to map, in request and page order
-    for (int b = 0; b < s.B; ++b) {
-        const long long lo = from[b], hi = to[b];
-        if (hi <= lo) continue;
-        const long long first = lo / kPage, count = std::min<long long>((hi - 1) / kPage - first + 1, np);
-        for (long long q = 0; q < count; ++q) {
-            const int lp = (int)((first + q) % np);
-            const size_t idx = (size_t)b * np + lp;
-            const int32_t e = h->table_h[idx];
-            if (e >= 0 && h->page_ref[e] == 1) continue;
-            if (e >= 0) --h->page_ref[e];
-            need.push_back(Need{(int)idx, e, e >= 0 && (s.ring || (!s.int8 && (long long)lp * kPage < lo))});
-        }
-    }
-    *status = KVC_OK;
-    if (need.empty()) return cudaSuccess;
+    auto undo = [&] {
+        for (const Need& x : need)
+            if (x.old >= 0) ++h->page_ref[x.old];
+    };
+    std::vector<int2> upd;
+    std::vector<Move> moves;
     bool copies = false;
-    for (const Need& x : need) copies |= x.old >= 0;
+    *status = KVC_OK;
+    try {
+        for (int b = 0; b < s.B; ++b) {
+            const long long lo = from[b], hi = to[b];
+            if (hi <= lo) continue;
+            const long long first = lo / kPage, count = std::min<long long>((hi - 1) / kPage - first + 1, np);
+            for (long long q = 0; q < count; ++q) {
+                const int lp = (int)((first + q) % np);
+                const size_t idx = (size_t)b * np + lp;
+                const int32_t e = h->table_h[idx];
+                if (e >= 0 && h->page_ref[e] == 1) continue;
+                need.push_back(Need{(int)idx, e, e >= 0 && (s.ring || (!s.int8 && (long long)lp * kPage < lo))});
+                if (e >= 0) --h->page_ref[e];
+                copies |= e >= 0;
+            }
+        }
+        upd.reserve(need.size());
+        moves.reserve(copies ? need.size() : 0);
+    } catch (...) {
+        undo();
+        throw;
+    }
+    if (need.empty()) return cudaSuccess;
     if (need.size() > h->page_free.size()) *status = KVC_ERR_CAPACITY;
     else if (copies && capturing(st)) *status = KVC_ERR_UNSUPPORTED;
     if (*status != KVC_OK) {
-        for (const Need& x : need)
-            if (x.old >= 0) ++h->page_ref[x.old];
+        undo();
         return cudaSuccess;
     }
     // one launch for copies and their table entries
-    std::vector<int2> upd;
-    std::vector<Move> moves;
     for (const Need& x : need) {
         const int page = h->page_free.back();
         h->page_free.pop_back();
@@ -487,7 +520,7 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
         if (has_restored(h, h_src[i])) return KVC_ERR_UNSUPPORTED;
     if (n == 0) return KVC_OK;
     if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
-    std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n);
+    const std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n), order = by_source(src);
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {
         const int npg = s.S / kPage;
@@ -502,7 +535,7 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
             }
     }
     const bool shared = s.pages > 0;       // rows stay where they are
-    if (copy_requests(h, h, src, dst, [&](int b) { return shared ? 0 : held_rows(h, b); }, shared, st) != cudaSuccess)
+    if (copy_requests(h, h, src, dst, order, [&](int b) { return shared ? 0 : held_rows(h, b); }, shared, st) != cudaSuccess)
         return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         h->np[dst[i]] = h->np[src[i]];
@@ -536,34 +569,21 @@ int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_
     }
     if (n == 0) return KVC_OK;
     if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
-    std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n);
+    const std::vector<int> src(h_src, h_src + n), dst(h_dst, h_dst + n), order = by_source(src);
     if (s.pages) {
         // the destinations give back their pages and map those that the rows need
-        const int npg = s.S / kPage;
-        std::vector<int> lo(to->np.begin(), to->np.end()), hi(lo);
-        long long need = 0;
+        std::vector<int> lo(n), hi(n);
         for (int i = 0; i < n; ++i) {
-            const int len = from->np[src[i]];
-            lo[dst[i]] = s.ring && len > s.S ? len - s.S : 0;
-            hi[dst[i]] = len;
-            for (int lp = 0; lp < npg; ++lp) need += page_touched(s, lp, lo[dst[i]], len) ? 1 : 0;
+            hi[i] = from->np[src[i]];
+            lo[i] = s.ring && hi[i] > s.S ? hi[i] - s.S : 0;
         }
-        if (need > pages_released(to, is_dst) + (long long)to->page_free.size()) return KVC_ERR_CAPACITY;
-        std::vector<int2> gone;
-        for (int i = 0; i < n; ++i)
-            for (int lp = 0; lp < npg; ++lp) {
-                int32_t& e = to->table_h[(size_t)dst[i] * npg + lp];
-                if (e < 0) continue;
-                drop_page(to, e);
-                if (!page_touched(s, lp, lo[dst[i]], hi[dst[i]])) gone.push_back(make_int2(dst[i] * npg + lp, -1));
-            }
         int rc = KVC_OK;
-        if (map_pages(to, lo, hi, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
-        if (rc) return rc;                 // not reached: the count above guarantees the pages
-        if (update_table(to, gone, st) != cudaSuccess) return KVC_ERR_CUDA;
+        if (remap_pages(to, dst, lo, hi, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
+        if (rc) return rc;
+    } else if (drop_restored(to, dst, st) != cudaSuccess) {      // (the gate's pool: unpaged caches)
+        return KVC_ERR_CUDA;
     }
-    if (drop_restored(to, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
-    if (copy_requests(to, from, src, dst, [&](int b) { return held_rows(from, b); }, false, st) != cudaSuccess) return KVC_ERR_CUDA;
+    if (copy_requests(to, from, src, dst, order, [&](int b) { return held_rows(from, b); }, false, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int i = 0; i < n; ++i) {
         to->np[dst[i]] = from->np[src[i]];
         to->held_lo[dst[i]] = from->held_lo[src[i]];
@@ -582,14 +602,14 @@ int kvc_free(kvc_t h, int32_t n, const int32_t* h_b, kvc_stream_t stream) try {
     if (!distinct(h_b, n, s.B, &seen)) return KVC_ERR_ARG;
     if (n == 0) return KVC_OK;
     if (capturing(st) || s.Hkv > kMaxGridHeads) return KVC_ERR_UNSUPPORTED;
-    std::vector<int> dst(h_b, h_b + n), none(n, -1);
+    const std::vector<int> dst(h_b, h_b + n), none(n, -1), order = by_source(none);
     if (drop_restored(h, dst, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages) {
         const int npg = s.S / kPage;
         for (int b : dst)
             for (int lp = 0, held = held_pages(h, b); lp < held; ++lp) drop_page(h, h->table_h[(size_t)b * npg + lp]);
     }
-    if (copy_requests(h, h, none, dst, [](int) { return 0; }, s.pages > 0, st) != cudaSuccess) return KVC_ERR_CUDA;
+    if (copy_requests(h, h, none, dst, order, [](int) { return 0; }, s.pages > 0, st) != cudaSuccess) return KVC_ERR_CUDA;
     for (int b : dst) h->np[b] = h->held_lo[b] = 0;
     return KVC_OK;
 } catch (...) {
@@ -617,13 +637,12 @@ int kvc_compact(kvc_t h, int32_t* h_used, kvc_stream_t stream) try {
     }
     if (!moves.empty()) {
         std::vector<int2> upd;
-        if (move_pages(h, moves, st) != cudaSuccess) return KVC_ERR_CUDA;
         for (size_t i = 0; i < h->table_h.size(); ++i) {
-            int32_t& e = h->table_h[i];
-            if (e < 0 || to[e] < 0) continue;
-            e = to[e];
-            upd.push_back(make_int2((int)i, e));
+            const int32_t e = h->table_h[i];
+            if (e >= 0 && to[e] >= 0) upd.push_back(make_int2((int)i, to[e]));
         }
+        if (move_pages(h, moves, st) != cudaSuccess) return KVC_ERR_CUDA;
+        for (const int2& u : upd) h->table_h[u.x] = u.y;
         for (const Move& m : moves) {
             h->page_ref[m.to] = h->page_ref[m.from];
             h->page_ref[m.from] = 0;

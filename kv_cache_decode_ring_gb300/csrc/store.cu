@@ -4,7 +4,7 @@
 // rows between the cache and a store slot of the state buffer.
 #include <algorithm>
 #include <cstring>
-#include <new>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -166,16 +166,17 @@ using namespace kvc;
 
 extern "C" {
 
-int kvc_pstore_create(const kvc_config* cfg, int32_t capacity, kvc_pstore_t* out) {
+int kvc_pstore_create(const kvc_config* cfg, int32_t capacity, kvc_pstore_t* out) try {
     if (!cfg || !out || capacity < 1) return KVC_ERR_ARG;
     Shape s;
     if (!make_shape(*cfg, &s)) return KVC_ERR_ARG;
-    kvc_pstore* ps = new (std::nothrow) kvc_pstore();
-    if (!ps) return KVC_ERR_ARG;
+    std::unique_ptr<kvc_pstore> ps(new kvc_pstore());
     ps->ring = s.ring;
     ps->e.resize(capacity);
-    *out = ps;
+    *out = ps.release();
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_pstore_destroy(kvc_pstore_t ps) {
@@ -185,7 +186,7 @@ int kvc_pstore_destroy(kvc_pstore_t ps) {
 }
 
 int kvc_pstore_insert(kvc_pstore_t ps, const int64_t* h_ids, int32_t n_ids, const char* scope,
-                      const void* h_sig, int32_t sig_bytes, int32_t* h_slot) {
+                      const void* h_sig, int32_t sig_bytes, int32_t* h_slot) try {
     if (!ps || !h_slot || !valid_ids(h_ids, n_ids) || !valid_key(scope, h_sig, sig_bytes)) return KVC_ERR_ARG;
     int slot = -1;
     for (size_t i = 0; i < ps->e.size() && slot < 0; ++i)
@@ -195,18 +196,21 @@ int kvc_pstore_insert(kvc_pstore_t ps, const int64_t* h_ids, int32_t n_ids, cons
         for (size_t i = 1; i < ps->e.size(); ++i)
             if (ps->e[i].seq < ps->e[slot].seq) slot = (int)i;
     }
-    kvc_pstore::Entry& e = ps->e[slot];
+    kvc_pstore::Entry e;                              // whole before it takes the slot
     e.used = true;
-    e.seq = ++ps->seq;
     e.ids.assign(h_ids, h_ids + n_ids);
     e.scope = scope;
     e.sig.assign(static_cast<const uint8_t*>(h_sig), static_cast<const uint8_t*>(h_sig) + sig_bytes);
+    e.seq = ++ps->seq;
+    ps->e[slot] = std::move(e);
     *h_slot = slot;
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_pstore_lookup(kvc_pstore_t ps, const int64_t* h_ids, int32_t n_ids, const char* scope,
-                      const void* h_sig, int32_t sig_bytes, int32_t* h_slot, int32_t* h_cut) {
+                      const void* h_sig, int32_t sig_bytes, int32_t* h_slot, int32_t* h_cut) try {
     if (!ps || !h_slot || !h_cut || !valid_ids(h_ids, n_ids) || !valid_key(scope, h_sig, sig_bytes))
         return KVC_ERR_ARG;
     int best = -1, best_cut = 0;
@@ -223,6 +227,8 @@ int kvc_pstore_lookup(kvc_pstore_t ps, const int64_t* h_ids, int32_t n_ids, cons
     *h_slot = best;
     *h_cut = best_cut;
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_store_save(kvc_t h, int32_t slot, int32_t b, int32_t n, kvc_stream_t stream) {
@@ -240,7 +246,7 @@ int kvc_store_save(kvc_t h, int32_t slot, int32_t b, int32_t n, kvc_stream_t str
 }
 
 int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32_t* h_b, const int32_t* h_cuts,
-                         kvc_stream_t stream) {
+                         kvc_stream_t stream) try {
     if (!h || !on_device(h) || n < 0) return KVC_ERR_ARG;
     const Shape& s = h->sh;
     if (s.store_slots == 0) return KVC_ERR_UNSUPPORTED;
@@ -259,25 +265,14 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.pages) {
         // the requests give back all their pages and map those that the kept rows need
-        const int npg = s.S / kPage;
-        std::vector<int> from(h->np.begin(), h->np.end()), to(from);
-        long long need = 0;
-        const long long held = pages_released(h, seen);      // pages held by these requests alone
+        std::vector<int> reqs(h_b, h_b + n), lo(n), hi(h_cuts, h_cuts + n);
         for (int i = 0; i < n; ++i) {
-            const int b = h_b[i], len = h_slots[i] < 0 ? 0 : h->store_n[h_slots[i]];
-            const long long lo = s.ring && len > s.S ? len - s.S : 0;
-            from[b] = (int)lo; to[b] = h_cuts[i];
-            for (int lp = 0; lp < npg; ++lp) need += page_touched(s, lp, lo, h_cuts[i]) ? 1 : 0;
+            const int len = h_slots[i] < 0 ? 0 : h->store_n[h_slots[i]];
+            lo[i] = s.ring && len > s.S ? len - s.S : 0;
         }
-        if (need > held + (long long)h->page_free.size()) return KVC_ERR_CAPACITY;
-        for (int i = 0; i < n; ++i)
-            for (int lp = 0; lp < npg; ++lp) drop_page(h, h->table_h[(size_t)h_b[i] * npg + lp]);
         int rc = KVC_OK;
-        if (map_pages(h, from, to, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
-        if (rc) return rc;               // not reached: the count above guarantees the pages
-        if (cudaMemcpyAsync(h->state + h->L.table, h->table_h.data(), h->table_h.size() * 4,
-                            cudaMemcpyHostToDevice, st) != cudaSuccess)
-            return KVC_ERR_CUDA;
+        if (remap_pages(h, reqs, lo, hi, st, &rc) != cudaSuccess) return KVC_ERR_CUDA;
+        if (rc) return rc;
     }
     for (int i0 = 0; i0 < n; i0 += kStoreBatch) {
         StoreArgs a = store_args(h, 1);
@@ -293,6 +288,8 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
         h->held_lo[h_b[i]] = s.ring && h_cuts[i] > 0 ? std::min(h->store_lo[h_slots[i]], h_cuts[i]) : 0;
     }
     return KVC_OK;
+} catch (...) {
+    return KVC_ERR_ARG;      // out of host memory
 }
 
 int kvc_store_load(kvc_t h, int32_t slot, int32_t b, int32_t cut, kvc_stream_t stream) {

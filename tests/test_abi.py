@@ -227,3 +227,27 @@ def test_config_struct_matches_the_header():
     assert [n for _, n in fields] == [n for n, _ in mirror]
     ctype = {"int32_t": ctypes.c_int32, "uint32_t": ctypes.c_uint32, "float": ctypes.c_float}
     assert [ctype[t] for t, _ in fields] == [t for _, t in mirror]
+
+
+def test_out_of_host_memory_is_a_status(lib):
+    # a table larger than the address space the process may have: an error code, no exception through the C boundary
+    import sys
+    code = """
+import ctypes, resource, sys
+sys.path.insert(0, %r)
+from kv_cache_decode_ring_gb300 import kvc
+cfg = kvc.make_config("f32", "contiguous", None, 1, 1, 1, 16, 16, store_slots=1)
+kvc.lib()
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (1 << 30),) * 2)
+ps = ctypes.c_void_p(0)
+rc = kvc.lib().kvc_pstore_create(ctypes.byref(cfg), 2 ** 31 - 1, ctypes.byref(ps))
+assert rc == kvc.KVC_ERR_ARG and not ps.value, (rc, ps.value)
+store = kvc.PrefixStore(cfg, 2)
+ids = (ctypes.c_int64 * 4)(1, 2, 3, 4)
+slot = ctypes.c_int32(-1)
+assert kvc.lib().kvc_pstore_insert(store.ps, ids, 4, b"s", None, 0, ctypes.byref(slot)) == kvc.KVC_OK
+assert store.lookup([1, 2, 3, 4, 5], "s") == (slot.value, 4)
+""" % ROOT
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
