@@ -452,3 +452,50 @@ def test_refusals():
     assert paged.page_counts() == (2, 0)
     paged.prompt(q, k, v, [16, 1])
     assert paged.page_counts() == (0, 0)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,window", [(128, 8, 2, 0), (64, 8, 1, 0), (128, 4, 4, 1500), (64, 4, 1, 1500)])
+@pytest.mark.parametrize("cut,n", [(2750, 250), (2990, 10), (0, 3000)])
+def test_long_rows_by_their_root_mean_square(d, Hq, Hkv, window, cut, n):
+    # The bound above has every weight rounded the same way; over many keys one lost key would hide in it.
+    # Roundings of p_j to bf16 do not depend on one another: |e_j| <= 2^-8, so an output's error has a root
+    # mean square of at most 2^-8 sqrt(sum p_j^2 v_j^2).  Scores of 128 products, 2^x and sums over 3000 keys
+    # in fp32 stay below 2^-13 sqrt(sum p_j^2 v_j^2) + 2^-16 |o| beside it.  The mean over thousands of
+    # outputs is held to that plus a tenth; a key left out of 3000 equal ones would read 5 times as much.
+    t = Twin("bf16", 1, Hq, Hkv, d, 3008, window=window, base=0.0, out="f32")
+    t.prefill([cut])
+    qkv = t.draw(n, Hq + 2 * Hkv)
+    qkv[:, :Hq] *= 0.25                                              # weights spread over the keys
+    got, _ = t.prompt([n], qkv=qkv)
+    rows = [i for i in range(n) if cut + i >= 1000][-300:]
+    q, K, V = qkv[rows, :Hq].double(), t.K[0].double(), t.V[0].double()
+    p = torch.tensor([cut + i for i in rows])[:, None]
+    j = torch.arange(cut + n)
+    seen = (j <= p) & ((j > p - window) if window else (j >= 0))
+    err, allowed = 0.0, 0.0
+    for h in range(Hq):
+        k, v = K[:, h * Hkv // Hq], V[:, h * Hkv // Hq]
+        w = torch.softmax((q[:, h] @ k.T / math.sqrt(d)).masked_fill(~seen, -math.inf), -1)
+        err += (got[rows, h].double() - w @ v).square().sum().item()
+        allowed += (2.0 ** -8 + 2.0 ** -13) ** 2 * (w.square() @ v.square()).sum().item() + (2.0 ** -16) ** 2 * (w @ v).square().sum().item()
+    assert err <= 1.1 ** 2 * allowed, math.sqrt(err / allowed)
+
+
+@pytest.mark.parametrize("d,n,cut", [(128, 130, 2800), (64, 130, 2800), (128, 2, 2990), (64, 2, 2990), (128, 1000, 0)])
+def test_equal_keys_lose_none(d, n, cut):
+    # equal scores: every weight is the same and rounds to 1 in bf16, so an output is the mean of the values
+    # to fp32 accumulation: at most 3000 / 16 + 32 sums, each off by 2^-22 of the largest partial sum (of any
+    # run of keys: twice the largest of those from the first one).  The weights' fp32 sum is off by the
+    # rounding of the scaled maximum, below 32: 2^-20 ln 2, and the quotient by 2^-22
+    t = Twin("bf16", 1, 4, 1, d, 3008, base=0.0, out="f32")
+    k = torch.ones(1, 1, cut, d, dtype=torch.bfloat16)
+    v = wl.normal((cut + n, 1, d), 9, "equal%d" % d, dtype=torch.bfloat16)
+    if cut:
+        t.cache.append_rows(k.cuda(), v[:cut].transpose(0, 1)[None].contiguous().cuda())
+    q = torch.ones(n, 4, d, dtype=torch.bfloat16, device="cuda")
+    out = t.cache.prompt(q, torch.ones(n, 1, d, dtype=torch.bfloat16, device="cuda"), v[cut:].cuda(), [n]).cpu().double()
+    sums = v[:, 0].double().cumsum(0)
+    count = torch.arange(1, cut + n + 1, dtype=torch.float64)[:, None]
+    mean = (sums / count)[cut:]
+    bound = (220 * 2.0 ** -22 * 2 * sums.abs().cummax(0).values / count)[cut:] + 2.0 ** -19 * mean.abs()
+    assert ((out - mean[:, None]).abs() <= bound[:, None]).all(), ((out - mean[:, None]).abs() / bound[:, None]).max()
