@@ -34,11 +34,16 @@ __device__ __forceinline__ bool position_ok(const AppendArgs& a, long long p) {
     return true;
 }
 
-// Whether a page is mapped for `slot` of request b.  The host maps the pages of every call, but a
-// captured call replays on from there: rows behind its pages are not written (kv_row and int8_block
-// would put them into page 0, which is some request's) and flagged.
-__device__ __forceinline__ bool page_mapped(const AppendArgs& a, int b, int slot) {
-    return !a.table || a.table[(size_t)b * (a.S / kPage) + slot / kPage] >= 0;
+// Page of `slot` of request b, < 0 if none is mapped (an unpaged cache: 0).  The host maps the pages
+// of every call, but a captured call replays on from there: rows behind its pages are not written
+// (kv_row and int8_block would put them into page 0, which is some request's) and flagged.
+__device__ __forceinline__ int slot_page(const AppendArgs& a, int b, int slot) {
+    return a.table ? a.table[(size_t)b * (a.S / kPage) + slot / kPage] : 0;
+}
+
+// Row of KV head h in that page (as kv_row, which would read the table again).
+__device__ __forceinline__ size_t slot_row(const AppendArgs& a, int b, int h, int slot, int page) {
+    return a.table ? ((size_t)page * a.Hkv + h) * kPage + slot % kPage : ((size_t)b * a.Hkv + h) * a.S + slot;
 }
 
 // Stored value of element pair (2i, 2i+1) of a key row at position p.
@@ -153,7 +158,7 @@ __device__ void quantize_block(const AppendArgs& a, const float* sK, const float
 // arrival counter, reset by that CTA) writes positions[slot] and advances
 // next_position[b], so no CTA can read the advanced value.
 // PAGED: rows go to the slot's page, read once beside the rows' loads; a row without one is flagged
-// (page_mapped).  One kernel for both took 2.25 us an append where these take 2.15, and 2.31 paged
+// (slot_page).  One kernel for both took 2.25 us an append where these take 2.15, and 2.31 paged
 // (16 requests of 8 KV heads of 128).
 template <bool PAGED>
 __global__ void __launch_bounds__(kThreads) append_token_kernel(const AppendArgs a) {
@@ -301,11 +306,12 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const AppendArgs 
     }
     const int slot = a.ring ? (int)(p % a.S) : (int)p;
     const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr;
-    if (!page_mapped(a, b, slot)) {
+    const int page = slot_page(a, b, slot);
+    if (page < 0) {
         flag(a.hdr, kErrPosition);
         return;
     }
-    const size_t dst = kv_row(a.table, b, h, slot, a.Hkv, a.S) * d;
+    const size_t dst = slot_row(a, b, h, slot, page) * d;
     float y0, y1;
     key_pair(a, a.k, src, i, (int)p, y0, y1);
     store_pair(a.kc, dst + 2 * i, y0, y1, a.bf16);
@@ -334,6 +340,7 @@ __global__ void __launch_bounds__(kThreads) append_rows_vec_kernel(const AppendA
         return;
     }
     const int slot = a.ring ? (int)(p % a.S) : (int)p;
+    const int page = slot_page(a, b, slot);           // (on its way while the row's loads are)
     const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr + 8 * (size_t)c;
     const uint4 kx = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src));
     const uint4 vx = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src));
@@ -354,11 +361,11 @@ __global__ void __launch_bounds__(kThreads) append_rows_vec_kernel(const AppendA
         }
         ko = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (!page_mapped(a, b, slot)) {
+    if (page < 0) {
         flag(a.hdr, kErrPosition);
         return;
     }
-    const size_t dst = kv_row(a.table, b, h, slot, a.Hkv, a.S) * a.d + 8 * (size_t)c;
+    const size_t dst = slot_row(a, b, h, slot, page) * a.d + 8 * (size_t)c;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.kc) + dst) = ko;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.vc) + dst) = vx;
     if (h == 0 && c == 0) a.pos[(size_t)b * a.S + slot] = (int)p;
@@ -378,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const AppendArg
     if (p0 + kQBlock > np + cnt) return;             // block not completed by this call
     // a ring keeps the newest S/16 complete blocks: one overwritten later in this call is skipped
     if (a.ring && p0 < ((np + cnt) / kQBlock) * kQBlock - a.S) return;
-    if (!position_ok(a, (long long)p0 + kQBlock - 1) || !page_mapped(a, b, a.ring ? p0 % a.S : p0)) {
+    if (!position_ok(a, (long long)p0 + kQBlock - 1) || slot_page(a, b, a.ring ? p0 % a.S : p0) < 0) {
         if (threadIdx.x == 0) flag(a.hdr, kErrPosition);
         return;
     }
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(kThreads) tail_kernel(const AppendArgs a, cons
         const int h = idx / ((end - first) * half);
         const int rem = idx % ((end - first) * half);
         const int p = first + rem / half, i = rem % half;
-        if (!position_ok(a, p) || !page_mapped(a, b, a.ring ? p % a.S : p)) { flag(a.hdr, kErrPosition); continue; }
+        if (!position_ok(a, p) || slot_page(a, b, a.ring ? p % a.S : p) < 0) { flag(a.hdr, kErrPosition); continue; }
         const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)(p - np) * a.sr;
         const size_t tail = (((size_t)b * a.Hkv + h) * kQBlock + p % kQBlock) * d;
         float k0, k1;
