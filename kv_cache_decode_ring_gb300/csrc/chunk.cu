@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int slot = a.ring ? pos % a.S : pos;
                         if (a.table) {
                             int page = a.table[(size_t)b * npages + slot / kPage];
-                            page = page < 0 ? 0 : page;      // never taken: every page the CTA reads is mapped
+                            page = page < 0 ? 0 : page;      // (unmapped: only where a replay's append was flagged)
                             r = (page * a.Hkv + kvh) * kPage;
                         } else {
                             r = head_row0 + slot;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
                 for (int j = 0, r = 0; j < kRuns; ++j) {
                     if (r >= nk) break;
                     const int run = min(nk - r, kPage - (k0 + r) % kPage);
-                    const int page = pf[j] < 0 ? 0 : pf[j];    // never taken: every slot read is mapped
+                    const int page = pf[j] < 0 ? 0 : pf[j];    // (unmapped: only behind a replay's flagged append)
                     const size_t row = ((size_t)page * a.Hkv + kvh) * kPage + (k0 + r) % kPage;
                     bulk_copy_g2s(myK + r * C::ROWB, Kg + row * D, (uint32_t)run * C::ROWB, &bar[warp_]);
                     bulk_copy_g2s(myV + r * C::ROWB, Vg + row * D, (uint32_t)run * C::ROWB, &bar[warp_]);
