@@ -620,3 +620,75 @@ def test_what_trimmed_rows_overwrote_stays_lost():
     c.decode(q)
     c.trim([1])
     c.decode(q)
+
+
+@pytest.mark.parametrize("seed", range(3))
+@pytest.mark.parametrize("pages", [0, 16], ids=["rows", "pages"])
+def test_random_ring_trims(pages, seed):
+    # what a ring may be trimmed to, loaded at and decoded from, against slots that are simulated one by one
+    W, B = 32, 3
+    m = Model(B=B, d=64, cap=W, layout="ring", pages=pages)
+    cfg = kvc.make_config(batch=B, page_pool=pages, store_slots=2, **m.kw)
+    m.cache = c = kvc.Cache(cfg)
+    m.rng = rng = random.Random(seed)
+    slots = [{} for _ in range(B)]                                # slot -> position
+    store = [None, None]                                          # (slots, tokens)
+    q = wl.normal((B, 4, 64), 3, "q", "cuda", c.torch_dtype)
+
+    def held(s, lo, hi):
+        return all(s.get(p % W) == p for p in range(max(0, lo), hi))
+
+    def put(b, lo):
+        for p in range(lo, len(m.ids[b])):
+            slots[b][p % W] = p
+
+    def accepted(f):
+        try:
+            f()
+            return True
+        except kvc.KvcError as e:
+            assert e.code in (kvc.KVC_ERR_EVICTED, kvc.KVC_ERR_ARG)
+            return False
+
+    for step in range(120):
+        n = [len(x) for x in m.ids]
+        op = rng.choice(["rows", "rows", "append", "prompt", "trim", "trim", "fork", "free", "save", "load", "copy"])
+        if op in ("rows", "prompt"):
+            m.append_rows([rng.choice([0, 0, 1, 2, 20, 60]) for _ in range(B)], op == "prompt")
+        elif op == "append":
+            m.append()
+        elif op == "trim":
+            cuts = [rng.choice([x, x, max(0, x - 1), max(0, x - 2), rng.randint(0, x)]) for x in n]
+            want = all(held(s, cut - W + 1, cut) for s, cut in zip(slots, cuts))
+            assert accepted(lambda: c.trim(cuts)) == want, (step, n, cuts)
+            if want:
+                m.ids = [ids[:cut] for ids, cut in zip(m.ids, cuts)]
+                slots = [{k: p for k, p in s.items() if p < cut} for s, cut in zip(slots, cuts)]
+        elif op in ("fork", "copy"):
+            a, b = rng.sample(range(B), 2)
+            m.fork([a], [b]) if op == "fork" else m.copy_from(m, [a], [b])
+            slots[b] = dict(slots[a])
+        elif op == "free":
+            b = rng.randrange(B)
+            m.free([b])
+            slots[b] = {}
+        elif op == "save" and max(n):
+            b, i = rng.choice([b for b in range(B) if n[b]]), rng.randrange(2)
+            c.store_save(i, b, n[b])
+            store[i] = (dict(slots[b]), list(m.ids[b]))
+        elif op == "load" and store[0] and store[1]:
+            b, i = rng.randrange(B), rng.randrange(2)
+            s, ids = store[i]
+            cut = rng.choice([len(ids), max(0, len(ids) - 1), max(0, len(ids) - 2)])
+            want = held(s, cut - W + 1, cut)
+            assert accepted(lambda: c.store_load(i, b, cut)) == want, (step, len(ids), cut)
+            if want:
+                m.ids[b], slots[b] = ids[:cut], {k: p for k, p in s.items() if p < cut}
+        for b in range(B):
+            if len(m.ids[b]) > n[b] and op in ("rows", "prompt", "append"):
+                put(b, n[b])
+        whole = [held(s, len(x) - W, len(x)) for s, x in zip(slots, m.ids)]
+        if min(len(x) for x in m.ids):
+            assert accepted(lambda: c.decode(q)) == all(whole), (step, op, whole)
+            if all(whole) and step % 5 == 0:
+                m.check()
