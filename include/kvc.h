@@ -297,9 +297,12 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * Appends every row as kvc_append_rows does and answers row i of request b at
  * p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32 and
  * rounded to the cache's type, as the keys are; sums and softmax are fp32.  bf16 caches with
- * head_dim 64 or 128 run on the tensor cores, where the softmax weights are rounded to bf16
- * too (relative error at most 2^-8 each; their sum is fp32); other shapes run in fp32
- * throughout.  What a masked key or value row holds, infinities and NaN among it, does not
+ * head_dim 64 or 128 (below 2^31 rows of all heads, at most 128 query heads a KV head) run on
+ * the tensor cores, where the softmax weights are rounded to bf16 too (relative error at most
+ * 2^-8 each; their sum is fp32); other shapes run on the CUDA cores in fp32 throughout, far
+ * slower.  Where a call's rows fill few SMs, the keys of a row are split over several, as far
+ * as the state's split-K workspace reaches: it holds the decode's partial sums, those of a
+ * few rows a request.  Calls of some hundred rows behind long prefixes run unsplit.  What a masked key or value row holds, infinities and NaN among it, does not
  * reach the result.
  * d_out must not overlap the ranges that the inputs span (from their first row to their last);
  * its rows hold intermediate values during the call.

@@ -17,14 +17,14 @@
 //  * Tensor memory: S of both slots (fp32), their weights P (bf16 pairs, the A operand of P.V) and
 //    O (fp32) in columns of their own: with d = 128 that leaves tiles of 80 keys, with d = 64
 //    of 128.  So S(j + 1) runs while the softmax works on S(j).  (Tiles of 128 keys with P over S,
-//    where S(j + 1) waits for P.V(j), took 2.4 ms against 1.4 for 16384 tokens of 32 heads.)
+//    where S(j + 1) waits for P.V(j), took 2.4 ms a call for 16384 tokens of 32 heads: 1.63 now.)
 //  * All operands are bf16: q and the keys as the cache's type holds them, the weights
 //    rounded once (relative error 2^-8, at most 2^8 in size).  fp16 weights (2^-11) would
 //    need the values in fp16 too: a conversion pass over every tile and a narrower range.
 //  * With RoPE the queries come rotated, in d_out's rows (prompt_rows_kernel): a unit copies its
 //    queries from the rows that it writes at its end.  Rotating them here, by two warps beside
-//    the softmax, took longer than a short unit's products (ragged prompts 0.30 against
-//    0.20 ms).
+//    the softmax, took longer than a short unit's products (ragged prompts 0.30 ms a call, 0.178
+//    now).
 //  * A row's reference maximum moves only when a tile exceeds it by more than 2^8 (log2
 //    domain); the softmax thread then rescales its O row itself (no P.V of its slot in flight).
 //  * Masked scores are replaced, not added to, so a masked key may hold anything.  A masked
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // (every box's row at hand before the first is issued, one tensor map unless the cache
                 // is a ring: with a shuffle before each, two maps to choose from, a tile's boxes took
-                // longer than its products, ragged prompts 0.176 against 0.161 ms)
+                // longer than its products, ragged prompts 0.192 ms a call against 0.177)
                 int r[kBN / 16];
 #pragma unroll
                 for (int gi = 0; gi < kBN / 16; ++gi) r[gi] = __shfl_sync(0xffffffffu, row, gi);
