@@ -302,8 +302,8 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * 2^-8 each; their sum is fp32); other shapes run on the CUDA cores in fp32 throughout, far
  * slower.  Where a call's rows fill few SMs, the keys of a row are split over several, as far
  * as the state's split-K workspace reaches: it holds the decode's partial sums, those of a
- * few rows a request.  Calls of some hundred rows behind long prefixes run unsplit.  What a masked key or value row holds, infinities and NaN among it, does not
- * reach the result.
+ * few rows a request.  Calls of some hundred rows behind long prefixes run unsplit.  What a
+ * masked key or value row holds, infinities and NaN among it, does not reach the result.
  * d_out must not overlap the ranges that the inputs span (from their first row to their last);
  * its rows hold intermediate values during the call.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
