@@ -183,8 +183,8 @@ int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n,
  * evaluated as split-K flash decoding with an online softmax and a cross-split
  * combine, fp32 accumulation, rounded once to the output dtype.  Needs at least
  * one cached token per request; KVC_ERR_ARG too while a request of a ring lacks a key of
- * that window: a ring that wrapped and was then trimmed (or loaded short of a slot's end)
- * has overwritten it, until the request itself appends.
+ * that window: a bf16 or fp32 ring that wrapped and was then trimmed (or loaded short of a
+ * slot's end) has overwritten it, until the request itself appends.
  * INT8 caches also return, per (request, query head), the witness bound
  * ([WITCERT] "频带酉性与双层证书"):
  *     c_t = (1/sqrt d) sum_b ||q_b|| w_{t,b}   for every cached token in the window,
@@ -259,10 +259,10 @@ int kvc_decode_attn_noalloc(kvc_t h, const void* d_q, void* d_out, kvc_stream_t 
  * = cut).  h_cut: host, B entries, 0 <= cut <= next_position.  Rows at
  * positions >= cut are dropped (positions set to -1).  A ring accepts the cut
  * only if every position the next query needs is still resident, i.e. with
- * lo = max(0, cut-W+1): lo == cut or lo >= max(0, top-W), top the largest next_position
- * since the ring last held lo (what earlier trims dropped had overwritten rows); an INT8
- * cache only if no quantized block is split (cut % 16 == 0 or cut within the
- * exact tail).  Otherwise KVC_ERR_EVICTED and nothing changes. */
+ * lo = max(0, cut-W+1): lo == cut, or lo >= max(0, next_position-W) and no row that
+ * an earlier trim dropped had overwritten lo; an INT8 cache only if no quantized
+ * block is split (cut % 16 == 0 or cut within the exact tail).  Otherwise
+ * KVC_ERR_EVICTED and nothing changes. */
 int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream);
 
 /* Chunked causal suffix attention after a trim ([PREFIX] model.chunk(tokens[cut:],

@@ -439,7 +439,7 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) try {
     for (int b = 0; b < s.B; ++b) {
         const int cut = h_cut[b], np = h->np[b];
         if (cut < 0 || cut > np) return KVC_ERR_ARG;
-        if (s.ring && !ring_cut_ok(h, h->held_lo[b], cut)) return KVC_ERR_EVICTED;
+        if (s.ring && !ring_cut_ok(h, np, h->held_lo[b], cut)) return KVC_ERR_EVICTED;
         if (s.int8 && (cut % kQBlock) && cut < (np / kQBlock) * kQBlock) return KVC_ERR_EVICTED;
     }
     if (launch_trim_cuts(at<int32_t>(h, h->L.next_pos), at<int32_t>(h, h->L.pos), h_cut, s.B, s.S, s.ring,

@@ -380,8 +380,9 @@ struct kvc_handle {
     int device;
     int num_sms;
     std::vector<int32_t> np;      // host mirror of next_position
-    // rings: positions [held_lo[b], np[b]) are all in their slots.  Appends move it up to np - W; a
-    // trim does not bring back what the dropped rows overwrote, so it stays
+    // rings: positions [held_lo[b], np[b]) are all in their slots.  Appends move it up to np - W (INT8
+    // tiers: blocks are overwritten whole, when a newer one completes); a trim does not bring back
+    // what the dropped rows overwrote, so it stays
     std::vector<int32_t> held_lo;
     std::vector<int32_t> counts;   // host staging for append_rows counts
     kvc::KvMaps kv_maps;           // built at create when the GQA decode serves the shape
@@ -409,7 +410,8 @@ inline bool on_device(const kvc_handle* h) {
 // Request b has n rows more.
 inline void add_rows(kvc_handle* h, int b, int n) {
     h->np[b] += n;
-    if (h->sh.ring && n > 0 && h->np[b] - h->sh.S > h->held_lo[b]) h->held_lo[b] = h->np[b] - h->sh.S;
+    const int written = h->sh.int8 ? h->np[b] / kvc::kQBlock * kvc::kQBlock : h->np[b];
+    if (h->sh.ring && written - h->sh.S > h->held_lo[b]) h->held_lo[b] = written - h->sh.S;
 }
 
 // Whether the window of every request's newest row is there: not on a ring that was trimmed (or
@@ -420,10 +422,11 @@ inline bool windows_held(const kvc_handle* h) {
     return true;
 }
 
-// Whether a ring's request that holds [held, ...) can go on at `cut`: the row there sees [cut - W + 1, cut].
-inline bool ring_cut_ok(const kvc_handle* h, int held, int cut) {
+// Whether a ring's request of `len` rows that holds [held, len) can go on at `cut`: the row there sees
+// [cut - W + 1, cut].  (One row back at a time, whatever else an INT8 ring's blocks still hold.)
+inline bool ring_cut_ok(const kvc_handle* h, int len, int held, int cut) {
     const int lo = cut - h->sh.S + 1 > 0 ? cut - h->sh.S + 1 : 0;
-    return lo == cut || lo >= held;
+    return lo == cut || (lo >= held && lo >= len - h->sh.S);
 }
 
 // Whether `st` is being captured into a graph (true also where the runtime cannot tell).

@@ -260,7 +260,7 @@ int kvc_store_load_batch(kvc_t h, int32_t n, const int32_t* h_slots, const int32
         seen[b] = 1;
         const int len = slot < 0 ? 0 : h->store_n[slot];
         if (len < 0 || cut < 0 || cut > len) return KVC_ERR_ARG;
-        if (s.ring && cut > 0 && !ring_cut_ok(h, h->store_lo[slot], cut)) return KVC_ERR_EVICTED;
+        if (s.ring && cut > 0 && !ring_cut_ok(h, len, h->store_lo[slot], cut)) return KVC_ERR_EVICTED;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (s.pages) {

@@ -516,14 +516,14 @@ def test_replayed_appends_past_the_mapped_pages_are_reported(kind, call):
 def test_a_trimmed_ring_waits_for_a_row_of_every_request_that_lost_one():
     # a wrapped ring has overwritten the first key of the window of the row at cut - 1: until the request
     # appends, its decode would lack that key.  Rows of other requests do not lift the guard
-    for quant, rows in ((None, "append_rows"), (None, "prompt"), ("int8", "append_rows")):
-        m = Model(B=3, d=64, cap=48, layout="ring", quant=quant)
+    for rows in ("append_rows", "prompt"):
+        m = Model(B=3, d=64, cap=48, layout="ring")
         m.append_rows([100, 20, 130])
         m.trim([99, 20, 130])
         q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
 
         def decodes():
-            calls = [m.cache.decode] + ([] if quant else [lambda q: kvc.kvc_decode_attn_noalloc(m.cache.h, q, torch.empty_like(q))])
+            calls = [m.cache.decode, lambda q: kvc.kvc_decode_attn_noalloc(m.cache.h, q, torch.empty_like(q))]
             answers = set()
             for f in calls:
                 try:
@@ -537,7 +537,7 @@ def test_a_trimmed_ring_waits_for_a_row_of_every_request_that_lost_one():
 
         assert not decodes()
         m.append_rows([0, 3, 1], rows == "prompt")
-        assert not decodes(), (quant, rows)
+        assert not decodes(), rows
         m.fork([0], [1])                                          # the branch lacks the same key
         m.append_rows([1, 0, 0], rows == "prompt")
         assert not decodes()
@@ -692,3 +692,28 @@ def test_random_ring_trims(pages, seed):
             assert accepted(lambda: c.decode(q)) == all(whole), (step, op, whole)
             if all(whole) and step % 5 == 0:
                 m.check()
+
+
+@pytest.mark.parametrize("quant", ["int8", "int8-dither"])
+def test_a_trimmed_int8_ring_still_holds_its_window(quant):
+    # an INT8 ring overwrites a block when a newer one completes, and a wrapped one is trimmed within its exact
+    # tail only: blocks and tail hold every key, before the next append and beside rows of other requests
+    def cache(counts):
+        m = Model(B=2, d=64, cap=48, layout="ring", quant=quant)
+        m.rng = random.Random(7)
+        m.append_rows(counts)
+        return m
+
+    q = wl.normal((2, 4, 64), 3, "q", "cuda", torch.bfloat16)
+    m = cache([105, 70])
+    for cut in (104, 103):
+        m.trim([cut, 70])
+        fresh = kvc.Cache(kvc.make_config(batch=2, **m.kw))
+        k, v = (torch.stack([t[:105] for t in x]).transpose(1, 2).contiguous() for x in zip(*(m.rows((ids + [0] * 105)[:105]) for ids in m.ids)))
+        fresh.append_rows(k, v, counts=[cut, 70])
+        assert torch.equal(m.cache.decode(q), fresh.decode(q)), cut
+    m.append_rows([0, 3])
+    assert torch.equal(m.cache.decode(q)[0], fresh.decode(q)[0])
+    with pytest.raises(kvc.KvcError) as e:
+        m.trim([100, 73])                                         # one row back at a time
+    assert e.value.code == kvc.KVC_ERR_EVICTED
