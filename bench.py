@@ -65,7 +65,7 @@ TRAFFIC_PER_BYTE = {
     "prefix-reuse-store": ("chunk.cu", "cf79894d12223712", (83959552 + 3649792) / 60850176),   # the same chunk launch
     # the store's batched row copy (8 requests' cuts, 297.9 MB read + written): writes still in L2
     # at the end of the launch are not counted, so the ratio is below 1
-    "store-load": ("store.cu", "19efb80c41d4a514", (149272576 + 95380736) / 297918464),
+    "store-load": ("store.cu", "0f1321b7e2b2ca27", (149272320 + 95259904) / 297918464),
 }
 
 
