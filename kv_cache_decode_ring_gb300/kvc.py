@@ -141,7 +141,8 @@ def _stream(stream) -> int:
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A new tensor in memory of ``stream``, which will write it: memory of the current stream may still
-    be in use there by work enqueued before its last owner let go of it."""
+    be in use there by work enqueued before its last owner let go of it.  The current stream, where the
+    caller goes on with it, is recorded: its work is over before the memory is handed out again."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     device = torch.device(device)
@@ -153,7 +154,9 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
         # (1 is the legacy default stream by its special handle)
         stream = torch.cuda.default_stream(index) if raw in (0, 1) else torch.cuda.ExternalStream(raw, index)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(index))
+    return out
 
 
 def _dev(t: Optional[torch.Tensor], dtype=None, shape=None, name="tensor") -> ctypes.c_void_p:
@@ -365,8 +368,8 @@ def kvc_rope_axes(x, pos, sections: Sequence[int], base: float = 10000.0, out=No
                   stream=None):
     """x [rows, heads, d] (bf16 or fp32, heads dense, row stride free) rotated by several axes:
     ``pos`` int32 [axes, rows], ``sections`` the pairs of each axis.  ``out`` may be x; a new dense
-    tensor (memory of ``stream``) if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1); ``per_axis``: a spectrum
-    for each axis.  See include/kvc.h."""
+    tensor (memory of ``stream``) if None.  ``halves``: pairs (p, P + p) instead of (2p, 2p + 1);
+    ``per_axis``: a spectrum for each axis.  See include/kvc.h."""
     dtype = _ROPE_DTYPES.get(x.dtype)
     if dtype is None:
         raise ValueError("x must be bfloat16 or float32, got %s" % x.dtype)

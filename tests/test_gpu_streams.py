@@ -79,3 +79,24 @@ def test_the_state_belongs_to_the_stream_that_clears_it():
     at = held.data_ptr()
     del held
     assert kvc.Cache(cfg, stream=torch.cuda.Stream()).state.data_ptr() != at
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_outputs_outlive_the_current_streams_work(raw):
+    # an output let go of while the current stream still has to read it is not handed to the next call
+    s = torch.cuda.Stream()
+    on = s.cuda_stream if raw else s
+    x = torch.randn(4096, 64, 128, device="cuda")
+    pos, zero = (torch.full((1, 4096), p, dtype=torch.int32, device="cuda") for p in (1, 0))
+    want, copy = kvc.kvc_rope_axes(x, pos, [64]), torch.empty_like(x)
+    torch.cuda.synchronize()
+    out = kvc.kvc_rope_axes(x, pos, [64], stream=on)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(200_000_000)
+    copy.copy_(out)
+    at = out.data_ptr()
+    del out
+    again = kvc.kvc_rope_axes(x, zero, [64], stream=on)
+    assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want) and torch.equal(again, x)
