@@ -68,7 +68,7 @@ typedef void* kvc_stream_t; /* a cudaStream_t */
 /* ---- configuration --------------------------------------------------- */
 enum { KVC_F32 = 0, KVC_BF16 = 1 };
 enum { KVC_CONTIGUOUS = 0, KVC_RING = 1 };
-enum { KVC_QUANT_NONE = 0, KVC_QUANT_INT8 = 1, KVC_QUANT_INT8_DITHER = 2 };
+enum { KVC_QUANT_NONE = 0, KVC_QUANT_INT8 = 1, KVC_QUANT_INT8_DITHER = 2, KVC_QUANT_INT4 = 3 };
 
 typedef struct {
     int32_t dtype;        /* KVC_F32 or KVC_BF16 */
@@ -76,7 +76,8 @@ typedef struct {
                              ([LOOP] §三, preallocated (B, H, max_S, D) buffers);
                              KVC_RING: slot = position mod W, capacity = W
                              ([LEAN] §3.4 ring buffer, §2.3 lastWindow) */
-    int32_t kv_quant;     /* KVC_QUANT_NONE, KVC_QUANT_INT8_DITHER (Tier B, see
+    int32_t kv_quant;     /* KVC_QUANT_NONE, KVC_QUANT_INT4 (see "4-bit rows" below),
+                             KVC_QUANT_INT8_DITHER (Tier B, see
                              dither_key_lo below) or KVC_QUANT_INT8 ([WITCERT]; bf16
                              caches, contiguous with any window or a ring.  Blocks are
                              16 positions; a ring of W slots, W % 16 == 0, keeps block n
@@ -248,7 +249,7 @@ int kvc_set_request_id(kvc_t h, int32_t b, uint32_t request_id, kvc_stream_t str
  *       64 otherwise.
  *   - KVC_ERR_ARG for the cases kvc_decode_attn refuses, or if the current device
  *     is not the handle's.
- *   - KVC_ERR_UNSUPPORTED for an INT8 cache.
+ *   - KVC_ERR_UNSUPPORTED for an INT8 or INT4 cache.
  * It calls no cudaMalloc, cudaFree or other allocating routine. */
 #define KVC_NOALLOC_SCRATCH_BYTES (64u << 20)
 /* See the comment above KVC_NOALLOC_SCRATCH_BYTES: d_q, d_out as for kvc_decode_attn. */
@@ -307,7 +308,7 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * d_out must not overlap the ranges that the inputs span (from their first row to their last);
  * its rows hold intermediate values during the call.
  * Rows of d_out at and after T, and requests with a count of 0, are left as they are.
- * All tiers but INT8; a ring needs a bf16 cache with W a multiple of 16, and counts of at
+ * All tiers but INT8 and INT4; a ring needs a bf16 cache with W a multiple of 16, and counts of at
  * most max_chunk (its rows are staged, as kvc_chunk_attn's are).
  * A captured call appends at the device's next_position.  A replay that passes the capacity, or
  * on a paged cache the pages mapped at capture (those of that one call), writes no row there
@@ -315,8 +316,8 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * KVC_ERR_ARG: a negative count, a count above max_chunk on a ring, T > 2^31 - 1, a stride
  * below the row or of 2^38 elements, or one that is no multiple of 16 bytes where a head's
  * row is one, or an overlap.
- * KVC_ERR_CAPACITY: as kvc_append_rows; nothing is written.  KVC_ERR_UNSUPPORTED: INT8
- * caches, other rings, more than 65534 query heads. */
+ * KVC_ERR_CAPACITY: as kvc_append_rows; nothing is written.  KVC_ERR_UNSUPPORTED: INT8 and
+ * INT4 caches, other rings, more than 65534 query heads. */
 int kvc_prompt_attn(kvc_t h, const void* d_q, int64_t q_stride, const void* d_k, const void* d_v,
                     int64_t kv_stride, const int32_t* h_counts, void* d_out, kvc_stream_t stream);
 
@@ -351,8 +352,8 @@ int kvc_fork(kvc_t h, int32_t n, const int32_t* h_src, const int32_t* h_dst, kvc
 
 /* Requests h_dst[i] of cache `to` become copies of requests h_src[i] of cache `from`, with
  * rows of their own (on a paged cache, pages of their own).  Both caches on the current
- * device, with the same dtype, kv_quant, layout, n_kv_heads, head_dim and rope_base (and,
- * in Tier B, layer and key); paged or not, batch, query heads and, on contiguous caches,
+ * device, with the same dtype, kv_quant (but for bf16 and INT4, which convert: "4-bit rows"),
+ * layout, n_kv_heads, head_dim and rope_base (and, in Tier B, layer and key); paged or not, batch, query heads and, on contiguous caches,
  * capacity and window may differ; rings are of the same W.  to == from is allowed: a
  * destination must not be a source then.  The caller orders the streams of the two handles.
  * KVC_ERR_ARG: other caches or a bad index.  KVC_ERR_CAPACITY: rows beyond the capacity
@@ -399,6 +400,26 @@ int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride
                   int64_t rows, int32_t heads, int32_t head_dim, const int32_t* d_pos,
                   int32_t n_axes, const int32_t* h_sections, double base, int32_t flags,
                   kvc_stream_t stream);
+
+/* ---- 4-bit rows (KVC_QUANT_INT4) ------------------------------------------------
+ * A cache of bf16 inputs and outputs whose rows are quantised as they are written: 4-bit codes u
+ * with a scale s and a minimum m per 32 dims of a row,
+ *     m = min x,  s = bf16((max x - min x) / 15),  u = rint((x - m) / s) in 0..15,  x ~ m + u s
+ * (differences and quotients in fp32, ties to even; s = 0 gives u = 0).  |x - (m + u s)| <= s / 2.  Keys
+ * are quantised as the bf16 cache would store them, rotated and rounded.  A group of 32 that
+ * holds an infinity or NaN (or spans more than fp32 holds) reads as NaN.
+ * 5 bits an element: a row takes 5 d / 8 bytes, the codes (d / 2 bytes) and then the bf16 pair
+ * (s, m) of each group in turn.  With G = d / 32 groups, dim 32 g + x of a K row is nibble x mod 8 of
+ * 32-bit word (x / 8) G + g, of a V row nibble x mod 4 of 16-bit word (x / 4) G + g (nibble 0 the lowest
+ * four bits).
+ * No row depends on another: kvc_append, kvc_append_rows, kvc_trim, kvc_fork, kvc_copy, kvc_free,
+ * kvc_compact and the store take this tier as they take a bf16 cache, contiguous with any window or a
+ * ring, paged or not.  head_dim 64 or 128, capacity a multiple of 16, any number of query heads.
+ * kvc_copy between a bf16 cache and one of this tier converts: rows written are quantised, rows
+ * read back are m + u s, rounded once to bf16.  (A prompt runs on a bf16 cache and is handed over.)
+ * kvc_decode_attn attends to the rows m + u s in fp32 (the query and the weights in two bf16 parts
+ * each, 16 significant bits); d_cmax and d_tanh receive 0 and d_ct must be NULL.
+ * kvc_prompt_attn, kvc_chunk_attn and kvc_decode_attn_noalloc return KVC_ERR_UNSUPPORTED. */
 
 /* ---- gated fallback of the INT8 tier ----------------------------------
  * [WITCERT] "SGLang 生产级落地与闭环门控修复": once the risk of a head or a block
@@ -457,13 +478,15 @@ enum {
     KVC_EXPORT_VTAIL = 10,
     KVC_EXPORT_XMAP = 11,         /* int32 [B][Hkv][capacity/16]: pool entry of a restored
                                      block, -1 = quantized (INT8) */
+    KVC_EXPORT_K4 = 13,           /* [B][Hkv][capacity] rows of 5 d / 8 bytes (INT4: "4-bit rows") */
+    KVC_EXPORT_V4 = 14,
     KVC_EXPORT_PAGE_TABLE = 12    /* int32 [B][capacity/16]: physical page of each logical
-                                     page, -1 = none (paged caches; K and V exports are
-                                     gathered through it into [B][Hkv][capacity][d]) */
+                                     page, -1 = none (paged caches; K, V, K4 and V4 exports are
+                                     gathered through it into [B][Hkv][capacity]) */
 };
 /* *bytes = the size of export `which` for this handle.  KVC_ERR_ARG for a null
- * pointer or an export the cache does not hold (K/V of an INT8 cache, INT8 arrays
- * of a bf16/fp32 cache, the page table of an unpaged cache). */
+ * pointer or an export the cache does not hold (K/V of an INT8 or INT4 cache, INT8 arrays
+ * of another, K4/V4 of any but INT4, the page table of an unpaged cache). */
 int kvc_export_bytes(kvc_t h, int32_t which, size_t* bytes);
 /* Copy export `which` into h_dst (host, `bytes` = kvc_export_bytes exactly, else
  * KVC_ERR_ARG), after the work already queued on `stream`; returns when the copy
@@ -472,7 +495,7 @@ int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t s
 
 /* Host only: where array `which` (KVC_EXPORT_*) lies inside the state buffer, as stored:
  * byte offset and size.  K and V: [B][Hkv][capacity][d], paged [page_pool][Hkv][16][d] in
- * physical page order.  For reading on the device, ordered behind the calls that write.
+ * physical page order; K4 and V4 the same with rows of 5 d / 8 bytes.  For reading on the device, ordered behind the calls that write.
  * KVC_ERR_ARG: a null pointer or an array the cache does not hold. */
 int kvc_region(kvc_t h, int32_t which, size_t* offset, size_t* bytes);
 

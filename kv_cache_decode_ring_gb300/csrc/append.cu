@@ -18,12 +18,7 @@ namespace kvc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxGroup = 1024;  // requests per launch when per-request values ride in params
-
-struct Group {
-    int32_t val[kMaxGroup];  // counts (append) or cuts (trim)
-    int b0, nb;
-};
+using Group = RowCounts;
 
 __device__ __forceinline__ void flag(uint32_t* hdr, uint32_t bit) { atomicOr(hdr, bit); }
 
@@ -480,6 +475,7 @@ size_t quant_smem(int d) { return (size_t)(2 * kQBlock * d + 64) * sizeof(float)
 }  // namespace
 
 cudaError_t launch_append_token(const AppendArgs& a, cudaStream_t st) {
+    if (a.int4) return launch_int4_append_token(a, st);
     const size_t smem = a.int8 ? quant_smem(a.d) : 0;
     return launch_dep(a.table ? append_token_kernel<true> : append_token_kernel<false>,
                       dim3(a.B, (a.Hkv + a.hpc - 1) / a.hpc), dim3(kThreads), smem, st, a);
@@ -488,10 +484,12 @@ cudaError_t launch_append_token(const AppendArgs& a, cudaStream_t st) {
 cudaError_t launch_append_rows_group(const AppendArgs& a, const Group& g, cudaStream_t st) {
     if (!a.int8) {
         cudaError_t e;
-        const bool vec = a.bf16 && a.d % 8 == 0 && a.d / 8 <= kThreads &&
+        const bool vec = a.bf16 && !a.int4 && a.d % 8 == 0 && a.d / 8 <= kThreads &&
                          reinterpret_cast<uintptr_t>(a.k) % 16 == 0 && reinterpret_cast<uintptr_t>(a.v) % 16 == 0 &&
                          a.sb % 8 == 0 && a.sh % 8 == 0 && a.sr % 8 == 0;
-        if (vec) {
+        if (a.int4) {
+            e = launch_int4_append_rows(a, g, st);
+        } else if (vec) {
             const int rows_per_cta = kThreads / (a.d / 8);
             dim3 grid((a.n + rows_per_cta - 1) / rows_per_cta, a.Hkv, g.nb);
             e = launch_dep(append_rows_vec_kernel, grid, dim3(kThreads), 0, st, a, g);

@@ -214,7 +214,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
 }  // namespace
 
 cudaError_t launch_decode(const DecodeArgs& a, const CombineArgs& c, bool fast, const KvMaps* maps, cudaStream_t st) {
-    if (a.gqa) {
+    if (a.int4) {
+        if (cudaError_t e = launch_int4_splits(a, st)) return e;
+    } else if (a.gqa) {
         if (!maps) return cudaErrorInvalidValue;
         cudaError_t e = launch_decode_gqa(a, *maps, st);
         if (e != cudaSuccess) return e;

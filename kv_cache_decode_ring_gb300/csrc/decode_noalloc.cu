@@ -54,7 +54,7 @@ extern "C" int kvc_decode_attn_noalloc(kvc_t h, const void* d_q, void* d_out, kv
     if (!h || !d_q || !d_out) return KVC_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(d_q) & 15u) || (reinterpret_cast<uintptr_t>(d_out) & 15u)) return KVC_ERR_ARG;
     const Shape& s = h->sh;
-    if (s.int8) return KVC_ERR_UNSUPPORTED;
+    if (s.int8 || s.int4) return KVC_ERR_UNSUPPORTED;
     for (int b = 0; b < s.B; ++b)
         if (h->np[b] < 1) return KVC_ERR_ARG;
     if (!windows_held(h)) return KVC_ERR_ARG;

@@ -58,7 +58,8 @@ __global__ void wait_path_kernel(uint32_t* hdr) {
 bool make_shape(const kvc_config& c, Shape* s) {
     if (c.dtype != KVC_F32 && c.dtype != KVC_BF16) return false;
     if (c.layout != KVC_CONTIGUOUS && c.layout != KVC_RING) return false;
-    if (c.kv_quant != KVC_QUANT_NONE && c.kv_quant != KVC_QUANT_INT8 && c.kv_quant != KVC_QUANT_INT8_DITHER)
+    if (c.kv_quant != KVC_QUANT_NONE && c.kv_quant != KVC_QUANT_INT8 && c.kv_quant != KVC_QUANT_INT8_DITHER &&
+        c.kv_quant != KVC_QUANT_INT4)
         return false;
     if (c.batch < 1 || c.n_q_heads < 1 || c.n_kv_heads < 1) return false;
     if (c.n_q_heads % c.n_kv_heads) return false;
@@ -68,7 +69,8 @@ bool make_shape(const kvc_config& c, Shape* s) {
     if (!(c.rope_base >= 0.f) || std::isinf(c.rope_base)) return false;
     const bool ring = c.layout == KVC_RING;
     if (ring && c.window != 0 && c.window != c.capacity) return false;
-    const bool int8 = c.kv_quant != KVC_QUANT_NONE;
+    const bool int4 = c.kv_quant == KVC_QUANT_INT4;
+    const bool int8 = c.kv_quant != KVC_QUANT_NONE && !int4;
     const bool dither = c.kv_quant == KVC_QUANT_INT8_DITHER;
     // the dither counter packs the KV head and the layer into 16 bits each
     if (dither && (c.layer_index < 0 || c.layer_index > 65535 || c.n_kv_heads > 65536)) return false;
@@ -87,6 +89,7 @@ bool make_shape(const kvc_config& c, Shape* s) {
         const int g = c.n_q_heads / c.n_kv_heads;
         if ((c.head_dim != 64 && c.head_dim != 128) || (g != 1 && g != 2 && g != 4 && g != 8)) return false;
     }
+    if (int4 && (c.dtype != KVC_BF16 || (c.head_dim != 64 && c.head_dim != 128) || c.capacity % kPage)) return false;
     const bool rope = c.rope_base > 0.f;
     int P = 0;
     if (rope) {
@@ -97,6 +100,7 @@ bool make_shape(const kvc_config& c, Shape* s) {
     s->d = c.head_dim; s->S = c.capacity; s->W = ring ? c.capacity : c.window;
     s->P = P; s->ring = ring; s->int8 = int8; s->rope = rope; s->bf16 = c.dtype == KVC_BF16;
     s->dither = dither;
+    s->int4 = int4;
     s->elem = s->bf16 ? 2 : 4;
     s->max_chunk = c.max_chunk;
     s->xpool = c.int8_exact_blocks;
@@ -104,17 +108,23 @@ bool make_shape(const kvc_config& c, Shape* s) {
     s->store_slots = c.store_slots;
     s->out_bf16 = c.out_dtype == 0 ? s->bf16 : c.out_dtype == KVC_BF16 + 1;
     s->split = kGenericSplit;
-    if (s->bf16 && !int8 && (s->d == 64 || s->d == 128) && s->g <= 8) s->split = kFastSplit;
+    if (s->bf16 && !int8 && !int4 && (s->d == 64 || s->d == 128) && s->g <= 8) s->split = kFastSplit;
     // (its tensor copies address cache rows with signed 32-bit coordinates)
     const long long rows = s->pages ? (long long)s->pages * s->Hkv * kPage : (long long)s->B * s->Hkv * s->S;
     const long long keys = (s->W > 0 && s->W < s->S) ? s->W : s->S;
-    s->gqa = s->bf16 && !int8 && gqa_decode_supported(s->d, s->g) && rows < (1ll << 31);
+    s->gqa = s->bf16 && !int8 && !int4 && gqa_decode_supported(s->d, s->g) && rows < (1ll << 31);
     if (s->gqa) s->split = keys >= kGqaLongKeys ? kGqaSplitLong : kGqaSplit;
+    if (int4) {
+        // long splits where their CTAs fill the SMs several times over, shorter ones otherwise
+        const long long rows_of_grid = (long long)s->B * s->Hkv * int4_chunks(*s);
+        s->split = kInt4SplitMost;
+        while (s->split > kInt4SplitLeast && rows_of_grid * ((keys + s->split - 1) / s->split) < kInt4Ctas) s->split /= 2;
+    }
     // the generic decode holds a CTA's g queries and g x split scores in shared memory
-    if (!int8 && s->split == kGenericSplit && (size_t)s->g * (s->d + kGenericSplit) * 4 > kMaxSmemPerBlock)
+    if (!int8 && !int4 && s->split == kGenericSplit && (size_t)s->g * (s->d + kGenericSplit) * 4 > kMaxSmemPerBlock)
         return false;
     // a paged cache may start its splits up to one page before the window
-    s->max_splits = (int)((keys + s->split - 1) / s->split) + (s->pages > 0 ? 1 : 0);
+    s->max_splits = (int)((keys + s->split - 1) / s->split) + (s->pages > 0 || int4 ? 1 : 0);
     if (int8) {
         // quantized splits (longer ones for long caches: less start-up per byte; a longer
         // split measured faster than one that fills the SMs' last wave of CTAs better), one
@@ -136,8 +146,8 @@ Layout make_layout(const Shape& s) {
     L.pos = take(B * S * 4);
     if (!s.int8) {
         const size_t rows = s.pages ? (size_t)s.pages * Hkv * kPage : B * Hkv * S;
-        L.k = take(rows * d * s.elem);
-        L.v = take(rows * d * s.elem);
+        L.k = take(rows * row_bytes(s));
+        L.v = take(rows * row_bytes(s));
         if (s.pages) L.table = take(B * (S / kPage) * 4);
     } else {
         // quantized blocks: [B][Hkv][S/16], or [pages][Hkv] on a paged cache
@@ -162,10 +172,10 @@ Layout make_layout(const Shape& s) {
     L.part_ml = take(B * Hq * s.max_splits * 8);
     L.part_acc = take(B * Hq * s.max_splits * d * 4);
     if (s.int8) L.part_c = take(B * Hq * s.max_splits * 4);
-    if (s.ring && s.bf16 && !s.int8 && s.max_chunk > 0)
+    if (s.ring && s.bf16 && !s.int8 && !s.int4 && s.max_chunk > 0)
         L.cws = take(2 * B * Hkv * (size_t)chunk_ws_rows(s) * d * 2);
     if (s.store_slots > 0) {
-        L.store_stride = align256(2 * Hkv * S * d * s.elem + S * 4);
+        L.store_stride = align256(2 * Hkv * S * row_bytes(s) + S * 4);
         L.store = take((size_t)s.store_slots * L.store_stride);
     }
     L.total = o;
@@ -217,7 +227,7 @@ AppendArgs append_args(kvc_handle* h, const void* k, const void* v, int n) {
     a.key0 = h->cfg.dither_key_lo; a.key1 = h->cfg.dither_key_hi;
     a.layer_ctr = 65536u * (uint32_t)h->cfg.layer_index;
     a.B = s.B; a.Hkv = s.Hkv; a.d = s.d; a.S = s.S; a.P = s.P;
-    a.ring = s.ring; a.bf16 = s.bf16; a.int8 = s.int8; a.dither = s.dither;
+    a.ring = s.ring; a.bf16 = s.bf16; a.int8 = s.int8; a.dither = s.dither; a.int4 = s.int4;
     a.arrive = at<int32_t>(h, h->L.arrive);
     // a one-token append into an INT8 cache quantizes a block per KV head every 16th row: up to
     // 8 CTAs per request share that work; a bf16/fp32 append is one CTA per request (its arrival
@@ -419,13 +429,13 @@ int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float*
     a.hdr = at<uint32_t>(h, h->L.hdr);
     a.table = s.pages ? at<int32_t>(h, h->L.table) : nullptr;
     a.B = s.B; a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W;
-    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16;
+    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16; a.int4 = s.int4;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     CombineArgs c{};
     c.part_ml = a.part_ml; c.part_acc = a.part_acc; c.next_pos = a.next_pos; c.out = d_out;
     c.B = s.B; c.Hq = s.Hq; c.d = s.d; c.S = s.S; c.W = s.W; c.max_splits = s.max_splits;
     c.split = s.split; c.ring = s.ring; c.bf16 = s.out_bf16;
-    c.align_lo = s.pages > 0 && s.gqa;
+    c.align_lo = (s.pages > 0 && s.gqa) || s.int4;
     const bool fast = s.split == kFastSplit && fast_decode_supported(a);
     if (launch_decode(a, c, fast, h->has_kv_maps ? &h->kv_maps : nullptr, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (d_cmax && cudaMemsetAsync(d_cmax, 0, (size_t)s.B * s.Hq * 4, st) != cudaSuccess) return KVC_ERR_CUDA;
@@ -558,8 +568,11 @@ int kvc_export_bytes(kvc_t h, int32_t which, size_t* bytes) {
     const size_t B = s.B, Hkv = s.Hkv, S = s.S, d = s.d;
     switch (which) {
         case KVC_EXPORT_K: case KVC_EXPORT_V:
-            if (s.int8) return KVC_ERR_ARG;
-            *bytes = B * Hkv * S * d * s.elem; return KVC_OK;
+            if (s.int8 || s.int4) return KVC_ERR_ARG;
+            *bytes = B * Hkv * S * row_bytes(s); return KVC_OK;
+        case KVC_EXPORT_K4: case KVC_EXPORT_V4:
+            if (!s.int4) return KVC_ERR_ARG;
+            *bytes = B * Hkv * S * row_bytes(s); return KVC_OK;
         case KVC_EXPORT_POSITIONS: *bytes = B * S * 4; return KVC_OK;
         case KVC_EXPORT_PAGE_TABLE:
             if (!s.pages) return KVC_ERR_ARG;
@@ -589,8 +602,8 @@ int kvc_region(kvc_t h, int32_t which, size_t* offset, size_t* bytes) {
     // blocks of 16 slots and one KV head, where the per-block arrays are paged
     const size_t blocks = s.pages ? (size_t)s.pages * s.Hkv : 0;
     switch (which) {
-        case KVC_EXPORT_K: *offset = L.k; if (blocks) *bytes = blocks * kPage * s.d * s.elem; break;
-        case KVC_EXPORT_V: *offset = L.v; if (blocks) *bytes = blocks * kPage * s.d * s.elem; break;
+        case KVC_EXPORT_K: case KVC_EXPORT_K4: *offset = L.k; if (blocks) *bytes = blocks * kPage * row_bytes(s); break;
+        case KVC_EXPORT_V: case KVC_EXPORT_V4: *offset = L.v; if (blocks) *bytes = blocks * kPage * row_bytes(s); break;
         case KVC_EXPORT_POSITIONS: *offset = L.pos; break;
         case KVC_EXPORT_NEXT_POSITION: *offset = L.next_pos; break;
         case KVC_EXPORT_KQ: *offset = L.kq; if (blocks) *bytes = blocks * kQBlock * s.d; break;
@@ -614,8 +627,8 @@ int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t s
     if (!h_dst || bytes != need || !on_device(h)) return KVC_ERR_ARG;
     size_t off = 0;
     switch (which) {
-        case KVC_EXPORT_K: off = h->L.k; break;
-        case KVC_EXPORT_V: off = h->L.v; break;
+        case KVC_EXPORT_K: case KVC_EXPORT_K4: off = h->L.k; break;
+        case KVC_EXPORT_V: case KVC_EXPORT_V4: off = h->L.v; break;
         case KVC_EXPORT_POSITIONS: off = h->L.pos; break;
         case KVC_EXPORT_NEXT_POSITION: off = h->L.next_pos; break;
         case KVC_EXPORT_KQ: off = h->L.kq; break;
@@ -630,10 +643,10 @@ int kvc_export(kvc_t h, int32_t which, void* h_dst, size_t bytes, kvc_stream_t s
         default: return KVC_ERR_ARG;
     }
     cudaStream_t st = S_(stream);
-    if (h->sh.pages && (which == KVC_EXPORT_K || which == KVC_EXPORT_V)) {
+    if (h->sh.pages && (which == KVC_EXPORT_K || which == KVC_EXPORT_V || which == KVC_EXPORT_K4 || which == KVC_EXPORT_V4)) {
         // gather the logical [B][Hkv][S][d] rows through the block table (zeros where unmapped)
         const Shape& s = h->sh;
-        const size_t rowb = (size_t)s.d * s.elem, npg = s.S / kPage;
+        const size_t rowb = row_bytes(s), npg = s.S / kPage;
         std::vector<uint8_t> pool((size_t)s.pages * s.Hkv * kPage * rowb);
         if (cudaMemcpyAsync(pool.data(), h->state + off, pool.size(), cudaMemcpyDeviceToHost, st) != cudaSuccess)
             return KVC_ERR_CUDA;

@@ -30,6 +30,8 @@ constexpr int kInt8LongKeys = 16384;
 constexpr int kGqaSplit = 1024;
 constexpr int kGqaSplitLong = 2048;
 constexpr int kGqaLongKeys = 16384;
+constexpr int kInt4SplitMost = 2048, kInt4SplitLeast = 128;   // keys per split, INT4 decode kernel
+constexpr long long kInt4Ctas = 3 * 152;                      // ... the shorter, until there are so many CTAs
 constexpr int kMaxRestored = 1024;    // INT8 blocks restored to full precision per (request, KV head)
 constexpr int kExactBlocksPerCta = 64; // restored blocks one CTA of the exact-block decode serves
 constexpr int kExactSplits = kMaxRestored / kExactBlocksPerCta;   // their split slots per query head
@@ -42,7 +44,7 @@ struct Layout {
     size_t hdr;       // uint32[64]: [0] error word, [1] work counter, [2] done counter
     size_t next_pos;  // int32 [B]
     size_t pos;       // int32 [B][S]
-    size_t k, v;      // [B][Hkv][S][d] cache dtype (non-INT8); paged: [pages][Hkv][16][d]
+    size_t k, v;      // [B][Hkv][S] rows of row_bytes() (non-INT8); paged: [pages][Hkv][16]
     size_t table;     // int32 [B][S/16] physical page of each logical page, -1 = none (paged)
     size_t kq, vq;    // int8 [B][Hkv][S][d]                   (INT8)
     size_t sk, sv;    // f32  [B][Hkv][S/16]                   (INT8)
@@ -71,6 +73,7 @@ struct Shape {
     int elem;                    // bytes per cache element (non-INT8)
     bool ring, int8, rope, bf16;
     bool dither;                 // INT8 Tier B: subtractive dither, no witnesses
+    bool int4;                   // rows of 4-bit codes (int4.h)
     bool out_bf16;               // attention outputs in bf16 (else fp32)
     int split;                   // keys per split of the decode kernel in use
     int max_splits;
@@ -94,6 +97,13 @@ inline int int8_grid(const Shape& s) {
 
 constexpr int kMaxGridHeads = 65534;      // heads (and one more plane) along a grid's y or z axis
 
+// Bytes of a K or V row of one head (non-INT8).
+inline size_t row_bytes(const Shape& s) { return s.int4 ? (size_t)s.d / 8 * 5 : (size_t)s.d * s.elem; }
+
+// INT4 decode: query heads of a KV head that a CTA serves (grid rows per KV head: int4_chunks)
+constexpr int kInt4Heads = 8;
+inline int int4_chunks(const Shape& s) { return (s.g + kInt4Heads - 1) / kInt4Heads; }
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool make_shape(const kvc_config& c, Shape* s);
@@ -115,6 +125,7 @@ struct DecodeArgs {
     const int32_t* table; // paged caches: the block table (else nullptr)
     int B, Hq, Hkv, g, d, S, W, max_splits, split;
     int gqa;              // the GQA decode kernel serves the shape (split kGqaSplit or kGqaSplitLong)
+    int int4;             // k and v hold rows of 4-bit codes: int4.cu serves the shape
     int ring;
     int bf16;             // cache dtype (1 = bf16, 0 = fp32)
     float scale_log2;     // log2(e) / sqrt(d)
@@ -147,8 +158,17 @@ struct AppendArgs {
     uint32_t key0, key1;      // Tier B: Philox key
     uint32_t layer_ctr;       // Tier B: 65536 * layer
     int B, Hkv, d, S, P, ring, bf16, int8, dither;
+    int int4;                 // kc and vc hold rows of 4-bit codes
     int32_t* arrive;          // [B] one-token append: CTAs of the request done (0 between calls)
     int hpc;                  // one-token append: KV heads per CTA
+};
+
+// Requests [b0, b0 + nb) of an append or trim and their values: rows to append, or cuts.  They
+// ride in the parameters of a launch.
+constexpr int kMaxGroup = 1024;
+struct RowCounts {
+    int32_t val[kMaxGroup];
+    int b0, nb;
 };
 
 // Tensor maps over the whole K and V caches, rows [B*Hkv*S][d] bf16, boxes of 64
@@ -192,6 +212,10 @@ inline bool page_touched(const Shape& s, int lp, long long lo, long long hi) {
 cudaError_t launch_int8_exact(kvc_handle* h, const void* q, float* ct, cudaStream_t st);
 // maps: required when the GQA kernel serves the shape (Shape::gqa)
 cudaError_t launch_decode(const DecodeArgs& d, const CombineArgs& c, bool fast, const KvMaps* maps, cudaStream_t st);
+// INT4 tier (int4.cu): appends of n rows of every request (n = 1: one token), and the decode's splits
+cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cudaStream_t st);
+cudaError_t launch_int4_splits(const DecodeArgs& a, cudaStream_t st);
 bool chunk_supported(const Shape& s);
 bool gqa_decode_supported(int d, int g);
 cudaError_t launch_decode_gqa(const DecodeArgs& a, const KvMaps& maps, cudaStream_t st);

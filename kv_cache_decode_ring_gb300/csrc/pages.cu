@@ -8,13 +8,14 @@
 // holds rows of that request.  A page is free once its last holder gave it up.
 //
 // A page is a physical page index into every per-page array of the state: K and V rows
-// [pages][Hkv][16][d], or for the INT8 tiers codes, scales and witnesses, one quantization
+// [pages][Hkv][16], or for the INT8 tiers codes, scales and witnesses, one quantization
 // block per KV head.
 #include <algorithm>
 #include <cstring>
 #include <new>
 #include <vector>
 
+#include "int4.h"
 #include "kvc_internal.h"
 
 namespace kvc {
@@ -120,8 +121,8 @@ int parts_of(const kvc_handle* h, Part* p) {
     auto part = [&](size_t off, long long bytes) { return Part{h->state + off, bytes}; };
     int n = 0;
     if (!s.int8) {
-        p[n++] = part(L.k, (long long)kPage * s.d * s.elem);
-        p[n++] = part(L.v, (long long)kPage * s.d * s.elem);
+        p[n++] = part(L.k, (long long)(kPage * row_bytes(s)));
+        p[n++] = part(L.v, (long long)(kPage * row_bytes(s)));
         return n;
     }
     p[n++] = part(L.kq, (long long)kQBlock * s.d);
@@ -191,6 +192,29 @@ struct CopyArgs {
 // y's rows of the group's source, read once and written to each of its destinations; its
 // scales, witnesses and exact tail for the INT8 tiers.  Plane Hkv, a CTA per destination:
 // positions, next_position, request ID and (share) block-table entries.
+__device__ __forceinline__ void copy_books(const CopyArgs& a, const CopyGroup& g, const int* target) {
+    for (int j = blockIdx.x; j < g.n; j += gridDim.x) {
+        const int b = target[j];
+        int32_t* pb = a.to.pos + (size_t)b * a.to.S;
+        // a ring's slots move with their positions (equal S on both sides); a contiguous
+        // cache holds position s in slot s, and nothing from next_position on
+        const int old = a.to.next_pos[b];
+        const int hi = a.ring ? a.to.S : min(a.to.S, max(g.len, old));
+        for (int s = threadIdx.x; s < hi; s += kCopyThreads)
+            pb[s] = g.src < 0 ? -1 : a.ring ? a.from.pos[(size_t)g.src * a.from.S + s] : s < g.len ? s : -1;
+        if (a.share) {
+            const int npg = a.to.S / kPage;
+            for (int lp = threadIdx.x; lp < npg; lp += kCopyThreads)
+                a.to.table[(size_t)b * npg + lp] = g.src < 0 ? -1 : a.from.table[(size_t)g.src * npg + lp];
+        }
+        __syncthreads();                  // every thread has read the old next_position
+        if (threadIdx.x == 0) {
+            a.to.next_pos[b] = g.len;
+            if (a.to.req_id && g.src >= 0) a.to.req_id[b] = g.req_id;
+        }
+    }
+}
+
 template <typename U>
 __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __grid_constant__ CopyArgs a) {
     dep_wait();
@@ -199,26 +223,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __gri
     const int h = blockIdx.y;
     const int* target = a.target + g.first;
     if (h == a.Hkv) {
-        for (int j = blockIdx.x; j < g.n; j += gridDim.x) {
-            const int b = target[j];
-            int32_t* pb = a.to.pos + (size_t)b * a.to.S;
-            // a ring's slots move with their positions (equal S on both sides); a contiguous
-            // cache holds position s in slot s, and nothing from next_position on
-            const int old = a.to.next_pos[b];
-            const int hi = a.ring ? a.to.S : min(a.to.S, max(g.len, old));
-            for (int s = threadIdx.x; s < hi; s += kCopyThreads)
-                pb[s] = g.src < 0 ? -1 : a.ring ? a.from.pos[(size_t)g.src * a.from.S + s] : s < g.len ? s : -1;
-            if (a.share) {
-                const int npg = a.to.S / kPage;
-                for (int lp = threadIdx.x; lp < npg; lp += kCopyThreads)
-                    a.to.table[(size_t)b * npg + lp] = g.src < 0 ? -1 : a.from.table[(size_t)g.src * npg + lp];
-            }
-            __syncthreads();              // every thread has read the old next_position
-            if (threadIdx.x == 0) {
-                a.to.next_pos[b] = g.len;
-                if (a.to.req_id && g.src >= 0) a.to.req_id[b] = g.req_id;
-            }
-        }
+        copy_books(a, g, target);
         return;
     }
     if (g.src < 0) return;
@@ -280,6 +285,68 @@ __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __gri
     }
 }
 
+// The same between a bf16 cache and an INT4 one of D dims: rows are quantised (QUANT) or read back
+// as bf16 (m + u s rounded once) on the way.  A thread takes 8 dims of a row, K and V, as int4.h
+// lays them out; kConvertUnroll rows in flight.
+constexpr int kConvertUnroll = 4;
+
+template <int D, bool QUANT>
+__global__ void __launch_bounds__(kCopyThreads) convert_requests_kernel(const __grid_constant__ CopyArgs a) {
+    dep_wait();
+    dep_release();
+    const CopyGroup g = a.group[blockIdx.z];
+    const int h = blockIdx.y;
+    const int* target = a.target + g.first;
+    if (h == a.Hkv) {
+        copy_books(a, g, target);
+        return;
+    }
+    constexpr int kVec = D / 8, kRow4 = int4::row_size(D), kStep = kCopyThreads / kVec;
+    const int s0 = blockIdx.x * kCopyBlocks * kPage, rows = min(g.rows - s0, kCopyBlocks * kPage);
+    if (g.src < 0 || rows <= 0) return;
+    const int e = threadIdx.x % kVec;
+    for (int r0 = threadIdx.x / kVec; r0 - (int)threadIdx.x / kVec < rows; r0 += kConvertUnroll * kStep) {
+        uint4 kx[kConvertUnroll], vx[kConvertUnroll];    // (QUANT: 8 values each; else codes and parameters)
+#pragma unroll
+        for (int j = 0; j < kConvertUnroll; ++j) {
+            const int r = r0 + j * kStep;
+            kx[j] = vx[j] = make_uint4(0, 0, 0, 0);
+            if (r >= rows) continue;
+            const size_t row = kv_row(a.from.table, g.src, h, s0 + r, a.Hkv, a.from.S);
+            if constexpr (QUANT) {
+                kx[j] = reinterpret_cast<const uint4*>(a.from.part[0].base)[row * kVec + e];
+                vx[j] = reinterpret_cast<const uint4*>(a.from.part[1].base)[row * kVec + e];
+            } else {
+                const uint32_t* k = reinterpret_cast<const uint32_t*>(a.from.part[0].base + row * kRow4);
+                const uint32_t* v = reinterpret_cast<const uint32_t*>(a.from.part[1].base + row * kRow4);
+                kx[j].x = k[int4::k_word<D>(e)]; kx[j].y = k[D / 8 + (e >> 2)];
+                vx[j].x = v[int4::v_word<D>(e)]; vx[j].y = v[D / 8 + (e >> 2)];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kConvertUnroll; ++j) {
+            const int r = r0 + j * kStep;
+            if constexpr (QUANT) {
+                uint32_t kp, vp;
+                const uint32_t kw = int4::quantise_bf16(kx[j], kp), vw = int4::v_codes(int4::quantise_bf16(vx[j], vp), e);
+                if (r >= rows) continue;
+                for (int t = 0; t < g.n; ++t) {
+                    const size_t row = kv_row(a.to.table, target[t], h, s0 + r, a.Hkv, a.to.S) * kRow4;
+                    int4::store_unit<D>(a.to.part[0].base + row, a.to.part[1].base + row, e, kw, kp, vw, vp);
+                }
+            } else {
+                const uint4 k = int4::values_bf16(kx[j].x, kx[j].y), v = int4::values_bf16(int4::v_codes(vx[j].x, e), vx[j].y);
+                if (r >= rows) continue;
+                for (int t = 0; t < g.n; ++t) {
+                    const size_t row = kv_row(a.to.table, target[t], h, s0 + r, a.Hkv, a.to.S) * kVec + e;
+                    reinterpret_cast<uint4*>(a.to.part[0].base)[row] = k;
+                    reinterpret_cast<uint4*>(a.to.part[1].base)[row] = v;
+                }
+            }
+        }
+    }
+}
+
 void side_of(kvc_handle* h, CopySide* c) {
     const Shape& s = h->sh;
     parts_of(h, c->part);
@@ -316,7 +383,7 @@ cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<in
     Part parts[kMaxParts];
     a.parts = parts_of(to, parts);
     a.Hkv = s.Hkv; a.d = s.d; a.ring = s.ring; a.int8 = s.int8; a.share = share;
-    const bool wide = (s.int8 ? s.d : s.d * s.elem) % 16 == 0;
+    const bool wide = (s.int8 ? s.d : row_bytes(s)) % 16 == 0;
     size_t i = 0;
     while (i < order.size()) {
         int ng = 0, nt = 0, most = 0, widest = 1;
@@ -339,7 +406,11 @@ cudaError_t copy_requests(kvc_handle* to, kvc_handle* from, const std::vector<in
         }
         const int per = kCopyBlocks * kPage;
         dim3 grid(std::max((most + per - 1) / per, widest), s.Hkv + 1, ng);
-        const cudaError_t e = launch_dep(wide ? copy_requests_kernel<uint4> : copy_requests_kernel<uint32_t>, grid, dim3(kCopyThreads), 0, st, a);
+        auto kernel = wide ? copy_requests_kernel<uint4> : copy_requests_kernel<uint32_t>;
+        if (s.int4 != from->sh.int4)
+            kernel = s.d == 128 ? (s.int4 ? convert_requests_kernel<128, true> : convert_requests_kernel<128, false>)
+                                : (s.int4 ? convert_requests_kernel<64, true> : convert_requests_kernel<64, false>);
+        const cudaError_t e = launch_dep(kernel, grid, dim3(kCopyThreads), 0, st, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -551,6 +622,7 @@ int kvc_copy(kvc_t to, kvc_t from, int32_t n, const int32_t* h_src, const int32_
     if (!to || !from || !on_device(to) || from->device != to->device || n < 0 || (n > 0 && (!h_src || !h_dst)))
         return KVC_ERR_ARG;
     const Shape &s = to->sh, &f = from->sh;
+    // (INT4 caches are bf16 ones here: the copy converts)
     if (s.bf16 != f.bf16 || s.int8 != f.int8 || s.dither != f.dither || s.Hkv != f.Hkv || s.d != f.d || s.ring != f.ring ||
         (s.ring && s.S != f.S) || to->cfg.rope_base != from->cfg.rope_base ||
         (s.dither && (to->cfg.layer_index != from->cfg.layer_index || to->cfg.dither_key_lo != from->cfg.dither_key_lo ||

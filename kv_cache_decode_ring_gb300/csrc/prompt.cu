@@ -504,7 +504,7 @@ cudaError_t launch_join(const AttnArgs& a, const Packed& g, cudaStream_t st) {
 }
 
 bool prompt_supported(const Shape& s) {
-    return !s.int8 && s.Hq <= kMaxGridHeads && (!s.ring || (s.bf16 && s.S % kPage == 0));
+    return !s.int8 && !s.int4 && s.Hq <= kMaxGridHeads && (!s.ring || (s.bf16 && s.S % kPage == 0));
 }
 
 cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* counts, cudaStream_t st) {

@@ -708,7 +708,7 @@ cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items
 bool prompt_tc_supported(const Shape& s) {
     const long long rows = s.pages ? (long long)s.pages * s.Hkv * kPage : (long long)s.B * s.Hkv * s.S;
     const long long staged = s.ring ? (long long)s.B * s.Hkv * chunk_ws_rows(s) : 0;
-    return s.bf16 && !s.int8 && (s.d == 64 || s.d == 128) && rows < (1ll << 31) - 128 && staged < (1ll << 31) && s.g <= kBM &&
+    return s.bf16 && !s.int8 && !s.int4 && (s.d == 64 || s.d == 128) && rows < (1ll << 31) - 128 && staged < (1ll << 31) && s.g <= kBM &&
            s.Hkv < (1 << 20);
 }
 

@@ -143,7 +143,7 @@ StoreArgs store_args(kvc_handle* h, int load) {
     a.next_pos = reinterpret_cast<int32_t*>(h->state + h->L.next_pos);
     a.store = h->state + h->L.store;
     a.stride = h->L.store_stride;
-    a.Hkv = s.Hkv; a.S = s.S; a.row_bytes = s.d * s.elem; a.ring = s.ring;
+    a.Hkv = s.Hkv; a.S = s.S; a.row_bytes = (int)row_bytes(s); a.ring = s.ring;
     a.load = load;
     return a;
 }

@@ -23,10 +23,10 @@ from . import build as _build
 KVC_OK, KVC_ERR_ARG, KVC_ERR_CAPACITY, KVC_ERR_EVICTED, KVC_ERR_CUDA, KVC_ERR_UNSUPPORTED, KVC_ERR_DEVICE = range(7)
 KVC_F32, KVC_BF16 = 0, 1
 KVC_CONTIGUOUS, KVC_RING = 0, 1
-KVC_QUANT_NONE, KVC_QUANT_INT8, KVC_QUANT_INT8_DITHER = 0, 1, 2
+KVC_QUANT_NONE, KVC_QUANT_INT8, KVC_QUANT_INT8_DITHER, KVC_QUANT_INT4 = 0, 1, 2, 3
 (KVC_EXPORT_K, KVC_EXPORT_V, KVC_EXPORT_POSITIONS, KVC_EXPORT_NEXT_POSITION, KVC_EXPORT_KQ, KVC_EXPORT_VQ,
  KVC_EXPORT_SK, KVC_EXPORT_SV, KVC_EXPORT_WITNESS, KVC_EXPORT_KTAIL, KVC_EXPORT_VTAIL, KVC_EXPORT_XMAP,
- KVC_EXPORT_PAGE_TABLE) = range(13)
+ KVC_EXPORT_PAGE_TABLE, KVC_EXPORT_K4, KVC_EXPORT_V4) = range(15)
 KVC_ROPE_HALVES, KVC_ROPE_PER_AXIS = 1, 2
 
 _STATUS_NAMES = {1: "KVC_ERR_ARG", 2: "KVC_ERR_CAPACITY", 3: "KVC_ERR_EVICTED", 4: "KVC_ERR_CUDA",
@@ -185,13 +185,14 @@ def make_config(dtype="bf16", layout="contiguous", kv_quant=None, batch=1, n_q_h
     entries for blocks the gated fallback restores (INT8 caches); ``page_pool``: pages of 16
     slots for paged K/V storage (0 = each request owns ``capacity`` slots); ``store_slots``:
     device slots for saved prefills (prefix store).  ``kv_quant``: None, "int8" (witness
-    tier) or "int8-dither" (Tier B, with ``layer_index`` and the 64-bit Philox ``dither_key``
+    tier), "int4" (4-bit rows) or "int8-dither" (Tier B, with ``layer_index`` and the 64-bit Philox ``dither_key``
     as (low, high) words); ``int8_split``: positions per quantized split of the INT8 decode
     (a multiple of 64 in [1024, 2048]; 0 = chosen for the device)."""
     od = 0 if out_dtype is None else (KVC_F32 + 1 if out_dtype == "f32" else KVC_BF16 + 1)
     return kvc_config(KVC_BF16 if dtype == "bf16" else KVC_F32,
                       KVC_RING if layout == "ring" else KVC_CONTIGUOUS,
-                      {None: KVC_QUANT_NONE, "int8": KVC_QUANT_INT8, "int8-dither": KVC_QUANT_INT8_DITHER}[kv_quant],
+                      {None: KVC_QUANT_NONE, "int8": KVC_QUANT_INT8, "int8-dither": KVC_QUANT_INT8_DITHER,
+                       "int4": KVC_QUANT_INT4}[kv_quant],
                       batch, n_q_heads, n_kv_heads, head_dim, capacity, window, max_position,
                       float(rope_base), max_chunk, od, int(int8_exact_blocks), int(page_pool), int(store_slots),
                       int(layer_index), int(dither_key[0]) & 0xFFFFFFFF, int(dither_key[1]) & 0xFFFFFFFF,
@@ -541,7 +542,8 @@ class Cache:
     _EXPORT_DTYPES = {KVC_EXPORT_POSITIONS: np.int32, KVC_EXPORT_NEXT_POSITION: np.int32, KVC_EXPORT_KQ: np.int8,
                       KVC_EXPORT_VQ: np.int8, KVC_EXPORT_SK: np.float32, KVC_EXPORT_SV: np.float32,
                       KVC_EXPORT_WITNESS: np.uint16, KVC_EXPORT_KTAIL: np.uint16, KVC_EXPORT_VTAIL: np.uint16,
-                      KVC_EXPORT_XMAP: np.int32, KVC_EXPORT_PAGE_TABLE: np.int32}
+                      KVC_EXPORT_XMAP: np.int32, KVC_EXPORT_PAGE_TABLE: np.int32, KVC_EXPORT_K4: np.uint8,
+                      KVC_EXPORT_V4: np.uint8}
 
     def __init__(self, cfg: kvc_config, device="cuda", stream=None):
         self.cfg = cfg
@@ -651,7 +653,8 @@ class Cache:
         kvc_fork(self.h, src, dst, stream)
 
     def copy_from(self, other: "Cache", src, dst, stream=None):
-        """Requests ``dst`` become copies of ``other``'s requests ``src``, with rows of their own."""
+        """Requests ``dst`` become copies of ``other``'s requests ``src``, with rows of their own.  A bf16 cache's rows
+        are quantised on the way into a 4-bit one and read back from it."""
         kvc_copy(self.h, other.h, src, dst, stream)
 
     def free(self, requests, stream=None):
@@ -666,13 +669,15 @@ class Cache:
         return kvc_page_counts(self.h)
 
     def rows(self) -> tuple:
-        """Views of the stored K and V rows: [B, Hkv, capacity, d], paged [pages, Hkv, 16, d].  For reading,
-        on the stream that the cache's calls run on."""
-        shape = (self.cfg.page_pool, self.Hkv, 16, self.d) if self.cfg.page_pool else (self.B, self.Hkv, self.S, self.d)
+        """Views of the stored K and V rows: [B, Hkv, capacity, d], paged [pages, Hkv, 16, d] (4-bit rows: uint8,
+        5 d / 8 bytes each).  For reading, on the stream that the cache's calls run on."""
+        bits4 = self.cfg.kv_quant == KVC_QUANT_INT4
+        row, dtype = (5 * self.d // 8, torch.uint8) if bits4 else (self.d, self.torch_dtype)
+        shape = (self.cfg.page_pool, self.Hkv, 16, row) if self.cfg.page_pool else (self.B, self.Hkv, self.S, row)
         views = []
-        for which in (KVC_EXPORT_K, KVC_EXPORT_V):
+        for which in (KVC_EXPORT_K4, KVC_EXPORT_V4) if bits4 else (KVC_EXPORT_K, KVC_EXPORT_V):
             off, n = kvc_region(self.h, which)
-            views.append(self.state[off:off + n].view(self.torch_dtype).view(shape))
+            views.append(self.state[off:off + n].view(dtype).view(shape))
         return tuple(views)
 
     def export(self, which, stream=None) -> np.ndarray:
@@ -688,7 +693,9 @@ class Cache:
                   KVC_EXPORT_WITNESS: (self.B, self.Hkv, self.S, 16), KVC_EXPORT_KTAIL: (self.B, self.Hkv, 16, self.d),
                   KVC_EXPORT_VTAIL: (self.B, self.Hkv, 16, self.d),
                   KVC_EXPORT_XMAP: (self.B, self.Hkv, self.S // 16),
-                  KVC_EXPORT_PAGE_TABLE: (self.B, self.S // 16)}
+                  KVC_EXPORT_PAGE_TABLE: (self.B, self.S // 16),
+                  KVC_EXPORT_K4: (self.B, self.Hkv, self.S, 5 * self.d // 8),
+                  KVC_EXPORT_V4: (self.B, self.Hkv, self.S, 5 * self.d // 8)}
         return arr.reshape(shapes[which])
 
     def next_positions(self) -> np.ndarray:
