@@ -138,6 +138,10 @@ typedef struct {
                              cache's window + 32) spans 16384 slots or more, else 1024.
                              A tuning knob only: results do not depend on it beyond
                              fp32 rounding order.  Must be 0 without INT8. */
+    int32_t sinks;        /* first positions that stay visible behind the window: the query at
+                             position t sees [max(0, t-W+1), t] and [0, min(sinks, t+1)).  0 = none.
+                             Contiguous caches with a window, all tiers but INT8 (a ring overwrites
+                             its first rows); decode and prompts, not kvc_chunk_attn */
 } kvc_config;
 
 /* Bytes of the device state buffer for `cfg` (cache rows, positions,
@@ -181,6 +185,7 @@ int kvc_append_rows(kvc_t h, const void* d_k, const void* d_v, int32_t n,
  * t = next_position - 1, is rotated at t (if RoPE) in fp32, and attends to the
  * cached positions [max(0, t-W+1), t]:
  *     out = softmax(q . K^T / sqrt(d)) . V            d_out: [B][Hq][d]
+ * (and to positions [0, sinks) of a cache with sinks),
  * evaluated as split-K flash decoding with an online softmax and a cross-split
  * combine, fp32 accumulation, rounded once to the output dtype.  Needs at least
  * one cached token per request; KVC_ERR_ARG too while a request of a ring lacks a key of
@@ -241,6 +246,7 @@ int kvc_set_request_id(kvc_t h, int32_t b, uint32_t request_id, kvc_stream_t str
  *     if B*Hq*splits*(8 + 4*d) bytes (+ 256 bytes of alignment) exceed
  *     KVC_NOALLOC_SCRATCH_BYTES, with
  *       splits = ceil(min(capacity, window) / split) + (page_pool > 0 ? 1 : 0)
+ *                + ceil(min(sinks, max(0, capacity - window)) / split)
  *     (window 0 = capacity), where split is the decode kernel's keys per split:
  *       1024, or 2048 when min(capacity, window) >= 16384, for bf16 caches with
  *         d = 64 or 128 and 4 or 8 query heads per KV head;
@@ -272,7 +278,7 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream);
  * positions [max(0, p-W+1), p]:
  *     d_q [B][n][Hq][d], d_k, d_v [B][n][Hkv][d]  ->  d_out [B][n][Hq][d].
  * Row i equals what kvc_decode_attn returns for that query after appending
- * rows 0..i.  bf16 caches with head_dim 128, without INT8: contiguous, or a ring
+ * rows 0..i.  bf16 caches with head_dim 128, without INT8, INT4 or sinks: contiguous, or a ring
  * whose size W is a multiple of 16 (paged or not); n <= max_chunk.  On a ring the
  * suffix may be longer than W: appending it first would evict rows that early
  * suffix queries need ([LEAN] §3.4), so the call stages the rotated suffix rows
@@ -296,7 +302,8 @@ int kvc_chunk_attn(kvc_t h, const void* d_q, const void* d_k, const void* d_v, i
  * and Hkv d), so that the three may be views of one projection's output (aligned to an
  * element where a head's row is no multiple of 16 bytes); the heads of a row are dense.
  * Appends every row as kvc_append_rows does and answers row i of request b at
- * p = next_position + i over positions [max(0, p-W+1), p].  The query is rotated in fp32 and
+ * p = next_position + i over positions [max(0, p-W+1), p], and over [0, min(sinks, p+1)) of a cache
+ * with sinks.  The query is rotated in fp32 and
  * rounded to the cache's type, as the keys are; sums and softmax are fp32.  bf16 caches with
  * head_dim 64 or 128 (below 2^31 rows of all heads, at most 128 query heads a KV head) run on
  * the tensor cores, where the softmax weights are rounded to bf16 too (relative error at most

@@ -796,7 +796,7 @@ bool make_tensor_map_bf16(CUtensorMap* tm, void* base, int rank, const cuuint64_
            CUDA_SUCCESS;
 }
 
-bool chunk_supported(const Shape& s) { return s.bf16 && !s.int8 && !s.int4 && s.d == kD && (!s.ring || s.S % 16 == 0); }
+bool chunk_supported(const Shape& s) { return s.bf16 && !s.int8 && !s.int4 && s.sinks == 0 && s.d == kD && (!s.ring || s.S % 16 == 0); }
 
 cudaError_t launch_chunk(kvc_handle* h, const void* q, const void* k, const void* v, void* out, int n,
                          cudaStream_t st) {

@@ -39,14 +39,18 @@ __device__ void load_query(const DecodeArgs& a, int b, int kvh, int t, int bf16,
 // Generic kernel: any dtype, any even d <= 256, any group size.  CTA =
 // (chunk of kGenericSplit keys, KV head, request).  Straightforward two-pass
 // evaluation of its chunk in shared memory.
-template <int BF16>
+template <int BF16, bool SINKS>
 __global__ void __launch_bounds__(kThreads) decode_generic_kernel(const DecodeArgs a) {
     extern __shared__ float smem[];
     const int b = blockIdx.z, kvh = blockIdx.y, chunk = blockIdx.x;
     const int len = a.next_pos[b];
     int lo, hi;
     key_range(len, a.S, a.W, a.ring, lo, hi);
-    const int k0 = lo + chunk * a.split;
+    int k0 = lo + chunk * a.split;
+    if (SINKS) {
+        if (chunk >= split_count(lo, lo, hi, a.split, a.sinks)) return;
+        split_keys(chunk, lo, a.split, a.sinks, lo, hi, k0);
+    }
     if (k0 >= hi) return;
     const int nk = min(hi - k0, a.split);
     const int d = a.d, g = a.g;
@@ -117,8 +121,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
         const int len = c.next_pos[b];
         int lo, hi;
         key_range(len, c.S, c.W, c.ring, lo, hi);
-        if (c.align_lo) lo &= ~(kPage - 1);         // the paged GQA decode's split origin
-        ns = (hi - lo + c.split - 1) / c.split;
+        // (the paged GQA and the INT4 decode's splits start at a page)
+        ns = split_count(c.align_lo ? lo & ~(kPage - 1) : lo, lo, hi, c.split, c.sinks);
     }
     if (valid && vec) {
         float m = -INFINITY, l = 0.f;
@@ -227,12 +231,11 @@ cudaError_t launch_decode(const DecodeArgs& a, const CombineArgs& c, bool fast, 
         dim3 grid(a.max_splits, a.Hkv, a.B);
         const size_t smem = (size_t)a.g * (a.d + a.split) * sizeof(float);
         // (the grant is always the largest, so shapes of different sizes never narrow it)
-        const void* k = a.bf16 ? reinterpret_cast<const void*>(decode_generic_kernel<1>)
-                               : reinterpret_cast<const void*>(decode_generic_kernel<0>);
+        auto k = a.sinks ? (a.bf16 ? decode_generic_kernel<1, true> : decode_generic_kernel<0, true>)
+                         : (a.bf16 ? decode_generic_kernel<1, false> : decode_generic_kernel<0, false>);
         if (smem > 48 * 1024)
-            if (cudaError_t e = allow_smem(k, kMaxSmemPerBlock)) return e;
-        if (a.bf16) decode_generic_kernel<1><<<grid, kThreads, smem, st>>>(a);
-        else decode_generic_kernel<0><<<grid, kThreads, smem, st>>>(a);
+            if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), kMaxSmemPerBlock)) return e;
+        k<<<grid, kThreads, smem, st>>>(a);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

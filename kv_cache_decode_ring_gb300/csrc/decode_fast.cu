@@ -61,7 +61,8 @@ struct Cfg {
 
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-template <int D, int G>
+// SINKS: the splits behind the window's are those of the first positions.
+template <int D, int G, bool SINKS>
 __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const DecodeArgs a) {
     using C = Cfg<D, G>;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -78,8 +79,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
     const int len = a.next_pos[b];
     int lo, hi;
     key_range(len, a.S, a.W, a.ring, lo, hi);
-    const int nsplit = (hi - lo + kSplitKeys - 1) / kSplitKeys;
+    const int nwindow = (hi - lo + kSplitKeys - 1) / kSplitKeys;
+    const int nsplit = SINKS ? split_count(lo, lo, hi, kSplitKeys, a.sinks) : nwindow;
     if ((int)blockIdx.x >= nsplit) return;
+    // first key of this warp's tile of a split, and the end of the keys that its part sees
+    auto first_of = [&](int split) {
+        return (SINKS && split >= nwindow ? (split - nwindow) * kSplitKeys : lo + split * kSplitKeys) + (int)(threadIdx.x >> 5) * kTile;
+    };
+    auto end_of = [&](int split) { return SINKS && split >= nwindow ? min(a.sinks, lo) : hi; };
 
     const int warp_ = threadIdx.x >> 5;
     const size_t head_row0 = ((size_t)b * a.Hkv + kvh) * a.S;
@@ -92,8 +99,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
     constexpr int kRuns = kTile / kPage + 1;              // pages a tile can touch
     int pf[kRuns];
     auto fetch_pages = [&](int split) {
-        const int k0 = lo + split * kSplitKeys + warp_ * kTile;
-        const int nk = max(0, min(kTile, hi - k0));
+        const int k0 = first_of(split);
+        const int nk = max(0, min(kTile, end_of(split) - k0));
         const int32_t* trow = a.table + (size_t)b * (a.S / kPage);
 #pragma unroll
         for (int j = 0; j < kRuns; ++j)
@@ -101,8 +108,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
     };
     // lane 0 of each warp: copy its K/V rows of `split` (paged: from the pages in pf)
     auto issue = [&](int split) {
-        const int k0 = lo + split * kSplitKeys + warp_ * kTile;
-        const int nk = max(0, min(kTile, hi - k0));
+        const int k0 = first_of(split);
+        const int nk = max(0, min(kTile, end_of(split) - k0));
         if ((threadIdx.x & 31) == 0 && nk > 0) {
             const uint32_t bytes = (uint32_t)nk * C::ROWB;
             mbar_arrive_expect_tx(&bar[warp_], 2 * bytes);
@@ -165,8 +172,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
     uint32_t phase = 0;
 
     for (int split = blockIdx.x; split < nsplit; split += gridDim.x) {
-        const int k0 = lo + split * kSplitKeys + warp * kTile;
-        const int nk = max(0, min(kTile, hi - k0));
+        const int k0 = first_of(split);
+        const int nk = max(0, min(kTile, end_of(split) - k0));
         float m_w[G], l_w[G], acc[G][8];
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -315,9 +322,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) decode_fast_kernel(const Decod
 template <int D, int G>
 cudaError_t launch_t(const DecodeArgs& a, int grid_x, cudaStream_t st) {
     using C = Cfg<D, G>;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_fast_kernel<D, G>), C::SMEM)) return e;
+    auto kernel = a.sinks ? decode_fast_kernel<D, G, true> : decode_fast_kernel<D, G, false>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM)) return e;
     dim3 grid(grid_x, a.Hkv, a.B);
-    return launch_dep(decode_fast_kernel<D, G>, grid, dim3(kWarps * 32), C::SMEM, st, a);
+    return launch_dep(kernel, grid, dim3(kWarps * 32), C::SMEM, st, a);
 }
 
 }  // namespace

@@ -93,7 +93,9 @@ struct GqaCfg {
     static_assert(HALF % 1024 == 0 && OFF_P % 1024 == 0, "swizzled boxes need 1024-byte alignment");
 };
 
-template <int D, int G>
+// SINKS: the splits behind the window's are those of the first positions; their last tile also holds rows
+// between them and the window, whose values are cleared in shared memory, whatever they hold.
+template <int D, int G, bool SINKS>
 __global__ void __launch_bounds__(kWarps * 32, 3)
     decode_gqa_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const DecodeArgs a) {
@@ -115,14 +117,20 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int lo_t = a.table ? (lo & ~(kPage - 1)) : lo;
     const int kSplit = a.split;                          // keys per CTA
     const int tpw = kSplit / (kWarps * kTileKeys);       // tiles per warp
-    const int nsplit = (hi - lo_t + kSplit - 1) / kSplit;
-    if (split >= nsplit) return;
+    int k_first = lo_t + split * kSplit;                 // the CTA's first key
+    if constexpr (SINKS) {
+        if (split >= split_count(lo_t, lo, hi, kSplit, a.sinks)) return;
+        split_keys(split, lo_t, kSplit, a.sinks, lo, hi, k_first);
+    } else {
+        const int nsplit = (hi - lo_t + kSplit - 1) / kSplit;
+        if (split >= nsplit) return;
+    }
 
     const int head_row0 = (b * a.Hkv + kvh) * a.S;       // tensor-map row of key slot 0 (unpaged)
     unsigned char* myS = smem + warp * C::WARPB;
     uint64_t* myBar = bar + warp * kStages;
     // keys of this warp's tile i: 16 consecutive rows, tiles of the 4 warps interleaved
-    auto tile_k0 = [&](int i) { return lo_t + split * kSplit + (i * kWarps + warp) * kTileKeys; };
+    auto tile_k0 = [&](int i) { return k_first + (i * kWarps + warp) * kTileKeys; };
     auto tile_nk = [&](int i) { return max(0, min(kTileKeys, hi - tile_k0(i))); };
     // paged: lane i holds the page of the warp's tile i (a tile is one page), all loaded in
     // one round trip at the start instead of one table read before each tile's copies
@@ -225,6 +233,16 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
             for (int j = i + 1; j < i + kStages && j < tpw; ++j)
                 if (tile_nk(j) > 0) mbar_wait(&myBar[j % kStages], (uint32_t)((j / kStages) & 1));
             break;
+        }
+        if constexpr (SINKS) {
+            if (nk < kTileKeys || kmin > 0) {
+                // (rows of 128 bytes in each box: the swizzle stays within a row)
+                for (int c = lane; c < kTileKeys * C::NBOX * 8; c += 32) {
+                    const int r = c / 8 % kTileKeys;
+                    if (r >= nk || r < kmin) *reinterpret_cast<uint4*>(tV + c * 16) = make_uint4(0, 0, 0, 0);
+                }
+                __syncwarp();
+            }
         }
         // ---- scores S^T = K Q^T
         const uint32_t kbase = smem_u32(tK) + krow;
@@ -340,8 +358,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 template <int D, int G>
 cudaError_t launch_t(const DecodeArgs& a, const KvMaps& m, cudaStream_t st) {
     using C = GqaCfg<D, G>;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(decode_gqa_kernel<D, G>), C::SMEM)) return e;
-    return launch_dep(decode_gqa_kernel<D, G>, dim3(a.max_splits, a.Hkv, a.B), dim3(kWarps * 32), C::SMEM, st,
+    auto kernel = a.sinks ? decode_gqa_kernel<D, G, true> : decode_gqa_kernel<D, G, false>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM)) return e;
+    return launch_dep(kernel, dim3(a.max_splits, a.Hkv, a.B), dim3(kWarps * 32), C::SMEM, st,
                       m.k, m.v, a);
 }
 

@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
     int lo, hi;
     key_range(len, a.S, a.W, a.ring, lo, hi);
     const int lo_t = lo & ~(kPage - 1);                  // tiles start at a page
-    const int nsplit = (hi - lo_t + a.split - 1) / a.split;
-    if (split >= nsplit) return;
-    const int k_first = lo_t + split * a.split;          // the CTA's keys
+    if (split >= split_count(lo_t, lo, hi, a.split, a.sinks)) return;
+    int k_first;                                         // the CTA's keys
+    split_keys(split, lo_t, a.split, a.sinks, lo, hi, k_first);
     const int k_end = min(hi, k_first + a.split);
 
     unsigned char* myS = smem + warp * C::WARPB;

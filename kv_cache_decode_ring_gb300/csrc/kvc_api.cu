@@ -1,5 +1,6 @@
 // kvc_api.cu -- the C ABI (include/kvc.h): argument checks, state layout, host
 // mirror of next_position, RoPE table, and kernel launches.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <memory>
@@ -90,6 +91,8 @@ bool make_shape(const kvc_config& c, Shape* s) {
         if ((c.head_dim != 64 && c.head_dim != 128) || (g != 1 && g != 2 && g != 4 && g != 8)) return false;
     }
     if (int4 && (c.dtype != KVC_BF16 || (c.head_dim != 64 && c.head_dim != 128) || c.capacity % kPage)) return false;
+    // sinks: for a window that leaves them behind (a ring overwrites them)
+    if (c.sinks < 0 || (c.sinks > 0 && (ring || int8 || c.window == 0))) return false;
     const bool rope = c.rope_base > 0.f;
     int P = 0;
     if (rope) {
@@ -101,6 +104,8 @@ bool make_shape(const kvc_config& c, Shape* s) {
     s->P = P; s->ring = ring; s->int8 = int8; s->rope = rope; s->bf16 = c.dtype == KVC_BF16;
     s->dither = dither;
     s->int4 = int4;
+    // (a query whose window leaves positions behind sits at S - 1 at most: more sinks than that change nothing)
+    s->sinks = c.window < c.capacity ? std::min(c.sinks, c.capacity - c.window) : 0;
     s->elem = s->bf16 ? 2 : 4;
     s->max_chunk = c.max_chunk;
     s->xpool = c.int8_exact_blocks;
@@ -125,6 +130,7 @@ bool make_shape(const kvc_config& c, Shape* s) {
         return false;
     // a paged cache may start its splits up to one page before the window
     s->max_splits = (int)((keys + s->split - 1) / s->split) + (s->pages > 0 || int4 ? 1 : 0);
+    s->max_splits += (s->sinks + s->split - 1) / s->split;
     if (int8) {
         // quantized splits (longer ones for long caches: less start-up per byte; a longer
         // split measured faster than one that fills the SMs' last wave of CTAs better), one
@@ -429,13 +435,14 @@ int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float*
     a.hdr = at<uint32_t>(h, h->L.hdr);
     a.table = s.pages ? at<int32_t>(h, h->L.table) : nullptr;
     a.B = s.B; a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W;
-    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16; a.int4 = s.int4;
+    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16; a.int4 = s.int4; a.sinks = s.sinks;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     CombineArgs c{};
     c.part_ml = a.part_ml; c.part_acc = a.part_acc; c.next_pos = a.next_pos; c.out = d_out;
     c.B = s.B; c.Hq = s.Hq; c.d = s.d; c.S = s.S; c.W = s.W; c.max_splits = s.max_splits;
     c.split = s.split; c.ring = s.ring; c.bf16 = s.out_bf16;
     c.align_lo = (s.pages > 0 && s.gqa) || s.int4;
+    c.sinks = s.sinks;
     const bool fast = s.split == kFastSplit && fast_decode_supported(a);
     if (launch_decode(a, c, fast, h->has_kv_maps ? &h->kv_maps : nullptr, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (d_cmax && cudaMemsetAsync(d_cmax, 0, (size_t)s.B * s.Hq * 4, st) != cudaSuccess) return KVC_ERR_CUDA;

@@ -69,6 +69,7 @@ struct Layout {
 
 struct Shape {
     int B, Hq, Hkv, g, d, S, W;  // W = attention window in positions (0 = full)
+    int sinks;                   // first positions that every query sees, whatever the window (0 = none)
     int P;                       // RoPE table rows (0 = no RoPE)
     int elem;                    // bytes per cache element (non-INT8)
     bool ring, int8, rope, bf16;
@@ -126,6 +127,7 @@ struct DecodeArgs {
     int B, Hq, Hkv, g, d, S, W, max_splits, split;
     int gqa;              // the GQA decode kernel serves the shape (split kGqaSplit or kGqaSplitLong)
     int int4;             // k and v hold rows of 4-bit codes: int4.cu serves the shape
+    int sinks;            // first positions that stay visible (contiguous caches with a window; 0 = none)
     int ring;
     int bf16;             // cache dtype (1 = bf16, 0 = fp32)
     float scale_log2;     // log2(e) / sqrt(d)
@@ -138,6 +140,7 @@ struct CombineArgs {
     void* out;            // [B][Hq][d] cache dtype
     int B, Hq, d, S, W, max_splits, split, ring, bf16;
     int align_lo;         // splits start at the window start rounded down to a page
+    int sinks;            // as DecodeArgs: their splits follow the window's
 };
 
 struct AppendArgs {
@@ -390,6 +393,22 @@ __host__ __device__ __forceinline__ int int8_abs_block(const Int8Window& w, int 
 __device__ __forceinline__ void key_range(int len, int S, int W, int ring, int& lo, int& hi) {
     if (ring) { lo = 0; hi = len < S ? len : S; }
     else { hi = len; lo = (W > 0 && len > W) ? len - W : 0; }
+}
+
+// Splits of `split` keys that the decode of a request has, in this order: those of the window [lo, hi) from
+// `first` on (lo, or lo rounded down to a page), then those of the sinks [0, min(sinks, lo)), which the
+// window left behind.  split_keys: the first key of split i, and in lo and hi the keys of its part.
+__device__ __forceinline__ int split_count(int first, int lo, int hi, int split, int sinks) {
+    return (hi - first + split - 1) / split + (min(sinks, lo) + split - 1) / split;
+}
+__device__ __forceinline__ void split_keys(int i, int first, int split, int sinks, int& lo, int& hi, int& k0) {
+    const int n = (hi - first + split - 1) / split;
+    k0 = first + i * split;
+    if (i >= n) {
+        hi = min(sinks, lo);
+        lo = 0;
+        k0 = (i - n) * split;
+    }
 }
 
 }  // namespace kvc

@@ -246,8 +246,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool there)
 
 enum { kLoadPairs, kLoadAsync, kLoadWide };           // rows of pairs; fp32 rows of 16-byte units; bf16 ones
 
-// DIMS: 64 (head_dim up to it), 128 or 256.
-template <int DIMS, int R, int LOAD>
+// DIMS: 64 (head_dim up to it), 128 or 256.  SINKS: the first tiles hold those of the first positions
+// that lie before the window of the CTA's first row; sinks in that window's tiles stay in sight there.
+template <int DIMS, int R, int LOAD, bool SINKS>
 __global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_kernel(const AttnArgs a, const __grid_constant__ Packed g) {
     constexpr int kBM = 8 * R, VW = DIMS == 64 ? 2 : 4, NV = DIMS == 256 ? 2 : 1;      // a lane's dims: NV runs of VW
     extern __shared__ float4 smem4[];
@@ -271,13 +272,15 @@ __global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_ker
     const int p_first = cut + (int)(row0 / a.g), p_last = cut + (int)((row0 + nrow - 1) / a.g);
     const int kmin = a.W > 0 ? max(0, p_first - a.W + 1) : 0;
     const int cal = cut & ~15;
-    const int tiles = p_last >= kmin ? (p_last - kmin) / kBN + 1 : 0;
+    const int sunk = SINKS ? min(a.sinks, kmin) : 0, nsunk = (sunk + kBN - 1) / kBN;
+    const int tiles = p_last >= kmin ? nsunk + (p_last - kmin) / kBN + 1 : 0;
+    auto first_of = [&](int j) { return SINKS && j < nsunk ? kBN * j - kmin : kBN * (j - nsunk); };   // of a tile, from kmin
     const int j0 = (int)((long long)tiles * part / a.parts), ntiles = (int)((long long)tiles * (part + 1) / a.parts);
 
     // rows of tile j into shared memory (what: 0 keys, 1 values), eight lanes a row
     auto fill = [&](int j, int what) {
         // (positions past the capacity, flagged before, have no rows to read)
-        const int kb = kmin + kBN * j, left = (a.ring ? p_last : min(p_last, a.S - 1)) - kb;
+        const int kb = kmin + first_of(j), left = (a.ring ? p_last : min(p_last, a.S - 1)) - kb;
         float* dst = what ? sV : sK;
         const int step = what ? d4 : kp;
 #pragma unroll
@@ -367,12 +370,15 @@ __global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_ker
                 s2[r][1] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k1.z, k1.w), s2[r][1]);
             }
         }
-        const int kb = kBN * j;           // (relative to kmin)
+        const int kb = first_of(j);       // (relative to kmin)
+        // keys c of the tile that a row sees by the sinks: those below this
+        const int cs = !SINKS ? 0 : j < nsunk ? sunk - kmin - kb : a.sinks - kmin - kb;
         bool whole = true;                // every key of the tile visible to every row of the warp
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int c0 = lo[r] - kb, c1 = p[r] - kb;             // visible: keys c0 .. c1 of the tile
-            const bool in0 = lane >= c0 && lane <= c1, in1 = lane + 32 >= c0 && lane + 32 <= c1;
+            const int c0 = SINKS && j < nsunk ? kBN : lo[r] - kb, c1 = p[r] - kb;      // visible: keys c0 .. c1 of the tile
+            const bool in0 = (lane >= c0 || (SINKS && lane < cs)) && lane <= c1;
+            const bool in1 = (lane + 32 >= c0 || (SINKS && lane + 32 < cs)) && lane + 32 <= c1;
             whole = whole && c0 <= 0 && c1 >= kBN - 1;
             const float x0 = in0 ? (s2[r][0].x + s2[r][0].y) * a.scale_log2 : -INFINITY;
             const float x1 = in1 ? (s2[r][1].x + s2[r][1].y) * a.scale_log2 : -INFINITY;
@@ -411,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_ker
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         // a masked key adds nothing, whatever its value row holds
-                        if (!all_seen && (kb + c + e < lo[r] || kb + c + e > p[r])) continue;
+                        if (!all_seen && (((SINKS && j < nsunk) || kb + c + e < lo[r]) && !(SINKS && c + e < cs))) continue;
+                        if (!all_seen && kb + c + e > p[r]) continue;
 #pragma unroll
                         for (int q = 0; q < VW / 2; ++q)
                             acc[r][v * VW / 2 + q] = __ffma2_rn(make_float2(we[e], we[e]), w4[e][q], acc[r][v * VW / 2 + q]);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, DIMS <= 128 ? 2 : 1) prompt_simt_ker
 
 template <int DIMS, int R, int LOAD>
 cudaError_t launch_rows(const AttnArgs& a, const Packed& g, int most, cudaStream_t st) {
-    auto kernel = prompt_simt_kernel<DIMS, R, LOAD>;
+    auto kernel = a.sinks ? prompt_simt_kernel<DIMS, R, LOAD, true> : prompt_simt_kernel<DIMS, R, LOAD, false>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), simt_smem(DIMS, R))) return e;
     const long long tiles = ((long long)most * a.g + 8 * R - 1) / (8 * R), per = std::min<long long>(tiles, 65535 / a.parts);
     const dim3 grid((unsigned)(a.Hkv * g.nb), (unsigned)(per * a.parts), (unsigned)((tiles + per - 1) / per));
@@ -479,7 +486,7 @@ cudaError_t launch_attention(const kvc_handle* h, const AttnArgs& args, const Pa
         if (n > 0) seen = std::max(seen, h->np[g.b0 + i] + n);
     }
     const bool tall = ctas[1] >= h->num_sms;
-    const long long longest = (a.W > 0 ? std::min(seen, (long long)a.W + 64) : seen) / kBN + 1;
+    const long long longest = (a.W > 0 ? std::min(seen, (long long)a.W + a.sinks + 64) : seen) / kBN + 1;
     const long long room = (long long)h->sh.B * h->sh.max_splits / g.off[g.nb];
     a.parts = (int)std::max(1ll, std::min({2 * h->num_sms / ctas[tall], longest / 2, room, (long long)kMaxKeyParts}));
     if (a.parts > 1) split_workspace(h, g, a.parts, &a);
@@ -532,6 +539,7 @@ cudaError_t launch_prompt(kvc_handle* h, const PromptArgs& p, const int32_t* cou
     a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W; a.P = s.P; a.ring = s.ring; a.bf16 = s.bf16;
     a.out_bf16 = s.out_bf16; a.ws_rows = r.ws_rows;
     a.parts = 1;
+    a.sinks = s.sinks;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     // the entry point checked alignment and strides
     const bool vec = s.bf16 && s.d % 8 == 0;

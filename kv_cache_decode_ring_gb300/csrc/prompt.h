@@ -28,6 +28,7 @@ struct AttnArgs {
     float* part_acc;                      // of [packed row][Hq][part]
     int Hq, Hkv, g, d, S, W, P, ring, bf16, out_bf16, ws_rows;
     int parts;                            // 1: no split
+    int sinks;                            // first positions that every row sees behind its window (0: none)
     float scale_log2;                     // log2(e) / sqrt(d)
 };
 

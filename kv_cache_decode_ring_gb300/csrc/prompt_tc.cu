@@ -119,11 +119,20 @@ struct Unit {
     int cut, p_last;                // position of the request's first row; of the unit's last
     int k0, nt;                     // first key, tiles
     int w0, w1;                     // tiles [w0, w1): every row sees every key; the others are boundary tiles
+    int ns, s0, sunk;               // tiles [0, ns) hold the sinks [s0, sunk) that lie before k0 (no key of a later tile)
 };
 
 __device__ __forceinline__ int first_key(const AttnArgs& a, int p) { return a.W > 0 ? max(0, p - a.W + 1) : 0; }
 
-template <int D>
+// First key of a unit's tile.
+template <int D, bool SINKS>
+__device__ __forceinline__ int tile_key(const Unit& w, int j) {
+    return (SINKS && j < w.ns ? w.s0 : w.k0) + Plan<D>::kBN * j;
+}
+
+// SINKS: the first tiles are those of the first positions, up to the window's first tile.  They are
+// boundary tiles, and w.k0 counts as if the window's tiles started in their place.
+template <int D, bool SINKS>
 __device__ __noinline__ Unit unit_of(const AttnArgs& a, const Items& items, int b0, int u) {
     constexpr int kBN = Plan<D>::kBN;
     Unit w;
@@ -139,18 +148,26 @@ __device__ __noinline__ Unit unit_of(const AttnArgs& a, const Items& items, int 
     w.p_last = p_first + w.ntok - 1;
     w.k0 = first_key(a, p_first) & ~15;
     w.nt = (w.p_last - w.k0) / kBN + 1;
-    int first = 0;
+    int first = 0, nsunk = 0;
+    if constexpr (SINKS) {
+        w.sunk = min(a.sinks, w.k0);
+        nsunk = (w.sunk + kBN - 1) / kBN;
+        w.nt += nsunk;
+    }
     if (items.parts > 1) {
         first = w.nt * w.part / items.parts;
         w.nt = w.nt * (w.part + 1) / items.parts - first;
     }
-    w.w0 = max(0, (first_key(a, w.p_last) - w.k0 + kBN - 1) / kBN - first);
+    w.ns = max(0, nsunk - first);
+    w.s0 = kBN * first;
+    first -= nsunk;
+    w.w0 = max(w.ns, (first_key(a, w.p_last) - w.k0 + kBN - 1) / kBN - first);
     w.w1 = max(w.w0, (p_first - w.k0 + 1) / kBN - first);
     w.k0 += kBN * first;
     return w;
 }
 
-template <int D>
+template <int D, bool SINKS>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CUtensorMap tmWK, const __grid_constant__ CUtensorMap tmWV,
@@ -267,16 +284,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[L::kSFree + slot]);          // the next S may overwrite it
-                const int kb = k0 + kBN * j;
+                const int kb = SINKS ? tile_key<D, SINKS>(w, j) : k0 + kBN * j;
                 if (!(kb >= sl && sh - kb >= kBN - 1) || !full) {
                     // (a word of visible keys per 16, which the compiler spreads over predicates: two
                     // comparisons a key took 3 to 6 % longer on short prompts; skipping groups that
                     // all or none of the warp's rows see costs the other tiles registers)
-                    const int c0 = valid ? key_lo - kb : kBN, c1 = valid ? p - kb : -1;       // visible: c0 .. c1
+                    const bool sunk = SINKS && j < w.ns;
+                    const int c0 = valid && !sunk ? key_lo - kb : kBN, c1 = valid ? p - kb : -1;       // visible: c0 .. c1
+                    const int cs = SINKS && valid ? (sunk ? w.sunk : min(a.sinks, p + 1)) - kb : 0;    // ... and 0 .. cs - 1
 #pragma unroll
                     for (int q = 0; q < kBN; q += 16) {
                         const int x0 = min(max(c0 - q, 0), 16), x1 = min(max(c1 - q + 1, 0), 16);
-                        const uint32_t seen = (0xffffffffu << x0) & ~(0xffffffffu << x1);
+                        uint32_t seen = (0xffffffffu << x0) & ~(0xffffffffu << x1);
+                        if constexpr (SINKS) seen |= ~(0xffffffffu << min(max(cs - q, 0), 16));
 #pragma unroll
                         for (int c = 0; c < 16; ++c) s[q + c] = seen >> c & 1 ? s[q + c] : -INFINITY;
                     }
@@ -426,9 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int c_last = min((a.ring ? p : min(p, a.S - 1)) - k0, nt * kBN - 1);
                     char* at = static_cast<char*>(parts ? static_cast<void*>(a.part_acc + (size_t)w.part * D) : a.out) + (orow + place[r]) * row_bytes;
 #pragma unroll 1
-                    for (int c = max(key_lo - k0, 0); c <= c_last; ++c) {
-                        const int j = c / kBN, key = k0 + c;
+                    for (int c = SINKS ? 0 : max(key_lo - k0, 0); c <= (SINKS ? nt * kBN - 1 : c_last); ++c) {
+                        const int j = c / kBN, key = SINKS ? tile_key<D, SINKS>(w, j) + c % kBN : k0 + c;
                         if (j >= w0 && j < w1) { c = w1 * kBN - 1; continue; }
+                        if (SINKS && !(j < w.ns ? key < w.sunk : key <= min(p, a.S - 1) && (key >= key_lo || key < a.sinks))) continue;
                         const bool staged = a.ring && key >= (w.cut & ~15);
                         const __nv_bfloat16* v = staged ? a.wv + stage_row(w.b, w.kvh, key, w.cut, a.Hkv, a.ws_rows) * D
                                                         : static_cast<const __nv_bfloat16*>(a.vc) +
@@ -491,22 +512,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         int k = 0, k_issued = 0, v_issued = 0;
         for (int rd = 0; rd * G < nunits && ok; ++rd) {
             if (mine(rd) >= nunits) continue;
-            const Unit w = unit_of<D>(a, items, b0, mine(rd));
+            const Unit w = unit_of<D, SINKS>(a, items, b0, mine(rd));
             const int head_row0 = (w.b * a.Hkv + w.kvh) * a.S, cal = w.cut & ~15;
             const int ws_row0 = (w.b * a.Hkv + w.kvh) * a.ws_rows;
             // where the lane's group of tile j lies: its page (read a tile ahead), or its first row
+            auto group_of = [&](int j) { return min(tile_key<D, SINKS>(w, j) + 16 * lane, w.p_last & ~15); };
             auto page_of = [&](int j) {
                 return a.table && lane < kBN / 16 && j < w.nt
-                           ? __ldg(a.table + (size_t)w.b * (a.S / kPage) + ((w.k0 + min(kBN * j + 16 * lane, (w.p_last & ~15) - w.k0)) / kPage) % (a.S / kPage))
+                           ? __ldg(a.table + (size_t)w.b * (a.S / kPage) + (group_of(j) / kPage) % (a.S / kPage))
                            : 0;
             };
             int page = page_of(0);
             for (int j = 0; j < w.nt; ++j, ++k) {
                 const int st = k % L::kStages;
                 const int ahead = page_of(j + 1);
-                int row = head_row0 + w.k0 + kBN * j;
+                int row = head_row0 + tile_key<D, SINKS>(w, j);
                 if (boxes) {
-                    const int pos = w.k0 + min(kBN * j + 16 * lane, (w.p_last & ~15) - w.k0);
+                    const int pos = group_of(j);
                     if (a.ring && pos >= cal) row = -1 - (ws_row0 + (pos - cal));      // a staged row
                     else row = a.table ? (max(page, 0) * a.Hkv + w.kvh) * kPage : head_row0 + pos % a.S;
                 }
@@ -599,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int k = 0;
         for (int rd = 0, i = 0; rd * G < nunits && ok; ++rd) {
             if (mine(rd) >= nunits) continue;
-            const Unit w = unit_of<D>(a, items, b0, mine(rd));
+            const Unit w = unit_of<D, SINKS>(a, items, b0, mine(rd));
             for (int j = 0; j < w.nt; ++j, ++k) {
                 const int st = k % L::kStages;
                 // (every tile in turn: a barrier's parity tells neighbouring phases apart only)
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int q = 0;
         for (int rd = 0; rd * G < nunits && ok; ++rd) {
             if (mine(rd) >= nunits) continue;
-            const Unit w = unit_of<D>(a, items, b0, mine(rd));
+            const Unit w = unit_of<D, SINKS>(a, items, b0, mine(rd));
             for (int slot = 0; slot < kSlots; ++slot, ++q) {
                 const int i = q >> 1, buf = q % L::kQBufs, uses = q / L::kQBufs;
                 if (uses > 0 && !(ok = all_ok(wait(&bar[L::kQFree + buf], (uint32_t)((uses - 1) & 1))))) break;
@@ -696,7 +718,7 @@ bool row_map(CUtensorMap* tm, const void* base, long long rows, int d, bool boxe
 
 template <int D>
 cudaError_t launch(const CUtensorMap* tm, const AttnArgs& a, int b0, const Items& items, int sms, cudaStream_t st) {
-    auto kernel = prompt_attn_kernel<D>;
+    auto kernel = a.sinks ? prompt_attn_kernel<D, true> : prompt_attn_kernel<D, false>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Plan<D>::kBytes)) return e;
     const long long units = (long long)items.n * a.Hkv;
     return launch_dep(kernel, dim3((unsigned)std::min<long long>(units, sms)), dim3(kThreads), Plan<D>::kBytes, st, tm[0], tm[1], tm[2],
@@ -753,7 +775,8 @@ cudaError_t launch_prompt_tc(const kvc_handle* h, const AttnArgs& a, const Packe
         for (int t = 0; t < n; t += kSlots * T) {
             const int first = cut + t, last = cut + std::min(n, t + kSlots * T) - 1;
             const int k0 = (s.W > 0 ? std::max(0, first - s.W + 1) : 0) & ~15;
-            work.push_back({-((last - k0) / bn + 1), make_int4(i, t, (int)(g.row0 + g.off[i]), n)});
+            const int sunk = (std::min(s.sinks, k0) + bn - 1) / bn;
+            work.push_back({-((last - k0) / bn + 1 + sunk), make_int4(i, t, (int)(g.row0 + g.off[i]), n)});
         }
     }
     std::stable_sort(work.begin(), work.end(), [](const auto& x, const auto& y) { return x.first < y.first; });

@@ -63,3 +63,17 @@ def test_refused_configurations(bad):
                                   dict(store_slots=2), dict(out_dtype="f32"), dict(max_chunk=16), dict(layout="ring", page_pool=9)])
 def test_accepted_configurations(good):
     assert kvc.kvc_state_bytes(config(**good)) > 0
+
+
+@pytest.mark.parametrize("bad", [dict(sinks=4), dict(sinks=-1, window=16), dict(sinks=4, layout="ring"),
+                                 dict(sinks=4, window=16, kv_quant="int8"), dict(sinks=4, window=16, kv_quant="int8-dither")])
+def test_refused_sinks(bad):
+    with pytest.raises(kvc.KvcError) as e:
+        kvc.kvc_state_bytes(config(**bad))
+    assert e.value.code == kvc.KVC_ERR_ARG
+
+
+@pytest.mark.parametrize("quant", [None, "int4"])
+def test_accepted_sinks(quant):
+    for sinks in (1, 48, 1 << 30):
+        assert kvc.kvc_state_bytes(config(kv_quant=quant, window=16, sinks=sinks)) > 0
