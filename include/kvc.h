@@ -424,8 +424,9 @@ int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride
  * ring, paged or not.  head_dim 64 or 128, capacity a multiple of 16, any number of query heads.
  * kvc_copy between a bf16 cache and one of this tier converts: rows written are quantised, rows
  * read back are m + u s, rounded once to bf16.  (A prompt runs on a bf16 cache and is handed over.)
- * kvc_decode_attn attends to the rows m + u s in fp32 (the query and the weights in two bf16 parts
- * each, 16 significant bits); d_cmax and d_tanh receive 0 and d_ct must be NULL.
+ * kvc_decode_attn attends to the rows m + u s with fp32 sums (the weights of codes rounded to fp16, relative
+ * error 2^-11 at most, and so is the query where a KV head has more than 4 query heads; else the query has 22
+ * bits); d_cmax and d_tanh receive 0 and d_ct must be NULL.
  * kvc_prompt_attn, kvc_chunk_attn and kvc_decode_attn_noalloc return KVC_ERR_UNSUPPORTED. */
 
 /* ---- gated fallback of the INT8 tier ----------------------------------

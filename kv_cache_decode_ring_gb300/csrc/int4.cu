@@ -5,8 +5,6 @@
 // codes, which are small integers, and terms per group (t a key, h a head):
 //     score_t   = sum_g s_tg (q_g . u_tg) + m_tg sum(q_g),
 //     out_x     = sum_t p_t s_tg u_tx + sum_t p_t m_tg          (x in group g).
-// Codes enter the tensor cores as the bf16 numbers 16 + u: a shift, an AND and an OR make two of
-// them; the 16 is taken back in the group's term, whose factor is m - 16 s instead of m.
 #include "async_copy.h"
 #include "int4.h"
 
@@ -118,21 +116,26 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 // ---- decode ------------------------------------------------------------------------------------
 // CTA = 4 warps = a split of the keys of one request and KV head, for up to 8 of its query heads; a warp
 // streams tiles of 32 keys through its stages of shared memory by bulk copies (a page, or 16 rows, is
-// contiguous).  Both products on the tensor cores (mma m16n8k16, bf16 operands, fp32
-// accumulation), operands unpacked in registers from the words that a lane loads:
-//  * scores, transposed: S^T[16 keys][cols] = U[16][32 dims of g] . Q^T, the columns (head, hi) and
-//    (head, lo): the rotated query times log2(e)/sqrt(d) in two bf16 parts (16 significant
-//    bits); the groups' sums are weighed by s_tg and joined by the lane that holds head and keys;
-//  * P.V, transposed: O^T[16 dims of g][cols] += U^T . P_g^T, P_g = p s_tg as bf16 hi + lo,
-//    brought from score order to operand order by movmatrix (the pair (hi, lo) of a key and head
-//    is one register of a score fragment).
+// contiguous).  Both products on the tensor cores (mma m16n8k16, fp16 operands, fp32
+// accumulation), operands unpacked in registers from the words that a lane loads.  A nibble
+// masked out of its 16-bit half is the fp16 number u 2^-24, one four bits higher u 2^-20, both exact
+// (subnormal) and without a bias, so a word's 8 codes take four ANDs and a shift; the factor 16 of
+// every other one is taken back in the query, or in the output.
+//  * scores, transposed: S^T[16 keys][cols] = U[16][32 dims of g] . Q^T, the query times log2(e)/sqrt(d) and
+//    a power of two that puts its largest value below 2^15.  Up to 4 heads: columns (head, hi) and
+//    (head, lo), two fp16 parts, 22 significant bits; up to 8: a column each, 11 bits.  The groups'
+//    sums are weighed by s_tg and joined by the lane that holds head and keys;
+//  * P.V, transposed: O^T[16 dims of g][heads] += U^T . P_g^T, P_g = p s_tg times a power of two of the head's
+//    (norm) as fp16, off by 2^-11 at most, brought from score order to operand order by movmatrix.
+//    The norm starts high and falls when a weight would pass 2^15, to put the largest at 2^9:
+//    weights down to 2^-23 of the largest stay normal.  The terms p m_tg are summed in fp32.
 // Row r of a fragment of 16 keys stands for key tok(r): rows are 80 bytes apart (d = 128), and with this
 // order the lanes' 16-byte loads of K (rows r, r + 1 together) and 8-byte loads of V (rows 0, 2, 4, 6
 // together) fall into different banks.
-// Lane L: g = L / 4 (fragment row), qd = L % 4 (head, and head 4 + qd).
+// Lane L: g = L / 4 (fragment row), qd = L % 4 (its head, or its heads 2 qd and 2 qd + 1).
 constexpr int kWarps = 4;
 constexpr int kTile = 32;
-constexpr float kLazyMax = 8.f;                          // log2-domain headroom of the reference maximum
+constexpr float kLazyMax = 4.f;                          // log2-domain headroom of the reference maximum
 
 __device__ __forceinline__ int tok(int r) { return r & 1 ? 8 + ((r + 3) & 7) : r; }      // rows 0..7; row r + 8: tok(r) + 1
 
@@ -142,12 +145,20 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// D (16x8, fp32) += A (16x16, bf16, row) . B (16x8, bf16, col)
+__device__ __forceinline__ float fmax3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// D (16x8, fp32) = A (16x16, fp16, row) . B (16x8, fp16, col) + C
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // 8 x 8 matrix of 16-bit elements, transposed across the warp.
@@ -157,26 +168,26 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return y;
 }
 
-// (16 + low nibble, 16 + high-half nibble) of nibble i of both halves of w, as bf16: 16 is 0x4180,
-// and between 16 and 32 the last 7 bits count eighths.
-template <int I>
-__device__ __forceinline__ uint32_t pair_of(uint32_t w) {
-    const uint32_t x = I == 0 ? w << 3 : w >> (I == 0 ? 0 : 4 * I - 3);
-    return (x & 0x00780078u) | 0x41804180u;
+// The four pairs of codes of a word: pair i is nibble i of its low and of its high half.
+struct Pairs {
+    uint32_t x[4];                                       // times 2^-24, 2^-20, 2^-24, 2^-20
+};
+__device__ __forceinline__ Pairs pairs_of(uint32_t w) {
+    const uint32_t v = w >> 8;
+    return Pairs{{w & 0x000f000fu, w & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u}};
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 t = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// (hi, lo) with hi = bf16(x), lo = bf16(x - hi), hi in the low half
-__device__ __forceinline__ uint32_t split_pair(float x) {
-    const float hi = __bfloat162float(__float2bfloat16_rn(x));
-    return pack_bf16(hi, x - hi);
-}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }      // -126 .. 127
 
-template <int D, int NT>
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// HL: heads per lane (1: up to 4 heads of the CTA, 2: up to 8).
+template <int D, int HL>
 struct I4 {
     static constexpr int G = D / int4::kGroup;           // groups of a row
     static constexpr int ROW = int4::row_size(D);
@@ -184,7 +195,7 @@ struct I4 {
     static constexpr int STAGEB = 2 * HALF;
     static constexpr int STAGES = 2;
     static constexpr int WARPB = STAGES * STAGEB;
-    static constexpr int HEADS = 4 * NT;
+    static constexpr int HEADS = 4 * HL;
     static constexpr int PARTF = HEADS * (D + 2);        // a warp's partial (m, l, acc), in its stages at the end
     static_assert(PARTF * 4 <= WARPB, "partial must fit in the warp's stages");
     static constexpr int OFF_Q = kWarps * WARPB;         // query [HEADS][D] fp32
@@ -193,9 +204,9 @@ struct I4 {
     static_assert(HALF % 16 == 0 && kPage * ROW % 16 == 0, "bulk copies");
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kernel(const DecodeArgs a, const int chunks) {
-    using C = I4<D, NT>;
+template <int D, int HL>
+__global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_decode_kernel(const DecodeArgs a, const int chunks) {
+    using C = I4<D, HL>;
     constexpr int G = C::G;
     extern __shared__ __align__(128) unsigned char smem[];
     float* sQ = reinterpret_cast<float*>(smem + C::OFF_Q);
@@ -271,38 +282,59 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
     __syncthreads();
 
     const int g = lane >> 2, qd = lane & 3;
-    // B operand of the scores: column n = 8 nt + g is (head 4 nt + g / 2, hi | lo); k-step s of group j takes
-    // dims 32 j + 8 qd + {2 s, 2 s + 4} and {2 s + 1, 2 s + 5}.  And the lane's heads' sums over a group.
-    uint32_t qb[NT][G][2][2];
-    float qsum[NT][G];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    // B operand of the scores: column g is (head g / 2, hi | lo) or head g; k-step s of group j takes dims
+    // 32 j + 8 qd + {2 s, 2 s + 4} and, with codes 16 times as large, {2 s + 1, 2 s + 5}.  Each column's
+    // head times 2^e: its largest value in [2^14, 2^15).
+    auto exponent = [&](int h) {                         // (4 lanes a row of values, D / 4 each)
+        float m = 0.f;
+        for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(sQ[h * D + qd * (D / 4) + ((i + g) & (D / 4 - 1))]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        return max(-103, min(100, 15 + 126 - (int)(__float_as_uint(m) >> 23)));
+    };
+    uint32_t qb[G][2][2];
+    const int hcol = HL == 1 ? g / 2 : g, ecol = exponent(hcol);
+    {
+        const float up = power_of_two(ecol);
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            const float* q = sQ + (4 * nt + g / 2) * D + 32 * j + 8 * qd;
+            const float* q = sQ + hcol * D + 32 * j + 8 * qd;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const uint32_t x = split_pair(q[2 * s + k]), y = split_pair(q[2 * s + k + 4]);
-                    qb[nt][j][s][k] = g & 1 ? __byte_perm(x, y, 0x7632) : __byte_perm(x, y, 0x5410);
+                    const float f = k == 0 ? up : up * 0.0625f, x = q[2 * s + k] * f, y = q[2 * s + k + 4] * f;
+                    const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
+                    qb[j][s][k] = HL == 1 && (g & 1) ? pack_half(x - __half2float(xh), y - __half2float(yh)) : pack_half(x, y);
                 }
-            float sum = 0.f;
-            for (int i = 0; i < 32; ++i) sum += sQ[(4 * nt + qd) * D + 32 * j + ((i + lane) & 31)];
-            qsum[nt][j] = sum;
-        }
-
-    float m_w[NT], l_w[NT], gacc[NT][G], acc[G][2][NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        m_w[nt] = -INFINITY; l_w[nt] = 0.f;
-#pragma unroll
-        for (int j = 0; j < G; ++j) {
-            gacc[nt][j] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][0][nt][e] = acc[j][1][nt][e] = 0.f;
         }
     }
+    // the lane's heads: exponents (of row h, held by the lanes of column h), sums of the query over a group in the
+    // accumulators' unit, and that unit
+    float qsum[HL][G], unit[HL];
+#pragma unroll
+    for (int n = 0; n < HL; ++n) {
+        const int h = HL * qd + n, e = __shfl_sync(0xffffffffu, ecol, HL == 1 ? 8 * h : 4 * h);
+        unit[n] = power_of_two(24 - e);
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            float sum = 0.f;
+            for (int i = 0; i < 32; ++i) sum += sQ[h * D + 32 * j + ((i + lane) & 31)];
+            qsum[n][j] = sum * power_of_two(e - 24);
+        }
+    }
+
+    float m_w[HL], l_w[HL], norm[HL], gacc[HL][G], acc[G][2][4];
+#pragma unroll
+    for (int n = 0; n < HL; ++n) {
+        m_w[n] = -INFINITY; l_w[n] = 0.f; norm[n] = 0x1p100f;
+#pragma unroll
+        for (int j = 0; j < G; ++j) gacc[n][j] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][0][e] = acc[j][1][e] = 0.f;
     const int tr = tok(g), ta = tok(2 * qd), tb = tok(2 * qd + 1);     // keys of rows g, 2 qd, 2 qd + 1 (and + 8: the next)
 
     const int tpw = a.split / (kWarps * kTile);
@@ -325,7 +357,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
         const bool whole = nk == kTile && kmin <= 0;
 
         // ---- scores of keys tr, tr + 1 of both blocks
-        float sc[2][2][NT];
+        float sc[2][2][HL];
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
             const unsigned char* r0 = tK + (16 * blk + tr) * C::ROW;
@@ -341,23 +373,31 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
                 w0[0] = u0.x; w0[1] = u0.y; w1[0] = u1.x; w1[1] = u1.y;
                 p0[0] = v0.x; p0[1] = v0.y; p1[0] = v1.x; p1[1] = v1.y;
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[blk][0][nt] = sc[blk][1][nt] = 0.f;
+            // sums of the keys' rows: by columns (hi and lo, or two heads), and (one head) of the minima's terms by rows
+            float2 x0 = both(0.f), x1 = both(0.f), xm = both(0.f);
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const uint32_t x0 = pair_of<0>(w0[j]), x1 = pair_of<0>(w1[j]), x2 = pair_of<1>(w0[j]), x3 = pair_of<1>(w1[j]);
-                const uint32_t y0 = pair_of<2>(w0[j]), y1 = pair_of<2>(w1[j]), y2 = pair_of<3>(w0[j]), y3 = pair_of<3>(w1[j]);
-                const float s0 = __uint_as_float(p0[j] << 16), s1 = __uint_as_float(p1[j] << 16);
-                const float t0 = fmaf(-16.f, s0, __uint_as_float(p0[j] & 0xffff0000u));
-                const float t1 = fmaf(-16.f, s1, __uint_as_float(p1[j] & 0xffff0000u));
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma(c, x0, x1, x2, x3, qb[nt][j][0][0], qb[nt][j][0][1]);
-                    mma(c, y0, y1, y2, y3, qb[nt][j][1][0], qb[nt][j][1][1]);
-                    sc[blk][0][nt] = fmaf(s0, c[0] + c[1], fmaf(t0, qsum[nt][j], sc[blk][0][nt]));
-                    sc[blk][1][nt] = fmaf(s1, c[2] + c[3], fmaf(t1, qsum[nt][j], sc[blk][1][nt]));
+                const Pairs u = pairs_of(w0[j]), v = pairs_of(w1[j]);
+                float c[4];
+                mma_first(c, u.x[0], v.x[0], u.x[1], v.x[1], qb[j][0][0], qb[j][0][1]);
+                mma(c, u.x[2], v.x[2], u.x[3], v.x[3], qb[j][1][0], qb[j][1][1]);
+                const float m0 = __uint_as_float(p0[j] & 0xffff0000u), m1 = __uint_as_float(p1[j] & 0xffff0000u);
+                x0 = __ffma2_rn(both(__uint_as_float(p0[j] << 16)), make_float2(c[0], c[1]), x0);
+                x1 = __ffma2_rn(both(__uint_as_float(p1[j] << 16)), make_float2(c[2], c[3]), x1);
+                if constexpr (HL == 1) {
+                    xm = __ffma2_rn(make_float2(m0, m1), both(qsum[0][j]), xm);
+                } else {
+                    const float2 q = make_float2(qsum[0][j], qsum[HL - 1][j]);
+                    x0 = __ffma2_rn(both(m0), q, x0);
+                    x1 = __ffma2_rn(both(m1), q, x1);
                 }
+            }
+            if constexpr (HL == 1) {
+                sc[blk][0][0] = (x0.x + x0.y + xm.x) * unit[0];
+                sc[blk][1][0] = (x1.x + x1.y + xm.y) * unit[0];
+            } else {
+                sc[blk][0][0] = x0.x * unit[0]; sc[blk][0][HL - 1] = x0.y * unit[HL - 1];
+                sc[blk][1][0] = x1.x * unit[0]; sc[blk][1][HL - 1] = x1.y * unit[HL - 1];
             }
         }
         if (!whole) {
@@ -367,89 +407,143 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
                 for (int e = 0; e < 2; ++e) {
                     const int key = 16 * blk + tr + e;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) sc[blk][e][nt] = key < nk && key >= kmin ? sc[blk][e][nt] : -INFINITY;
+                    for (int n = 0; n < HL; ++n) sc[blk][e][n] = key < nk && key >= kmin ? sc[blk][e][n] : -INFINITY;
                 }
         }
         // ---- online softmax of the lane's heads over the tile
         bool rescale = false;
-        float alpha[NT];
+        float alpha[HL];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float bm = fmaxf(fmaxf(sc[0][0][nt], sc[0][1][nt]), fmaxf(sc[1][0][nt], sc[1][1][nt]));
+        for (int n = 0; n < HL; ++n) {
+            float bm = fmaxf(fmax3(sc[0][0][n], sc[0][1][n], sc[1][0][n]), sc[1][1][n]);
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
             bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-            const float mn = bm > m_w[nt] + kLazyMax ? bm : m_w[nt];
-            alpha[nt] = ex2(m_w[nt] - mn);               // 0 while the maximum was -inf
-            rescale |= alpha[nt] != 1.f;
-            m_w[nt] = mn;
-            float sum = 0.f;
+            const float mn = bm > m_w[n] + kLazyMax ? bm : m_w[n];
+            alpha[n] = ex2(m_w[n] - mn);                 // 0 while the maximum was -inf
+            rescale |= alpha[n] != 1.f;
+            m_w[n] = mn;
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[blk][e][nt] = ex2(sc[blk][e][nt] - mn);        // masked keys: 0
-                    sum += sc[blk][e][nt];
-                }
-            l_w[nt] = fmaf(l_w[nt], alpha[nt], sum);
+                for (int e = 0; e < 2; ++e) sc[blk][e][n] = ex2(sc[blk][e][n] - mn);          // masked keys: 0
+            l_w[n] = fmaf(l_w[n], alpha[n], (sc[0][0][n] + sc[0][1][n]) + (sc[1][0][n] + sc[1][1][n]));
         }
-        if (__any_sync(0xffffffffu, rescale) && i > 0) {  // at i = 0 the accumulators are 0
+        // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
+        auto scale_acc = [&](const float (&f)[HL]) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < G; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
+                    acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
+                }
+        };
+        if (__any_sync(0xffffffffu, rescale) && i > 0) {  // at i = 0 the accumulators are 0
+            scale_acc(alpha);
+#pragma unroll
+            for (int n = 0; n < HL; ++n)
+#pragma unroll
+                for (int j = 0; j < G; ++j) gacc[n][j] *= alpha[n];
+        }
+        // ---- scales and minima of the values; a masked key adds nothing, whatever its row holds
+        uint32_t vp[2][2][G];
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const unsigned char* r = tV + (16 * blk + tr + e) * C::ROW + D / 2;
+                if constexpr (G == 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(r);
+                    vp[blk][e][0] = u.x; vp[blk][e][1] = u.y; vp[blk][e][2] = u.z; vp[blk][e][3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(r);
+                    vp[blk][e][0] = u.x; vp[blk][e][1] = u.y;
+                }
+                if (!whole) {
+                    const int key = 16 * blk + tr + e;
+#pragma unroll
+                    for (int j = 0; j < G; ++j)
+                        if (!(key < nk && key >= kmin)) vp[blk][e][j] = 0u;
+                }
+            }
+        // ---- weights times scales, and the minima's terms
+        float2 pw[2][G][HL];                             // of keys tr, tr + 1 (one head), else of two heads, for each key
+        auto weigh = [&]() {
+            float top = 0.f;
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    gacc[nt][j] *= alpha[nt];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { acc[j][0][nt][e] *= alpha[nt]; acc[j][1][nt][e] *= alpha[nt]; }
+                    const float s0 = __uint_as_float(vp[blk][0][j] << 16), s1 = __uint_as_float(vp[blk][1][j] << 16);
+                    if constexpr (HL == 1) {
+                        const float2 e = __fmul2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), both(norm[0]));
+                        pw[blk][j][0] = __fmul2_rn(e, make_float2(s0, s1));
+                        top = fmax3(top, pw[blk][j][0].x, pw[blk][j][0].y);
+                    } else {
+                        const float2 nn = make_float2(norm[0], norm[HL - 1]);
+                        pw[blk][j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][0][HL - 1]), nn), both(s0));
+                        pw[blk][j][HL - 1] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][1][0], sc[blk][1][HL - 1]), nn), both(s1));
+                        top = fmax3(top, pw[blk][j][0].x, pw[blk][j][0].y);
+                        top = fmax3(top, pw[blk][j][HL - 1].x, pw[blk][j][HL - 1].y);
+                    }
                 }
+            return top;
+        };
+        if (__any_sync(0xffffffffu, weigh() > 32768.f)) {
+            // a head whose largest weight passes 2^15 gets a norm that puts it into [2^9, 2^10)
+            float f[HL];
+#pragma unroll
+            for (int n = 0; n < HL; ++n) {
+                float top = 0.f;
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int j = 0; j < G; ++j) top = fmaxf(top, sc[blk][e][n] * __uint_as_float(vp[blk][e][j] << 16));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const int e = (int)(__float_as_uint(top) >> 23) - 127;
+                const float to = top * norm[n] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n];
+                f[n] = to / norm[n];
+                norm[n] = to;
+            }
+            scale_acc(f);
+            weigh();
         }
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                const float m0 = __uint_as_float(vp[blk][0][j] & 0xffff0000u), m1 = __uint_as_float(vp[blk][1][j] & 0xffff0000u);
+#pragma unroll
+                for (int n = 0; n < HL; ++n) gacc[n][j] = fmaf(sc[blk][0][n], m0, fmaf(sc[blk][1][n], m1, gacc[n][j]));
+            }
         // ---- P.V of both blocks
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
-            const unsigned char* v0 = tV + 16 * blk * C::ROW;
-            uint32_t p0[G], p1[G], wa[G / 2], wb[G / 2], wc[G / 2], wd[G / 2];
-            {
-                const unsigned char* r0 = v0 + tr * C::ROW + D / 2;
-                const unsigned char *xa = v0 + ta * C::ROW, *xb = v0 + tb * C::ROW;
-                if constexpr (G == 4) {
-                    const uint4 u0 = *reinterpret_cast<const uint4*>(r0), u1 = *reinterpret_cast<const uint4*>(r0 + C::ROW);
-                    p0[0] = u0.x; p0[1] = u0.y; p0[2] = u0.z; p0[3] = u0.w; p1[0] = u1.x; p1[1] = u1.y; p1[2] = u1.z; p1[3] = u1.w;
-                    const uint2 ya = *reinterpret_cast<const uint2*>(xa + 8 * g), yb = *reinterpret_cast<const uint2*>(xb + 8 * g);
-                    const uint2 yc = *reinterpret_cast<const uint2*>(xa + C::ROW + 8 * g), yd = *reinterpret_cast<const uint2*>(xb + C::ROW + 8 * g);
-                    wa[0] = ya.x; wa[1] = ya.y; wb[0] = yb.x; wb[1] = yb.y; wc[0] = yc.x; wc[1] = yc.y; wd[0] = yd.x; wd[1] = yd.y;
-                } else {
-                    const uint2 u0 = *reinterpret_cast<const uint2*>(r0), u1 = *reinterpret_cast<const uint2*>(r0 + C::ROW);
-                    p0[0] = u0.x; p0[1] = u0.y; p1[0] = u1.x; p1[1] = u1.y;
-                    wa[0] = *reinterpret_cast<const uint32_t*>(xa + 4 * g); wb[0] = *reinterpret_cast<const uint32_t*>(xb + 4 * g);
-                    wc[0] = *reinterpret_cast<const uint32_t*>(xa + C::ROW + 4 * g); wd[0] = *reinterpret_cast<const uint32_t*>(xb + C::ROW + 4 * g);
-                }
-            }
-            if (!whole) {
-                // a masked key adds nothing, whatever its row holds
-                const int k0 = 16 * blk + tr;
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    if (!(k0 < nk && k0 >= kmin)) p0[j] = 0u;
-                    if (!(k0 + 1 < nk && k0 + 1 >= kmin)) p1[j] = 0u;
-                }
+            const unsigned char* xa = tV + (16 * blk + ta) * C::ROW;
+            const unsigned char* xb = tV + (16 * blk + tb) * C::ROW;
+            uint32_t wa[G / 2], wb[G / 2], wc[G / 2], wd[G / 2];
+            if constexpr (G == 4) {
+                const uint2 ya = *reinterpret_cast<const uint2*>(xa + 8 * g), yb = *reinterpret_cast<const uint2*>(xb + 8 * g);
+                const uint2 yc = *reinterpret_cast<const uint2*>(xa + C::ROW + 8 * g), yd = *reinterpret_cast<const uint2*>(xb + C::ROW + 8 * g);
+                wa[0] = ya.x; wa[1] = ya.y; wb[0] = yb.x; wb[1] = yb.y; wc[0] = yc.x; wc[1] = yc.y; wd[0] = yd.x; wd[1] = yd.y;
+            } else {
+                wa[0] = *reinterpret_cast<const uint32_t*>(xa + 4 * g); wb[0] = *reinterpret_cast<const uint32_t*>(xb + 4 * g);
+                wc[0] = *reinterpret_cast<const uint32_t*>(xa + C::ROW + 4 * g); wd[0] = *reinterpret_cast<const uint32_t*>(xb + C::ROW + 4 * g);
             }
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const float s0 = __uint_as_float(p0[j] << 16), s1 = __uint_as_float(p1[j] << 16);
-                const float t0 = fmaf(-16.f, s0, __uint_as_float(p0[j] & 0xffff0000u));
-                const float t1 = fmaf(-16.f, s1, __uint_as_float(p1[j] & 0xffff0000u));
                 const int sel = j & 1 ? 0x7632 : 0x5410;
-                const uint32_t x = __byte_perm(wa[j / 2], wb[j / 2], sel), y = __byte_perm(wc[j / 2], wd[j / 2], sel);
-                const uint32_t x0 = pair_of<0>(x), x1 = pair_of<1>(x), x2 = pair_of<2>(x), x3 = pair_of<3>(x);
-                const uint32_t y0 = pair_of<0>(y), y1 = pair_of<1>(y), y2 = pair_of<2>(y), y3 = pair_of<3>(y);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float e0 = sc[blk][0][nt], e1 = sc[blk][1][nt];
-                    gacc[nt][j] = fmaf(e0, t0, fmaf(e1, t1, gacc[nt][j]));
-                    const uint32_t b0 = transposed(split_pair(e0 * s0)), b1 = transposed(split_pair(e1 * s1));
-                    mma(acc[j][0][nt], x0, x1, y0, y1, b0, b1);
-                    mma(acc[j][1][nt], x2, x3, y2, y3, b0, b1);
-                }
+                const Pairs u = pairs_of(__byte_perm(wa[j / 2], wb[j / 2], sel)), v = pairs_of(__byte_perm(wc[j / 2], wd[j / 2], sel));
+                const float2 p = pw[blk][j][0], r = pw[blk][j][HL - 1];
+                const uint32_t b0 = transposed(HL == 1 ? pack_half(p.x, 0.f) : pack_half(p.x, p.y));
+                const uint32_t b1 = transposed(HL == 1 ? pack_half(p.y, 0.f) : pack_half(r.x, r.y));
+                mma(acc[j][0], u.x[0], u.x[1], v.x[0], v.x[1], b0, b1);
+                mma(acc[j][1], u.x[2], u.x[3], v.x[2], v.x[3], b0, b1);
             }
         }
         // the stage is free once every lane is past its reads
@@ -459,26 +553,27 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
     }
 
     // ---- this warp's partial into its own stages (every issued tile was waited for): l and the
-    // groups' terms summed over the 8 lanes of a head; output = hi + lo columns + the group's term
+    // groups' terms summed over the 8 lanes of a head; output = products in their unit + the group's term
     __syncwarp();
     float* part_w = reinterpret_cast<float*>(myS);       // [HEADS][2 + D]
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int h = 4 * nt + qd;
-        float l = l_w[nt];
+    for (int n = 0; n < HL; ++n) {
+        const int h = HL * qd + n;
+        float l = l_w[n];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (g == 0) { part_w[h * (D + 2)] = m_w[nt]; part_w[h * (D + 2) + 1] = l; }
+        if (g == 0) { part_w[h * (D + 2)] = m_w[n]; part_w[h * (D + 2) + 1] = l; }
+        const float even = 0x1p24f / norm[n], odd = 0x1p20f / norm[n];
 #pragma unroll
         for (int j = 0; j < G; ++j) {
-            float t = gacc[nt][j];
+            float t = gacc[n][j];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
             float* o = part_w + h * (D + 2) + 2 + 32 * j + 4 * g;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                o[2 * k] = acc[j][k][nt][0] + acc[j][k][nt][1] + t;
-                o[2 * k + 1] = acc[j][k][nt][2] + acc[j][k][nt][3] + t;
+                o[2 * k] = fmaf(acc[j][k][n], even, t);
+                o[2 * k + 1] = fmaf(acc[j][k][2 + n], odd, t);
             }
         }
     }
@@ -502,11 +597,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) int4_decode_kern
     }
 }
 
-template <int D, int NT>
+template <int D, int HL>
 cudaError_t launch_t(const DecodeArgs& a, int chunks, cudaStream_t st) {
-    using C = I4<D, NT>;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(int4_decode_kernel<D, NT>), C::SMEM)) return e;
-    return launch_dep(int4_decode_kernel<D, NT>, dim3(a.max_splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
+    using C = I4<D, HL>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(int4_decode_kernel<D, HL>), C::SMEM)) return e;
+    return launch_dep(int4_decode_kernel<D, HL>, dim3(a.max_splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
 }
 
 }  // namespace

@@ -80,16 +80,16 @@ def attend(q, k, v):
 def decode_bound(q, kparts, vparts, p, steps=2048):
     """How far the kernel's fp32 result may be off, from its roundings (kparts, vparts: u, s, m of the visible rows).
 
-    Query and weights enter as two bf16 parts: 2^-17 relative, the query's times log2(e)/sqrt(d) in fp32 and rotated in fp32
-    from fp32 cosines (2^-23 of |q_i| + |q_j|).  Products are summed in fp32 as codes 16 + u <= 31 and a term
-    (m - 16 s): magnitudes of at most 47 s + |m| a dim, with at most d/16 + 8 roundings of 2^-23 (the matrix unit's adds
-    truncate) a score and `steps` / 32 + 24 for an output's chain of adds.  2^x is off by 2^-22.  A score off by e changes
-    weights by 2 e relative at most (numerator and sum)."""
+    The query enters as fp16 (2^-11 relative; up to 4 heads a KV head as two parts, 2^-21), times log2(e)/sqrt(d) in fp32 and
+    rotated in fp32 from fp32 cosines (2^-22 of |q_i| + |q_j|); the weights of codes as fp16 (2^-11).  Products are summed
+    in fp32 as codes of at most 15 s and a term m, with at most d/16 + 8 roundings of 2^-23 (the matrix unit's
+    adds truncate) a score and `steps` / 32 + 24 for an output's chain of adds.  2^x is off by 2^-22.  A score off by e
+    changes weights by 2 e relative at most (numerator and sum)."""
     d, r = q.shape[-1], q.shape[0] // kparts[1].shape[0]
-    wide = lambda parts: (47 * parts[1].double().abs() + parts[2].double().abs()).repeat_interleave(r, 0)  # noqa: E731
+    wide = lambda parts: (15 * parts[1].double().abs() + parts[2].double().abs()).repeat_interleave(r, 0)  # noqa: E731
     qg = q.abs().unflatten(-1, (-1, GROUP)).sum(-1)                                           # [hq, G]
     size = (wide(kparts) * qg[:, None]).sum(-1).amax(-1) / math.sqrt(d)                       # [hq]
-    score = size * (2.0 ** -17 + 2.0 ** -22 + (d / 16 + 8) * 2.0 ** -23) + 2.0 ** -22
-    rel = 2 * score[:, None] + 2.0 ** -17 + (steps / 32 + 24) * 2.0 ** -23
+    score = size * ((2.0 ** -21 if r <= 4 else 2.0 ** -11) + 2.0 ** -21 + (d / 16 + 8) * 2.0 ** -23) + 2.0 ** -22
+    rel = 2 * score[:, None] + 2.0 ** -11 + (steps / 32 + 24) * 2.0 ** -23
     wv = wide(vparts).repeat_interleave(GROUP, -1)
     return rel * torch.einsum("hn,hnd->hd", p, wv)
