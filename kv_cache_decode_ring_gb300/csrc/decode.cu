@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
         int lo, hi;
         key_range(len, c.S, c.W, c.ring, lo, hi);
         // (the paged GQA and the INT4 decode's splits start at a page)
-        ns = split_count(c.align_lo ? lo & ~(kPage - 1) : lo, lo, hi, c.split, c.sinks);
+        ns = c.int4 ? (int4_span(len, c.S, c.W, c.ring, c.sinks).steps * kInt4Step + c.split - 1) / c.split
+                    : split_count(c.align_lo ? lo & ~(kPage - 1) : lo, lo, hi, c.split, c.sinks);
     }
     if (valid && vec) {
         float m = -INFINITY, l = 0.f;
@@ -218,9 +219,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
 }  // namespace
 
 cudaError_t launch_decode(const DecodeArgs& a, const CombineArgs& c, bool fast, const KvMaps* maps, cudaStream_t st) {
-    if (a.int4) {
-        if (cudaError_t e = launch_int4_splits(a, st)) return e;
-    } else if (a.gqa) {
+    if (a.gqa) {
         if (!maps) return cudaErrorInvalidValue;
         cudaError_t e = launch_decode_gqa(a, *maps, st);
         if (e != cudaSuccess) return e;
@@ -239,8 +238,12 @@ cudaError_t launch_decode(const DecodeArgs& a, const CombineArgs& c, bool fast, 
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const size_t rows = (size_t)a.B * a.Hq;
-    if (a.max_splits <= 8)
+    return launch_combine(c, a.max_splits, st);
+}
+
+cudaError_t launch_combine(const CombineArgs& c, int splits, cudaStream_t st) {
+    const size_t rows = (size_t)c.B * c.Hq;
+    if (splits <= 8)
         return launch_dep(combine_rows_kernel<1>, dim3((unsigned)((rows + 7) / 8)), dim3(kCombineThreads), 0, st, c);
     if (rows < 1024) return launch_dep(combine_rows_kernel<8>, dim3((unsigned)rows), dim3(kCombineThreads), 0, st, c);
     return launch_dep(combine_rows_kernel<4>, dim3((unsigned)((rows + 1) / 2)), dim3(kCombineThreads), 0, st, c);

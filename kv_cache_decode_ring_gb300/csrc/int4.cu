@@ -5,6 +5,9 @@
 // codes, which are small integers, and terms per group (t a key, h a head):
 //     score_t   = sum_g s_tg (q_g . u_tg) + m_tg sum(q_g),
 //     out_x     = sum_t p_t s_tg u_tx + sum_t p_t m_tg          (x in group g).
+#include <algorithm>
+#include <cmath>
+
 #include "async_copy.h"
 #include "int4.h"
 
@@ -149,13 +152,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) { return fmaxf
 
 // D (16x8, fp32) = A (16x16, fp16, row) . B (16x8, fp16, col) + C
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -164,7 +167,7 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
 // 8 x 8 matrix of 16-bit elements, transposed across the warp.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -199,7 +202,8 @@ struct I4 {
     static constexpr int PARTF = HEADS * (D + 2);        // a warp's partial (m, l, acc), in its stages at the end
     static_assert(PARTF * 4 <= WARPB, "partial must fit in the warp's stages");
     static constexpr int OFF_Q = kWarps * WARPB;         // query [HEADS][D] fp32
-    static constexpr int OFF_BAR = OFF_Q + HEADS * D * 4;
+    static constexpr int OFF_SUM = OFF_Q + HEADS * D * 4; // its sums and largest magnitudes over a group [2][HEADS][G]
+    static constexpr int OFF_BAR = OFF_SUM + 2 * HEADS * G * 4;
     static constexpr size_t SMEM = OFF_BAR + kWarps * STAGES * 8;
     static_assert(HALF % 16 == 0 && kPage * ROW % 16 == 0, "bulk copies");
 };
@@ -210,30 +214,32 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     constexpr int G = C::G;
     extern __shared__ __align__(128) unsigned char smem[];
     float* sQ = reinterpret_cast<float*>(smem + C::OFF_Q);
+    float* sSum = reinterpret_cast<float*>(smem + C::OFF_SUM);
+    float* sTop = sSum + C::HEADS * G;
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, kvh = blockIdx.y / chunks, chunk = blockIdx.y % chunks, split = blockIdx.x;
+    const int b = blockIdx.z, kvh = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
     // the CTA's query heads: [h0, h0 + nh) of the KV head's g
     const int h0 = a.g * chunk / chunks, nh = a.g * (chunk + 1) / chunks - h0;
     dep_wait();                                          // launched dependent: see launch_dep
     dep_release();
     const int len = a.next_pos[b];
-    int lo, hi;
-    key_range(len, a.S, a.W, a.ring, lo, hi);
-    const int lo_t = lo & ~(kPage - 1);                  // tiles start at a page
-    if (split >= split_count(lo_t, lo, hi, a.split, a.sinks)) return;
-    int k_first;                                         // the CTA's keys
-    split_keys(split, lo_t, a.split, a.sinks, lo, hi, k_first);
-    const int k_end = min(hi, k_first + a.split);
+    const Int4Span sp = int4_span(len, a.S, a.W, a.ring, a.sinks);
+    const int per = a.split / kInt4Step, nsplit = (sp.steps + per - 1) / per;
+    if ((int)blockIdx.x >= nsplit) return;
+    int s_first = blockIdx.x * per, tiles = min(per, sp.steps - s_first);        // the split's steps: a tile each for this warp
 
     unsigned char* myS = smem + warp * C::WARPB;
     uint64_t* myBar = bar + warp * C::STAGES;
     const char* Kg = static_cast<const char*>(a.k);
     const char* Vg = static_cast<const char*>(a.v);
-    // tiles of the 4 warps interleaved; tile i of this warp
-    auto tile_k0 = [&](int i) { return k_first + (i * kWarps + warp) * kTile; };
-    auto tile_nk = [&](int i) { return max(0, min(kTile, k_end - tile_k0(i))); };
+    // tile i of this warp: its first key, and its keys (rows behind them may be anything)
+    auto tile_k0 = [&](int i) {
+        const int s = s_first + i;
+        return (s < sp.nwin ? sp.lo_t + s * kInt4Step : (s - sp.nwin) * kInt4Step) + warp * kTile;
+    };
+    auto tile_nk = [&](int i) { return max(0, min(kTile, (s_first + i < sp.nwin ? sp.hi : sp.sunk) - tile_k0(i))); };
     const int32_t* pages = a.table ? a.table + (size_t)b * (a.S / kPage) : nullptr;
     const size_t head_row0 = ((size_t)b * a.Hkv + kvh) * a.S;
     // blocks of 16 rows that hold a visible key (whole: the cache's rows are a multiple of 16)
@@ -264,10 +270,12 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < C::STAGES; ++i) issue(i);
+    for (int i = 0; i < C::STAGES; ++i)
+        if (i < tiles) issue(i);
 
-    // the queries, rotated at t = len - 1, times log2(e)/sqrt(d); heads past nh: 0
-    for (int idx = threadIdx.x; idx < C::HEADS * D / 2; idx += blockDim.x) {
+    // the queries, rotated at t = len - 1, times log2(e)/sqrt(d); heads past nh: 0.  16 lanes hold a group.
+#pragma unroll
+    for (int idx = threadIdx.x; idx < C::HEADS * D / 2; idx += kWarps * 32) {
         const int h = idx / (D / 2), i = idx % (D / 2);
         float y0 = 0.f, y1 = 0.f;
         if (h < nh) {
@@ -276,8 +284,19 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             y0 = x0; y1 = x1;
             if (a.rope) rope_pair(x0, x1, a.rope[(size_t)(len - 1) * (D / 2) + i], y0, y1);
         }
-        sQ[h * D + 2 * i] = y0 * a.scale_log2;
-        sQ[h * D + 2 * i + 1] = y1 * a.scale_log2;
+        y0 *= a.scale_log2;
+        y1 *= a.scale_log2;
+        *reinterpret_cast<float2*>(sQ + h * D + 2 * i) = make_float2(y0, y1);
+        float sum = y0 + y1, top = fmaxf(fabsf(y0), fabsf(y1));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        if ((lane & 15) == 0) {
+            sSum[idx / 16] = sum;
+            sTop[idx / 16] = top;
+        }
     }
     __syncthreads();
 
@@ -285,17 +304,16 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     // B operand of the scores: column g is (head g / 2, hi | lo) or head g; k-step s of group j takes dims
     // 32 j + 8 qd + {2 s, 2 s + 4} and, with codes 16 times as large, {2 s + 1, 2 s + 5}.  Each column's
     // head times 2^e: its largest value in [2^14, 2^15).
-    auto exponent = [&](int h) {                         // (4 lanes a row of values, D / 4 each)
-        float m = 0.f;
-        for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(sQ[h * D + qd * (D / 4) + ((i + g) & (D / 4 - 1))]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    auto exponent = [&](int h) {
+        float m = sTop[h * G];
+#pragma unroll
+        for (int j = 1; j < G; ++j) m = fmaxf(m, sTop[h * G + j]);
         return max(-103, min(100, 15 + 126 - (int)(__float_as_uint(m) >> 23)));
     };
     uint32_t qb[G][2][2];
-    const int hcol = HL == 1 ? g / 2 : g, ecol = exponent(hcol);
     {
-        const float up = power_of_two(ecol);
+        const int hcol = HL == 1 ? g / 2 : g;
+        const float up = power_of_two(exponent(hcol));
 #pragma unroll
         for (int j = 0; j < G; ++j) {
             const float* q = sQ + hcol * D + 32 * j + 8 * qd;
@@ -309,304 +327,307 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                 }
         }
     }
-    // the lane's heads: exponents (of row h, held by the lanes of column h), sums of the query over a group in the
-    // accumulators' unit, and that unit
+    // the lane's heads: sums of the query over a group in the accumulators' unit, and that unit
     float qsum[HL][G], unit[HL];
 #pragma unroll
     for (int n = 0; n < HL; ++n) {
-        const int h = HL * qd + n, e = __shfl_sync(0xffffffffu, ecol, HL == 1 ? 8 * h : 4 * h);
+        const int h = HL * qd + n, e = exponent(h);
         unit[n] = power_of_two(24 - e);
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            float sum = 0.f;
-            for (int i = 0; i < 32; ++i) sum += sQ[h * D + 32 * j + ((i + lane) & 31)];
-            qsum[n][j] = sum * power_of_two(e - 24);
-        }
+        for (int j = 0; j < G; ++j) qsum[n][j] = sSum[h * G + j] * power_of_two(e - 24);
     }
 
-    float m_w[HL], l_w[HL], norm[HL], gacc[HL][G], acc[G][2][4];
-#pragma unroll
-    for (int n = 0; n < HL; ++n) {
-        m_w[n] = -INFINITY; l_w[n] = 0.f; norm[n] = 0x1p100f;
-#pragma unroll
-        for (int j = 0; j < G; ++j) gacc[n][j] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][0][e] = acc[j][1][e] = 0.f;
     const int tr = tok(g), ta = tok(2 * qd), tb = tok(2 * qd + 1);     // keys of rows g, 2 qd, 2 qd + 1 (and + 8: the next)
 
-    const int tpw = a.split / (kWarps * kTile);
-    for (int i = 0; i < tpw; ++i) {
-        const int nk = tile_nk(i);
-        if (nk == 0) break;                              // later tiles of this warp are empty too
-        const int sg = i % C::STAGES;
-        if (!mbar_wait(&myBar[sg], (uint32_t)((i / C::STAGES) & 1))) {
-            // give up: flag it, and let this stage's copy and the later stages' (if issued) land
-            // before the stages are reused for the partial
-            if (lane == 0) atomicOr(a.hdr, kErrWait);
-            mbar_wait(&myBar[sg], (uint32_t)((i / C::STAGES) & 1));
-            for (int j = i + 1; j < i + C::STAGES && j < tpw; ++j)
-                if (tile_nk(j) > 0) mbar_wait(&myBar[j % C::STAGES], (uint32_t)((j / C::STAGES) & 1));
-            break;
-        }
-        const unsigned char* tK = myS + sg * C::STAGEB;
-        const unsigned char* tV = tK + C::HALF;
-        const int kmin = lo - tile_k0(i);                // keys of the tile before the window
-        const bool whole = nk == kTile && kmin <= 0;
-
-        // ---- scores of keys tr, tr + 1 of both blocks
-        float sc[2][2][HL];
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-            const unsigned char* r0 = tK + (16 * blk + tr) * C::ROW;
-            uint32_t w0[G], w1[G], p0[G], p1[G];
-            if constexpr (G == 4) {
-                const uint4 u0 = *reinterpret_cast<const uint4*>(r0 + 16 * qd), u1 = *reinterpret_cast<const uint4*>(r0 + C::ROW + 16 * qd);
-                const uint4 v0 = *reinterpret_cast<const uint4*>(r0 + D / 2), v1 = *reinterpret_cast<const uint4*>(r0 + C::ROW + D / 2);
-                w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w; w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
-                p0[0] = v0.x; p0[1] = v0.y; p0[2] = v0.z; p0[3] = v0.w; p1[0] = v1.x; p1[1] = v1.y; p1[2] = v1.z; p1[3] = v1.w;
-            } else {
-                const uint2 u0 = *reinterpret_cast<const uint2*>(r0 + 8 * qd), u1 = *reinterpret_cast<const uint2*>(r0 + C::ROW + 8 * qd);
-                const uint2 v0 = *reinterpret_cast<const uint2*>(r0 + D / 2), v1 = *reinterpret_cast<const uint2*>(r0 + C::ROW + D / 2);
-                w0[0] = u0.x; w0[1] = u0.y; w1[0] = u1.x; w1[1] = u1.y;
-                p0[0] = v0.x; p0[1] = v0.y; p1[0] = v1.x; p1[1] = v1.y;
-            }
-            // sums of the keys' rows: by columns (hi and lo, or two heads), and (one head) of the minima's terms by rows
-            float2 x0 = both(0.f), x1 = both(0.f), xm = both(0.f);
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const Pairs u = pairs_of(w0[j]), v = pairs_of(w1[j]);
-                float c[4];
-                mma_first(c, u.x[0], v.x[0], u.x[1], v.x[1], qb[j][0][0], qb[j][0][1]);
-                mma(c, u.x[2], v.x[2], u.x[3], v.x[3], qb[j][1][0], qb[j][1][1]);
-                const float m0 = __uint_as_float(p0[j] & 0xffff0000u), m1 = __uint_as_float(p1[j] & 0xffff0000u);
-                x0 = __ffma2_rn(both(__uint_as_float(p0[j] << 16)), make_float2(c[0], c[1]), x0);
-                x1 = __ffma2_rn(both(__uint_as_float(p1[j] << 16)), make_float2(c[2], c[3]), x1);
-                if constexpr (HL == 1) {
-                    xm = __ffma2_rn(make_float2(m0, m1), both(qsum[0][j]), xm);
-                } else {
-                    const float2 q = make_float2(qsum[0][j], qsum[HL - 1][j]);
-                    x0 = __ffma2_rn(both(m0), q, x0);
-                    x1 = __ffma2_rn(both(m1), q, x1);
-                }
-            }
-            if constexpr (HL == 1) {
-                sc[blk][0][0] = (x0.x + x0.y + xm.x) * unit[0];
-                sc[blk][1][0] = (x1.x + x1.y + xm.y) * unit[0];
-            } else {
-                sc[blk][0][0] = x0.x * unit[0]; sc[blk][0][HL - 1] = x0.y * unit[HL - 1];
-                sc[blk][1][0] = x1.x * unit[0]; sc[blk][1][HL - 1] = x1.y * unit[HL - 1];
-            }
-        }
-        if (!whole) {
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = 16 * blk + tr + e;
-#pragma unroll
-                    for (int n = 0; n < HL; ++n) sc[blk][e][n] = key < nk && key >= kmin ? sc[blk][e][n] : -INFINITY;
-                }
-        }
-        // ---- online softmax of the lane's heads over the tile
-        bool rescale = false;
-        float alpha[HL];
+    uint32_t parity = 0;                                 // of each stage's barrier (bit)
+    for (int split = blockIdx.x;; split += gridDim.x) {
+        float m_w[HL], l_w[HL], norm[HL], acc[G][2][4];
+        float2 gacc[G];                                      // sums of the minima's terms
 #pragma unroll
         for (int n = 0; n < HL; ++n) {
-            float bm = fmaxf(fmax3(sc[0][0][n], sc[0][1][n], sc[1][0][n]), sc[1][1][n]);
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-            const float mn = bm > m_w[n] + kLazyMax ? bm : m_w[n];
-            alpha[n] = ex2(m_w[n] - mn);                 // 0 while the maximum was -inf
-            rescale |= alpha[n] != 1.f;
-            m_w[n] = mn;
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sc[blk][e][n] = ex2(sc[blk][e][n] - mn);          // masked keys: 0
-            l_w[n] = fmaf(l_w[n], alpha[n], (sc[0][0][n] + sc[0][1][n]) + (sc[1][0][n] + sc[1][1][n]));
+            m_w[n] = -INFINITY; l_w[n] = 0.f; norm[n] = 0x1p100f;
         }
-        // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
-        auto scale_acc = [&](const float (&f)[HL]) {
 #pragma unroll
-            for (int j = 0; j < G; ++j)
+        for (int j = 0; j < G; ++j) {
+            gacc[j] = both(0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
-                    acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
-                }
-        };
-        if (__any_sync(0xffffffffu, rescale) && i > 0) {  // at i = 0 the accumulators are 0
-            scale_acc(alpha);
-#pragma unroll
-            for (int n = 0; n < HL; ++n)
-#pragma unroll
-                for (int j = 0; j < G; ++j) gacc[n][j] *= alpha[n];
+            for (int e = 0; e < 4; ++e) acc[j][0][e] = acc[j][1][e] = 0.f;
         }
-        // ---- scales and minima of the values; a masked key adds nothing, whatever its row holds
-        uint32_t vp[2][2][G];
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const unsigned char* r = tV + (16 * blk + tr + e) * C::ROW + D / 2;
-                if constexpr (G == 4) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(r);
-                    vp[blk][e][0] = u.x; vp[blk][e][1] = u.y; vp[blk][e][2] = u.z; vp[blk][e][3] = u.w;
-                } else {
-                    const uint2 u = *reinterpret_cast<const uint2*>(r);
-                    vp[blk][e][0] = u.x; vp[blk][e][1] = u.y;
-                }
-                if (!whole) {
-                    const int key = 16 * blk + tr + e;
-#pragma unroll
-                    for (int j = 0; j < G; ++j)
-                        if (!(key < nk && key >= kmin)) vp[blk][e][j] = 0u;
-                }
+        for (int i = 0; i < tiles; ++i) {
+            const int nk = tile_nk(i);
+            if (nk == 0) {                                   // (of the window's or the sinks' last step)
+                if (i + C::STAGES < tiles) issue(i + C::STAGES);
+                continue;
             }
-        // ---- weights times scales, and the minima's terms
-        float2 pw[2][G][HL];                             // of keys tr, tr + 1 (one head), else of two heads, for each key
-        auto weigh = [&]() {
-            float top = 0.f;
+            const int sg = i % C::STAGES;
+            if (!mbar_wait(&myBar[sg], parity >> sg & 1)) {
+                // give up: flag it, and let this stage's copy and the later stages' (if issued) land
+                // before the stages are reused for the partial
+                if (lane == 0) atomicOr(a.hdr, kErrWait);
+                for (int j = i; j < i + C::STAGES && j < tiles; ++j)
+                    if (tile_nk(j) > 0) {
+                        mbar_wait(&myBar[j % C::STAGES], parity >> (j % C::STAGES) & 1);
+                        parity ^= 1u << (j % C::STAGES);
+                    }
+                break;
+            }
+            parity ^= 1u << sg;
+            const unsigned char* tK = myS + sg * C::STAGEB;
+            const unsigned char* tV = tK + C::HALF;
+            const int kmin = s_first + i < sp.nwin ? sp.lo - tile_k0(i) : 0;         // keys of the tile before the window
+            const bool whole = nk == kTile && kmin <= 0;
+
+            // ---- scores of keys tr, tr + 1 of both blocks
+            float sc[2][2][HL];
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
+            for (int blk = 0; blk < 2; ++blk) {
+                const unsigned char* r0 = tK + (16 * blk + tr) * C::ROW;
+                uint32_t w0[G], w1[G], p0[G], p1[G];
+                if constexpr (G == 4) {
+                    const uint4 u0 = *reinterpret_cast<const uint4*>(r0 + 16 * qd), u1 = *reinterpret_cast<const uint4*>(r0 + C::ROW + 16 * qd);
+                    const uint4 v0 = *reinterpret_cast<const uint4*>(r0 + D / 2), v1 = *reinterpret_cast<const uint4*>(r0 + C::ROW + D / 2);
+                    w0[0] = u0.x; w0[1] = u0.y; w0[2] = u0.z; w0[3] = u0.w; w1[0] = u1.x; w1[1] = u1.y; w1[2] = u1.z; w1[3] = u1.w;
+                    p0[0] = v0.x; p0[1] = v0.y; p0[2] = v0.z; p0[3] = v0.w; p1[0] = v1.x; p1[1] = v1.y; p1[2] = v1.z; p1[3] = v1.w;
+                } else {
+                    const uint2 u0 = *reinterpret_cast<const uint2*>(r0 + 8 * qd), u1 = *reinterpret_cast<const uint2*>(r0 + C::ROW + 8 * qd);
+                    const uint2 v0 = *reinterpret_cast<const uint2*>(r0 + D / 2), v1 = *reinterpret_cast<const uint2*>(r0 + C::ROW + D / 2);
+                    w0[0] = u0.x; w0[1] = u0.y; w1[0] = u1.x; w1[1] = u1.y;
+                    p0[0] = v0.x; p0[1] = v0.y; p1[0] = v1.x; p1[1] = v1.y;
+                }
+                // sums of the keys' rows: by columns (hi and lo, or two heads), and (one head) of the minima's terms by rows
+                float2 x0 = both(0.f), x1 = both(0.f), xm = both(0.f);
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
-                    const float s0 = __uint_as_float(vp[blk][0][j] << 16), s1 = __uint_as_float(vp[blk][1][j] << 16);
+                    const Pairs u = pairs_of(w0[j]), v = pairs_of(w1[j]);
+                    float c[4];
+                    mma_first(c, u.x[0], v.x[0], u.x[1], v.x[1], qb[j][0][0], qb[j][0][1]);
+                    mma(c, u.x[2], v.x[2], u.x[3], v.x[3], qb[j][1][0], qb[j][1][1]);
+                    const float m0 = __uint_as_float(p0[j] & 0xffff0000u), m1 = __uint_as_float(p1[j] & 0xffff0000u);
+                    x0 = __ffma2_rn(both(__uint_as_float(p0[j] << 16)), make_float2(c[0], c[1]), x0);
+                    x1 = __ffma2_rn(both(__uint_as_float(p1[j] << 16)), make_float2(c[2], c[3]), x1);
                     if constexpr (HL == 1) {
-                        const float2 e = __fmul2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), both(norm[0]));
-                        pw[blk][j][0] = __fmul2_rn(e, make_float2(s0, s1));
-                        top = fmax3(top, pw[blk][j][0].x, pw[blk][j][0].y);
+                        xm = __ffma2_rn(make_float2(m0, m1), both(qsum[0][j]), xm);
                     } else {
-                        const float2 nn = make_float2(norm[0], norm[HL - 1]);
-                        pw[blk][j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][0][HL - 1]), nn), both(s0));
-                        pw[blk][j][HL - 1] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][1][0], sc[blk][1][HL - 1]), nn), both(s1));
-                        top = fmax3(top, pw[blk][j][0].x, pw[blk][j][0].y);
-                        top = fmax3(top, pw[blk][j][HL - 1].x, pw[blk][j][HL - 1].y);
+                        const float2 q = make_float2(qsum[0][j], qsum[HL - 1][j]);
+                        x0 = __ffma2_rn(both(m0), q, x0);
+                        x1 = __ffma2_rn(both(m1), q, x1);
                     }
                 }
-            return top;
-        };
-        if (__any_sync(0xffffffffu, weigh() > 32768.f)) {
-            // a head whose largest weight passes 2^15 gets a norm that puts it into [2^9, 2^10)
-            float f[HL];
-#pragma unroll
-            for (int n = 0; n < HL; ++n) {
-                float top = 0.f;
+                if constexpr (HL == 1) {
+                    sc[blk][0][0] = (x0.x + x0.y + xm.x) * unit[0];
+                    sc[blk][1][0] = (x1.x + x1.y + xm.y) * unit[0];
+                } else {
+                    sc[blk][0][0] = x0.x * unit[0]; sc[blk][0][HL - 1] = x0.y * unit[HL - 1];
+                    sc[blk][1][0] = x1.x * unit[0]; sc[blk][1][HL - 1] = x1.y * unit[HL - 1];
+                }
+            }
+            if (!whole) {
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = 16 * blk + tr + e;
 #pragma unroll
-                        for (int j = 0; j < G; ++j) top = fmaxf(top, sc[blk][e][n] * __uint_as_float(vp[blk][e][j] << 16));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                const float to = top * norm[n] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n];
-                f[n] = to / norm[n];
-                norm[n] = to;
+                        for (int n = 0; n < HL; ++n) sc[blk][e][n] = key < nk && key >= kmin ? sc[blk][e][n] : -INFINITY;
+                    }
             }
-            scale_acc(f);
-            weigh();
+            // ---- online softmax of the lane's heads over the tile
+            bool rescale = false;
+            float alpha[HL];
+#pragma unroll
+            for (int n = 0; n < HL; ++n) {
+                float bm = fmaxf(fmax3(sc[0][0][n], sc[0][1][n], sc[1][0][n]), sc[1][1][n]);
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
+                const float mn = bm > m_w[n] + kLazyMax ? bm : m_w[n];
+                alpha[n] = ex2(m_w[n] - mn);                 // 0 while the maximum was -inf
+                rescale |= alpha[n] != 1.f;
+                m_w[n] = mn;
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sc[blk][e][n] = ex2(sc[blk][e][n] - mn);          // masked keys: 0
+                l_w[n] = fmaf(l_w[n], alpha[n], (sc[0][0][n] + sc[0][1][n]) + (sc[1][0][n] + sc[1][1][n]));
+            }
+            // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
+            auto scale_acc = [&](const float (&f)[HL]) {
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
+                        acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
+                    }
+            };
+            if (__any_sync(0xffffffffu, rescale) && i > 0) {  // at i = 0 the accumulators are 0
+                scale_acc(alpha);
+#pragma unroll
+                for (int j = 0; j < G; ++j) gacc[j] = __fmul2_rn(gacc[j], make_float2(alpha[0], alpha[HL - 1]));
+            }
+            // ---- P.V, a block at a time
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                // scales and minima of keys tr and tr + 1; a masked key adds nothing, whatever its row holds
+                uint32_t p0[G], p1[G];
+                {
+                    const unsigned char* r = tV + (16 * blk + tr) * C::ROW + D / 2;
+                    if constexpr (G == 4) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(r), v = *reinterpret_cast<const uint4*>(r + C::ROW);
+                        p0[0] = u.x; p0[1] = u.y; p0[2] = u.z; p0[3] = u.w; p1[0] = v.x; p1[1] = v.y; p1[2] = v.z; p1[3] = v.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(r), v = *reinterpret_cast<const uint2*>(r + C::ROW);
+                        p0[0] = u.x; p0[1] = u.y; p1[0] = v.x; p1[1] = v.y;
+                    }
+                }
+                if (!whole) {
+                    const int key = 16 * blk + tr;
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        if (!(key < nk && key >= kmin)) p0[j] = 0u;
+                        if (!(key + 1 < nk && key + 1 >= kmin)) p1[j] = 0u;
+                    }
+                }
+                // weights times scales: of keys tr and tr + 1 (one head), else of two heads, for each key
+                float2 pw[G][HL];
+                auto weigh = [&]() {
+                    float top = 0.f;
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        const float s0 = __uint_as_float(p0[j] << 16), s1 = __uint_as_float(p1[j] << 16);
+                        if constexpr (HL == 1) {
+                            pw[j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), both(norm[0])), make_float2(s0, s1));
+                            top = fmax3(top, pw[j][0].x, pw[j][0].y);
+                        } else {
+                            const float2 nn = make_float2(norm[0], norm[HL - 1]);
+                            pw[j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][0][HL - 1]), nn), both(s0));
+                            pw[j][HL - 1] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][1][0], sc[blk][1][HL - 1]), nn), both(s1));
+                            top = fmax3(fmax3(top, pw[j][0].x, pw[j][0].y), pw[j][HL - 1].x, pw[j][HL - 1].y);
+                        }
+                    }
+                    return top;
+                };
+                if (__any_sync(0xffffffffu, weigh() > 32768.f)) {
+                    // a head whose largest weight passes 2^15 gets a norm that puts it into [2^9, 2^10)
+                    float f[HL];
+#pragma unroll
+                    for (int n = 0; n < HL; ++n) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < G; ++j)
+                            top = fmax3(top, sc[blk][0][n] * __uint_as_float(p0[j] << 16), sc[blk][1][n] * __uint_as_float(p1[j] << 16));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+                        const float to = top * norm[n] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n];
+                        f[n] = to / norm[n];
+                        norm[n] = to;
+                    }
+                    scale_acc(f);
+                    weigh();
+                }
+                const unsigned char* xa = tV + (16 * blk + ta) * C::ROW;
+                const unsigned char* xb = tV + (16 * blk + tb) * C::ROW;
+                uint32_t wa[G / 2], wb[G / 2], wc[G / 2], wd[G / 2];
+                if constexpr (G == 4) {
+                    const uint2 ya = *reinterpret_cast<const uint2*>(xa + 8 * g), yb = *reinterpret_cast<const uint2*>(xb + 8 * g);
+                    const uint2 yc = *reinterpret_cast<const uint2*>(xa + C::ROW + 8 * g), yd = *reinterpret_cast<const uint2*>(xb + C::ROW + 8 * g);
+                    wa[0] = ya.x; wa[1] = ya.y; wb[0] = yb.x; wb[1] = yb.y; wc[0] = yc.x; wc[1] = yc.y; wd[0] = yd.x; wd[1] = yd.y;
+                } else {
+                    wa[0] = *reinterpret_cast<const uint32_t*>(xa + 4 * g); wb[0] = *reinterpret_cast<const uint32_t*>(xb + 4 * g);
+                    wc[0] = *reinterpret_cast<const uint32_t*>(xa + C::ROW + 4 * g); wd[0] = *reinterpret_cast<const uint32_t*>(xb + C::ROW + 4 * g);
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    const float m0 = __uint_as_float(p0[j] & 0xffff0000u), m1 = __uint_as_float(p1[j] & 0xffff0000u);
+                    // (one head: the terms of keys tr and of keys tr + 1; else of the two heads)
+                    if constexpr (HL == 1) {
+                        gacc[j] = __ffma2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), make_float2(m0, m1), gacc[j]);
+                    } else {
+                        gacc[j] = __ffma2_rn(make_float2(sc[blk][0][0], sc[blk][0][HL - 1]), both(m0), gacc[j]);
+                        gacc[j] = __ffma2_rn(make_float2(sc[blk][1][0], sc[blk][1][HL - 1]), both(m1), gacc[j]);
+                    }
+                    const int sel = j & 1 ? 0x7632 : 0x5410;
+                    const Pairs u = pairs_of(__byte_perm(wa[j / 2], wb[j / 2], sel)), v = pairs_of(__byte_perm(wc[j / 2], wd[j / 2], sel));
+                    const float2 p = pw[j][0], r = pw[j][HL - 1];
+                    const uint32_t b0 = transposed(HL == 1 ? pack_half(p.x, 0.f) : pack_half(p.x, p.y));
+                    const uint32_t b1 = transposed(HL == 1 ? pack_half(p.y, 0.f) : pack_half(r.x, r.y));
+                    mma(acc[j][0], u.x[0], u.x[1], v.x[0], v.x[1], b0, b1);
+                    mma(acc[j][1], u.x[2], u.x[3], v.x[2], v.x[3], b0, b1);
+                }
+            }
+            // the stage is free once every lane is past its reads
+            __syncwarp();
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (i + C::STAGES < tiles) issue(i + C::STAGES);
         }
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const float m0 = __uint_as_float(vp[blk][0][j] & 0xffff0000u), m1 = __uint_as_float(vp[blk][1][j] & 0xffff0000u);
-#pragma unroll
-                for (int n = 0; n < HL; ++n) gacc[n][j] = fmaf(sc[blk][0][n], m0, fmaf(sc[blk][1][n], m1, gacc[n][j]));
-            }
-        // ---- P.V of both blocks
-#pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-            const unsigned char* xa = tV + (16 * blk + ta) * C::ROW;
-            const unsigned char* xb = tV + (16 * blk + tb) * C::ROW;
-            uint32_t wa[G / 2], wb[G / 2], wc[G / 2], wd[G / 2];
-            if constexpr (G == 4) {
-                const uint2 ya = *reinterpret_cast<const uint2*>(xa + 8 * g), yb = *reinterpret_cast<const uint2*>(xb + 8 * g);
-                const uint2 yc = *reinterpret_cast<const uint2*>(xa + C::ROW + 8 * g), yd = *reinterpret_cast<const uint2*>(xb + C::ROW + 8 * g);
-                wa[0] = ya.x; wa[1] = ya.y; wb[0] = yb.x; wb[1] = yb.y; wc[0] = yc.x; wc[1] = yc.y; wd[0] = yd.x; wd[1] = yd.y;
-            } else {
-                wa[0] = *reinterpret_cast<const uint32_t*>(xa + 4 * g); wb[0] = *reinterpret_cast<const uint32_t*>(xb + 4 * g);
-                wc[0] = *reinterpret_cast<const uint32_t*>(xa + C::ROW + 4 * g); wd[0] = *reinterpret_cast<const uint32_t*>(xb + C::ROW + 4 * g);
-            }
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-                const int sel = j & 1 ? 0x7632 : 0x5410;
-                const Pairs u = pairs_of(__byte_perm(wa[j / 2], wb[j / 2], sel)), v = pairs_of(__byte_perm(wc[j / 2], wd[j / 2], sel));
-                const float2 p = pw[blk][j][0], r = pw[blk][j][HL - 1];
-                const uint32_t b0 = transposed(HL == 1 ? pack_half(p.x, 0.f) : pack_half(p.x, p.y));
-                const uint32_t b1 = transposed(HL == 1 ? pack_half(p.y, 0.f) : pack_half(r.x, r.y));
-                mma(acc[j][0], u.x[0], u.x[1], v.x[0], v.x[1], b0, b1);
-                mma(acc[j][1], u.x[2], u.x[3], v.x[2], v.x[3], b0, b1);
-            }
-        }
-        // the stage is free once every lane is past its reads
-        __syncwarp();
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (i + C::STAGES < tpw) issue(i + C::STAGES);
-    }
 
-    // ---- this warp's partial into its own stages (every issued tile was waited for): l and the
-    // groups' terms summed over the 8 lanes of a head; output = products in their unit + the group's term
-    __syncwarp();
-    float* part_w = reinterpret_cast<float*>(myS);       // [HEADS][2 + D]
+        // ---- this warp's partial into its own stages (every issued tile was waited for): l and the
+        // groups' terms summed over the 8 lanes of a head; output = products in their unit + the group's term
+        __syncwarp();
+        float* part_w = reinterpret_cast<float*>(myS);       // [HEADS][2 + D]
 #pragma unroll
-    for (int n = 0; n < HL; ++n) {
-        const int h = HL * qd + n;
-        float l = l_w[n];
+        for (int n = 0; n < HL; ++n) {
+            const int h = HL * qd + n;
+            float l = l_w[n];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (g == 0) { part_w[h * (D + 2)] = m_w[n]; part_w[h * (D + 2) + 1] = l; }
-        const float even = 0x1p24f / norm[n], odd = 0x1p20f / norm[n];
+            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (g == 0) { part_w[h * (D + 2)] = m_w[n]; part_w[h * (D + 2) + 1] = l; }
+            const float even = 0x1p24f / norm[n], odd = 0x1p20f / norm[n];
 #pragma unroll
-        for (int j = 0; j < G; ++j) {
-            float t = gacc[n][j];
+            for (int j = 0; j < G; ++j) {
+                float t = HL == 1 ? gacc[j].x + gacc[j].y : n == 0 ? gacc[j].x : gacc[j].y;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            float* o = part_w + h * (D + 2) + 2 + 32 * j + 4 * g;
+                for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                float* o = part_w + h * (D + 2) + 2 + 32 * j + 4 * g;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                o[2 * k] = fmaf(acc[j][k][n], even, t);
-                o[2 * k + 1] = fmaf(acc[j][k][2 + n], odd, t);
+                for (int k = 0; k < 2; ++k) {
+                    o[2 * k] = fmaf(acc[j][k][n], even, t);
+                    o[2 * k + 1] = fmaf(acc[j][k][2 + n], odd, t);
+                }
             }
         }
-    }
-    __syncthreads();
-    for (int idx = threadIdx.x; idx < nh * D; idx += blockDim.x) {
-        const int h = idx / D, x = idx % D;
-        float mx = -INFINITY;
+        __syncthreads();
+        for (int idx = threadIdx.x; idx < nh * D; idx += blockDim.x) {
+            const int h = idx / D, x = idx % D;
+            float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, reinterpret_cast<const float*>(smem + w * C::WARPB)[h * (D + 2)]);
-        float l = 0.f, sum = 0.f;
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, reinterpret_cast<const float*>(smem + w * C::WARPB)[h * (D + 2)]);
+            float l = 0.f, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float* pw = reinterpret_cast<const float*>(smem + w * C::WARPB) + h * (D + 2);
-            const float f = pw[0] == -INFINITY ? 0.f : exp2f(pw[0] - mx);
-            l += pw[1] * f;
-            sum += pw[2 + x] * f;
+            for (int w = 0; w < kWarps; ++w) {
+                const float* pw = reinterpret_cast<const float*>(smem + w * C::WARPB) + h * (D + 2);
+                const float f = pw[0] == -INFINITY ? 0.f : exp2f(pw[0] - mx);
+                l += pw[1] * f;
+                sum += pw[2 + x] * f;
+            }
+            const size_t row = ((size_t)b * a.Hq + (size_t)kvh * a.g + h0 + h) * a.max_splits + split;
+            a.part_acc[row * D + x] = sum;
+            if (x == 0) a.part_ml[row] = make_float2(mx, l);
         }
-        const size_t row = ((size_t)b * a.Hq + (size_t)kvh * a.g + h0 + h) * a.max_splits + split;
-        a.part_acc[row * D + x] = sum;
-        if (x == 0) a.part_ml[row] = make_float2(mx, l);
+        if (split + (int)gridDim.x >= nsplit) return;
+        // a launch of fewer CTAs than splits (lengths that the host does not know): the stages are free once read
+        s_first = (split + gridDim.x) * per;
+        tiles = min(per, sp.steps - s_first);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i)
+            if (i < tiles) issue(i);
     }
 }
 
 template <int D, int HL>
-cudaError_t launch_t(const DecodeArgs& a, int chunks, cudaStream_t st) {
+cudaError_t launch_t(const DecodeArgs& a, int splits, int chunks, cudaStream_t st) {
     using C = I4<D, HL>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(int4_decode_kernel<D, HL>), C::SMEM)) return e;
-    return launch_dep(int4_decode_kernel<D, HL>, dim3(a.max_splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
+    return launch_dep(int4_decode_kernel<D, HL>, dim3(splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
 }
 
 }  // namespace
 
-static_assert(kInt4SplitLeast % (kWarps * kTile) == 0 && kInt4Heads == 8, "split and head shapes");
+static_assert(kInt4Step == kWarps * kTile && kInt4Heads == 8, "split and head shapes");
 
 cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st) {
     return launch_dep(a.d == 128 ? int4_token_kernel<128> : int4_token_kernel<64>, dim3(a.B), dim3(kThreads), 0, st, a);
@@ -618,10 +639,47 @@ cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cud
                       dim3(kThreads), 0, st, a, g);
 }
 
-cudaError_t launch_int4_splits(const DecodeArgs& a, cudaStream_t st) {
-    const int chunks = (a.g + kInt4Heads - 1) / kInt4Heads, heads = (a.g + chunks - 1) / chunks;
-    if (a.d == 128) return heads <= 4 ? launch_t<128, 1>(a, chunks, st) : launch_t<128, 2>(a, chunks, st);
-    return heads <= 4 ? launch_t<64, 1>(a, chunks, st) : launch_t<64, 2>(a, chunks, st);
+// Steps per split, by the host's lengths.  Three CTAs or four keep an SM as busy as it gets, so the SM with the longest
+// CTAs counts: as many of one length as fill the SMs evenly, or many more than are resident.  The
+// estimate: a step takes an SM kStepUs, a CTA kCtaUs of its own, which resident ones hide from each other.
+int steps_per_split(const kvc_handle* h, int chunks, int resident) {
+    const Shape& s = h->sh;
+    constexpr float kStepUs = 0.5f, kCtaUs = 5.f;
+    const float rows = (float)s.Hkv * chunks, sms = (float)h->num_sms;
+    const int lowest = s.split / kInt4Step, most = s.B <= 64 ? s.B : 64;
+    int steps[64];                                       // of each request, of a sample of many
+    for (int i = 0; i < most; ++i) steps[i] = int4_span(h->np[(size_t)i * s.B / most], s.S, s.W, s.ring, s.sinks).steps;
+    int best = lowest;
+    float least = INFINITY;
+    for (int per = lowest; per <= kInt4StepsMost; ++per) {
+        int ctas = 0, longest = 0;
+        for (int i = 0; i < most; ++i) {
+            ctas += (steps[i] + per - 1) / per;
+            longest = std::max(longest, std::min(steps[i], per));
+        }
+        const float per_sm = ctas * rows * s.B / most / sms, waves = per_sm / resident;
+        const float load = waves <= 1.f ? std::ceil(per_sm) : per_sm + 0.5f;
+        const float us = load * longest * kStepUs + kCtaUs * (waves <= 1.f ? 1.f : waves + 0.5f);
+        if (us < least) { least = us; best = per; }
+    }
+    return best;
+}
+
+cudaError_t launch_int4_decode(const kvc_handle* h, DecodeArgs a, CombineArgs c, cudaStream_t st) {
+    const Shape& s = h->sh;
+    const int chunks = int4_chunks(s), heads = (s.g + chunks - 1) / chunks;
+    // a captured call serves lengths that nobody knows: as many CTAs as the cache may need
+    const bool fixed = capturing(st);
+    const int per = fixed ? std::max(s.split / kInt4Step, 4) : steps_per_split(h, chunks, heads <= 4 || s.d == 64 ? 4 : 3);
+    a.split = c.split = per * kInt4Step;
+    int splits = 1;
+    for (int b = 0; b < s.B && !fixed; ++b)
+        splits = std::max(splits, (int4_span(h->np[b], s.S, s.W, s.ring, s.sinks).steps + per - 1) / per);
+    if (fixed) splits = (s.max_splits * s.split + a.split - 1) / a.split;
+    cudaError_t e;
+    if (s.d == 128) e = heads <= 4 ? launch_t<128, 1>(a, splits, chunks, st) : launch_t<128, 2>(a, splits, chunks, st);
+    else e = heads <= 4 ? launch_t<64, 1>(a, splits, chunks, st) : launch_t<64, 2>(a, splits, chunks, st);
+    return e != cudaSuccess ? e : launch_combine(c, splits, st);
 }
 
 }  // namespace kvc

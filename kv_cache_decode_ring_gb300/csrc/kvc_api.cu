@@ -120,17 +120,17 @@ bool make_shape(const kvc_config& c, Shape* s) {
     s->gqa = s->bf16 && !int8 && !int4 && gqa_decode_supported(s->d, s->g) && rows < (1ll << 31);
     if (s->gqa) s->split = keys >= kGqaLongKeys ? kGqaSplitLong : kGqaSplit;
     if (int4) {
-        // long splits where their CTAs fill the SMs several times over, shorter ones otherwise
-        const long long rows_of_grid = (long long)s->B * s->Hkv * int4_chunks(*s);
-        s->split = kInt4SplitMost;
-        while (s->split > kInt4SplitLeast && rows_of_grid * ((keys + s->split - 1) / s->split) < kInt4Ctas) s->split /= 2;
+        const long long grid_rows = (long long)s->B * s->Hkv * int4_chunks(*s);
+        if ((long long)s->Hkv * int4_chunks(*s) > kMaxGridHeads) return false;
+        s->split = kInt4Step;
+        while (s->split < 4 * kInt4Step && grid_rows * ((keys + s->split - 1) / s->split) > kInt4Rows) s->split *= 2;
     }
     // the generic decode holds a CTA's g queries and g x split scores in shared memory
     if (!int8 && !int4 && s->split == kGenericSplit && (size_t)s->g * (s->d + kGenericSplit) * 4 > kMaxSmemPerBlock)
         return false;
     // a paged cache may start its splits up to one page before the window
     s->max_splits = (int)((keys + s->split - 1) / s->split) + (s->pages > 0 || int4 ? 1 : 0);
-    s->max_splits += (s->sinks + s->split - 1) / s->split;
+    s->max_splits += (s->sinks + s->split - 1) / s->split;       // (INT4: of no more splits than window and sinks have apart)
     if (int8) {
         // quantized splits (longer ones for long caches: less start-up per byte; a longer
         // split measured faster than one that fills the SMs' last wave of CTAs better), one
@@ -435,16 +435,18 @@ int kvc_decode_attn(kvc_t h, const void* d_q, void* d_out, float* d_cmax, float*
     a.hdr = at<uint32_t>(h, h->L.hdr);
     a.table = s.pages ? at<int32_t>(h, h->L.table) : nullptr;
     a.B = s.B; a.Hq = s.Hq; a.Hkv = s.Hkv; a.g = s.g; a.d = s.d; a.S = s.S; a.W = s.W;
-    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16; a.int4 = s.int4; a.sinks = s.sinks;
+    a.max_splits = s.max_splits; a.split = s.split; a.gqa = s.gqa; a.ring = s.ring; a.bf16 = s.bf16; a.sinks = s.sinks;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.d));
     CombineArgs c{};
     c.part_ml = a.part_ml; c.part_acc = a.part_acc; c.next_pos = a.next_pos; c.out = d_out;
     c.B = s.B; c.Hq = s.Hq; c.d = s.d; c.S = s.S; c.W = s.W; c.max_splits = s.max_splits;
     c.split = s.split; c.ring = s.ring; c.bf16 = s.out_bf16;
-    c.align_lo = (s.pages > 0 && s.gqa) || s.int4;
+    c.align_lo = s.pages > 0 && s.gqa;
+    c.int4 = s.int4;
     c.sinks = s.sinks;
     const bool fast = s.split == kFastSplit && fast_decode_supported(a);
-    if (launch_decode(a, c, fast, h->has_kv_maps ? &h->kv_maps : nullptr, st) != cudaSuccess) return KVC_ERR_CUDA;
+    if ((s.int4 ? launch_int4_decode(h, a, c, st) : launch_decode(a, c, fast, h->has_kv_maps ? &h->kv_maps : nullptr, st)) != cudaSuccess)
+        return KVC_ERR_CUDA;
     if (d_cmax && cudaMemsetAsync(d_cmax, 0, (size_t)s.B * s.Hq * 4, st) != cudaSuccess) return KVC_ERR_CUDA;
     if (d_tanh && cudaMemsetAsync(d_tanh, 0, (size_t)s.B * s.Hq * 4, st) != cudaSuccess) return KVC_ERR_CUDA;
     return KVC_OK;

@@ -30,8 +30,9 @@ constexpr int kInt8LongKeys = 16384;
 constexpr int kGqaSplit = 1024;
 constexpr int kGqaSplitLong = 2048;
 constexpr int kGqaLongKeys = 16384;
-constexpr int kInt4SplitMost = 2048, kInt4SplitLeast = 128;   // keys per split, INT4 decode kernel
-constexpr long long kInt4Ctas = 3 * 152;                      // ... the shorter, until there are so many CTAs
+// The INT4 decode counts keys in steps of kInt4Step; steps per split are chosen at each call by the lengths, as
+// few as the state's workspace reaches (Shape::split / kInt4Step: 4 at most, of no more than kInt4Rows splits of all rows)
+constexpr int kInt4Step = 128, kInt4StepsMost = 32, kInt4Rows = 16384;
 constexpr int kMaxRestored = 1024;    // INT8 blocks restored to full precision per (request, KV head)
 constexpr int kExactBlocksPerCta = 64; // restored blocks one CTA of the exact-block decode serves
 constexpr int kExactSplits = kMaxRestored / kExactBlocksPerCta;   // their split slots per query head
@@ -101,7 +102,7 @@ constexpr int kMaxGridHeads = 65534;      // heads (and one more plane) along a 
 // Bytes of a K or V row of one head (non-INT8).
 inline size_t row_bytes(const Shape& s) { return s.int4 ? (size_t)s.d / 8 * 5 : (size_t)s.d * s.elem; }
 
-// INT4 decode: query heads of a KV head that a CTA serves (grid rows per KV head: int4_chunks)
+// INT4 decode: query heads of a KV head that a CTA serves at most (grid rows per KV head: int4_chunks)
 constexpr int kInt4Heads = 8;
 inline int int4_chunks(const Shape& s) { return (s.g + kInt4Heads - 1) / kInt4Heads; }
 
@@ -126,7 +127,6 @@ struct DecodeArgs {
     const int32_t* table; // paged caches: the block table (else nullptr)
     int B, Hq, Hkv, g, d, S, W, max_splits, split;
     int gqa;              // the GQA decode kernel serves the shape (split kGqaSplit or kGqaSplitLong)
-    int int4;             // k and v hold rows of 4-bit codes: int4.cu serves the shape
     int sinks;            // first positions that stay visible (contiguous caches with a window; 0 = none)
     int ring;
     int bf16;             // cache dtype (1 = bf16, 0 = fp32)
@@ -141,6 +141,7 @@ struct CombineArgs {
     int B, Hq, d, S, W, max_splits, split, ring, bf16;
     int align_lo;         // splits start at the window start rounded down to a page
     int sinks;            // as DecodeArgs: their splits follow the window's
+    int int4;             // splits of the INT4 decode's steps (int4_span)
 };
 
 struct AppendArgs {
@@ -215,10 +216,12 @@ inline bool page_touched(const Shape& s, int lp, long long lo, long long hi) {
 cudaError_t launch_int8_exact(kvc_handle* h, const void* q, float* ct, cudaStream_t st);
 // maps: required when the GQA kernel serves the shape (Shape::gqa)
 cudaError_t launch_decode(const DecodeArgs& d, const CombineArgs& c, bool fast, const KvMaps* maps, cudaStream_t st);
-// INT4 tier (int4.cu): appends of n rows of every request (n = 1: one token), and the decode's splits
+// the partials of `splits` splits at most of each row, joined
+cudaError_t launch_combine(const CombineArgs& c, int splits, cudaStream_t st);
+// INT4 tier (int4.cu): appends of one token and of many rows, and the decode
 cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cudaStream_t st);
-cudaError_t launch_int4_splits(const DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_int4_decode(const kvc_handle* h, DecodeArgs a, CombineArgs c, cudaStream_t st);
 bool chunk_supported(const Shape& s);
 bool gqa_decode_supported(int d, int g);
 cudaError_t launch_decode_gqa(const DecodeArgs& a, const KvMaps& maps, cudaStream_t st);
@@ -336,6 +339,22 @@ __device__ __forceinline__ float ld_elem(const void* p, size_t i, int bf16) {
 __device__ __forceinline__ void rope_pair(float x0, float x1, float2 cs, float& y0, float& y1) {
     y0 = __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, cs.y));
     y1 = __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, cs.y));
+}
+
+// INT4 decode: the steps of kInt4Step keys that the newest token of a request attends to: `nwin` of the window [lo, hi)
+// from lo rounded down to a page, then those of the sinks [0, sunk) that the window left behind.
+struct Int4Span {
+    int lo, hi, lo_t, sunk, nwin, steps;
+};
+__host__ __device__ __forceinline__ Int4Span int4_span(int len, int S, int W, int ring, int sinks) {
+    Int4Span s;
+    s.hi = ring && len > S ? S : len;
+    s.lo = !ring && W > 0 && len > W ? len - W : 0;
+    s.lo_t = s.lo & ~(kPage - 1);
+    s.sunk = sinks < s.lo ? sinks : s.lo;
+    s.nwin = (s.hi - s.lo_t + kInt4Step - 1) / kInt4Step;
+    s.steps = s.nwin + (s.sunk + kInt4Step - 1) / kInt4Step;
+    return s;
 }
 
 // Row (in rows of d elements) holding slot `slot` of (request b, KV head h): a

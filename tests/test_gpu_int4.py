@@ -366,3 +366,28 @@ def test_refusals():
         c.append_rows(*(rows(9 + i, 3, 2, 509, 128) for i in range(2)))
     assert e.value.code == kvc.KVC_ERR_CAPACITY
     assert c.rows()[0].shape == (3, 2, 512, 80) and c.rows()[0].dtype == torch.uint8
+
+
+@pytest.mark.parametrize("hq,d", [(4, 128), (8, 64)])
+def test_decode_of_lengths_that_the_host_does_not_know(hq, d):
+    # replayed appends move the lengths on the device: a decode launched for the host's lengths still covers them
+    c = make(batch=2, n_q_heads=hq, n_kv_heads=1, head_dim=d, capacity=2048, window=1500, sinks=5, rope_base=10000.0)
+    m = Model(c, 10000.0, 1500, 5)
+    k, v = rows(1, 2, 1, 1, d), rows(2, 2, 1, 1, d, False)
+    k0, v0 = rows(3, 2, 1, 9, d), rows(4, 2, 1, 9, d, False)
+    c.append_rows(k0, v0, counts=[9, 2])
+    m.append(k0, v0, (9, 2))
+    k1, v1 = k[:, :, 0].contiguous(), v[:, :, 0].contiguous()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.append(k1, v1)
+    for _ in range(1800):
+        graph.replay()
+    torch.cuda.synchronize()
+    for x, y, z in ((m.k, k, 0), (m.v, v, 0)):
+        for b in range(2):
+            x[b] = torch.cat((x[b], y[b].expand(-1, 1800, -1)), 1)
+    q = rows(5, 2, hq, 1, d, False)[:, :, 0].contiguous()
+    m.check_decode(q, c.decode(q))
+    assert c.device_status() == 0
