@@ -88,32 +88,46 @@ __global__ void __launch_bounds__(kThreads) int4_token_kernel(const AppendArgs a
     }
 }
 
-// Many rows: grid (groups of rows, KV heads, requests), a thread per 8 dims of a row.
-// next_position is advanced by the launch that follows.
+// Many rows: grid (groups of kRowsUnroll x 256 / (D / 8) rows, KV heads, requests), a thread per 8 dims of every
+// 256 / (D / 8)-th row of its group, their loads all issued first.  next_position is advanced by the launch that follows.
+constexpr int kRowsUnroll = 4;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a, const __grid_constant__ RowCounts g) {
     dep_wait();                                        // (no early release, as the bf16 appends)
-    constexpr int kVec = D / 8;
+    constexpr int kVec = D / 8, kStep = kThreads / kVec;
     const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y, cnt = g.val[bi];
-    const int r0 = blockIdx.x * (kThreads / kVec);
+    const int r0 = blockIdx.x * (kRowsUnroll * kStep);
     if (r0 >= cnt) return;
-    const int r = r0 + threadIdx.x / kVec, e = threadIdx.x % kVec;
-    const long long p = (long long)a.next_pos[b] + r;
-    bool there = r < cnt && !(a.ring && r < cnt - a.S);         // a ring: not overwritten later in this call
-    if (there && !position_ok(a, p)) { flag(a.hdr, kErrPosition); there = false; }
-    const int slot = there ? (a.ring ? (int)(p % a.S) : (int)p) : 0;
-    const int page = there ? slot_page(a, b, slot) : 0;
-    uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-    if (there) {
+    const int e = threadIdx.x % kVec, np = a.next_pos[b];
+    uint4 kx[kRowsUnroll], vx[kRowsUnroll];
+    int to[kRowsUnroll];                               // the row's slot, -1: no row, or none that stays
+#pragma unroll
+    for (int j = 0; j < kRowsUnroll; ++j) {
+        const int r = r0 + j * kStep + threadIdx.x / kVec;
+        const long long p = (long long)np + r;
+        kx[j] = vx[j] = make_uint4(0, 0, 0, 0);
+        to[j] = -1;
+        if (r >= cnt || (a.ring && r < cnt - a.S)) continue;       // a ring: overwritten later in this call
+        if (!position_ok(a, p)) { flag(a.hdr, kErrPosition); continue; }
+        to[j] = a.ring ? (int)(p % a.S) : (int)p;
         const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr + 8 * (size_t)e;
-        kx = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src));
-        vx = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src));
-        if (a.rope) kx = turned(a, kx, (int)p, e);
-        if (page < 0) { flag(a.hdr, kErrPosition); there = false; }
+        kx[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src));
+        vx[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src));
     }
-    const size_t o = slot_row(a, b, h, slot, page < 0 ? 0 : page) * int4::row_size(D);
-    int4::store_row<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e, kx, vx, there);
-    if (there && h == 0 && e == 0) a.pos[(size_t)b * a.S + slot] = (int)p;
+    int page[kRowsUnroll];
+#pragma unroll
+    for (int j = 0; j < kRowsUnroll; ++j) page[j] = to[j] < 0 ? -1 : slot_page(a, b, to[j]);
+#pragma unroll
+    for (int j = 0; j < kRowsUnroll; ++j) {
+        const int p = np + r0 + j * kStep + threadIdx.x / kVec;
+        if (a.rope && to[j] >= 0) kx[j] = turned(a, kx[j], p, e);
+        if (to[j] >= 0 && page[j] < 0) flag(a.hdr, kErrPosition);
+        const bool there = page[j] >= 0;
+        const size_t o = there ? slot_row(a, b, h, to[j], page[j]) * int4::row_size(D) : 0;
+        int4::store_row<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e, kx[j], vx[j], there);
+        if (there && h == 0 && e == 0) a.pos[(size_t)b * a.S + to[j]] = p;
+    }
 }
 
 // ---- decode ------------------------------------------------------------------------------------
@@ -634,7 +648,7 @@ cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cudaStream_t st) {
-    const int per = kThreads / (a.d / 8);
+    const int per = kRowsUnroll * (kThreads / (a.d / 8));
     return launch_dep(a.d == 128 ? int4_rows_kernel<128> : int4_rows_kernel<64>, dim3((a.n + per - 1) / per, a.Hkv, g.nb),
                       dim3(kThreads), 0, st, a, g);
 }

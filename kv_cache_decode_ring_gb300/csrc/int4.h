@@ -24,60 +24,75 @@ namespace int4 {
 constexpr int kGroup = 32;                 // dims that share a scale and a minimum
 __host__ __device__ constexpr int row_size(int d) { return d / 8 * 5; }
 
-// Minimum and maximum that a NaN operand makes NaN.
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {       // of two bf16 pairs; NaN where either is
+    uint32_t y;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
+
+// Any scale, any values: the quotients divided out.
+static __device__ __noinline__ uint32_t quantise_slowly(uint4 v, float lo, float d, uint32_t& scale) {
+    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(d, 15.f));
+    const float s = __bfloat162float(sb);
+    const bool number = fabsf(s) < INFINITY;
+    scale = number ? __bfloat16_as_ushort(sb) : 0x7fffu;
+    uint32_t w = 0;
+    if (number && s > 0.f)
+        for (int j = 7; j >= 0; --j) {
+            const uint32_t pair = j / 2 == 0 ? v.x : j / 2 == 1 ? v.y : j / 2 == 2 ? v.z : v.w;
+            const float x = __uint_as_float(j & 1 ? pair & 0xffff0000u : pair << 16);
+            w = (w << 4) + (uint32_t)fminf(rintf(__fdiv_rn(x - lo, s)), 15.f);
+        }
+    return w;
 }
 
 // The thread's 8 dims (bf16 values) of a group that lanes 4 k .. 4 k + 3 hold: their codes, dim j in
 // nibble j, and the group's (s, m).  Every lane of the warp calls it.
-// The quotients: t = y r with r = 1 / s correctly rounded is within an ulp or so of y / s; the fused
-// residual y - t s is exact, and t + (y - t s) r rounds correctly (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000", 1990), where neither over- nor underflows: scales
-// out of [2^-100, 2^100] divide instead.  Adding 1.5 2^23 rounds to an integer, ties to even.
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& params) {
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) { lo = min_nan(lo, x[j]); hi = max_nan(hi, x[j]); }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+// Quotients: with r = 1 / s to an ulp or two, t = y r is as close to y / s; the fused residual
+// y - t s is exact, and t + (y - t s) r is off by some 2^-45 before its last rounding, so a quotient half-way
+// between two codes (y and s are numbers of few bits: others are further away) stays there.  The scale the same
+// way, with 1 / 15 (Markstein, "Computation of elementary functions on the IBM RISC System/6000", 1990).
+// Adding 1.5 2^23 rounds to an integer, ties to even, in a float's last bits.
+// About 60 instructions for 8 values, half of them on pairs (min2 on the bf16 values, fp32 pairs behind): with
+// two values' instructions apart, divisions and an exact reciprocal, 140, a bf16 cache of 66,000 rows of 8 heads of 128 was handed
+// over in 89 us.
+__device__ __forceinline__ uint32_t quantise(const uint4& v, uint32_t& params) {
+    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+    constexpr uint32_t kSigns = 0x80008000u;
+    const uint32_t lo2 = min2(min2(a[0], a[1]), min2(a[2], a[3]));
+    const uint32_t hi2 = min2(min2(a[0] ^ kSigns, a[1] ^ kSigns), min2(a[2] ^ kSigns, a[3] ^ kSigns));    // of -x
+    uint32_t r2 = min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));                      // (min x, min -x)
+    r2 = min2(r2, __shfl_xor_sync(0xffffffffu, r2, 1));
+    r2 = min2(r2, __shfl_xor_sync(0xffffffffu, r2, 2));
+    const float lo = __uint_as_float(r2 << 16), d = -(__uint_as_float(r2 & 0xffff0000u) + lo);
+    params = r2 << 16;
+    if (!(d >= 0x1p-96f && d <= 0x1p100f)) {               // (equal values, and what is not a number, too)
+        uint32_t scale;
+        const uint32_t w = quantise_slowly(v, lo, d, scale);
+        params |= scale;
+        return w;
     }
-    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
-    float s = __bfloat162float(sb);
-    if (!(fabsf(s) < INFINITY)) {
-        sb = __ushort_as_bfloat16(0x7fff);
-        s = 0.f;                                       // codes 0
-    }
-    params = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
-    constexpr float kMagic = 12582912.f;               // 0x4B400000
-    uint32_t w = 0;
-    if (s >= 0x1p-100f && s <= 0x1p100f) {
-        const float r = __frcp_rn(s);
+    constexpr float k15 = 1.f / 15.f;
+    const float d15 = d * k15;
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fmaf_rn(__fmaf_rn(-15.f, d15, d), k15, d15));
+    const float s = __bfloat162float(sb);
+    params |= __bfloat16_as_ushort(sb);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const float2 lo_ = make_float2(-lo, -lo), s_ = make_float2(-s, -s), r_ = make_float2(r, r);
+    constexpr float kMagic = 12582912.f;                   // 0x4B400000
+    uint32_t f[8];
 #pragma unroll
-        for (int j = 7; j >= 0; --j) {
-            const float y = x[j] - lo, t = y * r;
-            const float q = __fmaf_rn(__fmaf_rn(-t, s, y), r, t);
-            w = (w << 4) + (__float_as_uint(q + kMagic) & 15u);
-        }
-    } else if (s > 0.f) {
-#pragma unroll 1
-        for (int j = 7; j >= 0; --j) {
-            float v = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v = i == j ? x[i] : v;
-            w = (w << 4) + (uint32_t)fminf(rintf(__fdiv_rn(v - lo, s)), 15.f);
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = __fadd2_rn(make_float2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u)), lo_);
+        const float2 t = __fmul2_rn(y, r_);
+        const float2 q = __fadd2_rn(__ffma2_rn(__ffma2_rn(t, s_, y), r_, t), make_float2(kMagic, kMagic));
+        f[2 * i] = __float_as_uint(q.x);
+        f[2 * i + 1] = __float_as_uint(q.y);
     }
-    return w;
+    const uint32_t even = __byte_perm(__byte_perm(f[0], f[2], 0x0040), __byte_perm(f[4], f[6], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(f[1], f[3], 0x0040), __byte_perm(f[5], f[7], 0x0040), 0x5410);
+    return even + odd * 16u;
 }
 
 // Where thread e's word of codes goes: K's word holds its 8 dims; of V's two half-words (r = 2 c and
@@ -96,14 +111,7 @@ __device__ __forceinline__ uint32_t v_codes(uint32_t w, int e) {
 
 // Swapping is its own inverse: from the words at v_word it gives each thread its 8 codes again.
 
-// The same for 8 bf16 values, and the inverse: m + u s, rounded once to bf16.
-__device__ __forceinline__ uint32_t quantise_bf16(const uint4& u, uint32_t& params) {
-    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { x[2 * i] = __uint_as_float(a[i] << 16); x[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u); }
-    return quantise(x, params);
-}
+// The inverse: 8 values m + u s, rounded once to bf16.
 __device__ __forceinline__ uint4 values_bf16(uint32_t w, uint32_t params) {
     const float s = __uint_as_float(params << 16), m = __uint_as_float(params & 0xffff0000u);
     uint32_t a[4];
@@ -131,7 +139,7 @@ __device__ __forceinline__ void store_unit(char* k, char* v, int e, uint32_t kw,
 template <int D>
 __device__ __forceinline__ void store_row(char* k, char* v, int e, const uint4& kx, const uint4& vx, bool there) {
     uint32_t kp, vp;
-    const uint32_t kw = quantise_bf16(kx, kp), vw = v_codes(quantise_bf16(vx, vp), e);
+    const uint32_t kw = quantise(kx, kp), vw = v_codes(quantise(vx, vp), e);
     if (there) store_unit<D>(k, v, e, kw, kp, vw, vp);
 }
 

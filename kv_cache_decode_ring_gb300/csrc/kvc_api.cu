@@ -467,18 +467,7 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) try {
     if (s.int8 && int8_drop_restored(h, h_cut, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
     if (s.pages && !s.ring) {
         // a contiguous cache returns the pages that lie wholly past the cut
-        bool freed = false;
-        const int npg = s.S / kPage;
-        for (int b = 0; b < s.B; ++b)
-            for (int lp = (h_cut[b] + kPage - 1) / kPage; lp < npg; ++lp) {
-                int32_t& e = h->table_h[(size_t)b * npg + lp];
-                if (e < 0) continue;
-                drop_page(h, e);
-                freed = true;
-            }
-        if (freed && cudaMemcpyAsync(h->state + h->L.table, h->table_h.data(), h->table_h.size() * 4,
-                                     cudaMemcpyHostToDevice, S_(stream)) != cudaSuccess)
-            return KVC_ERR_CUDA;
+        if (unmap_pages(h, h_cut, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
     }
     for (int b = 0; b < s.B; ++b) {
         h->np[b] = h_cut[b];

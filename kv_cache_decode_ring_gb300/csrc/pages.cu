@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kCopyThreads) convert_requests_kernel(const __
             const int r = r0 + j * kStep;
             if constexpr (QUANT) {
                 uint32_t kp, vp;
-                const uint32_t kw = int4::quantise_bf16(kx[j], kp), vw = int4::v_codes(int4::quantise_bf16(vx[j], vp), e);
+                const uint32_t kw = int4::quantise(kx[j], kp), vw = int4::v_codes(int4::quantise(vx[j], vp), e);
                 if (r >= rows) continue;
                 for (int t = 0; t < g.n; ++t) {
                     const size_t row = kv_row(a.to.table, target[t], h, s0 + r, a.Hkv, a.to.S) * kRow4;
@@ -465,6 +465,17 @@ void drop_page(kvc_handle* h, int32_t& entry) {
     if (entry < 0) return;
     if (--h->page_ref[entry] == 0) h->page_free.push_back(entry);
     entry = -1;
+}
+
+cudaError_t unmap_pages(kvc_handle* h, const int32_t* cut, cudaStream_t st) {
+    const Shape& s = h->sh;
+    const int npg = s.S / kPage;
+    std::vector<int2> upd;
+    for (int b = 0; b < s.B; ++b)
+        for (int lp = (cut[b] + kPage - 1) / kPage; lp < npg && h->table_h[(size_t)b * npg + lp] >= 0; ++lp)
+            upd.push_back(make_int2((int)((size_t)b * npg + lp), -1));     // (no page is mapped behind the rows)
+    for (const int2& u : upd) drop_page(h, h->table_h[u.x]);
+    return upd.empty() ? cudaSuccess : update_table(h, upd, st);
 }
 
 // Too few pages: nothing changes and *status = KVC_ERR_CAPACITY.  Everything is allocated before
