@@ -32,9 +32,9 @@ __device__ __forceinline__ size_t slot_row(const AppendArgs& a, int b, int h, in
     return a.table ? ((size_t)page * a.Hkv + h) * kPage + slot % kPage : ((size_t)b * a.Hkv + h) * a.S + slot;
 }
 
-// Eight dims of a key (from dim 8 e) rotated at position p, rounded to bf16 as in the bf16 cache.
-__device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4 u, int p, int e) {
-    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (a.d / 2) + 4 * e);
+// Chunk c (8 dims) of a key rotated at position p, rounded to bf16 as in the bf16 cache.
+__device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4 u, int p, int c) {
+    const float4* rp = reinterpret_cast<const float4*>(a.rope + (size_t)p * (a.d / 2) + 4 * c);
     const float4 c0 = __ldg(rp), c1 = __ldg(rp + 1);
     const float2 cs[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y), make_float2(c1.z, c1.w)};
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -48,7 +48,7 @@ __device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4 u, int 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One token per request: a CTA per request, a thread per 8 dims of a head.
+// One token per request: a CTA per request, a thread per 16 dims of a head.
 template <int D>
 __global__ void __launch_bounds__(kThreads) int4_token_kernel(const AppendArgs a) {
     dep_wait();                                        // launched dependent: see launch_dep
@@ -61,25 +61,22 @@ __global__ void __launch_bounds__(kThreads) int4_token_kernel(const AppendArgs a
         if (threadIdx.x == 0) flag(a.hdr, kErrPosition);
         return;
     }
-    constexpr int kVec = D / 8, kU = 2;
+    constexpr int kVec = D / 16;
     const int n = a.Hkv * kVec;
-    const uint4* K = static_cast<const uint4*>(a.k) + (size_t)b * n;
-    const uint4* V = static_cast<const uint4*>(a.v) + (size_t)b * n;
-    for (int base = 0; base < n; base += kU * kThreads) {
-        uint4 kx[kU] = {}, vx[kU] = {};
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = base + u * kThreads + threadIdx.x;
-            if (i < n) { kx[u] = __ldg(K + i); vx[u] = __ldg(V + i); }
+    const uint4* K = static_cast<const uint4*>(a.k) + (size_t)b * 2 * n;
+    const uint4* V = static_cast<const uint4*>(a.v) + (size_t)b * 2 * n;
+    for (int base = 0; base < n; base += kThreads) {   // (a warp's lanes stay together)
+        const int i = base + threadIdx.x, h = i < n ? i / kVec : 0, e = i % kVec, c = int4::chunk_of(e);
+        uint4 k[2] = {}, v[2] = {};
+        if (i < n) {
+            const size_t at = (size_t)h * (D / 8) + c;
+            k[0] = __ldg(K + at); k[1] = __ldg(K + at + 2);
+            v[0] = __ldg(V + at); v[1] = __ldg(V + at + 2);
+            if (a.rope) { k[0] = turned(a, k[0], p, c); k[1] = turned(a, k[1], p, c + 2); }
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = base + u * kThreads + threadIdx.x, h = i / kVec, e = i % kVec;
-            if (base + u * kThreads >= n) break;       // (the whole CTA; a warp's lanes stay together)
-            const size_t o = slot_row(a, b, i < n ? h : 0, slot, page) * int4::row_size(D);
-            int4::store_row<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e,
-                               a.rope ? turned(a, kx[u], p, e) : kx[u], vx[u], i < n);
-        }
+        const int4::Unit u = int4::quantise(k, v, e);
+        const size_t o = slot_row(a, b, h, slot, page) * int4::row_size(D);
+        if (i < n) int4::store<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e, u);
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -88,32 +85,36 @@ __global__ void __launch_bounds__(kThreads) int4_token_kernel(const AppendArgs a
     }
 }
 
-// Many rows: grid (groups of kRowsUnroll x 256 / (D / 8) rows, KV heads, requests), a thread per 8 dims of every
-// 256 / (D / 8)-th row of its group, their loads all issued first.  next_position is advanced by the launch that follows.
-constexpr int kRowsUnroll = 4;
+// Many rows: grid (groups of kRowsUnroll x 256 / (D / 16) rows, KV heads, requests), a thread per 16 dims of every
+// 256 / (D / 16)-th row of its group, their loads all issued first.  next_position is advanced by the launch that follows.
+constexpr int kRowsUnroll = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a, const __grid_constant__ RowCounts g) {
     dep_wait();                                        // (no early release, as the bf16 appends)
-    constexpr int kVec = D / 8, kStep = kThreads / kVec;
+    constexpr int kVec = D / 16, kStep = kThreads / kVec;
     const int bi = blockIdx.z, b = g.b0 + bi, h = blockIdx.y, cnt = g.val[bi];
     const int r0 = blockIdx.x * (kRowsUnroll * kStep);
     if (r0 >= cnt) return;
-    const int e = threadIdx.x % kVec, np = a.next_pos[b];
-    uint4 kx[kRowsUnroll], vx[kRowsUnroll];
+    const int e = threadIdx.x % kVec, c = int4::chunk_of(e), np = a.next_pos[b];
+    // rows [skip, fit): those before are overwritten later in this call (a ring), those behind have no place (replays)
+    const int skip = a.ring ? cnt - a.S : 0;
+    const int fit = (int)min((long long)cnt, min(a.ring ? 1ll << 31 : (long long)a.S, a.rope ? (long long)a.P : 1ll << 31) - np);
+    uint4 k[kRowsUnroll][2], v[kRowsUnroll][2];
     int to[kRowsUnroll];                               // the row's slot, -1: no row, or none that stays
 #pragma unroll
     for (int j = 0; j < kRowsUnroll; ++j) {
         const int r = r0 + j * kStep + threadIdx.x / kVec;
-        const long long p = (long long)np + r;
-        kx[j] = vx[j] = make_uint4(0, 0, 0, 0);
+        k[j][0] = k[j][1] = v[j][0] = v[j][1] = make_uint4(0, 0, 0, 0);
         to[j] = -1;
-        if (r >= cnt || (a.ring && r < cnt - a.S)) continue;       // a ring: overwritten later in this call
-        if (!position_ok(a, p)) { flag(a.hdr, kErrPosition); continue; }
-        to[j] = a.ring ? (int)(p % a.S) : (int)p;
-        const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr + 8 * (size_t)e;
-        kx[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src));
-        vx[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src));
+        if (r >= fit && r < cnt) flag(a.hdr, kErrPosition);
+        if (r >= fit || r < skip) continue;
+        to[j] = a.ring ? (np + r) % a.S : np + r;
+        const size_t src = (size_t)b * a.sb + (size_t)h * a.sh + (size_t)r * a.sr + 8 * (size_t)c;
+        const uint4* K = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + src);
+        const uint4* V = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + src);
+        k[j][0] = __ldg(K); k[j][1] = __ldg(K + 2);
+        v[j][0] = __ldg(V); v[j][1] = __ldg(V + 2);
     }
     int page[kRowsUnroll];
 #pragma unroll
@@ -121,12 +122,13 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 #pragma unroll
     for (int j = 0; j < kRowsUnroll; ++j) {
         const int p = np + r0 + j * kStep + threadIdx.x / kVec;
-        if (a.rope && to[j] >= 0) kx[j] = turned(a, kx[j], p, e);
+        if (a.rope && to[j] >= 0) { k[j][0] = turned(a, k[j][0], p, c); k[j][1] = turned(a, k[j][1], p, c + 2); }
         if (to[j] >= 0 && page[j] < 0) flag(a.hdr, kErrPosition);
-        const bool there = page[j] >= 0;
-        const size_t o = there ? slot_row(a, b, h, to[j], page[j]) * int4::row_size(D) : 0;
-        int4::store_row<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e, kx[j], vx[j], there);
-        if (there && h == 0 && e == 0) a.pos[(size_t)b * a.S + to[j]] = p;
+        const int4::Unit u = int4::quantise(k[j], v[j], e);
+        if (page[j] < 0) continue;
+        const size_t o = slot_row(a, b, h, to[j], page[j]) * int4::row_size(D);
+        int4::store<D>(static_cast<char*>(a.kc) + o, static_cast<char*>(a.vc) + o, e, u);
+        if (h == 0 && e == 0) a.pos[(size_t)b * a.S + to[j]] = p;
     }
 }
 
@@ -648,7 +650,7 @@ cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cudaStream_t st) {
-    const int per = kRowsUnroll * (kThreads / (a.d / 8));
+    const int per = kRowsUnroll * (kThreads / (a.d / 16));
     return launch_dep(a.d == 128 ? int4_rows_kernel<128> : int4_rows_kernel<64>, dim3((a.n + per - 1) / per, a.Hkv, g.nb),
                       dim3(kThreads), 0, st, a, g);
 }

@@ -12,8 +12,8 @@
 // as the decode's matrix operands take them (d/32 = G groups):
 //  K: word c G + g (c = 0..3) holds dims 32 g + 8 c + j, j = 0..7, in nibble j;
 //  V: half-word r G + g (r = 0..7) holds dims 32 g + 4 r + i, i = 0..3, in nibble i.
-// The threads that write or read a row take 8 dims each: thread e of d / 8 those of group e / 4,
-// from 8 (e mod 4) on.  The four threads of a group are neighbouring lanes of one warp.
+// The threads that write or read a row take 16 dims each, as two chunks of 8: thread e of d / 16 chunks
+// c = e mod 2 and c + 2 of group e / 2.  The two threads of a group are neighbouring lanes of one warp.
 #pragma once
 
 #include "kvc_internal.h"
@@ -30,45 +30,65 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {       // of t
     return y;
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+
 // Any scale, any values: the quotients divided out.
-static __device__ __noinline__ uint32_t quantise_slowly(uint4 v, float lo, float d, uint32_t& scale) {
-    __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(d, 15.f));
+static __device__ __noinline__ uint2 quantise_slowly(uint4 x, uint4 y, float lo, float d, uint32_t& scale) {
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(d, 15.f));
     const float s = __bfloat162float(sb);
     const bool number = fabsf(s) < INFINITY;
     scale = number ? __bfloat16_as_ushort(sb) : 0x7fffu;
-    uint32_t w = 0;
+    const uint32_t a[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t w[2] = {0, 0};
     if (number && s > 0.f)
-        for (int j = 7; j >= 0; --j) {
-            const uint32_t pair = j / 2 == 0 ? v.x : j / 2 == 1 ? v.y : j / 2 == 2 ? v.z : v.w;
-            const float x = __uint_as_float(j & 1 ? pair & 0xffff0000u : pair << 16);
-            w = (w << 4) + (uint32_t)fminf(rintf(__fdiv_rn(x - lo, s)), 15.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v0 = __uint_as_float(a[i] << 16), v1 = __uint_as_float(a[i] & 0xffff0000u);
+            w[i / 4] |= (uint32_t)fminf(rintf(__fdiv_rn(v0 - lo, s)), 15.f) << 8 * (i % 4);
+            w[i / 4] |= (uint32_t)fminf(rintf(__fdiv_rn(v1 - lo, s)), 15.f) << (8 * (i % 4) + 4);
         }
-    return w;
+    return make_uint2(w[0], w[1]);
 }
 
-// The thread's 8 dims (bf16 values) of a group that lanes 4 k .. 4 k + 3 hold: their codes, dim j in
-// nibble j, and the group's (s, m).  Every lane of the warp calls it.
-// Quotients: with r = 1 / s to an ulp or two, t = y r is as close to y / s; the fused residual
-// y - t s is exact, and t + (y - t s) r is off by some 2^-45 before its last rounding, so a quotient half-way
-// between two codes (y and s are numbers of few bits: others are further away) stays there.  The scale the same
-// way, with 1 / 15 (Markstein, "Computation of elementary functions on the IBM RISC System/6000", 1990).
-// Adding 1.5 2^23 rounds to an integer, ties to even, in a float's last bits.
-// About 60 instructions for 8 values, half of them on pairs (min2 on the bf16 values, fp32 pairs behind): with
-// two values' instructions apart, divisions and an exact reciprocal, 140, a bf16 cache of 66,000 rows of 8 heads of 128 was handed
-// over in 89 us.
-__device__ __forceinline__ uint32_t quantise(const uint4& v, uint32_t& params) {
-    const uint32_t a[4] = {v.x, v.y, v.z, v.w};
-    constexpr uint32_t kSigns = 0x80008000u;
-    const uint32_t lo2 = min2(min2(a[0], a[1]), min2(a[2], a[3]));
-    const uint32_t hi2 = min2(min2(a[0] ^ kSigns, a[1] ^ kSigns), min2(a[2] ^ kSigns, a[3] ^ kSigns));    // of -x
-    uint32_t r2 = min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));                      // (min x, min -x)
+// Codes of a chunk of 8 values y / s, dim j in nibble j: minus = (-m, -m), r = (1 / s, 1 / s), s = (-s, -s).
+// With 1 / s to an ulp or two, t = y r is as close to y / s; the fused residual y - t s is exact, and
+// t + (y - t s) r is off by some 2^-45 before its last rounding, so a quotient half-way between two codes
+// (y and s are numbers of few bits: others are further away) stays there.  Adding 1.5 2^23 rounds to an
+// integer, ties to even, in a float's last bits.
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, float2 minus, float2 r, float2 s) {
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w};
+    constexpr float kMagic = 12582912.f;                   // 0x4B400000
+    uint32_t f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = __fadd2_rn(make_float2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u)), minus);
+        const float2 t = __fmul2_rn(y, r);
+        const float2 q = __fadd2_rn(__ffma2_rn(__ffma2_rn(t, s, y), r, t), make_float2(kMagic, kMagic));
+        f[2 * i] = __float_as_uint(q.x);
+        f[2 * i + 1] = __float_as_uint(q.y);
+    }
+    const uint32_t even = __byte_perm(__byte_perm(f[0], f[2], 0x0040), __byte_perm(f[4], f[6], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(f[1], f[3], 0x0040), __byte_perm(f[5], f[7], 0x0040), 0x5410);
+    return even + odd * 16u;
+}
+
+// The thread's two chunks (bf16 values) of a group: their codes, and the group's (s, m).  Every lane of the warp calls it.
+// The scale is divided as the quotients are, with 1 / 15 (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000", 1990).
+__device__ __forceinline__ uint2 quantise(const uint4& x, const uint4& y, uint32_t& params) {
+    const uint32_t lo2 = min2(min2(min2(x.x, x.y), min2(x.z, x.w)), min2(min2(y.x, y.y), min2(y.z, y.w)));
+    const uint32_t hi2 = max2(max2(max2(x.x, x.y), max2(x.z, x.w)), max2(max2(y.x, y.y), max2(y.z, y.w))) ^ 0x80008000u;
+    uint32_t r2 = min2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));      // (min x, -max x)
     r2 = min2(r2, __shfl_xor_sync(0xffffffffu, r2, 1));
-    r2 = min2(r2, __shfl_xor_sync(0xffffffffu, r2, 2));
     const float lo = __uint_as_float(r2 << 16), d = -(__uint_as_float(r2 & 0xffff0000u) + lo);
     params = r2 << 16;
     if (!(d >= 0x1p-96f && d <= 0x1p100f)) {               // (equal values, and what is not a number, too)
         uint32_t scale;
-        const uint32_t w = quantise_slowly(v, lo, d, scale);
+        const uint2 w = quantise_slowly(x, y, lo, d, scale);
         params |= scale;
         return w;
     }
@@ -79,69 +99,86 @@ __device__ __forceinline__ uint32_t quantise(const uint4& v, uint32_t& params) {
     params |= __bfloat16_as_ushort(sb);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-    const float2 lo_ = make_float2(-lo, -lo), s_ = make_float2(-s, -s), r_ = make_float2(r, r);
-    constexpr float kMagic = 12582912.f;                   // 0x4B400000
-    uint32_t f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 y = __fadd2_rn(make_float2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u)), lo_);
-        const float2 t = __fmul2_rn(y, r_);
-        const float2 q = __fadd2_rn(__ffma2_rn(__ffma2_rn(t, s_, y), r_, t), make_float2(kMagic, kMagic));
-        f[2 * i] = __float_as_uint(q.x);
-        f[2 * i + 1] = __float_as_uint(q.y);
-    }
-    const uint32_t even = __byte_perm(__byte_perm(f[0], f[2], 0x0040), __byte_perm(f[4], f[6], 0x0040), 0x5410);
-    const uint32_t odd = __byte_perm(__byte_perm(f[1], f[3], 0x0040), __byte_perm(f[5], f[7], 0x0040), 0x5410);
-    return even + odd * 16u;
+    const float2 minus = make_float2(-lo, -lo), s_ = make_float2(-s, -s), r_ = make_float2(r, r);
+    return make_uint2(codes_of(x, minus, r_, s_), codes_of(y, minus, r_, s_));
 }
 
-// Where thread e's word of codes goes: K's word holds its 8 dims; of V's two half-words (r = 2 c and
-// 2 c + 1) the threads of groups 2 k and 2 k + 1, four lanes apart, swap one, so that each writes a word.
+// Where thread e's words of codes go.  K's words hold a chunk each, c + 2 two steps of G words behind c.  Of a
+// chunk's two half-words in V (r = 2 c and 2 c + 1) the threads of groups 2 k and 2 k + 1, two lanes apart,
+// swap one, so that each writes a word; chunk c + 2's lies four rows of half-words behind.
 template <int D>
-__device__ __forceinline__ int k_word(int e) { return (e & 3) * (D / kGroup) + (e >> 2); }
+__device__ __forceinline__ int k_word(int e) { return (e & 1) * (D / kGroup) + (e >> 1); }
 template <int D>
-__device__ __forceinline__ int v_word(int e) {         // the word that thread e writes
-    return (2 * (e & 3) + (e >> 2 & 1)) * (D / 64) + (e >> 3);
-}
+__device__ __forceinline__ int v_word(int e) { return (2 * (e & 1) + (e >> 1 & 1)) * (D / 64) + (e >> 2); }
+template <int D> constexpr int kSecondK = 2 * (D / kGroup);
+template <int D> constexpr int kSecondV = 4 * (D / 64);
+
+// From a chunk's codes to the word that the thread writes in V; its own inverse.
 __device__ __forceinline__ uint32_t v_codes(uint32_t w, int e) {
-    const bool odd = e >> 2 & 1;                       // of an odd group: takes r = 2 c + 1
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w & 0xffffu : w >> 16, 4);
+    const bool odd = e >> 1 & 1;                       // of an odd group: takes r = 2 c + 1
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? w & 0xffffu : w >> 16, 2);
     return odd ? (other & 0xffffu) | (w & 0xffff0000u) : (w & 0xffffu) | other << 16;
 }
 
-// Swapping is its own inverse: from the words at v_word it gives each thread its 8 codes again.
-
-// The inverse: 8 values m + u s, rounded once to bf16.
+// 8 values m + u s, rounded once to bf16.  Codes become the bf16 numbers 128 + u, then u; the fused multiply-add
+// of bf16 pairs rounds once.
 __device__ __forceinline__ uint4 values_bf16(uint32_t w, uint32_t params) {
-    const float s = __uint_as_float(params << 16), m = __uint_as_float(params & 0xffff0000u);
+    const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
+    const uint32_t s2 = __byte_perm(params, 0, 0x1010), m2 = __byte_perm(params, 0, 0x3232);
+    constexpr uint32_t kBias = 0x43004300u, kMinusBias = 0xc300c300u, kOne = 0x3f803f80u;
     uint32_t a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 t = __floats2bfloat162_rn(__fmaf_rn((float)(w >> 8 * i & 15u), s, m),
-                                                       __fmaf_rn((float)(w >> (8 * i + 4) & 15u), s, m));
-        a[i] = *reinterpret_cast<const uint32_t*>(&t);
+        uint32_t u, x;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(u) : "r"(even), "r"(odd), "r"(0xc480u + 0x1111u * i));   // (8 + k: the top bit of byte k, 0)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(x) : "r"(u | kBias), "r"(kOne), "r"(kMinusBias));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(x), "r"(s2), "r"(m2));
     }
     return make_uint4(a[0], a[1], a[2], a[3]);
 }
 
-// Thread e's words and, from one thread a group, its parameters into a K and a V row.
+// What thread e has of a K and a V row.
+struct Unit {
+    uint2 k, v;                                        // words
+    uint32_t kp, vp;                                   // parameters of its group
+};
+
+__device__ __forceinline__ Unit quantise(const uint4 (&k)[2], const uint4 (&v)[2], int e) {
+    Unit u;
+    u.k = quantise(k[0], k[1], u.kp);
+    u.v = quantise(v[0], v[1], u.vp);
+    u.v = make_uint2(v_codes(u.v.x, e), v_codes(u.v.y, e));
+    return u;
+}
+
 template <int D>
-__device__ __forceinline__ void store_unit(char* k, char* v, int e, uint32_t kw, uint32_t kp, uint32_t vw, uint32_t vp) {
-    reinterpret_cast<uint32_t*>(k)[k_word<D>(e)] = kw;
-    reinterpret_cast<uint32_t*>(v)[v_word<D>(e)] = vw;
-    if ((e & 3) == 0) {
-        reinterpret_cast<uint32_t*>(k + D / 2)[e >> 2] = kp;
-        reinterpret_cast<uint32_t*>(v + D / 2)[e >> 2] = vp;
+__device__ __forceinline__ void store(char* k, char* v, int e, const Unit& u) {
+    uint32_t* kw = reinterpret_cast<uint32_t*>(k) + k_word<D>(e);
+    uint32_t* vw = reinterpret_cast<uint32_t*>(v) + v_word<D>(e);
+    kw[0] = u.k.x;
+    kw[kSecondK<D>] = u.k.y;
+    vw[0] = u.v.x;
+    vw[kSecondV<D>] = u.v.y;
+    if ((e & 1) == 0) {
+        reinterpret_cast<uint32_t*>(k + D / 2)[e >> 1] = u.kp;
+        reinterpret_cast<uint32_t*>(v + D / 2)[e >> 1] = u.vp;
     }
 }
 
-// Thread e's 16 bytes of a K and a V row, quantised and stored (all lanes of the warp calling).
 template <int D>
-__device__ __forceinline__ void store_row(char* k, char* v, int e, const uint4& kx, const uint4& vx, bool there) {
-    uint32_t kp, vp;
-    const uint32_t kw = quantise(kx, kp), vw = v_codes(quantise(vx, vp), e);
-    if (there) store_unit<D>(k, v, e, kw, kp, vw, vp);
+__device__ __forceinline__ Unit load(const char* k, const char* v, int e) {
+    const uint32_t* kw = reinterpret_cast<const uint32_t*>(k) + k_word<D>(e);
+    const uint32_t* vw = reinterpret_cast<const uint32_t*>(v) + v_word<D>(e);
+    Unit u;
+    u.k = make_uint2(kw[0], kw[kSecondK<D>]);
+    u.v = make_uint2(vw[0], vw[kSecondV<D>]);
+    u.kp = reinterpret_cast<const uint32_t*>(k + D / 2)[e >> 1];
+    u.vp = reinterpret_cast<const uint32_t*>(v + D / 2)[e >> 1];
+    return u;
 }
+
+// The 16-byte unit of a bf16 row that is thread e's first chunk; the second lies two units behind.
+__device__ __forceinline__ int chunk_of(int e) { return 4 * (e >> 1) + (e & 1); }
 
 }  // namespace int4
 }  // namespace kvc

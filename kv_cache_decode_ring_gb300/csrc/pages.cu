@@ -286,9 +286,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_requests_kernel(const __gri
 }
 
 // The same between a bf16 cache and an INT4 one of D dims: rows are quantised (QUANT) or read back
-// as bf16 (m + u s rounded once) on the way.  A thread takes 8 dims of a row, K and V, as int4.h
-// lays them out; kConvertUnroll rows in flight.
-constexpr int kConvertUnroll = 4;
+// as bf16 (m + u s rounded once) on the way.  A thread takes 16 dims of a row, K and V, as int4.h
+// lays them out, kConvertUnroll rows in flight.
+constexpr int kConvertUnroll = 2;
 
 template <int D, bool QUANT>
 __global__ void __launch_bounds__(kCopyThreads) convert_requests_kernel(const __grid_constant__ CopyArgs a) {
@@ -301,46 +301,57 @@ __global__ void __launch_bounds__(kCopyThreads) convert_requests_kernel(const __
         copy_books(a, g, target);
         return;
     }
-    constexpr int kVec = D / 8, kRow4 = int4::row_size(D), kStep = kCopyThreads / kVec;
+    constexpr int kVec = D / 16, kRow4 = int4::row_size(D), kStep = kCopyThreads / kVec;
     const int s0 = blockIdx.x * kCopyBlocks * kPage, rows = min(g.rows - s0, kCopyBlocks * kPage);
     if (g.src < 0 || rows <= 0) return;
     const int e = threadIdx.x % kVec;
+    // row r from s0 of request b, as kv_row
+    auto head_row = [&](const CopySide& c, int b) { return c.table ? (size_t)h * kPage : ((size_t)b * a.Hkv + h) * c.S + s0; };
+    auto row_of = [&](const CopySide& c, int b, size_t head, int r) -> size_t {
+        if (!c.table) return head + r;
+        const int page = max(c.table[(size_t)b * (c.S / kPage) + (s0 + r) / kPage], 0);
+        return (size_t)page * (a.Hkv * kPage) + head + r % kPage;
+    };
+    const size_t from = head_row(a.from, g.src);
     for (int r0 = threadIdx.x / kVec; r0 - (int)threadIdx.x / kVec < rows; r0 += kConvertUnroll * kStep) {
-        uint4 kx[kConvertUnroll], vx[kConvertUnroll];    // (QUANT: 8 values each; else codes and parameters)
+        uint4 kx[kConvertUnroll][2], vx[kConvertUnroll][2];
+        int4::Unit u[kConvertUnroll];
 #pragma unroll
         for (int j = 0; j < kConvertUnroll; ++j) {
             const int r = r0 + j * kStep;
-            kx[j] = vx[j] = make_uint4(0, 0, 0, 0);
+            kx[j][0] = kx[j][1] = vx[j][0] = vx[j][1] = make_uint4(0, 0, 0, 0);
+            u[j] = int4::Unit{};
             if (r >= rows) continue;
-            const size_t row = kv_row(a.from.table, g.src, h, s0 + r, a.Hkv, a.from.S);
+            const size_t row = row_of(a.from, g.src, from, r);
             if constexpr (QUANT) {
-                kx[j] = reinterpret_cast<const uint4*>(a.from.part[0].base)[row * kVec + e];
-                vx[j] = reinterpret_cast<const uint4*>(a.from.part[1].base)[row * kVec + e];
+                const uint4* k = reinterpret_cast<const uint4*>(a.from.part[0].base) + row * (D / 8) + int4::chunk_of(e);
+                const uint4* v = reinterpret_cast<const uint4*>(a.from.part[1].base) + row * (D / 8) + int4::chunk_of(e);
+                kx[j][0] = k[0]; kx[j][1] = k[2];
+                vx[j][0] = v[0]; vx[j][1] = v[2];
             } else {
-                const uint32_t* k = reinterpret_cast<const uint32_t*>(a.from.part[0].base + row * kRow4);
-                const uint32_t* v = reinterpret_cast<const uint32_t*>(a.from.part[1].base + row * kRow4);
-                kx[j].x = k[int4::k_word<D>(e)]; kx[j].y = k[D / 8 + (e >> 2)];
-                vx[j].x = v[int4::v_word<D>(e)]; vx[j].y = v[D / 8 + (e >> 2)];
+                u[j] = int4::load<D>(a.from.part[0].base + row * kRow4, a.from.part[1].base + row * kRow4, e);
             }
         }
 #pragma unroll
         for (int j = 0; j < kConvertUnroll; ++j) {
             const int r = r0 + j * kStep;
             if constexpr (QUANT) {
-                uint32_t kp, vp;
-                const uint32_t kw = int4::quantise(kx[j], kp), vw = int4::v_codes(int4::quantise(vx[j], vp), e);
-                if (r >= rows) continue;
-                for (int t = 0; t < g.n; ++t) {
-                    const size_t row = kv_row(a.to.table, target[t], h, s0 + r, a.Hkv, a.to.S) * kRow4;
-                    int4::store_unit<D>(a.to.part[0].base + row, a.to.part[1].base + row, e, kw, kp, vw, vp);
-                }
+                u[j] = int4::quantise(kx[j], vx[j], e);
             } else {
-                const uint4 k = int4::values_bf16(kx[j].x, kx[j].y), v = int4::values_bf16(int4::v_codes(vx[j].x, e), vx[j].y);
-                if (r >= rows) continue;
-                for (int t = 0; t < g.n; ++t) {
-                    const size_t row = kv_row(a.to.table, target[t], h, s0 + r, a.Hkv, a.to.S) * kVec + e;
-                    reinterpret_cast<uint4*>(a.to.part[0].base)[row] = k;
-                    reinterpret_cast<uint4*>(a.to.part[1].base)[row] = v;
+                kx[j][0] = int4::values_bf16(u[j].k.x, u[j].kp); kx[j][1] = int4::values_bf16(u[j].k.y, u[j].kp);
+                vx[j][0] = int4::values_bf16(int4::v_codes(u[j].v.x, e), u[j].vp);
+                vx[j][1] = int4::values_bf16(int4::v_codes(u[j].v.y, e), u[j].vp);
+            }
+            if (r >= rows) continue;
+            for (int t = 0; t < g.n; ++t) {
+                const size_t row = row_of(a.to, target[t], head_row(a.to, target[t]), r);
+                if constexpr (QUANT) {
+                    int4::store<D>(a.to.part[0].base + row * kRow4, a.to.part[1].base + row * kRow4, e, u[j]);
+                } else {
+                    uint4* k = reinterpret_cast<uint4*>(a.to.part[0].base) + row * (D / 8) + int4::chunk_of(e);
+                    uint4* v = reinterpret_cast<uint4*>(a.to.part[1].base) + row * (D / 8) + int4::chunk_of(e);
+                    k[0] = kx[j][0]; k[2] = kx[j][1];
+                    v[0] = vx[j][0]; v[2] = vx[j][1];
                 }
             }
         }
