@@ -229,9 +229,8 @@ def kvc_append_rows(h, k: torch.Tensor, v: torch.Tensor, n: int, counts: Optiona
 
 
 def kvc_decode_attn(h, q, out, cmax=None, tanh=None, ct=None, stream=None) -> None:
-    _check(lib().kvc_decode_attn(h, _dev(q, name="q"), _dev(out, name="out"), _dev(cmax, torch.float32, name="cmax"),
-                                 _dev(tanh, torch.float32, name="tanh"), _dev(ct, torch.float32, name="ct"),
-                                 _stream(stream)), "kvc_decode_attn")
+    bounds = [None if t is None else _dev(t, torch.float32, name=n) for t, n in ((cmax, "cmax"), (tanh, "tanh"), (ct, "ct"))]
+    _check(lib().kvc_decode_attn(h, _dev(q, name="q"), _dev(out, name="out"), *bounds, _stream(stream)), "kvc_decode_attn")
 
 
 def kvc_int8_block_risk(h, ct, risk, stream=None) -> None:
@@ -603,7 +602,8 @@ class Cache:
     def decode(self, q, out=None, cmax=None, tanh=None, ct=None, stream=None):
         _dev(q, self.torch_dtype, (self.B, self.Hq, self.d), "q")
         if out is None:
-            out = _empty(q.shape, self.out_dtype, q.device, stream)
+            # (a third of the time that a tensor of a given shape, type and device takes)
+            out = torch.empty_like(q) if stream is None and self.out_dtype == q.dtype else _empty(q.shape, self.out_dtype, q.device, stream)
         _dev(out, self.out_dtype, (self.B, self.Hq, self.d), "out")
         kvc_decode_attn(self.h, q, out, cmax, tanh, ct, stream)
         return out
