@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 //    (head, lo), two fp16 parts, 22 significant bits; up to 8: a column each, 11 bits.  The groups'
 //    sums are weighed by s_tg and joined by the lane that holds head and keys;
 //  * P.V, transposed: O^T[16 dims of g][heads] += U^T . P_g^T, P_g = p s_tg times a power of two of the head's
-//    (norm) as fp16, off by 2^-11 at most, brought from score order to operand order by movmatrix.
+//    group (norm) as fp16, off by 2^-11 at most, brought from score order to operand order by movmatrix.
 //    The norm starts high and falls when a weight would pass 2^15, to put the largest at 2^9:
 //    weights down to 2^-23 of the largest stay normal.  The terms p m_tg are summed in fp32.
 // Row r of a fragment of 16 keys stands for key tok(r): rows are 80 bytes apart (d = 128), and with this
@@ -357,11 +357,11 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 
     uint32_t parity = 0;                                 // of each stage's barrier (bit)
     for (int split = blockIdx.x;; split += gridDim.x) {
-        float m_w[HL], l_w[HL], norm[HL], acc[G][2][4];
+        float m_w[HL], l_w[HL], norm[HL][G], acc[G][2][4];
         float2 gacc[G];                                      // sums of the minima's terms
 #pragma unroll
         for (int n = 0; n < HL; ++n) {
-            m_w[n] = -INFINITY; l_w[n] = 0.f; norm[n] = 0x1p100f;
+            m_w[n] = -INFINITY; l_w[n] = 0.f; for (int j = 0; j < G; ++j) norm[n][j] = 0x1p100f;
         }
 #pragma unroll
         for (int j = 0; j < G; ++j) {
@@ -512,10 +512,10 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                     for (int j = 0; j < G; ++j) {
                         const float s0 = __uint_as_float(p0[j] << 16), s1 = __uint_as_float(p1[j] << 16);
                         if constexpr (HL == 1) {
-                            pw[j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), both(norm[0])), make_float2(s0, s1));
+                            pw[j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][1][0]), both(norm[0][j])), make_float2(s0, s1));
                             top = fmax3(top, pw[j][0].x, pw[j][0].y);
                         } else {
-                            const float2 nn = make_float2(norm[0], norm[HL - 1]);
+                            const float2 nn = make_float2(norm[0][j], norm[HL - 1][j]);
                             pw[j][0] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][0][0], sc[blk][0][HL - 1]), nn), both(s0));
                             pw[j][HL - 1] = __fmul2_rn(__fmul2_rn(make_float2(sc[blk][1][0], sc[blk][1][HL - 1]), nn), both(s1));
                             top = fmax3(fmax3(top, pw[j][0].x, pw[j][0].y), pw[j][HL - 1].x, pw[j][HL - 1].y);
@@ -524,23 +524,27 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                     return top;
                 };
                 if (__any_sync(0xffffffffu, weigh() > 32768.f)) {
-                    // a head whose largest weight passes 2^15 gets a norm that puts it into [2^9, 2^10)
-                    float f[HL];
+                    // a group of a head whose largest weight passes 2^15 gets a norm that puts it into [2^9, 2^10)
 #pragma unroll
-                    for (int n = 0; n < HL; ++n) {
-                        float top = 0.f;
+                    for (int j = 0; j < G; ++j) {
+                        float f[HL];
 #pragma unroll
-                        for (int j = 0; j < G; ++j)
-                            top = fmax3(top, sc[blk][0][n] * __uint_as_float(p0[j] << 16), sc[blk][1][n] * __uint_as_float(p1[j] << 16));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                        const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                        const float to = top * norm[n] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n];
-                        f[n] = to / norm[n];
-                        norm[n] = to;
+                        for (int n = 0; n < HL; ++n) {
+                            float top = fmaxf(sc[blk][0][n] * __uint_as_float(p0[j] << 16), sc[blk][1][n] * __uint_as_float(p1[j] << 16));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                            const int e = (int)(__float_as_uint(top) >> 23) - 127;
+                            const float to = top * norm[n][j] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n][j];
+                            f[n] = to / norm[n][j];
+                            norm[n][j] = to;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
+                            acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
+                        }
                     }
-                    scale_acc(f);
                     weigh();
                 }
                 const unsigned char* xa = tV + (16 * blk + ta) * C::ROW;
@@ -590,9 +594,9 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (g == 0) { part_w[h * (D + 2)] = m_w[n]; part_w[h * (D + 2) + 1] = l; }
-            const float even = 0x1p24f / norm[n], odd = 0x1p20f / norm[n];
 #pragma unroll
             for (int j = 0; j < G; ++j) {
+                const float even = 0x1p24f / norm[n][j], odd = 0x1p20f / norm[n][j];
                 float t = HL == 1 ? gacc[j].x + gacc[j].y : n == 0 ? gacc[j].x : gacc[j].y;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);

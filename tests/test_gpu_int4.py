@@ -211,6 +211,37 @@ def test_visible_rows_that_are_not_finite_spoil_what_sees_them():
     assert out[1, 0].isnan().all()
 
 
+@pytest.mark.parametrize("hq,d", [(4, 128), (8, 128), (3, 64)])
+@pytest.mark.parametrize("what", ["large", "small", "groups", "outlier", "growing", "sharp", "query"])
+def test_decode_of_values_of_all_sizes(hq, d, what):
+    """Weights times scales stay within fp16's range, whatever the rows hold, and what is small next to them keeps its bits."""
+    n = 700
+    c = make(batch=1, n_q_heads=hq, n_kv_heads=1, head_dim=d, capacity=1024)
+    m = Model(c)
+    k, v = rows(1, 1, 1, n, d), rows(2, 1, 1, n, d, False)
+    q = rows(3, 1, hq, 1, d, False)[:, :, 0].contiguous()
+    if what == "large":
+        v *= 2.0 ** 110
+    elif what == "small":
+        v *= 2.0 ** -95
+    elif what == "groups":                           # a group of dims 2^30 times as large as the next
+        v[..., :32] *= 2.0 ** 30
+    elif what == "outlier":                          # a row of large values that hardly anything weighs
+        v[0, 0, 300] *= 2.0 ** 20
+        k[0, 0, 300] = -q[0, :1].float().sign().bfloat16() * 6
+    elif what == "growing":                          # ever larger values, and scores
+        v *= (2.0 ** torch.linspace(-20, 40, n, device="cuda"))[:, None].bfloat16()
+        k *= torch.linspace(0.1, 4, n, device="cuda")[:, None].bfloat16()
+    elif what == "sharp":
+        k *= 40
+    else:
+        q[0, :, ::7] *= 2.0 ** 12                    # a few dims decide
+        k *= 2.0 ** -8
+    c.append_rows(k, v)
+    m.append(k, v, (n,))
+    m.check_decode(q, c.decode(q), what)
+
+
 def dense(like, **kw):
     cfg = dict(batch=like.B, n_q_heads=like.Hq, n_kv_heads=like.Hkv, head_dim=like.d, capacity=like.S,
                layout="ring" if like.cfg.layout == kvc.KVC_RING else "contiguous", rope_base=like.cfg.rope_base,
