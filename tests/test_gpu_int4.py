@@ -422,3 +422,94 @@ def test_decode_of_lengths_that_the_host_does_not_know(hq, d):
     q = rows(5, 2, hq, 1, d, False)[:, :, 0].contiguous()
     m.check_decode(q, c.decode(q))
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("hkv,d", [(1, 64), (1, 128), (3, 64), (40, 128)])
+def test_token_appends_of_any_number_of_heads(hkv, d):
+    c = make(n_q_heads=hkv, n_kv_heads=hkv, head_dim=d, capacity=32, rope_base=500.0)
+    m = Model(c, 500.0)
+    for step in range(18):
+        k, v = (rows(10 * step + i, 3, hkv, 1, d) for i in range(2))
+        c.append(k[:, :, 0].contiguous(), v[:, :, 0].contiguous())
+        m.append(k, v, (1, 1, 1))
+    m.check_rows()
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "ring"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_copies_between_4_bit_caches(layout, d):
+    cap = 96 if layout == "ring" else 256
+    a, b = make(layout, head_dim=d, capacity=cap, page_pool=60), make(layout, head_dim=d, capacity=cap, batch=2)
+    m = Model(b)
+    k, v = rows(1, 3, 2, 200, d), rows(2, 3, 2, 200, d)
+    a.append_rows(k, v, counts=[200, 0, 77])
+    b.copy_from(a, [2, 0], [0, 1])
+    m.append(k[[2, 0]], v[[2, 0]], (77, 200))
+    m.check_rows()
+    a.copy_from(b, [1, 1], [1, 2])
+    m = Model(a)
+    m.append(k[[0, 0, 0]], v[[0, 0, 0]], (200, 200, 200))
+    m.check_rows()
+
+
+@pytest.mark.parametrize("B", [70, 1100])
+def test_many_requests(B):
+    # more than a sample of lengths, and than one launch of appends
+    c = make(batch=B, n_q_heads=4, n_kv_heads=1, head_dim=64, capacity=64, window=20, sinks=3)
+    k, v, q = rows(1, B, 1, 33, 64), rows(2, B, 1, 33, 64, False), rows(3, B, 4, 1, 64, False)[:, :, 0].contiguous()
+    counts = [1 + i * 7 % 33 for i in range(B)]
+    c.append_rows(k, v, counts=counts)
+    out = c.decode(q)
+    for b in range(0, B, 23 if B > 100 else 3):
+        n = counts[b]
+        p = torch.arange(n, device="cuda")
+        seen = (p >= n - 20) | (p < 3)
+        kp, vp = i4.quantise(k[b, :, :n][:, seen]), i4.quantise(v[b, :, :n][:, seen])
+        ref, w = i4.attend(q[b].double(), i4.values(*kp), i4.values(*vp))
+        assert ((out[b].double() - ref).abs() <= i4.decode_bound(q[b].double(), kp, vp, w)).all(), b
+
+
+def test_offsets_past_32_bits():
+    # rows of the last requests lie past 4 GB of K
+    c = make(batch=5, n_q_heads=16, n_kv_heads=16, capacity=1 << 20)
+    m = Model(c)
+    k, v = rows(1, 5, 16, 40, 128), rows(2, 5, 16, 40, 128)
+    c.append_rows(k, v, counts=[0, 40, 1, 3, 39])
+    k1, v1 = rows(3, 5, 16, 1, 128), rows(4, 5, 16, 1, 128)
+    c.append(k1[:, :, 0].contiguous(), v1[:, :, 0].contiguous())
+    m.append(k, v, (0, 40, 1, 3, 39))
+    m.append(k1, v1, (1,) * 5)
+    kr, vr = (x[:, :, :64] for x in c.rows())
+    for b in range(5):
+        n = m.k[b].shape[1]
+        assert torch.equal(kr[b, :, :n], i4.row_bytes(m.k[b], False)) and torch.equal(vr[b, :, :n], i4.row_bytes(m.v[b], True))
+    q = rows(5, 5, 16, 1, 128, False)[:, :, 0].contiguous()
+    m.check_decode(q, c.decode(q))
+    other = kvc.Cache(kvc.make_config(batch=5, n_q_heads=16, n_kv_heads=16, capacity=64))
+    other.copy_from(c, [4], [4])
+    got = other.rows()[0][4, :, :40]
+    assert torch.equal(got, i4.held(m.k[4]).float().bfloat16())
+
+
+def test_replayed_appends_past_the_mapped_pages_write_nothing():
+    c = make(batch=2, capacity=64, page_pool=8)
+    m = Model(c)
+    k, v = rows(1, 2, 2, 30, 128), rows(2, 2, 2, 30, 128)
+    c.append_rows(k, v, counts=[30, 14])
+    m.append(k, v, (30, 14))
+    k1, v1 = k[:, :, 0].contiguous(), v[:, :, 0].contiguous()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.append(k1, v1)
+    before = [x.clone() for x in c.rows()]
+    for _ in range(4):
+        graph.replay()                                # both requests have room for two rows in the pages of the capture
+    torch.cuda.synchronize()
+    assert c.device_status() & 1
+    table = c.export(kvc.KVC_EXPORT_PAGE_TABLE)
+    for x, y, rows_, value in ((before[0], c.rows()[0], k1, False), (before[1], c.rows()[1], v1, True)):
+        for b, n in enumerate((30, 14)):
+            page = table[b][n // 16]
+            x[page, :, n % 16:] = i4.row_bytes(rows_[b], value)[:, None]
+        assert torch.equal(x, y)

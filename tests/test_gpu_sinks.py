@@ -258,3 +258,23 @@ def test_refusals():
     with pytest.raises(kvc.KvcError) as e:
         t.c.chunk(x, x[:, :, :2].contiguous(), x[:, :, :2].contiguous())
     assert e.value.code == kvc.KVC_ERR_UNSUPPORTED
+
+
+def test_prompt_as_a_graph():
+    # a captured prompt replayed: its window leaves the sinks behind on the device
+    t = Twin("bf16", None, 1, 8, 2, 128, 512, 40, 5)
+    t.append((30,))
+    qkv = t.draw(50, 12, 128)
+    q, k, v = qkv.split([8, 2, 2], 1)
+    out = torch.empty((50, 8, 128), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.c.prompt(q, k, v, [50], out)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        cut = t.K[0].shape[1]
+        t.take(0, k.transpose(0, 1), v.transpose(0, 1))
+        t.compare(out.double(), q, 0, cut)
+    assert t.c.device_status() == 0
