@@ -254,19 +254,24 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     uint64_t* myBar = bar + warp * C::STAGES;
     const char* Kg = static_cast<const char*>(a.k);
     const char* Vg = static_cast<const char*>(a.v);
-    // tile i of this warp: its first key, and its keys (rows behind them may be anything)
-    auto tile_k0 = [&](int i) {
-        const int s = s_first + i;
-        return (s < sp.nwin ? sp.lo_t + s * kInt4Step : (s - sp.nwin) * kInt4Step) + warp * kTile;
+    // this warp's tile of a step: its first key, the end of the keys of its part, and the first (rows of others may be anything)
+    struct Tile {
+        int k0, end, lo;
     };
-    auto tile_nk = [&](int i) { return max(0, min(kTile, (s_first + i < sp.nwin ? sp.hi : sp.sunk) - tile_k0(i))); };
+    auto tile_at = [&](int s) {
+        return s < sp.nwin ? Tile{sp.lo_t + s * kInt4Step + warp * kTile, sp.hi, sp.lo}
+                           : Tile{(s - sp.nwin) * kInt4Step + warp * kTile, sp.sunk, 0};
+    };
+    auto next = [&](Tile& t, int s) {                    // to step s, the one behind
+        t.k0 += kInt4Step;
+        if (s == sp.nwin) t = Tile{warp * kTile, sp.sunk, 0};
+    };
     const int32_t* pages = a.table ? a.table + (size_t)b * (a.S / kPage) : nullptr;
     const size_t head_row0 = ((size_t)b * a.Hkv + kvh) * a.S;
     // blocks of 16 rows that hold a visible key (whole: the cache's rows are a multiple of 16)
-    auto issue = [&](int i) {
-        const int nk = tile_nk(i);
-        if (lane == 0 && nk > 0) {
-            const int sg = i % C::STAGES, k0 = tile_k0(i), nb = (nk + kPage - 1) / kPage;
+    auto issue = [&](const Tile& t, int sg) {
+        if (lane == 0 && t.k0 < t.end) {
+            const int k0 = t.k0, nb = (min(kTile, t.end - k0) + kPage - 1) / kPage;
             unsigned char* st = myS + sg * C::STAGEB;
             mbar_arrive_expect_tx(&myBar[sg], (uint32_t)(2 * nb * kPage * C::ROW));
             if (!pages) {
@@ -289,9 +294,13 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < C::STAGES; ++i)
-        if (i < tiles) issue(i);
+    static_assert(C::STAGES == 2, "stages are filled by name");
+    Tile cur = tile_at(s_first), ahead = cur;            // of the tile in use and of the last one issued
+    issue(ahead, 0);
+    if (tiles > 1) {
+        next(ahead, s_first + 1);
+        issue(ahead, 1);
+    }
 
     // the queries, rotated at t = len - 1, times log2(e)/sqrt(d); heads past nh: 0.  16 lanes hold a group.
 #pragma unroll
@@ -361,11 +370,11 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 
     uint32_t parity = 0;                                 // of each stage's barrier (bit)
     for (int split = blockIdx.x;; split += gridDim.x) {
-        float m_w[HL], l_w[HL], norm[HL][G], acc[G][2][4];
+        float base[HL], limit[HL], l_w[HL], norm[HL][G], acc[G][2][4];
         float2 gacc[G];                                      // sums of the minima's terms
 #pragma unroll
         for (int n = 0; n < HL; ++n) {
-            m_w[n] = -INFINITY;
+            base[n] = limit[n] = -INFINITY;
             l_w[n] = 0.f;
 #pragma unroll
             for (int j = 0; j < G; ++j) norm[n][j] = 0x1p100f;
@@ -376,29 +385,33 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[j][0][e] = acc[j][1][e] = 0.f;
         }
-        for (int i = 0; i < tiles; ++i) {
-            const int nk = tile_nk(i);
-            if (nk == 0) {                                   // (of the window's or the sinks' last step)
-                if (i + C::STAGES < tiles) issue(i + C::STAGES);
+        for (int i = 0; i < tiles; ++i, next(cur, s_first + i)) {
+            const int nk = cur.end - cur.k0, kmin = cur.lo - cur.k0, sg = i & 1;     // keys of the tile; those before the window
+            auto refill = [&]() {
+                if (i + 2 >= tiles) return;
+                next(ahead, s_first + i + 2);
+                issue(ahead, sg);
+            };
+            if (nk <= 0) {                                   // (of the window's or the sinks' last step)
+                refill();
                 continue;
             }
-            const int sg = i % C::STAGES;
             if (!mbar_wait(&myBar[sg], parity >> sg & 1)) {
-                // give up: flag it, and let this stage's copy and the later stages' (if issued) land
-                // before the stages are reused for the partial
+                // give up: flag it, and let this stage's copy and the other's (if issued) land before the stages are
+                // reused for the partial
                 if (lane == 0) atomicOr(a.hdr, kErrWait);
-                for (int j = i; j < i + C::STAGES && j < tiles; ++j)
-                    if (tile_nk(j) > 0) {
-                        mbar_wait(&myBar[j % C::STAGES], parity >> (j % C::STAGES) & 1);
-                        parity ^= 1u << (j % C::STAGES);
-                    }
+                mbar_wait(&myBar[sg], parity >> sg & 1);
+                parity ^= 1u << sg;
+                if (i + 1 < tiles && ahead.k0 < ahead.end) {
+                    mbar_wait(&myBar[sg ^ 1], parity >> (sg ^ 1) & 1);
+                    parity ^= 2u >> sg;
+                }
                 break;
             }
             parity ^= 1u << sg;
             const unsigned char* tK = myS + sg * C::STAGEB;
             const unsigned char* tV = tK + C::HALF;
-            const int kmin = s_first + i < sp.nwin ? sp.lo - tile_k0(i) : 0;         // keys of the tile before the window
-            const bool whole = nk == kTile && kmin <= 0;
+            const bool whole = nk >= kTile && kmin <= 0;
 
             // ---- scores of keys tr, tr + 1 of both blocks
             float sc[2][2][HL];
@@ -437,11 +450,11 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                     }
                 }
                 if constexpr (HL == 1) {
-                    sc[blk][0][0] = (x0.x + x0.y + xm.x) * unit[0];
-                    sc[blk][1][0] = (x1.x + x1.y + xm.y) * unit[0];
+                    sc[blk][0][0] = x0.x + x0.y + xm.x;
+                    sc[blk][1][0] = x1.x + x1.y + xm.y;
                 } else {
-                    sc[blk][0][0] = x0.x * unit[0]; sc[blk][0][HL - 1] = x0.y * unit[HL - 1];
-                    sc[blk][1][0] = x1.x * unit[0]; sc[blk][1][HL - 1] = x1.y * unit[HL - 1];
+                    sc[blk][0][0] = x0.x; sc[blk][0][HL - 1] = x0.y;
+                    sc[blk][1][0] = x1.x; sc[blk][1][HL - 1] = x1.y;
                 }
             }
             if (!whole) {
@@ -454,39 +467,46 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                         for (int n = 0; n < HL; ++n) sc[blk][e][n] = key < nk && key >= kmin ? sc[blk][e][n] : -INFINITY;
                     }
             }
-            // ---- online softmax of the lane's heads over the tile
-            bool rescale = false;
-            float alpha[HL];
+            // ---- online softmax of the lane's heads over the tile (base: its reference, in log2; scores above `limit`, in their own
+            // unit, move it)
+            bool grow = false;
+            float bm[HL];
 #pragma unroll
             for (int n = 0; n < HL; ++n) {
-                float bm = fmaxf(fmax3(sc[0][0][n], sc[0][1][n], sc[1][0][n]), sc[1][1][n]);
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-                const float mn = bm > m_w[n] + kLazyMax ? bm : m_w[n];
-                alpha[n] = ex2(m_w[n] - mn);                 // 0 while the maximum was -inf
-                rescale |= alpha[n] != 1.f;
-                m_w[n] = mn;
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) sc[blk][e][n] = ex2(sc[blk][e][n] - mn);          // masked keys: 0
-                l_w[n] = fmaf(l_w[n], alpha[n], (sc[0][0][n] + sc[0][1][n]) + (sc[1][0][n] + sc[1][1][n]));
+                bm[n] = fmaxf(fmax3(sc[0][0][n], sc[0][1][n], sc[1][0][n]), sc[1][1][n]);
+                bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 4));
+                bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 8));
+                bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 16));
+                grow |= bm[n] > limit[n];
             }
-            // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
-            auto scale_acc = [&](const float (&f)[HL]) {
+            if (__any_sync(0xffffffffu, grow)) {
+                // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
+                float f[HL];
 #pragma unroll
-                for (int j = 0; j < G; ++j)
+                for (int n = 0; n < HL; ++n) {
+                    const float m = bm[n] > limit[n] ? bm[n] * unit[n] : base[n];
+                    f[n] = base[n] == -INFINITY ? 0.f : ex2(base[n] - m);
+                    base[n] = m;
+                    if (bm[n] > limit[n]) limit[n] = bm[n] + kLazyMax / unit[n];
+                    l_w[n] *= f[n];
+                }
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    gacc[j] = __fmul2_rn(gacc[j], make_float2(f[0], f[HL - 1]));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
                         acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
                     }
-            };
-            if (__any_sync(0xffffffffu, rescale) && i > 0) {  // at i = 0 the accumulators are 0
-                scale_acc(alpha);
+                }
+            }
 #pragma unroll
-                for (int j = 0; j < G; ++j) gacc[j] = __fmul2_rn(gacc[j], make_float2(alpha[0], alpha[HL - 1]));
+            for (int n = 0; n < HL; ++n) {
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sc[blk][e][n] = ex2(fmaf(sc[blk][e][n], unit[n], -base[n]));     // masked keys: 0
+                l_w[n] += (sc[0][0][n] + sc[0][1][n]) + (sc[1][0][n] + sc[1][1][n]);
             }
             // ---- P.V, a block at a time
 #pragma unroll
@@ -587,7 +607,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             // the stage is free once every lane is past its reads
             __syncwarp();
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (i + C::STAGES < tiles) issue(i + C::STAGES);
+            refill();
         }
 
         // ---- this warp's partial into its own stages (every issued tile was waited for): l and the
@@ -600,7 +620,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             float l = l_w[n];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (g == 0) { part_w[h * (D + 2)] = m_w[n]; part_w[h * (D + 2) + 1] = l; }
+            if (g == 0) { part_w[h * (D + 2)] = base[n]; part_w[h * (D + 2) + 1] = l; }
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 const float even = 0x1p24f / norm[n][j], odd = 0x1p20f / norm[n][j];
@@ -639,9 +659,12 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         tiles = min(per, sp.steps - s_first);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < C::STAGES; ++i)
-            if (i < tiles) issue(i);
+        cur = ahead = tile_at(s_first);
+        issue(ahead, 0);
+        if (tiles > 1) {
+            next(ahead, s_first + 1);
+            issue(ahead, 1);
+        }
     }
 }
 
