@@ -421,7 +421,8 @@ int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride
  * four bits).
  * No row depends on another: kvc_append, kvc_append_rows, kvc_trim, kvc_fork, kvc_copy, kvc_free,
  * kvc_compact and the store take this tier as they take a bf16 cache, contiguous with any window or a
- * ring, paged or not.  head_dim 64 or 128, capacity a multiple of 16, any number of query heads.
+ * ring, paged or not.  head_dim 64 or 128, capacity a multiple of 16, any number of query heads a KV head (at
+ * most 65534 groups of 8 in all).
  * kvc_copy between a bf16 cache and one of this tier converts: rows written are quantised, rows
  * read back are m + u s, rounded once to bf16.  (A prompt runs on a bf16 cache and is handed over.)
  * kvc_decode_attn attends to the rows m + u s with fp32 sums (the weights of codes rounded to fp16, relative
