@@ -228,7 +228,7 @@ struct I4 {
     static_assert(HALF % 16 == 0 && kPage * ROW % 16 == 0, "bulk copies");
 };
 
-template <int D, int HL>
+template <int D, int HL, bool PAGED>
 __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_decode_kernel(const DecodeArgs a, const int chunks) {
     using C = I4<D, HL>;
     constexpr int G = C::G;
@@ -266,22 +266,35 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         t.k0 += kInt4Step;
         if (s == sp.nwin) t = Tile{warp * kTile, sp.sunk, 0};
     };
-    const int32_t* pages = a.table ? a.table + (size_t)b * (a.S / kPage) : nullptr;
+    const int32_t* pages = PAGED ? a.table + (size_t)b * (a.S / kPage) : nullptr;
     const size_t head_row0 = ((size_t)b * a.Hkv + kvh) * a.S;
-    // blocks of 16 rows that hold a visible key (whole: the cache's rows are a multiple of 16)
-    auto issue = [&](const Tile& t, int sg) {
+    // paged: lane i holds the pages of both blocks of the warp's tile i of the split, all loaded in one round trip (looked up
+    // tile by tile, before each copy, 16 requests of 8192 keys and 64 query heads took 65 us, 60 us so)
+    int2 page = make_int2(0, 0);
+    auto look_up = [&]() {
+        if (!PAGED || lane >= tiles) return;
+        const Tile t = tile_at(s_first + lane);
+        // (unmapped: only behind a replay's flagged append)
+        if (t.k0 < t.end) page.x = max(pages[t.k0 / kPage], 0);
+        if (t.k0 + kPage < t.end) page.y = max(pages[t.k0 / kPage + 1], 0);
+    };
+    // tile i of the split into stage i mod 2: blocks of 16 rows that hold a visible key (whole: the cache's rows are a
+    // multiple of 16); called by the whole warp
+    auto issue = [&](const Tile& t, int i) {
+        const int sg = i & 1;
+        int2 at = make_int2(0, 0);
+        if (PAGED) at = make_int2(__shfl_sync(0xffffffffu, page.x, i), __shfl_sync(0xffffffffu, page.y, i));
         if (lane == 0 && t.k0 < t.end) {
             const int k0 = t.k0, nb = (min(kTile, t.end - k0) + kPage - 1) / kPage;
             unsigned char* st = myS + sg * C::STAGEB;
             mbar_arrive_expect_tx(&myBar[sg], (uint32_t)(2 * nb * kPage * C::ROW));
-            if (!pages) {
+            if (!PAGED) {
                 const size_t o = (head_row0 + k0) * C::ROW;
                 bulk_copy_g2s(st, Kg + o, nb * kPage * C::ROW, &myBar[sg]);
                 bulk_copy_g2s(st + C::HALF, Vg + o, nb * kPage * C::ROW, &myBar[sg]);
             } else {
                 for (int j = 0; j < nb; ++j) {
-                    const int page = max(pages[k0 / kPage + j], 0);    // (unmapped: only behind a replay's flagged append)
-                    const size_t o = ((size_t)page * a.Hkv + kvh) * kPage * C::ROW;
+                    const size_t o = ((size_t)(j ? at.y : at.x) * a.Hkv + kvh) * kPage * C::ROW;
                     bulk_copy_g2s(st + j * kPage * C::ROW, Kg + o, kPage * C::ROW, &myBar[sg]);
                     bulk_copy_g2s(st + C::HALF + j * kPage * C::ROW, Vg + o, kPage * C::ROW, &myBar[sg]);
                 }
@@ -296,6 +309,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     __syncwarp();
     static_assert(C::STAGES == 2, "stages are filled by name");
     Tile cur = tile_at(s_first), ahead = cur;            // of the tile in use and of the last one issued
+    look_up();
     issue(ahead, 0);
     if (tiles > 1) {
         next(ahead, s_first + 1);
@@ -390,7 +404,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             auto refill = [&]() {
                 if (i + 2 >= tiles) return;
                 next(ahead, s_first + i + 2);
-                issue(ahead, sg);
+                issue(ahead, i + 2);
             };
             if (nk <= 0) {                                   // (of the window's or the sinks' last step)
                 refill();
@@ -660,6 +674,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
         cur = ahead = tile_at(s_first);
+        look_up();
         issue(ahead, 0);
         if (tiles > 1) {
             next(ahead, s_first + 1);
@@ -671,12 +686,14 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 template <int D, int HL>
 cudaError_t launch_t(const DecodeArgs& a, int splits, int chunks, cudaStream_t st) {
     using C = I4<D, HL>;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(int4_decode_kernel<D, HL>), C::SMEM)) return e;
-    return launch_dep(int4_decode_kernel<D, HL>, dim3(splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
+    auto kernel = a.table ? int4_decode_kernel<D, HL, true> : int4_decode_kernel<D, HL, false>;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), C::SMEM)) return e;
+    return launch_dep(kernel, dim3(splits, a.Hkv * chunks, a.B), dim3(kWarps * 32), C::SMEM, st, a, chunks);
 }
 
 }  // namespace
 
+static_assert(kInt4StepsMost <= 32, "a split's tiles (their pages) fit in a warp's lanes");
 static_assert(kInt4Step == kWarps * kTile && kInt4Heads == 8, "split and head shapes");
 
 cudaError_t launch_int4_append_token(const AppendArgs& a, cudaStream_t st) {
