@@ -637,15 +637,15 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             if (g == 0) { part_w[h * (D + 2)] = base[n]; part_w[h * (D + 2) + 1] = l; }
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                const float even = 0x1p24f / norm[n][j], odd = 0x1p20f / norm[n][j];
+                const float unit_w = 1.f / norm[n][j];   // (codes' units first: 2^24 / norm may pass fp32's range)
                 float t = HL == 1 ? gacc[j].x + gacc[j].y : n == 0 ? gacc[j].x : gacc[j].y;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
                 float* o = part_w + h * (D + 2) + 2 + 32 * j + 4 * g;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    o[2 * k] = fmaf(acc[j][k][n], even, t);
-                    o[2 * k + 1] = fmaf(acc[j][k][2 + n], odd, t);
+                    o[2 * k] = fmaf(acc[j][k][n] * 0x1p24f, unit_w, t);
+                    o[2 * k + 1] = fmaf(acc[j][k][2 + n] * 0x1p20f, unit_w, t);
                 }
             }
         }

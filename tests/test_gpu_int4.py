@@ -242,6 +242,19 @@ def test_decode_of_values_of_all_sizes(hq, d, what):
     m.check_decode(q, c.decode(q), what)
 
 
+@pytest.mark.parametrize("hq,d", [(4, 128), (8, 128), (3, 64)])
+def test_decode_of_values_near_the_end_of_the_range(hq, d):
+    # scales of 2^113: the norm of their weights is below 2^-104, its inverse times a code's unit past fp32
+    n = 700
+    c = make(batch=1, n_q_heads=hq, n_kv_heads=1, head_dim=d, capacity=1024)
+    m = Model(c)
+    k, v = rows(1, 1, 1, n, d), rows(2, 1, 1, n, d, False) * 2.0 ** 115
+    c.append_rows(k, v)
+    m.append(k, v, (n,))
+    q = rows(3, 1, hq, 1, d, False)[:, :, 0].contiguous()
+    m.check_decode(q, c.decode(q))
+
+
 def dense(like, **kw):
     cfg = dict(batch=like.B, n_q_heads=like.Hq, n_kv_heads=like.Hkv, head_dim=like.d, capacity=like.S,
                layout="ring" if like.cfg.layout == kvc.KVC_RING else "contiguous", rope_base=like.cfg.rope_base,
