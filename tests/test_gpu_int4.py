@@ -255,6 +255,17 @@ def test_decode_of_values_near_the_end_of_the_range(hq, d):
     m.check_decode(q, c.decode(q))
 
 
+@pytest.mark.parametrize("hq,d", [(4, 128), (8, 64)])
+@pytest.mark.parametrize("n,spoilt", [(1, 1), (300, 300), (5000, 5000), (5000, 4096)])
+def test_keys_that_are_all_nan_spoil_the_answer(hq, d, n, spoilt):
+    # (whole splits of them too: those have no largest score)
+    c = make(batch=1, n_q_heads=hq, n_kv_heads=1, head_dim=d, capacity=5008)
+    k, v = rows(1, 1, 1, n, d), rows(2, 1, 1, n, d)
+    k[:, :, :spoilt] = math.nan
+    c.append_rows(k, v)
+    assert c.decode(rows(3, 1, hq, 1, d, False)[:, :, 0].contiguous()).isnan().all()
+
+
 def dense(like, **kw):
     cfg = dict(batch=like.B, n_q_heads=like.Hq, n_kv_heads=like.Hkv, head_dim=like.d, capacity=like.S,
                layout="ring" if like.cfg.layout == kvc.KVC_RING else "contiguous", rope_base=like.cfg.rope_base,
