@@ -11,6 +11,7 @@
 // GQA: the g query heads of a KV head are served by the same CTA, so every K/V
 // row is read from memory once per KV head.  Single-query decode needs no
 // causal mask: every cached row precedes the query ([LOOP] §六).
+#include <cfloat>
 #include <type_traits>
 
 #include "kvc_internal.h"
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
     const size_t row = (size_t)blockIdx.x * kRowsPerCta + r;
     const bool valid = row < (size_t)c.B * c.Hq;
     const bool vec = c.d % 4 == 0;
+    const bool spoils = c.int4 || c.sinks;
     int ns = 0;
     const float2* ml = c.part_ml + row * c.max_splits;
     const float* pa = c.part_acc + row * c.max_splits * c.d;
@@ -176,6 +178,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_rows_kernel(const Com
             for (int u = 0; u < kCombineU; ++u) {
                 const int s = s0 + u * kWarpsPerRow;
                 v[u] = s < ns ? __ldg(ml + s) : make_float2(-INFINITY, 0.f);
+                // (keys that are all NaN have no largest score: their split must not pass for an empty one)
+                if (spoils && v[u].y != v[u].y) v[u].x = fmaxf(v[u].x, -FLT_MAX);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int i0 = 4 * lane + 128 * k;

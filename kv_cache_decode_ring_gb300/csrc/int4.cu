@@ -6,7 +6,6 @@
 //     score_t   = sum_g s_tg (q_g . u_tg) + m_tg sum(q_g),
 //     out_x     = sum_t p_t s_tg u_tx + sum_t p_t m_tg          (x in group g).
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 
 #include "async_copy.h"
@@ -666,8 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
             }
             const size_t row = ((size_t)b * a.Hq + (size_t)kvh * a.g + h0 + h) * a.max_splits + split;
             a.part_acc[row * D + x] = sum;
-            // (keys that are all NaN have no largest score: their split must not pass for an empty one)
-            if (x == 0) a.part_ml[row] = make_float2(l == l ? mx : fmaxf(mx, -FLT_MAX), l);
+            if (x == 0) a.part_ml[row] = make_float2(mx, l);
         }
         if (split + (int)gridDim.x >= nsplit) return;
         // a launch of fewer CTAs than splits (lengths that the host does not know): the stages are free once read

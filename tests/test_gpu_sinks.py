@@ -167,6 +167,27 @@ def test_decode_masked_rows_may_hold_anything(kernel, pages):
     assert torch.isfinite(t.decode()[1]).all()
 
 
+@pytest.mark.parametrize("kernel", KERNELS, ids=lambda k: "-".join(map(str, k)))
+@pytest.mark.parametrize("n", [1, 300])
+def test_decode_of_keys_that_are_all_nan(kernel, n):
+    dtype, quant, hq, hkv, d = kernel
+    c = Twin(dtype, quant, 1, hq, hkv, d, 512, 100, 20, base=0.0).c
+    k = draw(1, (1, hkv, n, d), c.torch_dtype) * math.nan
+    c.append_rows(k, draw(2, k.shape, c.torch_dtype))
+    assert c.decode(draw(3, (1, hq, d), c.torch_dtype)).isnan().all()
+
+
+@pytest.mark.parametrize("d", [64, 80])
+def test_splits_of_sinks_that_are_all_nan_spoil_the_answer(d):
+    # 1 split of the window and 24 of the sinks, 64 keys each, joined by 8 warps: all that the third one takes
+    c = Twin("f32", None, 1, 2, 1, d, 2048, 17, 1500, base=0.0).c
+    k = draw(1, (1, 1, 2000, d), torch.float32)
+    for i in (1, 9, 17):
+        k[:, :, 64 * i:64 * i + 64] = math.nan
+    c.append_rows(k, draw(2, k.shape, torch.float32))
+    assert c.decode(draw(3, (1, 2, d), torch.float32)).isnan().all()
+
+
 def test_decode_as_a_graph_and_without_allocation():
     """Replays move the window past the sinks on the device; the fixed-scratch variant agrees."""
     t = Twin("bf16", None, 2, 8, 2, 128, 256, 20, 3)
