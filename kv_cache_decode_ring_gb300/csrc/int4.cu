@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 //  * P.V, transposed: O^T[16 dims of g][heads] += U^T . P_g^T, P_g = p s_tg times a power of two of the head's
 //    group (norm) as fp16, off by 2^-11 at most, brought from score order to operand order by movmatrix.
 //    The norm starts high and falls when a weight would pass 2^15, to put the largest at 2^9:
-//    weights down to 2^-23 of the largest stay normal.  The terms p m_tg are summed in fp32.
+//    weights down to 2^-23 of the largest stay normal.  It rises as earlier weights fall behind a
+//    softmax reference that moves.  The terms p m_tg are summed in fp32.
 // Row r of a fragment of 16 keys stands for key tok(r): rows are 80 bytes apart (d = 128), and with this
 // order the lanes' 16-byte loads of K (rows r, r + 1 together) and 8-byte loads of V (rows 0, 2, 4, 6
 // together) fall into different banks.
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 constexpr int kWarps = 4;
 constexpr int kTile = 32;
 constexpr float kLazyMax = 4.f;                          // log2-domain headroom of the reference maximum
+constexpr int kNormMost = 100;                           // the highest norm: 2^kNormMost
 
 __device__ __forceinline__ int tok(int r) { return r & 1 ? 8 + ((r + 3) & 7) : r; }      // rows 0..7; row r + 8: tok(r) + 1
 
@@ -384,14 +386,14 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
 
     uint32_t parity = 0;                                 // of each stage's barrier (bit)
     for (int split = blockIdx.x;; split += gridDim.x) {
-        float base[HL], limit[HL], l_w[HL], norm[HL][G], acc[G][2][4];
+        float base[HL], l_w[HL], norm[HL][G], acc[G][2][4];
         float2 gacc[G];                                      // sums of the minima's terms
 #pragma unroll
         for (int n = 0; n < HL; ++n) {
-            base[n] = limit[n] = -INFINITY;
+            base[n] = -INFINITY;
             l_w[n] = 0.f;
 #pragma unroll
-            for (int j = 0; j < G; ++j) norm[n][j] = 0x1p100f;
+            for (int j = 0; j < G; ++j) norm[n][j] = power_of_two(kNormMost);
         }
 #pragma unroll
         for (int j = 0; j < G; ++j) {
@@ -481,8 +483,8 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                         for (int n = 0; n < HL; ++n) sc[blk][e][n] = key < nk && key >= kmin ? sc[blk][e][n] : -INFINITY;
                     }
             }
-            // ---- online softmax of the lane's heads over the tile (base: its reference, in log2; scores above `limit`, in their own
-            // unit, move it)
+            // ---- online softmax of the lane's heads over the tile (base: its reference, in log2; scores kLazyMax
+            // above move it)
             bool grow = false;
             float bm[HL];
 #pragma unroll
@@ -491,26 +493,36 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                 bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 4));
                 bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 8));
                 bm[n] = fmaxf(bm[n], __shfl_xor_sync(0xffffffffu, bm[n], 16));
-                grow |= bm[n] > limit[n];
+                grow |= bm[n] * unit[n] > base[n] + kLazyMax;
             }
             if (__any_sync(0xffffffffu, grow)) {
-                // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing
+                // the accumulators' columns are heads 2 qd and 2 qd + 1, or the lane's head and nothing.  A reference is a whole
+                // number, so it moves by a power of two, which the products take up in their norm: what they hold stays as it is,
+                // and weights to come keep their bits however much larger the values were that no longer weigh
+                int up[HL];                                  // 2^up: by how much earlier weights fall
                 float f[HL];
 #pragma unroll
                 for (int n = 0; n < HL; ++n) {
-                    const float m = bm[n] > limit[n] ? bm[n] * unit[n] : base[n];
-                    f[n] = base[n] == -INFINITY ? 0.f : ex2(base[n] - m);
-                    base[n] = m;
-                    if (bm[n] > limit[n]) limit[n] = bm[n] + kLazyMax / unit[n];
+                    const float m = bm[n] * unit[n];
+                    up[n] = m > base[n] + kLazyMax ? (int)fminf(ceilf(m) - base[n], 400.f) : 0;
+                    if (up[n] > 0) base[n] = ceilf(m);
+                    f[n] = up[n] > 126 ? 0.f : power_of_two(-up[n]);
                     l_w[n] *= f[n];
                 }
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
                     gacc[j] = __fmul2_rn(gacc[j], make_float2(f[0], f[HL - 1]));
+                    float left[HL];                          // 1, but where the norm reaches its highest
+#pragma unroll
+                    for (int n = 0; n < HL; ++n) {
+                        const int e = (int)(__float_as_uint(norm[n][j]) >> 23) - 127 + up[n], to = min(e, kNormMost);
+                        norm[n][j] = power_of_two(to);
+                        left[n] = e - to > 126 ? 0.f : power_of_two(to - e);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        acc[j][0][e] *= f[HL == 1 ? 0 : e & 1];
-                        acc[j][1][e] *= f[HL == 1 ? 0 : e & 1];
+                        acc[j][0][e] *= left[HL == 1 ? 0 : e & 1];
+                        acc[j][1][e] *= left[HL == 1 ? 0 : e & 1];
                     }
                 }
             }
@@ -576,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                             const int e = (int)(__float_as_uint(top) >> 23) - 127;
-                            const float to = top * norm[n][j] > 32768.f ? power_of_two(max(-118, min(100, 9 - e))) : norm[n][j];
+                            const float to = top * norm[n][j] > 32768.f ? power_of_two(max(-118, min(kNormMost, 9 - e))) : norm[n][j];
                             f[n] = to / norm[n][j];
                             norm[n][j] = to;
                         }
