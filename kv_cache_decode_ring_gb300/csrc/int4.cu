@@ -160,7 +160,9 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 constexpr int kWarps = 4;
 constexpr int kTile = 32;
 constexpr float kLazyMax = 4.f;                          // log2-domain headroom of the reference maximum
-constexpr int kNormMost = 100;                           // the highest norm: 2^kNormMost
+// The highest norm: a weight, 2^kLazyMax at most, stays within fp32 with it, and the least normal scale (2^-126) leaves weights down
+// to 2^-8 normal in fp16.
+constexpr int kNormMost = 120;
 
 __device__ __forceinline__ int tok(int r) { return r & 1 ? 8 + ((r + 3) & 7) : r; }      // rows 0..7; row r + 8: tok(r) + 1
 

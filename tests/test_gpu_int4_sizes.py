@@ -70,3 +70,17 @@ def test_values_that_fall_step_by_step(hq, d):
     c.append_rows(k, v)
     m.append(k, v, (n,) * B)
     check(m, q, c.decode(q), (0, 9, B - 1))
+
+
+@pytest.mark.parametrize("hq,d", SHAPES)
+@pytest.mark.parametrize("size", [-108, -115, -120])
+def test_tiny_values_keep_their_bits(hq, d, size):
+    # (scales of 2^-122 at the last size, normal numbers of bf16)
+    B, hkv, n = 2, 16, 300
+    c = make(batch=B, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, capacity=304)
+    m = Model(c)
+    q, k = scores_rise(hq, hkv, d, B, n, 100)
+    v = rows(2, B, hkv, n, d, False) * 2.0 ** size
+    c.append_rows(k, v)
+    m.append(k, v, (n,) * B)
+    check(m, q, c.decode(q), range(B))
