@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         y0 *= a.scale_log2;
         y1 *= a.scale_log2;
         *reinterpret_cast<float2*>(sQ + h * D + 2 * i) = make_float2(y0, y1);
-        float sum = y0 + y1, top = fmaxf(fabsf(y0), fabsf(y1));
+        float sum = (y0 + y1) * 0x1p-5f, top = fmaxf(fabsf(y0), fabsf(y1));     // (32 dims of any size stay within fp32)
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         float m = sTop[h * G];
 #pragma unroll
         for (int j = 1; j < G; ++j) m = fmaxf(m, sTop[h * G + j]);
-        return max(-102, min(100, 15 + 126 - (int)(__float_as_uint(m) >> 23)));
+        return min(120, 15 + 126 - (int)(__float_as_uint(m) >> 23));         // -114 for infinities and NaN
     };
     uint32_t qb[G][2][2];
     {
@@ -376,13 +376,16 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
     }
     // the lane's heads: sums of the query over a group in the accumulators' unit, and that unit
     float qsum[HL][G], unit[HL];
+    bool vast = false;                                   // a unit past 2^126 (queries from 2^119 on): its rest goes into the scores
 #pragma unroll
     for (int n = 0; n < HL; ++n) {
         const int h = HL * qd + n, e = exponent(h);
-        unit[n] = power_of_two(24 - e);
+        unit[n] = power_of_two(min(24 - e, 126));
+        vast |= 24 - e > 126;
 #pragma unroll
-        for (int j = 0; j < G; ++j) qsum[n][j] = sSum[h * G + j] * power_of_two(e - 24);
+        for (int j = 0; j < G; ++j) qsum[n][j] = ldexpf(sSum[h * G + j], e - 24 + 5);
     }
+    vast = __any_sync(0xffffffffu, vast);
 
     const int tr = tok(g), ta = tok(2 * qd), tb = tok(2 * qd + 1);     // keys of rows g, 2 qd, 2 qd + 1 (and + 8: the next)
 
@@ -473,6 +476,16 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                 } else {
                     sc[blk][0][0] = x0.x; sc[blk][0][HL - 1] = x0.y;
                     sc[blk][1][0] = x1.x; sc[blk][1][HL - 1] = x1.y;
+                }
+            }
+            if (vast) {
+#pragma unroll
+                for (int n = 0; n < HL; ++n) {
+                    const float rest = power_of_two(max(24 - exponent(HL * qd + n) - 126, 0));
+#pragma unroll
+                    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) sc[blk][e][n] *= rest;
                 }
             }
             if (!whole) {

@@ -84,3 +84,19 @@ def test_tiny_values_keep_their_bits(hq, d, size):
     c.append_rows(k, v)
     m.append(k, v, (n,) * B)
     check(m, q, c.decode(q), range(B))
+
+
+@pytest.mark.parametrize("hq,d", SHAPES)
+@pytest.mark.parametrize("size", [-124, -100, 100, 118, 122, 127])
+def test_queries_of_all_sizes(hq, d, size):
+    # keys as small as the queries are large, or as large as they are small; a head's largest dim up to the end of bf16's range
+    B, hkv, n = 2, 16, 300
+    c = make(batch=B, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, capacity=304)
+    m = Model(c)
+    g = torch.Generator().manual_seed(7)
+    q = (torch.rand((B, hq, d), generator=g) * 0.99).bfloat16().cuda() * 2.0 ** size
+    k, v = rows(1, B, hkv, n, d, False) * 2.0 ** min(-size, 120), rows(2, B, hkv, n, d, False)
+    k[:, :, ::3] *= 4
+    c.append_rows(k, v)
+    m.append(k, v, (n,) * B)
+    check(m, q, c.decode(q), range(B))
