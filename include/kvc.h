@@ -425,9 +425,9 @@ int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride
  * most 65534 groups of 8 in all).
  * kvc_copy between a bf16 cache and one of this tier converts: rows written are quantised, rows
  * read back are m + u s, rounded once to bf16.  (A prompt runs on a bf16 cache and is handed over.)
- * kvc_decode_attn attends to the rows m + u s with fp32 sums (the weights of codes rounded to fp16, relative
- * error 2^-11 at most, and so is the query where a KV head has more than 4 query heads; else the query has 22
- * bits); d_cmax and d_tanh receive 0 and d_ct must be NULL.
+ * kvc_decode_attn attends to the rows m + u s with fp32 sums; query and weights meet the codes in two fp16 parts
+ * (relative error 2^-21 at most; of a query's dim 2^-39 of its head's largest, of a weight times its scale 2^-32 of
+ * the largest in its group, where that is more); d_cmax and d_tanh receive 0 and d_ct must be NULL.
  * kvc_prompt_attn, kvc_chunk_attn and kvc_decode_attn_noalloc return KVC_ERR_UNSUPPORTED. */
 
 /* ---- gated fallback of the INT8 tier ----------------------------------

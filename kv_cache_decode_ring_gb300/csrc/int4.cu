@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 
 // ---- decode ------------------------------------------------------------------------------------
 // Bound by the matrix instructions and the ALU pipe, close to the memory's rate: 8 requests of 131072 keys, 8 KV
-// heads of 128, 32 query heads in 250 us (5.4 TB/s; copies alone 198).  An SM takes some 260 cycles for a tile of 32 keys,
-// 32 matrix instructions of 8 and 350 ALU instructions of 2 on each of its quarters for four of them.
+// heads of 128, 32 query heads in 256 us (5.2 TB/s; copies alone 198).  An SM takes some 270 cycles for a tile of 32 keys,
+// 32 matrix instructions of 8 and 370 ALU instructions of 2 on each of its quarters for four of them.
 // CTA = 4 warps = a split of the keys of one request and KV head, for up to 8 of its query heads; a warp
 // streams tiles of 32 keys through its stages of shared memory by bulk copies (a page, or 16 rows, is
 // contiguous).  Both products on the tensor cores (mma m16n8k16, fp16 operands, fp32
@@ -145,11 +145,12 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 // (subnormal) and without a bias, so a word's 8 codes take four ANDs and a shift; the factor 16 of
 // every other one is taken back in the query, or in the output.
 //  * scores, transposed: S^T[16 keys][cols] = U[16][32 dims of g] . Q^T, the query times log2(e)/sqrt(d) and
-//    a power of two that puts its largest value below 2^15.  Up to 4 heads: columns (head, hi) and
-//    (head, lo), two fp16 parts, 22 significant bits; up to 8: a column each, 11 bits.  The groups'
-//    sums are weighed by s_tg and joined by the lane that holds head and keys;
+//    a power of two that puts its largest value below 2^15.  It enters in two fp16 parts, 21 significant
+//    bits: up to 4 heads as columns (head, hi) and (head, lo), up to 8 as columns of two instructions (one part
+//    of 11 bits: rings of 32768, 64 query heads, 49 us, with both parts of query and weights 57).  The groups' sums are weighed by
+//    s_tg and joined by the lane that holds head and keys;
 //  * P.V, transposed: O^T[16 dims of g][heads] += U^T . P_g^T, P_g = p s_tg times a power of two of the head's
-//    group (norm) as fp16, off by 2^-11 at most, brought from score order to operand order by movmatrix.
+//    group (norm) in two fp16 parts as the query's, brought from score order to operand order by movmatrix.
 //    The norm starts high and falls when a weight would pass 2^15, to put the largest at 2^9:
 //    weights down to 2^-23 of the largest stay normal.  It rises as earlier weights fall behind a
 //    softmax reference that moves.  The terms p m_tg are summed in fp32.
@@ -208,6 +209,12 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
     const __half2 t = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&t);
 }
+
+// The leading 11 bits of a pair, exact in fp16 from 2^-14 on, and what they leave.
+__device__ __forceinline__ float2 first_part(float2 x) {
+    return make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffffe000u), __uint_as_float(__float_as_uint(x.y) & 0xffffe000u));
+}
+__device__ __forceinline__ float2 rest_of(float2 x, float2 first) { return __ffma2_rn(first, make_float2(-1.f, -1.f), x); }
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }      // -126 .. 127
 
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
         for (int j = 1; j < G; ++j) m = fmaxf(m, sTop[h * G + j]);
         return min(120, 15 + 126 - (int)(__float_as_uint(m) >> 23));         // -114 for infinities and NaN
     };
-    uint32_t qb[G][2][2];
+    uint32_t qb[G][2][2], ql[HL == 1 ? 1 : G][2][2];       // (up to 4 heads: both parts in qb's columns)
     {
         const int hcol = HL == 1 ? g / 2 : g;
         const float up = power_of_two(exponent(hcol));
@@ -370,7 +377,9 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                 for (int k = 0; k < 2; ++k) {
                     const float f = k == 0 ? up : up * 0.0625f, x = q[2 * s + k] * f, y = q[2 * s + k + 4] * f;
                     const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
-                    qb[j][s][k] = HL == 1 && (g & 1) ? pack_half(x - __half2float(xh), y - __half2float(yh)) : pack_half(x, y);
+                    const uint32_t rest = pack_half(x - __half2float(xh), y - __half2float(yh));
+                    qb[j][s][k] = HL == 1 && (g & 1) ? rest : pack_half(x, y);
+                    if constexpr (HL == 2) ql[j][s][k] = rest;
                 }
         }
     }
@@ -459,6 +468,10 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                     float c[4];
                     mma_first(c, u.x[0], v.x[0], u.x[1], v.x[1], qb[j][0][0], qb[j][0][1]);
                     mma(c, u.x[2], v.x[2], u.x[3], v.x[3], qb[j][1][0], qb[j][1][1]);
+                    if constexpr (HL == 2) {
+                        mma(c, u.x[0], v.x[0], u.x[1], v.x[1], ql[j][0][0], ql[j][0][1]);
+                        mma(c, u.x[2], v.x[2], u.x[3], v.x[3], ql[j][1][0], ql[j][1][1]);
+                    }
                     const float m0 = __uint_as_float(p0[j] & 0xffff0000u), m1 = __uint_as_float(p1[j] & 0xffff0000u);
                     x0 = __ffma2_rn(both(__uint_as_float(p0[j] << 16)), make_float2(c[0], c[1]), x0);
                     x1 = __ffma2_rn(both(__uint_as_float(p1[j] << 16)), make_float2(c[2], c[3]), x1);
@@ -639,10 +652,16 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                     const int sel = j & 1 ? 0x7632 : 0x5410;
                     const Pairs u = pairs_of(__byte_perm(wa[j / 2], wb[j / 2], sel)), v = pairs_of(__byte_perm(wc[j / 2], wd[j / 2], sel));
                     const float2 p = pw[j][0], r = pw[j][HL - 1];
-                    const uint32_t b0 = transposed(HL == 1 ? pack_half(p.x, 0.f) : pack_half(p.x, p.y));
-                    const uint32_t b1 = transposed(HL == 1 ? pack_half(p.y, 0.f) : pack_half(r.x, r.y));
+                    const float2 ph = first_part(p), rh = first_part(r), pl = rest_of(p, ph), rl = rest_of(r, rh);
+                    const uint32_t b0 = transposed(HL == 1 ? pack_half(ph.x, pl.x) : pack_half(ph.x, ph.y));
+                    const uint32_t b1 = transposed(HL == 1 ? pack_half(ph.y, pl.y) : pack_half(rh.x, rh.y));
                     mma(acc[j][0], u.x[0], u.x[1], v.x[0], v.x[1], b0, b1);
                     mma(acc[j][1], u.x[2], u.x[3], v.x[2], v.x[3], b0, b1);
+                    if constexpr (HL == 2) {
+                        const uint32_t c0 = transposed(pack_half(pl.x, pl.y)), c1 = transposed(pack_half(rl.x, rl.y));
+                        mma(acc[j][0], u.x[0], u.x[1], v.x[0], v.x[1], c0, c1);
+                        mma(acc[j][1], u.x[2], u.x[3], v.x[2], v.x[3], c0, c1);
+                    }
                 }
             }
             // the stage is free once every lane is past its reads
@@ -671,8 +690,10 @@ __global__ void __launch_bounds__(kWarps * 32, HL == 1 || D == 64 ? 4 : 3) int4_
                 float* o = part_w + h * (D + 2) + 2 + 32 * j + 4 * g;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    o[2 * k] = fmaf(acc[j][k][n] * 0x1p24f, unit_w, t);
-                    o[2 * k + 1] = fmaf(acc[j][k][2 + n] * 0x1p20f, unit_w, t);
+                    // (one head: the second column is its weights' second part)
+                    const float x = HL == 1 ? acc[j][k][0] + acc[j][k][1] : acc[j][k][n], y = HL == 1 ? acc[j][k][2] + acc[j][k][3] : acc[j][k][2 + n];
+                    o[2 * k] = fmaf(x * 0x1p24f, unit_w, t);
+                    o[2 * k + 1] = fmaf(y * 0x1p20f, unit_w, t);
                 }
             }
         }
