@@ -759,23 +759,33 @@ cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cud
 // estimate: a step takes an SM kStepUs, a CTA kCtaUs of its own, which resident ones hide from each other.  Over one to
 // 32 steps it picked the fastest or one within 4 % of it in nine of ten batches (one request of 8192 keys: 14 us with 1 step,
 // 27 with 16; 64 query heads over 4 rings of 32768: 47 with 27, 57 with 16).
-int steps_per_split(const kvc_handle* h, int chunks, int resident) {
+int steps_per_split(const kvc_handle* h, int whole, int chunks, int resident) {
     const Shape& s = h->sh;
     constexpr float kStepUs = 0.5f, kCtaUs = 5.f;
     const float rows = (float)s.Hkv * chunks, sms = (float)h->num_sms;
-    const int lowest = s.split / kInt4Step, most = s.B <= 64 ? s.B : 64;
-    int steps[64];                                       // of each request, of a sample of many
-    for (int i = 0; i < most; ++i) steps[i] = int4_span(h->np[(size_t)i * s.B / most], s.S, s.W, s.ring, s.sinks).steps;
-    const int whole = *std::max_element(steps, steps + most);
+    const int lowest = s.split / kInt4Step;
+    // every request counts, wherever it stands in the batch: in classes of alike numbers of steps, by a class's mean
+    constexpr int kClasses = 64;
+    const int width = (whole + kClasses - 1) / kClasses;
+    int count[kClasses] = {}, steps[kClasses], classes = 0;
+    long long sum[kClasses] = {};
+    for (int b = 0; b < s.B; ++b) {
+        const int n = int4_span(h->np[b], s.S, s.W, s.ring, s.sinks).steps;
+        ++count[(n - 1) / width];
+        sum[(n - 1) / width] += n;
+    }
+    for (int i = 0; i < kClasses; ++i) {
+        if (count[i] == 0) continue;
+        count[classes] = count[i];
+        steps[classes++] = (int)((sum[i] + count[i] - 1) / count[i]);
+    }
     int best = lowest;
     float least = INFINITY;
     for (int per = lowest; per <= std::max(lowest, std::min(kInt4StepsMost, whole)); ++per) {
-        int ctas = 0, longest = 0;
-        for (int i = 0; i < most; ++i) {
-            ctas += (steps[i] + per - 1) / per;
-            longest = std::max(longest, std::min(steps[i], per));
-        }
-        const float per_sm = ctas * rows * s.B / most / sms, waves = per_sm / resident;
+        float ctas = 0.f;
+        for (int i = 0; i < classes; ++i) ctas += (float)count[i] * (float)((steps[i] + per - 1) / per);
+        const int longest = std::min(whole, per);
+        const float per_sm = ctas * rows / sms, waves = per_sm / resident;
         const float load = waves <= 1.f ? std::ceil(per_sm) : per_sm + 0.5f;
         const float us = load * longest * kStepUs + kCtaUs * (waves <= 1.f ? 1.f : waves + 0.5f);
         if (us < least) { least = us; best = per; }
@@ -788,12 +798,11 @@ cudaError_t launch_int4_decode(const kvc_handle* h, DecodeArgs a, CombineArgs c,
     const int chunks = int4_chunks(s), heads = (s.g + chunks - 1) / chunks;
     // a captured call serves lengths that nobody knows: as many CTAs as the cache may need
     const bool fixed = capturing(st);
-    const int per = fixed ? std::max(s.split / kInt4Step, 4) : steps_per_split(h, chunks, heads <= 4 || s.d == 64 ? 4 : 3);
+    int whole = 1;                                       // steps of the longest request
+    for (int b = 0; b < s.B && !fixed; ++b) whole = std::max(whole, int4_span(h->np[b], s.S, s.W, s.ring, s.sinks).steps);
+    const int per = fixed ? std::max(s.split / kInt4Step, 4) : steps_per_split(h, whole, chunks, heads <= 4 || s.d == 64 ? 4 : 3);
     a.split = c.split = per * kInt4Step;
-    int splits = 1;
-    for (int b = 0; b < s.B && !fixed; ++b)
-        splits = std::max(splits, (int4_span(h->np[b], s.S, s.W, s.ring, s.sinks).steps + per - 1) / per);
-    if (fixed) splits = (s.max_splits * s.split + a.split - 1) / a.split;
+    const int splits = fixed ? (s.max_splits * s.split + a.split - 1) / a.split : (whole + per - 1) / per;
     cudaError_t e;
     if (s.d == 128) e = heads <= 4 ? launch_t<128, 1>(a, splits, chunks, st) : launch_t<128, 2>(a, splits, chunks, st);
     else e = heads <= 4 ? launch_t<64, 1>(a, splits, chunks, st) : launch_t<64, 2>(a, splits, chunks, st);

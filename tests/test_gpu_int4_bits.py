@@ -67,3 +67,19 @@ def test_long(n, hq, d, sharp):
     m.append(k, v, (n,))
     q = rows(3, 1, hq, 1, d, False)[:, :, 0].contiguous()
     m.check_decode(q, c.decode(q))
+
+
+def test_answers_do_not_depend_on_the_order_of_requests():
+    # 128 requests, 32 of them long: where those stand in the batch changes neither the splits nor, with them, any bit
+    B, hkv, hq, d, long_, short = 128, 4, 16, 128, 6000, 90
+    g = torch.Generator().manual_seed(1)
+    lens = [long_ - 7 * b if b % 4 == 3 else 1 + (short + b) % 100 for b in range(B)]
+    k, v = rows(1, 1, hkv, long_, d), rows(2, 1, hkv, long_, d, False)
+    q = rows(3, B, hq, 1, d, False)[:, :, 0].contiguous()
+    outs = []
+    for order in (list(range(B)), sorted(range(B), key=lambda b: lens[b]), torch.randperm(B, generator=g).tolist()):
+        c = make(batch=B, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, capacity=6000)
+        c.append_rows(k.expand(B, -1, -1, -1).contiguous(), v.expand(B, -1, -1, -1).contiguous(), counts=[lens[b] for b in order])
+        out = c.decode(q[order].contiguous())
+        outs.append(torch.empty_like(out).index_copy_(0, torch.tensor(order, device="cuda"), out))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
