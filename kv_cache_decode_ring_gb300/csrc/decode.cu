@@ -39,11 +39,15 @@ __device__ void load_query(const DecodeArgs& a, int b, int kvh, int t, int bf16,
     }
 }
 
+constexpr size_t kSmemPerSm = 228 * 1024;
+constexpr int kFewCtas = 256;            // a grid bound by latency
+
 // Generic kernel: any dtype, any even d <= 256, any group size.  CTA =
 // (chunk of kGenericSplit keys, KV head, request).  Straightforward two-pass
 // evaluation of its chunk in shared memory.  Where the keys and values fit there too (STAGE), they are
 // copied first, all loads on their way together: with a thread's loads along a row, or down a column, of its own 4
-// requests of 500 fp32 keys of 80 dims in pages took 35 us, 17 so.
+// requests of 500 fp32 keys of 80 dims in pages took 35 us, 17 so; 32 of 8192 bf16 keys of 256 dims, 4 query heads on each of 8
+// KV heads, 7.7 and 4.3 ms.
 template <int BF16, bool SINKS, bool STAGE>
 __global__ void __launch_bounds__(kThreads) decode_generic_kernel(const DecodeArgs a) {
     extern __shared__ float smem[];
@@ -71,13 +75,18 @@ __global__ void __launch_bounds__(kThreads) decode_generic_kernel(const DecodeAr
     __syncthreads();
     if constexpr (STAGE) {
         const int half = d / 2;
+        // (pairs stay as they are loaded until all are on their way: a conversion beside each load waits for it)
+        using Pair = std::conditional_t<BF16, __nv_bfloat162, float2>;
         auto pair = [&](const void* p, size_t at) {
-            return BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(static_cast<const __nv_bfloat16*>(p) + at))
-                        : *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+            return *reinterpret_cast<const Pair*>(static_cast<const char*>(p) + at * (sizeof(Pair) / 2));
+        };
+        auto wide = [](Pair x) {
+            if constexpr (BF16) return __bfloat1622float2(x);
+            else return x;
         };
         constexpr int kU = 10;                 // pairs of K and of V a thread has on their way
         for (int base = threadIdx.x; base < nk * half; base += kU * kThreads) {
-            float2 x[kU], y[kU];
+            Pair x[kU], y[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 const int idx = base + u * kThreads, j = idx / half;
@@ -90,8 +99,9 @@ __global__ void __launch_bounds__(kThreads) decode_generic_kernel(const DecodeAr
             for (int u = 0; u < kU; ++u) {
                 const int idx = base + u * kThreads, j = idx / half, to = j * (d + 1) + 2 * (idx - j * half);
                 if (idx >= nk * half) continue;
-                keys[to] = x[u].x; keys[to + 1] = x[u].y;
-                vals[to] = y[u].x; vals[to + 1] = y[u].y;
+                const float2 xw = wide(x[u]), yw = wide(y[u]);
+                keys[to] = xw.x; keys[to + 1] = xw.y;
+                vals[to] = yw.x; vals[to + 1] = yw.y;
             }
         }
         __syncthreads();
@@ -276,7 +286,11 @@ cudaError_t launch_decode(const DecodeArgs& a, const CombineArgs& c, bool fast, 
         size_t smem = (size_t)a.g * (a.d + a.split) * sizeof(float);
         const size_t staged = smem + (size_t)a.split * (2 * (a.d + 1) * sizeof(float) + sizeof(size_t));
         // (the grant is always the largest, so shapes of different sizes never narrow it)
-        const bool stage = staged <= kMaxSmemPerBlock;
+        // Where no heads share the rows, a copy is read once only and pays by its latency: not in a large grid whose rows
+        // are read as fast without (32 requests of 2048 keys, 8 heads: bf16 of 256 dims 520 us without, 780 with; of 80, 90 and
+        // 88), fp32 rows with one CTA left on an SM (256 dims: 540 and 800; 128 dims 276 and 190).
+        const bool pair = 2 * (staged + 1024) <= kSmemPerSm, few = (long long)grid.x * grid.y * grid.z <= kFewCtas;
+        const bool stage = staged <= kMaxSmemPerBlock && (a.g > 1 || few || (pair && !a.bf16));
         auto pick = [&](auto sinks, auto st) {
             return a.bf16 ? decode_generic_kernel<1, decltype(sinks)::value, decltype(st)::value>
                           : decode_generic_kernel<0, decltype(sinks)::value, decltype(st)::value>;
