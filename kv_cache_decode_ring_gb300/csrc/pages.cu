@@ -479,13 +479,17 @@ void drop_page(kvc_handle* h, int32_t& entry) {
     entry = -1;
 }
 
-cudaError_t unmap_pages(kvc_handle* h, const int32_t* cut, cudaStream_t st) {
+std::vector<int2> pages_past(const kvc_handle* h, const int32_t* cut) {
     const Shape& s = h->sh;
     const int npg = s.S / kPage;
     std::vector<int2> upd;
     for (int b = 0; b < s.B; ++b)
         for (int lp = (cut[b] + kPage - 1) / kPage; lp < npg && h->table_h[(size_t)b * npg + lp] >= 0; ++lp)
             upd.push_back(make_int2((int)((size_t)b * npg + lp), -1));     // (no page is mapped behind the rows)
+    return upd;
+}
+
+cudaError_t unmap_pages(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st) {
     for (const int2& u : upd) drop_page(h, h->table_h[u.x]);
     return upd.empty() ? cudaSuccess : update_table(h, upd, st);
 }
