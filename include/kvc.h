@@ -412,7 +412,8 @@ int kvc_rope_axes(const void* d_x, int64_t x_stride, void* d_y, int64_t y_stride
  * A cache of bf16 inputs and outputs whose rows are quantised as they are written: 4-bit codes u
  * with a scale s and a minimum m per 32 dims of a row,
  *     m = min x,  s = bf16((max x - min x) / 15),  u = rint((x - m) / s) in 0..15,  x ~ m + u s
- * (differences and quotients in fp32, ties to even; s = 0 gives u = 0).  |x - (m + u s)| <= s / 2.  Keys
+ * (differences and quotients in fp32, ties to even; s = 0 gives u = 0).  |x - (m + u s)| <= s / 2 for
+ * s >= 2^-126; at most the group's range max x - min x for smaller s.  Keys
  * are quantised as the bf16 cache would store them, rotated and rounded.  A group of 32 that
  * holds an infinity or NaN (or spans more than fp32 holds) reads as NaN.
  * 5 bits an element: a row takes 5 d / 8 bytes, the codes (d / 2 bytes) and then the bf16 pair

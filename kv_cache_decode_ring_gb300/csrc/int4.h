@@ -6,6 +6,7 @@
 // too small for a scale) gives u = 0, and a group that holds an infinity or NaN, or whose range
 // passes fp32's, reads back as NaN (s = NaN).  m is one of the row's bf16 values, so it is exact;
 // s off by 2^-8 leaves the largest quotient below 15.06, so |x - (m + u s)| <= s / 2.
+// That is for s >= 2^-126: a subnormal s, or one that underflows, is off by more, and x by the group's range at most.
 //
 // 5 d / 8 bytes: d / 2 of codes, then for each group the bf16 pair (s, m).  A row depends on no
 // other row, so a cache may be trimmed, wrapped, paged and copied at any row.  The codes lie
