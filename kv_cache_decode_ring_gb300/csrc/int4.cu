@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) int4_rows_kernel(const AppendArgs a,
 // ---- decode ------------------------------------------------------------------------------------
 // Bound by the matrix instructions and the ALU pipe, close to the memory's rate: 8 requests of 131072 keys, 8 KV
 // heads of 128, 32 query heads in 256 us (5.2 TB/s; copies alone 198).  An SM takes some 270 cycles for a tile of 32 keys,
-// 32 matrix instructions of 8 and 370 ALU instructions of 2 on each of its quarters for four of them.
+// 32 matrix instructions of 8 and 360 ALU instructions of 2 on each of its quarters for four of them.
 // CTA = 4 warps = a split of the keys of one request and KV head, for up to 8 of its query heads; a warp
 // streams tiles of 32 keys through its stages of shared memory by bulk copies (a page, or 16 rows, is
 // contiguous).  Both products on the tensor cores (mma m16n8k16, fp16 operands, fp32
@@ -756,9 +756,9 @@ cudaError_t launch_int4_append_rows(const AppendArgs& a, const RowCounts& g, cud
 
 // Steps per split, by the host's lengths.  Three CTAs or four keep an SM as busy as it gets, so the SM with the longest
 // CTAs counts: as many of one length as fill the SMs evenly, or many more than are resident.  The
-// estimate: a step takes an SM kStepUs, a CTA kCtaUs of its own, which resident ones hide from each other.  Over one to
-// 32 steps it picked the fastest or one within 4 % of it in nine of ten batches (one request of 8192 keys: 14 us with 1 step,
-// 27 with 16; 64 query heads over 4 rings of 32768: 47 with 27, 57 with 16).
+// estimate: a step takes an SM kStepUs, a CTA kCtaUs of its own, which resident ones hide from each other.  Over 30
+// batches and one to 32 steps it picked the fastest, or one within 3 % or 2 us of it (64 query heads over 4 x 32768 keys: 57 us with 19
+// steps, 148 with 1, 66 with 32).
 int steps_per_split(const kvc_handle* h, int whole, int chunks, int resident) {
     const Shape& s = h->sh;
     constexpr float kStepUs = 0.5f, kCtaUs = 5.f;
