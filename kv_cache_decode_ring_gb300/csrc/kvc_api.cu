@@ -461,14 +461,14 @@ int kvc_trim(kvc_t h, const int32_t* h_cut, kvc_stream_t stream) try {
         if (s.ring && !ring_cut_ok(h, np, h->held_lo[b], cut)) return KVC_ERR_EVICTED;
         if (s.int8 && (cut % kQBlock) && cut < (np / kQBlock) * kQBlock) return KVC_ERR_EVICTED;
     }
-    // a contiguous cache returns the pages that lie wholly past the cut (listed before anything changes)
-    std::vector<int2> freed;
-    if (s.pages && !s.ring) freed = pages_past(h, h_cut);
     if (launch_trim_cuts(at<int32_t>(h, h->L.next_pos), at<int32_t>(h, h->L.pos), h_cut, s.B, s.S, s.ring,
                          S_(stream)) != cudaSuccess)
         return KVC_ERR_CUDA;
     if (s.int8 && int8_drop_restored(h, h_cut, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
-    if (unmap_pages(h, freed, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
+    if (s.pages && !s.ring) {
+        // a contiguous cache returns the pages that lie wholly past the cut
+        if (unmap_pages(h, h_cut, S_(stream)) != cudaSuccess) return KVC_ERR_CUDA;
+    }
     for (int b = 0; b < s.B; ++b) {
         h->np[b] = h_cut[b];
         if (s.ring && h->held_lo[b] > h_cut[b]) h->held_lo[b] = h_cut[b];

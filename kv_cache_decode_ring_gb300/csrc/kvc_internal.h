@@ -196,9 +196,8 @@ cudaError_t map_pages(kvc_handle* h, const std::vector<int>& from, const std::ve
 // one entry of the host block table gives its page up (entry = -1); the page is free once
 // its last holder did
 void drop_page(kvc_handle* h, int32_t& entry);
-// ... the table entries of a contiguous cache whose pages lie wholly past cut[b]; they give them up
-std::vector<int2> pages_past(const kvc_handle* h, const int32_t* cut);
-cudaError_t unmap_pages(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st);
+// ... every request b of a contiguous cache gives up the pages that lie wholly past cut[b]
+cudaError_t unmap_pages(kvc_handle* h, const int32_t* cut, cudaStream_t st);
 // ... the distinct requests reqs[i] give all their pages up and map those of slots [lo[i], hi[i])
 cudaError_t remap_pages(kvc_handle* h, const std::vector<int>& reqs, const std::vector<int>& lo,
                         const std::vector<int>& hi, cudaStream_t st, int* status);

@@ -46,18 +46,25 @@ cudaError_t update_some(int32_t* table, const int2* upd, size_t n, cudaStream_t 
     return launch_dep(table_update_kernel<N>, dim3(((int)n + 255) / 256), dim3(256), 0, st, u, table);
 }
 
+cudaError_t send_table(kvc_handle* h, cudaStream_t st) {
+    return cudaMemcpyAsync(h->state + h->L.table, h->table_h.data(), h->table_h.size() * 4, cudaMemcpyHostToDevice, st);
+}
+
 // The changed entries; very many at once (a large prefill), the whole table.
-cudaError_t update_table(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st) {
+cudaError_t update_table(kvc_handle* h, const int2* upd, size_t count, cudaStream_t st) {
     int32_t* table = reinterpret_cast<int32_t*>(h->state + h->L.table);
-    if (upd.size() > 4 * (size_t)kMany)
-        return cudaMemcpyAsync(table, h->table_h.data(), h->table_h.size() * 4, cudaMemcpyHostToDevice, st);
-    for (size_t i0 = 0; i0 < upd.size(); i0 += kMany) {
-        const size_t n = std::min<size_t>(kMany, upd.size() - i0);
-        const cudaError_t e = n <= kFew ? update_some<kFew>(table, upd.data() + i0, n, st)
-                                        : update_some<kMany>(table, upd.data() + i0, n, st);
+    if (count > 4 * (size_t)kMany) return send_table(h, st);
+    for (size_t i0 = 0; i0 < count; i0 += kMany) {
+        const size_t n = std::min<size_t>(kMany, count - i0);
+        const cudaError_t e = n <= kFew ? update_some<kFew>(table, upd + i0, n, st)
+                                        : update_some<kMany>(table, upd + i0, n, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+cudaError_t update_table(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st) {
+    return update_table(h, upd.data(), upd.size(), st);
 }
 
 // ---- copies of whole pages -------------------------------------------------------
@@ -479,19 +486,22 @@ void drop_page(kvc_handle* h, int32_t& entry) {
     entry = -1;
 }
 
-std::vector<int2> pages_past(const kvc_handle* h, const int32_t* cut) {
+// Nothing is allocated (page_free has room for every page).  More entries than one launch takes go with the whole table where
+// that is not much larger: 32 requests of 512 table entries each that give up 125 pages, 38 us a trim, in four launches 52.
+cudaError_t unmap_pages(kvc_handle* h, const int32_t* cut, cudaStream_t st) {
+    static thread_local int2 upd[4 * kMany];
     const Shape& s = h->sh;
     const int npg = s.S / kPage;
-    std::vector<int2> upd;
+    size_t n = 0;
     for (int b = 0; b < s.B; ++b)
-        for (int lp = (cut[b] + kPage - 1) / kPage; lp < npg && h->table_h[(size_t)b * npg + lp] >= 0; ++lp)
-            upd.push_back(make_int2((int)((size_t)b * npg + lp), -1));     // (no page is mapped behind the rows)
-    return upd;
-}
-
-cudaError_t unmap_pages(kvc_handle* h, const std::vector<int2>& upd, cudaStream_t st) {
-    for (const int2& u : upd) drop_page(h, h->table_h[u.x]);
-    return upd.empty() ? cudaSuccess : update_table(h, upd, st);
+        for (int lp = (cut[b] + kPage - 1) / kPage; lp < npg; ++lp, ++n) {
+            const size_t idx = (size_t)b * npg + lp;
+            if (h->table_h[idx] < 0) break;                // (no page is mapped behind the rows)
+            if (n < 4 * kMany) upd[n] = make_int2((int)idx, -1);
+            drop_page(h, h->table_h[idx]);
+        }
+    if (n == 0) return cudaSuccess;
+    return n > kMany && h->table_h.size() <= 16 * n ? send_table(h, st) : update_table(h, upd, n, st);
 }
 
 // Too few pages: nothing changes and *status = KVC_ERR_CAPACITY.  Everything is allocated before
