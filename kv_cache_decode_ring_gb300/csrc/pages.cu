@@ -501,7 +501,8 @@ cudaError_t unmap_pages(kvc_handle* h, const int32_t* cut, cudaStream_t st) {
             drop_page(h, h->table_h[idx]);
         }
     if (n == 0) return cudaSuccess;
-    return n > kMany && h->table_h.size() <= 16 * n ? send_table(h, st) : update_table(h, upd, n, st);
+    // (a graph gets the entries themselves: a captured copy would read the host's table at each replay)
+    return n > kMany && h->table_h.size() <= 16 * n && !capturing(st) ? send_table(h, st) : update_table(h, upd, n, st);
 }
 
 // Too few pages: nothing changes and *status = KVC_ERR_CAPACITY.  Everything is allocated before

@@ -36,3 +36,25 @@ def test_tables_and_answers_after_a_trim(capacity, cuts):
             # two bf16 parts of query and weights, fp32 sums: far below the rows' own size
             assert ((out[b, 0].double() - w @ vv).abs() <= 2e-3 * (w @ vv.abs())).all()
     assert c.device_status() == 0
+
+
+def test_captured_trims_give_up_the_pages_of_their_capture():
+    # 1280 pages, more than a launch carries: what the host's table becomes later does not reach a replay
+    B, n, d = 40, 2048, 64
+    c = kvc.Cache(kvc.make_config(batch=B, n_q_heads=1, n_kv_heads=1, head_dim=d, capacity=n, page_pool=B * n // 16))
+    k = torch.randn((B, 1, n, d), device="cuda").bfloat16()
+    c.append_rows(k, k)
+    torch.cuda.synchronize()
+    before = c.export(kvc.KVC_EXPORT_PAGE_TABLE)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.trim([1536] * B)
+    assert np.array_equal(c.export(kvc.KVC_EXPORT_PAGE_TABLE), before)             # nothing has run yet
+    graph.replay()
+    torch.cuda.synchronize()
+    after = c.export(kvc.KVC_EXPORT_PAGE_TABLE)
+    assert np.array_equal(after[:, :96], before[:, :96]) and (after[:, 96:] == -1).all()
+    c.append_rows(k[:, :, :512].contiguous(), k[:, :, :512].contiguous())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(c.export(kvc.KVC_EXPORT_PAGE_TABLE), after)
